@@ -425,6 +425,162 @@ TP_API tp_status tp_layer_bwd(tp_layer *h, const void *const *dY, const void *co
 TP_API tp_status tp_fp8_quantize(const void *const *in, void *const *out, const int64_t *n, int nbuf,
                                  int fmt, float *amax, void *stream);
 
+/* ---- block norm: the residual stream between one block and the next ---------
+ * (the walk-through s03: every sub-block's input norm and the add after it;
+ * "Megatron-LM 源码精读" s3.5: both run on token shards under sequence
+ * parallelism.)  With the block's output F (the MLP's Y without residual):
+ *   p = P(F)                      post-norm of the block's output
+ *   Y = residual_scale * X + block_scale * gate (.) p
+ *   N = N(Y)                      the next block's pre-norm, of Y as stored
+ * P and N are, per token over H, none, RMS: x / sqrt(mean(x^2) + eps) * w, or
+ * LAYER: (x - mean) / sqrt(var + eps) * w + b (population variance); with
+ * zero_centered the weight is 1 + w.  gate: none, one value per channel [H]
+ * (a parameter), per token [M], or per element [M, H].  Without a block
+ * (has_block = 0, the norm before the first block) Y is X and N = N(X).
+ * All sums and products are fp32; Y and N are rounded once each.
+ *   Types.  dtype is that of F, N, gate and the norms' weights and biases
+ *     (TP_DT_F32 or TP_DT_BF16); X and Y (and dX, dY) have it too, or are fp32
+ *     with residual_f32.  Parameter gradients are fp32.
+ *   Shards.  X, F, Y, N, token and element gates and their gradients are
+ *     1-entry pointer arrays, or T token shards under seq_parallel (any M/T).
+ *     stats is one [M, 4] fp32 buffer in token order.
+ *   Overlap.  Y may be X, and dX may be dY (the same buffers); no other output
+ *     may overlap an input.
+ * Results are deterministic (no atomics).  The handle holds host state only
+ * and takes no device status word: the kernels wait on nothing. */
+typedef enum { TP_NORM_NONE = 0, TP_NORM_RMS = 1, TP_NORM_LAYER = 2 } tp_norm_kind;
+typedef enum { TP_GATE_NONE = 0, TP_GATE_CHANNEL = 1, TP_GATE_TOKEN = 2, TP_GATE_ELEMENT = 3 } tp_gate_kind;
+typedef struct {
+    int S, B, H, T;        /* M = S*B tokens of H channels; T token shards under seq_parallel */
+    int dtype;             /* TP_DT_F32 or TP_DT_BF16 */
+    int residual_f32;      /* X, Y, dX, dY are fp32 */
+    int seq_parallel;
+    int has_block;         /* 0: no F, no Y: N = N(X) */
+    int post, pre;         /* tp_norm_kind */
+    int gate;              /* tp_gate_kind */
+    int zero_centered;     /* norm weights are 1 + w */
+    float eps;             /* > 0 */
+    float residual_scale, block_scale;
+} tp_block_norm_desc;
+
+typedef struct tp_block_norm tp_block_norm;
+
+/* Validate and create (host only).  TP_ERR_ARG for bad enums, flags, eps or
+ * scales, or a descriptor without a block that has a post-norm, a gate, scales
+ * other than 1 or no pre-norm; TP_ERR_SHAPE for H not a positive multiple of 8,
+ * T outside 1..TP_MAX_SHARDS, S % T != 0 under seq_parallel or M above 2^24;
+ * TP_ERR_UNSUPPORTED for H above 16384. */
+TP_API tp_status tp_block_norm_create(const tp_block_norm_desc *desc, tp_block_norm **out);
+TP_API void tp_block_norm_destroy(tp_block_norm *h);
+
+/* Bytes of device workspace of tp_block_norm_bwd (256-byte aligned start):
+ * fp32 partial column sums of the parameter gradients; 0 without parameters. */
+TP_API size_t tp_block_norm_workspace_bytes(const tp_block_norm *h);
+
+/* Forward.  gate: 1 pointer [H] (channel), or like X with [M] or [M, H]
+ * elements; NULL without a gate.  post_w, post_b, pre_w, pre_b: [H], NULL where
+ * the norm has none.  F, gate, Y: NULL without a block.  N: NULL without a
+ * pre-norm.  stats (or NULL when no backward follows): per token the post
+ * mean, post rstd, pre mean and pre rstd (mean 0 for RMS; 0 and 1 where there
+ * is no norm).  M = 0 enqueues nothing. */
+TP_API tp_status tp_block_norm_fwd(tp_block_norm *h, const void *const *X, const void *const *F,
+                                   const void *const *gate, const void *post_w, const void *post_b,
+                                   const void *pre_w, const void *pre_b, void *const *Y, void *const *N,
+                                   float *stats, void *stream);
+
+/* Backward.  dY: gradient reaching Y from past N (like Y; NULL: zero, allowed
+ * with a pre-norm); dN: like N (unused without a pre-norm); Y, F, gate, weights
+ * and stats as in the forward (Y: X without a block; Y is unused without a
+ * pre-norm, F without post-norm and gate).  Computes, with D = dY + the
+ * pre-norm's gradient of dN:
+ *   dX = residual_scale * D,  dF = P'(block_scale * gate (.) D),
+ *   dgate = block_scale * D (.) p, summed over tokens (channel, fp32 [H]) or
+ *   channels (token, [M]) or not (element, [M, H], both of the gate's type),
+ *   dpost_w, dpost_b, dpre_w, dpre_b: fp32 [H], overwritten (zero for M = 0).
+ * workspace: >= tp_block_norm_workspace_bytes, 256-byte aligned. */
+TP_API tp_status tp_block_norm_bwd(tp_block_norm *h, const void *const *dY, const void *const *dN,
+                                   const void *const *Y, const void *const *F, const void *const *gate,
+                                   const void *post_w, const void *post_b, const void *pre_w, const float *stats,
+                                   void *const *dX, void *const *dF, void *const *dgate, float *dpost_w,
+                                   float *dpost_b, float *dpre_w, float *dpre_b, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* ---- AdamW over a list of tensors ------------------------------------------
+ * (the distributed optimizer of "Megatron-LM 源码精读" s5.3 on one GPU: every
+ * shard is local, so the step is one pass over the list.)  Per element, with
+ * l = lr * lr_scale and t the step, counted from 1:
+ *   g' = scale * g
+ *   m  = beta1 m + (1 - beta1) g',   v = beta2 v + (1 - beta2) g'^2
+ *   w  = w - l * weight_decay * w
+ *          - l / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32.  w is the parameter (fp32), or its fp32 master copy, rounded into
+ * the bf16 parameter after the update.
+ * States in 32 bits are fp32 m and v.  States in 8 bits are E4M3 codes of m
+ * and of sqrt(v), one fp32 scale for every 256 consecutive elements of the
+ * tensor (the last block may be short): value = code * scale, scale = largest
+ * magnitude / 448 (0 for a block below 2^-100).  A value is rounded to one of
+ * its two neighbouring codes, the nearer one with the larger probability
+ * (stochastic rounding: its expectation is the value), from a hash of seed,
+ * step, tensor index, block and element; sqrt(v) > 0 is never rounded to 0.
+ * Results are deterministic functions of the arguments.
+ * The control block is TP_ADAMW_CTL_BYTES of device memory of the caller
+ * (256-byte aligned), initialised once by tp_adamw_ctl_init.  It begins with
+ *   float norm; float scale; int32 finite; int32 steps;
+ * and lets a step be clipped, skipped and counted without the host, so that a
+ * captured graph can be replayed step after step. */
+#define TP_ADAMW_CTL_BYTES 8192
+#define TP_ADAMW_MAX_TENSORS 65536
+typedef struct {
+    int n_tensors;             /* 1..TP_ADAMW_MAX_TENSORS */
+    int param_dtype;           /* TP_DT_F32, or TP_DT_BF16 with fp32 master copies */
+    int grad_dtype;            /* TP_DT_F32 or TP_DT_BF16 */
+    int state_bits;            /* 32 or 8 */
+    double beta1, beta2;       /* in [0, 1) */
+    float eps;                 /* > 0 */
+    uint32_t seed;             /* of the 8-bit states' rounding */
+} tp_adamw_desc;
+typedef struct {
+    void *param;               /* [n] */
+    float *master;             /* [n] (TP_DT_BF16), else ignored */
+    const void *grad;          /* [n] */
+    void *m, *v;               /* [n] fp32, or [n] bytes */
+    float *m_scale, *v_scale;  /* [ceil(n / 256)] (8 bits; 4-byte aligned), else ignored */
+    int64_t n;                 /* >= 0; 0: the tensor is skipped and needs no pointers */
+    float lr_scale, weight_decay;
+} tp_adamw_tensor;
+
+typedef struct tp_adamw tp_adamw;
+
+/* Validate the list and keep a copy of it on the host (no CUDA call).  The
+ * tensors must not overlap; they stay the caller's.  TP_ERR_ARG for bad
+ * enums, constants or pointers (NULL, not aligned), TP_ERR_SHAPE for counts out
+ * of range. */
+TP_API tp_status tp_adamw_create(const tp_adamw_desc *desc, const tp_adamw_tensor *tensors, tp_adamw **out);
+TP_API void tp_adamw_destroy(tp_adamw *h);
+
+/* Replace the gradients' addresses (n_tensors pointers) for the calls made
+ * after this one.  Host only. */
+TP_API tp_status tp_adamw_set_grads(tp_adamw *h, const void *const *grads);
+
+/* Initialise a control block: `steps_done` steps taken so far, nothing
+ * measured (a step that used it would change nothing). */
+TP_API tp_status tp_adamw_ctl_init(void *ctl, int steps_done, void *stream);
+
+/* The norm of all gradients of the list, sqrt(sum g^2) * grad_scale, in the
+ * control block, with what the next step takes from it: scale = grad_scale *
+ * min(1, max_norm / norm), the step count (one more) and its bias corrections.
+ * A norm that is not finite (a gradient is NaN or infinite, or its square
+ * overflows fp32) clears `finite` and counts no step: the step then changes
+ * nothing.  max_norm: > 0, infinity for no clipping.  Summed in a fixed order.
+ * Two calls on one control block must not overlap. */
+TP_API tp_status tp_adamw_grad_norm(tp_adamw *h, float grad_scale, float max_norm, void *ctl, void *stream);
+
+/* One step.  With ctl: scale, t and whether to step at all come from the
+ * control block (grad_scale and step are ignored).  Without (NULL): scale =
+ * grad_scale and t = step >= 1; a gradient that is not finite then spreads
+ * into its weight and states. */
+TP_API tp_status tp_adamw_step(tp_adamw *h, float lr, float grad_scale, int step, const void *ctl, void *stream);
+
 /* ---- status, limits, diagnostics ---------------------------------------- */
 
 /* Synchronise `stream`, then read and clear the status word shared by the

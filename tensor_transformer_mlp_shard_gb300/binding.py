@@ -41,6 +41,27 @@ class LayerDesc(ctypes.Structure):
     _fields_ = [("mlp", Desc), ("dropout_p", ctypes.c_float), ("ln_eps", ctypes.c_float)]
 
 
+class BlockNormDesc(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("residual_f32", ctypes.c_int), ("seq_parallel", ctypes.c_int),
+                ("has_block", ctypes.c_int), ("post", ctypes.c_int), ("pre", ctypes.c_int), ("gate", ctypes.c_int),
+                ("zero_centered", ctypes.c_int), ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("block_scale", ctypes.c_float)]
+
+
+class AdamWDesc(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int), ("param_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int),
+                ("state_bits", ctypes.c_int), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_float), ("seed", ctypes.c_uint32)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("master", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("lr_scale", ctypes.c_float),
+                ("weight_decay", ctypes.c_float)]
+
+
 class ProfEntry(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_int), ("total_ms", ctypes.c_double),
                 ("sm_cycles", ctypes.c_uint64), ("sm_ns", ctypes.c_uint64)]
@@ -80,6 +101,18 @@ SIGNATURES = {
                                     ctypes.c_size_t, VP]),
     "tp_layer_bwd": (ctypes.c_int, [VP, PP, PP, VP, VP, VP, VP, PP, PP, PP, PP, ctypes.c_uint64, PP, VP, VP, PP,
                                     PP, PP, VP, VP, ctypes.c_size_t, VP]),
+    "tp_block_norm_create": (ctypes.c_int, [ctypes.POINTER(BlockNormDesc), ctypes.POINTER(VP)]),
+    "tp_block_norm_destroy": (None, [VP]),
+    "tp_block_norm_workspace_bytes": (ctypes.c_size_t, [VP]),
+    "tp_block_norm_fwd": (ctypes.c_int, [VP, PP, PP, PP, VP, VP, VP, VP, PP, PP, VP, VP]),
+    "tp_block_norm_bwd": (ctypes.c_int, [VP, PP, PP, PP, PP, PP, VP, VP, VP, VP, PP, PP, PP, VP, VP, VP, VP, VP,
+                                         ctypes.c_size_t, VP]),
+    "tp_adamw_create": (ctypes.c_int, [ctypes.POINTER(AdamWDesc), ctypes.POINTER(AdamWTensor), ctypes.POINTER(VP)]),
+    "tp_adamw_destroy": (None, [VP]),
+    "tp_adamw_set_grads": (ctypes.c_int, [VP, PP]),
+    "tp_adamw_ctl_init": (ctypes.c_int, [VP, ctypes.c_int, VP]),
+    "tp_adamw_grad_norm": (ctypes.c_int, [VP, ctypes.c_float, ctypes.c_float, VP, VP]),
+    "tp_adamw_step": (ctypes.c_int, [VP, ctypes.c_float, ctypes.c_float, ctypes.c_int, VP, VP]),
     "tp_fp8_quantize": (ctypes.c_int, [PP, PP, ctypes.POINTER(ctypes.c_int64), ctypes.c_int, ctypes.c_int, VP, VP]),
     "tp_sync_status": (ctypes.c_int, [VP]),
     "tp_mlp_sync_status": (ctypes.c_int, [VP, VP]),
@@ -514,6 +547,257 @@ def fp8_quantize(inputs, outputs, fmt: str, amax, stream=None):
     n = (ctypes.c_int64 * len(inputs))(*[t.numel() for t in inputs])
     _check(lib().tp_fp8_quantize(_arr([t.data_ptr() for t in inputs]), _arr([t.data_ptr() for t in outputs]), n,
                                  len(inputs), FP8_FORMATS[fmt], amax.data_ptr(), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# block norm
+# ---------------------------------------------------------------------------
+NORM = {"none": 0, "rms": 1, "layer": 2}
+GATE = {"none": 0, "channel": 1, "token": 2, "element": 3}
+
+
+class TPBlockNorm:
+    """Handle for the residual stream between one block and the next
+    (tp_block_norm_create):
+
+        Y = residual_scale * X + block_scale * gate * post(F)      N = pre(Y)
+
+    post, pre: "none", "rms" or "layer"; gate: "none", "channel" ([H]), "token"
+    ([M]) or "element" ([M, H]).  X and Y are fp32 with residual_f32.  With
+    block=False there is no F and no Y: N = pre(X).  Under seq_parallel X, F, Y,
+    N, token and element gates and their gradients are lists of T token shards;
+    otherwise one tensor each (or a list of one).  An argument that the
+    configuration has no use for is None."""
+
+    def __init__(self, S, B, H, T=1, dtype="bf16", post="none", pre="rms", gate="none", block=True,
+                 residual_f32=False, seq_parallel=False, zero_centered=False, eps=1e-5, residual_scale=1.0,
+                 block_scale=1.0):
+        self._d = BlockNormDesc(int(S), int(B), int(H), int(T), DTYPE[dtype], int(bool(residual_f32)),
+                                int(bool(seq_parallel)), int(bool(block)), NORM[post], NORM[pre], GATE[gate],
+                                int(bool(zero_centered)), float(eps), float(residual_scale), float(block_scale))
+        h = VP()
+        _check(lib().tp_block_norm_create(ctypes.byref(self._d), ctypes.byref(h)))
+        self._h = h
+        self.S, self.B, self.H, self.T, self.M = int(S), int(B), int(H), int(T), int(S) * int(B)
+        self.dtype, self.post, self.pre, self.gate, self.block = dtype, post, pre, gate, bool(block)
+        self.seq_parallel, self.residual_f32 = bool(seq_parallel), bool(residual_f32)
+        self.nx = self.T if seq_parallel else 1
+        self._act = TORCH_DTYPE[dtype]
+        self._res = torch.float32 if residual_f32 else self._act
+        rows = self.M // self.nx
+        self._n = rows * self.H
+        # elements and type of a gate's gradient are those of the gate, but a channel gate's is fp32
+        self._gate_n = {"none": 0, "channel": self.H, "token": rows, "element": self._n}[gate]
+        self._gate_nx = 1 if gate == "channel" else self.nx
+        self._array = VP * self.nx
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and _lib is not None:
+            _lib.tp_block_norm_destroy(h)
+            self._h = None
+
+    def workspace_bytes(self) -> int:
+        return int(lib().tp_block_norm_workspace_bytes(self._h))
+
+    @staticmethod
+    def _ptr(name, t, n, dtype):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name}: must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+        if t.numel() != n:
+            raise ValueError(f"{name}: {tuple(t.shape)} has {t.numel()} elements, expected {n}")
+        return t.data_ptr()
+
+    def _shards(self, name, ts, n, dtype, count=None):
+        if isinstance(ts, torch.Tensor):
+            ts = (ts,)
+        elif ts is None:
+            raise ValueError(f"{name}: required")
+        count = self.nx if count is None else count
+        if len(ts) != count:
+            raise ValueError(f"{name}: expected {count} tensors, got {len(ts)}")
+        if count == 1:
+            return self._array(self._ptr(name, ts[0], n, dtype))
+        return self._array(*[self._ptr(f"{name}[{i}]", t, n, dtype) for i, t in enumerate(ts)])
+
+    def fwd(self, X, F=None, gate=None, post_w=None, post_b=None, pre_w=None, pre_b=None, Y=None, N=None, stats=None,
+            stream=None):
+        """Forward into Y and N (Y may be X).  stats: an fp32 [M, 4] tensor that
+        keeps what the backward needs, or None."""
+        n, H, act, ptr = self._n, self.H, self._act, self._ptr
+        x = self._shards("X", X, n, self._res)
+        f = y = g = None
+        if self.block:
+            f, y = self._shards("F", F, n, act), self._shards("Y", Y, n, self._res)
+            if self._gate_n:
+                g = self._shards("gate", gate, self._gate_n, act, self._gate_nx)
+        out = None if self.pre == "none" else self._shards("N", N, n, act)
+        _check(lib().tp_block_norm_fwd(
+            self._h, x, f, g,
+            None if self.post == "none" else ptr("post_w", post_w, H, act),
+            ptr("post_b", post_b, H, act) if self.post == "layer" else None,
+            None if self.pre == "none" else ptr("pre_w", pre_w, H, act),
+            ptr("pre_b", pre_b, H, act) if self.pre == "layer" else None,
+            y, out, None if stats is None else ptr("stats", stats, 4 * self.M, torch.float32), _stream(stream)))
+
+    def bwd(self, dY, dN, Y, F, gate, post_w, post_b, pre_w, stats, dX, dF, dgate, dpost_w, dpost_b, dpre_w, dpre_b,
+            workspace=None, stream=None):
+        """Backward from dY (None: zero) and dN, with the forward's Y (X without
+        a block), F and stats.  dX may be dY.  Parameter gradients are fp32 and
+        overwritten; a token or element gate's gradient has the gate's type."""
+        n, H, act, f32, ptr = self._n, self.H, self._act, torch.float32, self._ptr
+        has_pre, has_post = self.pre != "none", self.post != "none"
+        need_f = has_post or self.gate != "none"
+        dy = None if dY is None else self._shards("dY", dY, n, self._res)
+        dn = self._shards("dN", dN, n, act) if has_pre else None
+        y = self._shards("Y", Y, n, self._res) if has_pre else None
+        dx = self._shards("dX", dX, n, self._res)
+        f = self._shards("F", F, n, act) if need_f else None
+        df = self._shards("dF", dF, n, act) if self.block else None
+        g = dg = None
+        if self._gate_n:
+            g = self._shards("gate", gate, self._gate_n, act, self._gate_nx)
+            dg = self._shards("dgate", dgate, self._gate_n, f32 if self.gate == "channel" else act, self._gate_nx)
+        ws, nws = (None, 0) if workspace is None else _workspace(workspace)
+        _check(lib().tp_block_norm_bwd(
+            self._h, dy, dn, y, f, g, ptr("post_w", post_w, H, act) if has_post else None,
+            ptr("post_b", post_b, H, act) if self.post == "layer" else None,
+            ptr("pre_w", pre_w, H, act) if has_pre else None, ptr("stats", stats, 4 * self.M, f32), dx, df, dg,
+            ptr("dpost_w", dpost_w, H, f32) if has_post else None,
+            ptr("dpost_b", dpost_b, H, f32) if self.post == "layer" else None,
+            ptr("dpre_w", dpre_w, H, f32) if has_pre else None,
+            ptr("dpre_b", dpre_b, H, f32) if self.pre == "layer" else None, ws, nws, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# AdamW
+# ---------------------------------------------------------------------------
+class TPAdamW:
+    """AdamW over a list of tensors (tp_adamw_create): weight shards, biases and
+    norm weights, updated in place by one launch.
+
+    params: bf16 (with fp32 `master` copies, made here when not given) or fp32
+    CUDA tensors; grads: fp32 or bf16, one for each.  Both are read and written
+    where they are at every step (set_grads changes the gradients).  m, v (and
+    m_scale, v_scale with state_bits=8) are the states, zeros when not given:
+    fp32, or one byte an element (E4M3 codes of m and sqrt(v)) and one fp32
+    scale for every 256 elements.  weight_decay and lr_scale: a number, or one
+    for each tensor.  steps_done: steps taken before, as grad_norm counts them.
+    """
+
+    QBLOCK, CTL_BYTES = 256, 8192
+
+    def __init__(self, params, grads, master=None, m=None, v=None, m_scale=None, v_scale=None, state_bits=32,
+                 beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, lr_scale=1.0, seed=0, steps_done=0):
+        params, grads = list(params), list(grads)
+        if not params:
+            raise ValueError("params: at least one tensor required")
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits: {state_bits}, expected 8 or 32")
+        half = params[0].dtype == torch.bfloat16
+        if not half and params[0].dtype != torch.float32:
+            raise ValueError(f"params: dtype {params[0].dtype}, expected bfloat16 or float32")
+        dev, sizes = params[0].device, [p.numel() for p in params]
+        blocks = [-(-k // self.QBLOCK) for k in sizes]
+        f32 = torch.float32
+
+        def own(ts, counts, dtype):
+            return [torch.zeros(k, dtype=dtype, device=dev) for k in counts] if ts is None else list(ts)
+
+        self.params = self._each("params", params, sizes, params[0].dtype)
+        if half and master is None:
+            master = [p.detach().float().contiguous() for p in params]
+        self.master = self._each("master", list(master), sizes, f32) if half else None
+        state = f32 if state_bits == 32 else torch.uint8
+        self.m = self._each("m", own(m, sizes, state), sizes, state)
+        self.v = self._each("v", own(v, sizes, state), sizes, state)
+        self.m_scale = self.v_scale = None
+        if state_bits == 8:
+            self.m_scale = self._each("m_scale", own(m_scale, blocks, f32), blocks, f32)
+            self.v_scale = self._each("v_scale", own(v_scale, blocks, f32), blocks, f32)
+        self._sizes = sizes
+        self.grads = self._grads(grads, grads[0].dtype if grads else None)
+        self.state_bits, self.lr_scale, self.weight_decay = state_bits, lr_scale, weight_decay
+        table = (AdamWTensor * len(params))()
+
+        def value(name, x, i):
+            if not isinstance(x, (list, tuple)):
+                return float(x)
+            if len(x) != len(params):
+                raise ValueError(f"{name}: expected {len(params)} values, got {len(x)}")
+            return float(x[i])
+
+        for i, t in enumerate(table):
+            t.param, t.grad = params[i].data_ptr(), grads[i].data_ptr()
+            t.master = self.master[i].data_ptr() if half else None
+            t.m, t.v = self.m[i].data_ptr(), self.v[i].data_ptr()
+            if state_bits == 8:
+                t.m_scale, t.v_scale = self.m_scale[i].data_ptr(), self.v_scale[i].data_ptr()
+            t.n = sizes[i]
+            t.lr_scale, t.weight_decay = value("lr_scale", lr_scale, i), value("weight_decay", weight_decay, i)
+        d = AdamWDesc(len(params), DTYPE["bf16" if half else "f32"],
+                      DTYPE["bf16" if grads[0].dtype == torch.bfloat16 else "f32"], int(state_bits), float(beta1),
+                      float(beta2), float(eps), int(seed) & 0xFFFFFFFF)
+        h = VP()
+        _check(lib().tp_adamw_create(ctypes.byref(d), table, ctypes.byref(h)))
+        self._h = h
+        self.ctl = torch.empty(self.CTL_BYTES // 4, dtype=f32, device=dev)
+        _check(lib().tp_adamw_ctl_init(self.ctl.data_ptr(), int(steps_done), _stream(None)))
+        self._ctl = VP(self.ctl.data_ptr())
+        self.norm, self.scale = self.ctl[0:1], self.ctl[1:2]
+        self.finite, self.steps = self.ctl.view(torch.int32)[2:3], self.ctl.view(torch.int32)[3:4]
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and _lib is not None:
+            _lib.tp_adamw_destroy(h)
+            self._h = None
+
+    @staticmethod
+    def _each(name, ts, counts, dtype):
+        if len(ts) != len(counts):
+            raise ValueError(f"{name}: expected {len(counts)} tensors, got {len(ts)}")
+        for i, (t, n) in enumerate(zip(ts, counts)):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise ValueError(f"{name}[{i}]: must be a CUDA tensor")
+            if t.dtype != dtype:
+                raise ValueError(f"{name}[{i}]: dtype {t.dtype}, expected {dtype}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}]: must be contiguous")
+            if t.numel() != n:
+                raise ValueError(f"{name}[{i}]: {tuple(t.shape)} has {t.numel()} elements, expected {n}")
+        return ts
+
+    def _grads(self, grads, dtype):
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"grads: dtype {dtype}, expected float32 or bfloat16")
+        return self._each("grads", grads, self._sizes, dtype)
+
+    def set_grads(self, grads):
+        """Take the gradients from these tensors (same sizes and type) from now on."""
+        grads = self._grads(list(grads), self.grads[0].dtype)
+        _check(lib().tp_adamw_set_grads(self._h, _arr([g.data_ptr() for g in grads])))
+        self.grads = grads
+
+    def grad_norm(self, grad_scale=1.0, max_norm=float("inf"), stream=None):
+        """Enqueue the norm of grad_scale * grads and what the next step() takes
+        from it: the clip factor, the step count and whether the norm is finite
+        (if not, that step changes nothing).  Returns the norm as a one-element
+        CUDA tensor that the next call overwrites."""
+        _check(lib().tp_adamw_grad_norm(self._h, grad_scale, max_norm, self._ctl, _stream(stream)))
+        return self.norm
+
+    def step(self, lr, step=None, grad_scale=1.0, stream=None):
+        """Enqueue one step: number `step` (from 1) on grad_scale * grads, or,
+        with step=None, as the last grad_norm() call left it."""
+        if step is None:
+            _check(lib().tp_adamw_step(self._h, lr, 1.0, 0, self._ctl, _stream(stream)))
+        else:
+            _check(lib().tp_adamw_step(self._h, lr, grad_scale, step, None, _stream(stream)))
 
 
 # ---------------------------------------------------------------------------
