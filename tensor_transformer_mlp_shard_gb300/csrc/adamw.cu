@@ -66,7 +66,7 @@ struct Table {
 };
 
 struct Hyper {
-    float lr, beta1, beta2, eps, scale, inv_bc1, inv_root_bc2;
+    float lr, b1, b2, c1, c2, eps, scale, inv_bc1, inv_root_bc2;  // c: 1 - b, rounded once
     uint32_t seed, step;
     const Ctl *ctl;
 };
@@ -187,8 +187,8 @@ __device__ __forceinline__ void quantise(const float (&x)[2][4], const uint32_t 
     // as integers the order is that of the magnitudes, with NaN above all
     const float t = __uint_as_float(__reduce_max_sync(0xffffffffu, top));
     // below 2^-100 (where 448 / t nears the range of fp32) a block is zero
-    const float inv = t < 7.888609e-31f ? 0.0f : 448.0f / t;
-    scale = t < 7.888609e-31f ? 0.0f : t / 448.0f;
+    const float inv = t < 7.888609e-31f ? 0.0f : __fmul_rn(__frcp_rn(t), 448.0f);
+    scale = t < 7.888609e-31f ? 0.0f : __fmul_rn(t, 1.0f / 448.0f);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         float q[4];
@@ -223,7 +223,6 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
         inv_root_bc2 = hy.ctl->inv_root_bc2;
         step = static_cast<uint32_t>(hy.ctl->steps);
     }
-    const float b1 = hy.beta1, b2 = hy.beta2, c1 = 1.0f - b1, c2 = 1.0f - b2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t at_step = mix(hy.seed + kMix1 * step);
     for (int c = blockIdx.x; c < tab.chunk0[tab.count]; c += gridDim.x) {
@@ -268,9 +267,11 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
                     v[j][i] *= vs;
                     v[j][i] *= v[j][i];
                 }
-                const float gi = g[j][i] * scale;
-                m[j][i] = b1 * m[j][i] + c1 * gi;
-                v[j][i] = b2 * v[j][i] + c2 * gi * gi;
+                // the states are those of separately rounded products and sums: contracted
+                // into fused operations, which of them is fused would be part of the result
+                const float gi = __fmul_rn(g[j][i], scale);
+                m[j][i] = __fadd_rn(__fmul_rn(hy.b1, m[j][i]), __fmul_rn(hy.c1, gi));
+                v[j][i] = __fadd_rn(__fmul_rn(hy.b2, v[j][i]), __fmul_rn(__fmul_rn(hy.c2, gi), gi));
                 const float root = sqrtf(v[j][i]);
                 w[j][i] -= decay * w[j][i] + rate * m[j][i] / fmaf(root, inv_root_bc2, hy.eps);
                 if (BITS == 8) v[j][i] = root;
@@ -307,9 +308,14 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------------------
-// The gradient norm.  Every block leaves one sum of squares (fp32 within 8
-// elements, fp64 beyond); the block that finishes last adds them in their
-// order, so the result does not depend on which it is.
+// The gradient norm.  Every block leaves one sum of squares; the block that
+// finishes last adds them in their order, so the result does not depend on
+// which it is.  Within a thread the squares (rounded to fp32) are added with
+// the error of every addition kept beside the sum (Knuth's two-sum), 6
+// additions an element; fp64 additions, which this machine has few units for,
+// come once a chunk.  The norm is then the rounded norm of the rounded
+// squares, whatever the order, and the clip factor that scales every gradient
+// does not move with the list's grouping.
 // ---------------------------------------------------------------------------
 struct NormArgs {
     Ctl *ctl;
@@ -340,15 +346,20 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
         const int ti = tensor_of(tab, c);
         const long long n = tab.t[ti].n;
         const long long e = static_cast<long long>(c - tab.chunk0[ti]) * kChunk + threadIdx.x * 4;
-        float s = 0.0f;
+        float s = 0.0f, rest = 0.0f;
 #pragma unroll
         for (int j = 0; j < kChunk / (4 * kThreads); ++j) {
             float g[4];
             load4(static_cast<const G *>(tab.t[ti].g), e + j * 4 * kThreads, n, g);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s = fmaf(g[i], g[i], s);
+            for (int i = 0; i < 4; ++i) {
+                const float q = __fmul_rn(g[i], g[i]);
+                const float z = __fadd_rn(s, q), a = __fsub_rn(z, s);
+                rest += __fadd_rn(__fsub_rn(s, __fsub_rn(z, a)), __fsub_rn(q, a));
+                s = z;
+            }
         }
-        sum += static_cast<double>(s);
+        sum += static_cast<double>(s) + static_cast<double>(rest);
     }
     sum = block_sum(sum, red);
     if (threadIdx.x == 0) {
@@ -367,12 +378,12 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     for (int i = threadIdx.x; i < gridDim.x; i += kThreads) sum += __ldcg(&a.ctl->partial[i]);
     sum = block_sum(sum, red);
     if (threadIdx.x) return;
-    const float norm = static_cast<float>(sqrt(sum)) * a.grad_scale;
+    const float norm = static_cast<float>(sqrt(sum) * a.grad_scale);
     const bool finite = norm <= 3.402823466e38f;
     a.ctl->ticket = 0;
     a.ctl->norm = norm;
     a.ctl->finite = finite;
-    a.ctl->scale = norm > a.max_norm ? a.grad_scale * (a.max_norm / norm) : a.grad_scale;
+    a.ctl->scale = a.grad_scale * fminf(__frcp_rn(norm) * a.max_norm, 1.0f);
     if (finite) {
         const int t = ++a.ctl->steps;
         a.ctl->inv_bc1 = static_cast<float>(1.0 / (1.0 - pow(a.beta1, t)));
@@ -618,8 +629,10 @@ tp_status tp_adamw_step(tp_adamw *h, float lr, float grad_scale, int step, const
     if (!std::isfinite(lr)) return set_error(TP_ERR_ARG, "lr must be finite");
     adam::Hyper hy = {};
     hy.lr = lr;
-    hy.beta1 = static_cast<float>(h->d.beta1);
-    hy.beta2 = static_cast<float>(h->d.beta2);
+    hy.b1 = static_cast<float>(h->d.beta1);
+    hy.b2 = static_cast<float>(h->d.beta2);
+    hy.c1 = static_cast<float>(1.0 - h->d.beta1);
+    hy.c2 = static_cast<float>(1.0 - h->d.beta2);
     hy.eps = h->d.eps;
     hy.seed = h->d.seed;
     if (ctl) {
