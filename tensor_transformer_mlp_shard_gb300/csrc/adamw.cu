@@ -30,7 +30,8 @@ namespace adam {
 constexpr int kThreads = 256;
 constexpr int kBlock = 256;                     // elements that share a scale: a warp's, 8 a lane
 constexpr int kChunk = kThreads / 32 * kBlock;  // elements a thread block takes at a time
-constexpr int kNormBlocks = 608;
+constexpr int kNormChunk = 8 * 4 * kThreads;    // the gradient norm's chunk: 8 loads of 4 a thread in flight
+constexpr int kNormBlocks = 912;
 constexpr uint32_t kMix1 = 0x9E3779B9u, kMix2 = 0xB504F333u;  // fractions of the golden ratio and of sqrt(2)
 
 // The control block in device memory: what the gradient norm leaves for the step.
@@ -85,78 +86,90 @@ __device__ __forceinline__ int tensor_of(const Table<CAP> &tab, int c) {
     return lo;
 }
 
-// 4 elements from e, those past n read as zero
-__device__ __forceinline__ void load4(const float *p, long long e, long long n, float *v) {
-    if (e + 4 <= n) {
+// 4 elements from e, as two pairs; unless FULL, those past n read as zero
+template <bool FULL>
+__device__ __forceinline__ void load4(const float *p, long long e, long long n, float2 *v) {
+    if (FULL || e + 4 <= n) {
         const float4 w = *reinterpret_cast<const float4 *>(p + e);
-        v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+        v[0] = make_float2(w.x, w.y);
+        v[1] = make_float2(w.z, w.w);
     } else {
+        float t[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = e + j < n ? p[e + j] : 0.0f;
+        for (int j = 0; j < 4; ++j) t[j] = e + j < n ? p[e + j] : 0.0f;
+        v[0] = make_float2(t[0], t[1]);
+        v[1] = make_float2(t[2], t[3]);
     }
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, long long e, long long n, float *v) {
-    if (e + 4 <= n) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p + e);
-        v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+template <bool FULL>
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, long long e, long long n, float2 *v) {
+    uint2 w = make_uint2(0u, 0u);
+    if (FULL || e + 4 <= n) {
+        w = *reinterpret_cast<const uint2 *>(p + e);
     } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = e + j < n ? __bfloat162float(p[e + j]) : 0.0f;
+        const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
+        if (e < n) w.x = q[e];
+        if (e + 1 < n) w.x |= static_cast<uint32_t>(q[e + 1]) << 16;
+        if (e + 2 < n) w.y = q[e + 2];
+    }
+    v[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
+    v[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
+}
+template <bool FULL>
+__device__ __forceinline__ void store4(float *p, long long e, long long n, const float2 *v) {
+    if (FULL || e + 4 <= n) {
+        *reinterpret_cast<float4 *>(p + e) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    } else {
+        if (e < n) p[e] = v[0].x;
+        if (e + 1 < n) p[e + 1] = v[0].y;
+        if (e + 2 < n) p[e + 2] = v[1].x;
     }
 }
-__device__ __forceinline__ void store4(float *p, long long e, long long n, const float *v) {
-    if (e + 4 <= n) {
-        *reinterpret_cast<float4 *>(p + e) = make_float4(v[0], v[1], v[2], v[3]);
+template <bool FULL>
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, long long e, long long n, const float2 *v) {
+    const uint2 w = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
+    if (FULL || e + 4 <= n) {
+        *reinterpret_cast<uint2 *>(p + e) = w;
     } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (e + j < n) p[e + j] = v[j];
-    }
-}
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, long long e, long long n, const float *v) {
-    if (e + 4 <= n) {
-        *reinterpret_cast<uint2 *>(p + e) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (e + j < n) p[e + j] = __float2bfloat16_rn(v[j]);
+        unsigned short *q = reinterpret_cast<unsigned short *>(p);
+        if (e < n) q[e] = static_cast<unsigned short>(w.x);
+        if (e + 1 < n) q[e + 1] = static_cast<unsigned short>(w.x >> 16);
+        if (e + 2 < n) q[e + 2] = static_cast<unsigned short>(w.y);
     }
 }
 
 // e4m3 codes, 4 in a word
+template <bool FULL>
 __device__ __forceinline__ uint32_t load4_codes(const uint8_t *p, long long e, long long n) {
-    if (e + 4 <= n) return *reinterpret_cast<const uint32_t *>(p + e);
+    if (FULL || e + 4 <= n) return *reinterpret_cast<const uint32_t *>(p + e);
     uint32_t w = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 3; ++j)
         if (e + j < n) w |= static_cast<uint32_t>(p[e + j]) << (8 * j);
     return w;
 }
+template <bool FULL>
 __device__ __forceinline__ void store4_codes(uint8_t *p, long long e, long long n, uint32_t w) {
-    if (e + 4 <= n) {
+    if (FULL || e + 4 <= n) {
         *reinterpret_cast<uint32_t *>(p + e) = w;
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 3; ++j)
             if (e + j < n) p[e + j] = static_cast<uint8_t>(w >> (8 * j));
     }
 }
-__device__ __forceinline__ void decode4(uint32_t w, float *v) {
+__device__ __forceinline__ void decode4(uint32_t w, float2 *v) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t two;
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(static_cast<unsigned short>(w >> (16 * h))));
-        const __half2 x = *reinterpret_cast<const __half2 *>(&two);
-        v[2 * h] = __low2float(x);
-        v[2 * h + 1] = __high2float(x);
+        v[h] = __half22float2(*reinterpret_cast<const __half2 *>(&two));
     }
 }
-__device__ __forceinline__ uint32_t encode4(const float *v) {
-    unsigned short lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1]), "f"(v[0]));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3]), "f"(v[2]));
-    return lo | (static_cast<uint32_t>(hi) << 16);
-}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// two products that no addition is fused with
+__device__ __forceinline__ float2 mul(float a, float2 x) { return make_float2(__fmul_rn(a, x.x), __fmul_rn(a, x.y)); }
 
 // 32 bits to 32 well-spread bits: xor-shifts and odd multipliers
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
@@ -165,55 +178,245 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
     return x ^ (x >> 16);
 }
 
-// x >= 0, at most 448 but for rounding, to a neighbouring e4m3 value, the
-// upper one with a probability of its nearness (16 random bits of it).  Below
-// 2^-6 the steps stop shrinking (2^-9): adding 2^-6 puts x where its 3 leading
-// mantissa bits are those steps.
-__device__ __forceinline__ float round_e4m3(float x, uint32_t bits) {
-    const float lift = x < 0.015625f ? 0.015625f : 0.0f;
-    const uint32_t u = (__float_as_uint(x + lift) + (bits << 4)) & 0xFFF00000u;
-    return fminf(__uint_as_float(u) - lift, 448.0f);
+// The hash of element e of a block is mix(key ^ e kMix1), its low half the
+// random bits of m and its high half those of the root.  The first xor-shift
+// is linear: taken of the key and of e kMix1 apart, it costs one xor an
+// element.  Both halves come out where round_e4m3 adds them, at bits 8..23.
+__device__ __forceinline__ uint32_t hash_of_element(uint32_t e) {
+    e *= kMix1;
+    return e ^ (e >> 16);
+}
+__device__ __forceinline__ void random_bits(uint32_t shifted_key, uint32_t element, uint32_t &of_m, uint32_t &of_r) {
+    uint32_t x = (shifted_key ^ element) * kMix1;
+    x = (x ^ (x >> 15)) * kMix2;
+    const uint32_t t = x >> 8;
+    of_m = ((x << 8) ^ t) & 0x00FFFF00u;
+    of_r = t & 0x00FFFF00u;
 }
 
-// Codes and scale of a block's values, 8 a lane: element j * 128 + 4 lane + i.
-template <bool ROOT>
-__device__ __forceinline__ void quantise(const float (&x)[2][4], const uint32_t (&bits)[2][4], uint32_t (&codes)[2],
-                                         float &scale) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[j][i]) & 0x7FFFFFFFu);
-    // as integers the order is that of the magnitudes, with NaN above all
+// |x|, 0 .. 448 but for rounding, scaled by 2^-120, to the bits of one of its
+// two neighbouring e4m3 values in the top byte, the upper one with a
+// probability of its nearness (16 random bits of it).  At that scale e4m3's
+// smallest normal value, 2^-6, is fp32's, 2^-126, so the formats' subnormal
+// values coincide too: a code's 7 bits are bits 20..26 of the fp32 value, and
+// one integer addition rounds in both ranges.  Largest code 0x7E (448): 0x7F
+// is NaN.
+__device__ __forceinline__ uint32_t round_e4m3(float x, uint32_t bits) {
+    return min((__float_as_uint(x) << 4) + bits, 0x7EFFFFFFu);  // the shift drops the sign
+}
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+// Scale of a block from its largest magnitude's bits, and what multiplies its
+// values before rounding.  Below 2^-100 (where 448 / t nears the range of
+// fp32) a block is kept as zero.  `poison` is all ones where the block holds a
+// NaN or an infinity (as integers the magnitudes' bits order NaN above all):
+// its codes are then NaN.
+__device__ __forceinline__ void block_scale(uint32_t top, float &inv, float &scale, uint32_t &poison) {
     const float t = __uint_as_float(__reduce_max_sync(0xffffffffu, top));
-    // below 2^-100 (where 448 / t nears the range of fp32) a block is zero
-    const float inv = t < 7.888609e-31f ? 0.0f : __fmul_rn(__frcp_rn(t), 448.0f);
-    scale = t < 7.888609e-31f ? 0.0f : __fmul_rn(t, 1.0f / 448.0f);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        float q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = fabsf(x[j][i]) * inv;
-            q[i] = round_e4m3(a, ROOT ? bits[j][i] >> 16 : bits[j][i] & 0xFFFFu);
-            if (a != a) q[i] = a;  // fminf would drop a NaN
-            if (ROOT) {
-                if (x[j][i] > 0.0f && inv > 0.0f) q[i] = fmaxf(q[i], 0.001953125f);
-            } else {
-                q[i] = copysignf(q[i], x[j][i]);
-            }
-        }
-        codes[j] = encode4(q);
-    }
+    const bool zero = t < 7.888609e-31f;
+    inv = zero ? 0.0f : __fmul_rn(__frcp_rn(t), 448.0f);
+    scale = zero ? 0.0f : __fmul_rn(t, 1.0f / 448.0f);
+    poison = t < __uint_as_float(0x7F800000u) ? 0u : 0x7F7F7F7Fu;
 }
 
 // ---------------------------------------------------------------------------
 // The step.  A warp takes 256 consecutive elements (a block of the 8-bit
 // states), 8 a lane in two runs of 4.
 // ---------------------------------------------------------------------------
+// What a lane reads of a block.
+template <typename G, int BITS>
+struct Values {
+    float2 w[2][2], g[2][2], m[2][2], v[2][2];
+    uint32_t mc[2], vc[2];
+    float ms, vs;
+};
+
+template <bool FULL, typename G, int BITS>
+__device__ __forceinline__ void read_block(const Entry &t, long long blk, Values<G, BITS> &x) {
+    const long long n = t.n;
+    if (BITS == 8) {
+        x.ms = t.ms[blk];
+        x.vs = t.vs[blk];
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const long long e = blk * kBlock + (threadIdx.x & 31) * 4 + j * 128;
+        load4<FULL>(static_cast<const float *>(t.w), e, n, x.w[j]);
+        load4<FULL>(static_cast<const G *>(t.g), e, n, x.g[j]);
+        if (BITS == 32) {
+            load4<FULL>(static_cast<const float *>(t.m), e, n, x.m[j]);
+            load4<FULL>(static_cast<const float *>(t.v), e, n, x.v[j]);
+        } else {
+            x.mc[j] = load4_codes<FULL>(static_cast<const uint8_t *>(t.m), e, n);
+            x.vc[j] = load4_codes<FULL>(static_cast<const uint8_t *>(t.v), e, n);
+        }
+    }
+}
+
+template <bool FULL, bool HALF, typename G, int BITS>
+__device__ __forceinline__ void step_block(const Entry &t, long long blk, Values<G, BITS> &x, uint32_t key,
+                                           const uint32_t (&elem)[2][4], const Hyper &hy, float scale,
+                                           float decay, float rate, float inv_root_bc2) {
+    const int lane = threadIdx.x & 31;
+    const long long n = t.n, e0 = blk * kBlock + lane * 4;
+    float2 (&w)[2][2] = x.w, (&g)[2][2] = x.g, (&m)[2][2] = x.m, (&v)[2][2] = x.v;
+    uint32_t (&mc)[2] = x.mc, (&vc)[2] = x.vc;
+    float &ms = x.ms, &vs = x.vs;
+    uint32_t top_m = 0, top_r = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const long long e = e0 + j * 128;
+        if (BITS == 8) {
+            decode4(mc[j], m[j]);
+            decode4(vc[j], v[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (BITS == 8) {
+                m[j][i] = __fmul2_rn(m[j][i], both(ms));
+                v[j][i] = __fmul2_rn(v[j][i], both(vs));
+                v[j][i] = __fmul2_rn(v[j][i], v[j][i]);
+            }
+            // The states are those of separately rounded products and sums: contracted
+            // into fused operations, which of them is fused would be part of the result.
+            // The compiler does contract the paired forms, so products that are added
+            // are single ones.
+            const float2 gi = __fmul2_rn(g[j][i], both(scale)), cg = __fmul2_rn(both(hy.c2), gi);
+            m[j][i] = __fadd2_rn(mul(hy.b1, m[j][i]), mul(hy.c1, gi));
+            v[j][i] = __fadd2_rn(mul(hy.b2, v[j][i]), make_float2(__fmul_rn(cg.x, gi.x), __fmul_rn(cg.y, gi.y)));
+            const float2 root = make_float2(sqrtf(v[j][i].x), sqrtf(v[j][i].y));
+            const float2 d = __ffma2_rn(root, both(inv_root_bc2), both(hy.eps));
+            const float2 q = __fmul2_rn(m[j][i], both(-rate));
+            w[j][i] = __fadd2_rn(__ffma2_rn(both(-decay), w[j][i], w[j][i]),
+                                 make_float2(__fdividef(q.x, d.x), __fdividef(q.y, d.y)));
+            if (BITS == 8) {
+                v[j][i] = root;
+                top_m = max(top_m, max(__float_as_uint(m[j][i].x) & 0x7FFFFFFFu, __float_as_uint(m[j][i].y) & 0x7FFFFFFFu));
+                top_r = max(top_r, max(__float_as_uint(root.x) & 0x7FFFFFFFu, __float_as_uint(root.y) & 0x7FFFFFFFu));
+            }
+        }
+        store4<FULL>(static_cast<float *>(t.w), e, n, w[j]);
+        if (HALF) store4<FULL>(static_cast<__nv_bfloat16 *>(t.p), e, n, w[j]);
+        if (BITS == 32) {
+            store4<FULL>(static_cast<float *>(t.m), e, n, m[j]);
+            store4<FULL>(static_cast<float *>(t.v), e, n, v[j]);
+        }
+    }
+    if (BITS == 32) return;
+    float inv_m, inv_r;
+    uint32_t bad_m, bad_r;
+    block_scale(top_m, inv_m, ms, bad_m);
+    block_scale(top_r, inv_r, vs, bad_r);
+    const float2 down = both(7.52316385e-37f);  // 2^-120
+    const uint32_t shifted_key = key ^ (key >> 16);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t cm[4], cr[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 a = __fmul2_rn(__fmul2_rn(m[j][i], both(inv_m)), down);
+            const float2 b = __fmul2_rn(__fmul2_rn(v[j][i], both(inv_r)), down);
+            uint32_t of_m, of_r;
+            random_bits(shifted_key, elem[j][2 * i], of_m, of_r);
+            cm[2 * i] = round_e4m3(a.x, of_m);
+            // a root above zero (at least 2^-75, the root of fp32's smallest value) keeps a code above zero
+            cr[2 * i] = max(round_e4m3(b.x, of_r), min(__float_as_uint(v[j][i].x), 0x01000000u));
+            random_bits(shifted_key, elem[j][2 * i + 1], of_m, of_r);
+            cm[2 * i + 1] = round_e4m3(a.y, of_m);
+            cr[2 * i + 1] = max(round_e4m3(b.y, of_r), min(__float_as_uint(v[j][i].y), 0x01000000u));
+        }
+        const uint32_t sign = top_bytes(__float_as_uint(m[j][0].x), __float_as_uint(m[j][0].y),
+                                        __float_as_uint(m[j][1].x), __float_as_uint(m[j][1].y)) & 0x80808080u;
+        mc[j] = top_bytes(cm[0], cm[1], cm[2], cm[3]) | sign | bad_m;
+        vc[j] = top_bytes(cr[0], cr[1], cr[2], cr[3]) | bad_r;
+        store4_codes<FULL>(static_cast<uint8_t *>(t.m), e0 + j * 128, n, mc[j]);
+        store4_codes<FULL>(static_cast<uint8_t *>(t.v), e0 + j * 128, n, vc[j]);
+    }
+    if (lane == 0) {
+        t.ms[blk] = ms;
+        t.vs[blk] = vs;
+    }
+}
+
+// A run of consecutive chunks for every thread block, and the tensor that the
+// current one lies in.
+template <int CAP>
+struct Walk {
+    int c, end, ti;
+    __device__ __forceinline__ Walk(const Table<CAP> &tab) {
+        const int chunks = tab.chunk0[tab.count];
+        // even runs: the first `chunks % blocks` are one longer
+        const int each = chunks / gridDim.x, more = chunks - each * gridDim.x;
+        const int b = blockIdx.x;
+        c = b * each + min(b, more);
+        end = c + each + (b < more);
+        ti = c < end ? tensor_of(tab, c) : 0;
+    }
+    __device__ __forceinline__ void next(const Table<CAP> &tab) {
+        if (++c < end)
+            while (tab.chunk0[ti + 1] <= c) ++ti;
+    }
+};
+
+// The asynchronous copies of the 8-bit form: every lane stages its own values
+// of the blocks ahead, and reads back only those, so a wait on its own copies
+// is all the synchronisation there is.
+constexpr int kStages = 2;
+template <typename G>
+constexpr int stage_bytes() { return kThreads * (2 * 16 + 2 * 4 * static_cast<int>(sizeof(G)) + 6 * 4); }
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async8(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <typename G>
+__device__ __forceinline__ void stage_block(const Entry &t, long long blk, uint32_t at) {
+    at += threadIdx.x * 16;
+    const long long e = blk * kBlock + (threadIdx.x & 31) * 4;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        copy_async16(at + j * kThreads * 16, static_cast<const float *>(t.w) + e + j * 128);
+        if (sizeof(G) == 4)
+            copy_async16(at + (2 + j) * kThreads * 16, static_cast<const G *>(t.g) + e + j * 128);
+        else
+            copy_async8(at + 2 * kThreads * 16 + (j * kThreads - static_cast<int>(threadIdx.x)) * 8,
+                        static_cast<const G *>(t.g) + e + j * 128);
+    }
+    at += kThreads * (32 + 8 * sizeof(G)) - threadIdx.x * 12;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        copy_async4(at + j * kThreads * 4, static_cast<const uint8_t *>(t.m) + e + j * 128);
+        copy_async4(at + (2 + j) * kThreads * 4, static_cast<const uint8_t *>(t.v) + e + j * 128);
+    }
+    copy_async4(at + 4 * kThreads * 4, t.ms + blk);  // every lane its own copy of the scales
+    copy_async4(at + 5 * kThreads * 4, t.vs + blk);
+}
+template <typename G>
+__device__ __forceinline__ void staged_block(const uint8_t *at, Values<G, 8> &x) {
+    const uint32_t *codes = reinterpret_cast<const uint32_t *>(at + kThreads * (32 + 8 * sizeof(G)));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        load4<true>(reinterpret_cast<const float *>(at), (j * kThreads + threadIdx.x) * 4, 0, x.w[j]);
+        load4<true>(reinterpret_cast<const G *>(at + 2 * kThreads * 16), (j * kThreads + threadIdx.x) * 4, 0, x.g[j]);
+        x.mc[j] = codes[j * kThreads + threadIdx.x];
+        x.vc[j] = codes[(2 + j) * kThreads + threadIdx.x];
+    }
+    x.ms = __uint_as_float(codes[4 * kThreads + threadIdx.x]);
+    x.vs = __uint_as_float(codes[5 * kThreads + threadIdx.x]);
+}
+
 template <int CAP, bool HALF, typename G, int BITS>
-__global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Table<CAP> tab,
-                                                        const __grid_constant__ Hyper hy) {
+__global__ void __launch_bounds__(kThreads, 4) step_kernel(const __grid_constant__ Table<CAP> tab,
+                                                           const __grid_constant__ Hyper hy) {
+    extern __shared__ __align__(16) uint8_t stages[];
     float scale = hy.scale, inv_bc1 = hy.inv_bc1, inv_root_bc2 = hy.inv_root_bc2;
     uint32_t step = hy.step;
     if (hy.ctl) {
@@ -225,85 +428,55 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t at_step = mix(hy.seed + kMix1 * step);
-    for (int c = blockIdx.x; c < tab.chunk0[tab.count]; c += gridDim.x) {
-        const int ti = tensor_of(tab, c);
+    uint32_t elem[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) elem[j][i] = BITS == 8 ? hash_of_element(j * 128 + lane * 4 + i) : 0u;
+    const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(stages));
+    Walk<CAP> now(tab), ahead = now;
+    // stages the next whole block of this warp; a group is committed in any case, so that the count of groups is that of chunks
+    auto fetch = [&](int slot) {
+        if (ahead.c < ahead.end) {
+            const Entry &t = tab.t[ahead.ti];
+            const long long blk = static_cast<long long>(ahead.c - tab.chunk0[ahead.ti]) * (kThreads / 32) + warp;
+            if ((blk + 1) * kBlock <= t.n) stage_block<G>(t, blk, smem + slot * stage_bytes<G>());
+            ahead.next(tab);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (BITS == 8) {
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    }
+    int slot = 0;
+    for (; now.c < now.end; now.next(tab)) {
+        const int ti = now.ti;
         const Entry &t = tab.t[ti];
-        const long long n = t.n;
-        const long long blk = static_cast<long long>(c - tab.chunk0[ti]) * (kThreads / 32) + warp;
-        if (blk * kBlock >= n) continue;
+        const long long blk = static_cast<long long>(now.c - tab.chunk0[ti]) * (kThreads / 32) + warp;
         const float lr = hy.lr * tab.lr_scale[ti];
         const float decay = lr * tab.decay[ti], rate = lr * inv_bc1;
-        float w[2][4], g[2][4], m[2][4], v[2][4];
-        uint32_t mc[2], vc[2];
-        float ms = 0.0f, vs = 0.0f;
+        const bool full = (blk + 1) * kBlock <= t.n, some = blk * kBlock < t.n;
+        uint32_t key = 0;
         if (BITS == 8) {
-            ms = t.ms[blk];
-            vs = t.vs[blk];
+            key = mix(mix(at_step ^ (static_cast<uint32_t>(tab.base + ti) * kMix2 + 1u)) + static_cast<uint32_t>(blk));
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const long long e = blk * kBlock + j * 128 + lane * 4;
-            load4(static_cast<const float *>(t.w), e, n, w[j]);
-            load4(static_cast<const G *>(t.g), e, n, g[j]);
-            if (BITS == 32) {
-                load4(static_cast<const float *>(t.m), e, n, m[j]);
-                load4(static_cast<const float *>(t.v), e, n, v[j]);
-            } else {
-                mc[j] = load4_codes(static_cast<const uint8_t *>(t.m), e, n);
-                vc[j] = load4_codes(static_cast<const uint8_t *>(t.v), e, n);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const long long e = blk * kBlock + j * 128 + lane * 4;
-            if (BITS == 8) {
-                decode4(mc[j], m[j]);
-                decode4(vc[j], v[j]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (BITS == 8) {
-                    m[j][i] *= ms;
-                    v[j][i] *= vs;
-                    v[j][i] *= v[j][i];
-                }
-                // the states are those of separately rounded products and sums: contracted
-                // into fused operations, which of them is fused would be part of the result
-                const float gi = __fmul_rn(g[j][i], scale);
-                m[j][i] = __fadd_rn(__fmul_rn(hy.b1, m[j][i]), __fmul_rn(hy.c1, gi));
-                v[j][i] = __fadd_rn(__fmul_rn(hy.b2, v[j][i]), __fmul_rn(__fmul_rn(hy.c2, gi), gi));
-                const float root = sqrtf(v[j][i]);
-                w[j][i] -= decay * w[j][i] + rate * m[j][i] / fmaf(root, inv_root_bc2, hy.eps);
-                if (BITS == 8) v[j][i] = root;
-            }
-            store4(static_cast<float *>(t.w), e, n, w[j]);
-            if (HALF) store4(static_cast<__nv_bfloat16 *>(t.p), e, n, w[j]);
-            if (BITS == 32) {
-                store4(static_cast<float *>(t.m), e, n, m[j]);
-                store4(static_cast<float *>(t.v), e, n, v[j]);
-            }
-        }
+        Values<G, BITS> x;
         if (BITS == 8) {
-            const uint32_t key = mix(mix(at_step ^ (static_cast<uint32_t>(tab.base + ti) * kMix2 + 1u)) +
-                                     static_cast<uint32_t>(blk));
-            uint32_t bits[2][4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) bits[j][i] = mix(key ^ ((j * 128 + lane * 4 + i) * kMix1));
-            quantise<false>(m, bits, mc, ms);
-            quantise<true>(v, bits, vc, vs);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const long long e = blk * kBlock + j * 128 + lane * 4;
-                store4_codes(static_cast<uint8_t *>(t.m), e, n, mc[j]);
-                store4_codes(static_cast<uint8_t *>(t.v), e, n, vc[j]);
-            }
-            if (lane == 0) {
-                t.ms[blk] = ms;
-                t.vs[blk] = vs;
-            }
+            fetch(slot == 0 ? kStages - 1 : slot - 1);  // the slot read in the last round
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         }
+        if (full) {
+            if constexpr (BITS == 8)
+                staged_block<G>(stages + slot * stage_bytes<G>(), x);
+            else
+                read_block<true, G, BITS>(t, blk, x);
+            step_block<true, HALF, G, BITS>(t, blk, x, key, elem, hy, scale, decay, rate, inv_root_bc2);
+        } else if (some) {
+            read_block<false, G, BITS>(t, blk, x);
+            step_block<false, HALF, G, BITS>(t, blk, x, key, elem, hy, scale, decay, rate, inv_root_bc2);
+        }
+        slot = slot + 1 == kStages ? 0 : slot + 1;
     }
 }
 
@@ -311,18 +484,28 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
 // The gradient norm.  Every block leaves one sum of squares; the block that
 // finishes last adds them in their order, so the result does not depend on
 // which it is.  Within a thread the squares (rounded to fp32) are added with
-// the error of every addition kept beside the sum (Knuth's two-sum), 6
-// additions an element; fp64 additions, which this machine has few units for,
-// come once a chunk.  The norm is then the rounded norm of the rounded
+// the error of every addition kept beside the sum (Knuth's two-sum), 7
+// additions an element, in pairs; fp64, which this machine has few units for,
+// comes once at the end (one fp64 addition for 8 elements was the bound before:
+// 157 us for 134M fp32 gradients).  The norm is then the rounded norm of the rounded
 // squares, whatever the order, and the clip factor that scales every gradient
 // does not move with the list's grouping.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return __fadd2_rn(a, make_float2(-b.x, -b.y)); }
+
 struct NormArgs {
     Ctl *ctl;
     float grad_scale, max_norm;
-    double beta1, beta2;
+    float log_beta1, log_beta2;
     int first, last;  // of the launches over one list
 };
+
+// (s, rest) += (a, b): the error of s + a joins the rests
+__device__ __forceinline__ void add_pair(float &s, float &rest, float a, float b) {
+    const float z = __fadd_rn(s, a), d = __fsub_rn(z, s);
+    rest = rest + b + (__fsub_rn(s, __fsub_rn(z, d)) + __fsub_rn(a, d));
+    s = z;
+}
 
 __device__ __forceinline__ double block_sum(double s, double *red) {
 #pragma unroll
@@ -341,28 +524,40 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
                                                         const __grid_constant__ NormArgs a) {
     __shared__ double red[kThreads / 32];
     __shared__ int is_last;
-    double sum = 0.0;
-    for (int c = blockIdx.x; c < tab.chunk0[tab.count]; c += gridDim.x) {
-        const int ti = tensor_of(tab, c);
-        const long long n = tab.t[ti].n;
-        const long long e = static_cast<long long>(c - tab.chunk0[ti]) * kChunk + threadIdx.x * 4;
-        float s = 0.0f, rest = 0.0f;
+    float2 s = both(0.0f), rest = both(0.0f);
+    for (Walk<CAP> now(tab); now.c < now.end; now.next(tab)) {
+        const long long n = tab.t[now.ti].n;
+        const long long e = static_cast<long long>(now.c - tab.chunk0[now.ti]) * kNormChunk + threadIdx.x * 4;
+        const G *in = static_cast<const G *>(tab.t[now.ti].g);
+        constexpr int L = kNormChunk / (4 * kThreads);
+        float2 g[L][2];
+        if (e - threadIdx.x * 4 + kNormChunk <= n) {
 #pragma unroll
-        for (int j = 0; j < kChunk / (4 * kThreads); ++j) {
-            float g[4];
-            load4(static_cast<const G *>(tab.t[ti].g), e + j * 4 * kThreads, n, g);
+            for (int j = 0; j < L; ++j) load4<true>(in, e + j * 4 * kThreads, n, g[j]);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float q = __fmul_rn(g[i], g[i]);
-                const float z = __fadd_rn(s, q), a = __fsub_rn(z, s);
-                rest += __fadd_rn(__fsub_rn(s, __fsub_rn(z, a)), __fsub_rn(q, a));
+            for (int j = 0; j < L; ++j) load4<false>(in, e + j * 4 * kThreads, n, g[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 q = make_float2(__fmul_rn(g[j][i].x, g[j][i].x), __fmul_rn(g[j][i].y, g[j][i].y));
+                const float2 z = __fadd2_rn(s, q), d = sub2(z, s);
+                rest = __fadd2_rn(rest, __fadd2_rn(sub2(s, sub2(z, d)), sub2(q, d)));
                 s = z;
             }
-        }
-        sum += static_cast<double>(s) + static_cast<double>(rest);
     }
-    sum = block_sum(sum, red);
+    add_pair(s.x, rest.x, s.y, rest.y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        add_pair(s.x, rest.x, __shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, rest.x, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = static_cast<double>(s.x) + rest.x;
+    __syncthreads();
+    double sum = 0.0;
     if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) sum += red[w];
         if (!a.first) sum += a.ctl->partial[blockIdx.x];
         a.ctl->partial[blockIdx.x] = sum;
         is_last = 0;
@@ -386,8 +581,9 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     a.ctl->scale = a.grad_scale * fminf(__frcp_rn(norm) * a.max_norm, 1.0f);
     if (finite) {
         const int t = ++a.ctl->steps;
-        a.ctl->inv_bc1 = static_cast<float>(1.0 / (1.0 - pow(a.beta1, t)));
-        a.ctl->inv_root_bc2 = static_cast<float>(1.0 / sqrt(1.0 - pow(a.beta2, t)));
+        // 1 - b^t = -expm1(t log b), without fp64's slow powers and without cancellation
+        a.ctl->inv_bc1 = -1.0f / expm1f(t * a.log_beta1);
+        a.ctl->inv_root_bc2 = 1.0f / sqrtf(-expm1f(t * a.log_beta2));
     }
 }
 
@@ -466,7 +662,7 @@ namespace adam {
 
 // tensors [i, i + tab.count) of the list; returns the index after the last
 template <int CAP>
-static int fill(const tp_adamw *h, int i, Table<CAP> &tab) {
+static int fill(const tp_adamw *h, int i, int chunk, Table<CAP> &tab) {
     tab.base = i;
     tab.count = 0;
     tab.chunk0[0] = 0;
@@ -484,7 +680,7 @@ static int fill(const tp_adamw *h, int i, Table<CAP> &tab) {
         e.n = s.n;
         tab.lr_scale[tab.count] = s.lr_scale;
         tab.decay[tab.count] = s.weight_decay;
-        tab.chunk0[tab.count + 1] = tab.chunk0[tab.count] + static_cast<int>((s.n + kChunk - 1) / kChunk);
+        tab.chunk0[tab.count + 1] = tab.chunk0[tab.count] + static_cast<int>((s.n + chunk - 1) / chunk);
         ++tab.count;
     }
     return i;
@@ -502,10 +698,12 @@ static tp_status step_launch(const Table<CAP> &tab, const tp_adamw_desc &d, cons
     else
         k = half ? (gh ? step_kernel<CAP, true, bf, 8> : step_kernel<CAP, true, float, 8>)
                  : (gh ? step_kernel<CAP, false, bf, 8> : step_kernel<CAP, false, float, 8>);
-    const int chunks = tab.chunk0[tab.count], most = 8 * num_sms();
+    const int chunks = tab.chunk0[tab.count], most = 4 * num_sms();
     if (!chunks) return TP_OK;
+    const int smem = d.state_bits == 8 ? kStages * (gh ? stage_bytes<bf>() : stage_bytes<float>()) : 0;
+    if (smem) TRY(cuda_check(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), "adamw_step"));
     launch_begin("adamw_step", st);
-    k<<<chunks < most ? chunks : most, kThreads, 0, st>>>(tab, hy);
+    k<<<chunks < most ? chunks : most, kThreads, smem, st>>>(tab, hy);
     cudaError_t e = cudaGetLastError();
     launch_end("adamw_step", st);
     return cuda_check(e, "adamw_step");
@@ -528,7 +726,7 @@ template <int CAP>
 static tp_status step_all(const tp_adamw *h, const Hyper &hy, cudaStream_t st) {
     Table<CAP> tab;
     for (int i = 0; i < h->d.n_tensors;) {
-        i = fill(h, i, tab);
+        i = fill(h, i, kChunk, tab);
         TRY(step_launch(tab, h->d, hy, st));
     }
     return TP_OK;
@@ -538,12 +736,12 @@ template <int CAP>
 static tp_status norm_all(const tp_adamw *h, NormArgs a, cudaStream_t st) {
     Table<CAP> tab;
     long long chunks = 0;
-    for (int i = 0; i < h->d.n_tensors; ++i) chunks += (h->t[i].n + kChunk - 1) / kChunk;
-    int grid = kNormBlocks < 4 * num_sms() ? kNormBlocks : 4 * num_sms();
+    for (int i = 0; i < h->d.n_tensors; ++i) chunks += (h->t[i].n + kNormChunk - 1) / kNormChunk;
+    int grid = kNormBlocks < 6 * num_sms() ? kNormBlocks : 6 * num_sms();
     if (chunks < grid) grid = chunks > 0 ? static_cast<int>(chunks) : 1;
     for (int i = 0; i < h->d.n_tensors;) {
         a.first = i == 0;
-        i = fill(h, i, tab);
+        i = fill(h, i, kNormChunk, tab);
         a.last = i == h->d.n_tensors;
         TRY(norm_launch(tab, h->d, a, grid, st));
     }
@@ -618,8 +816,8 @@ tp_status tp_adamw_grad_norm(tp_adamw *h, float grad_scale, float max_norm, void
     a.ctl = static_cast<adam::Ctl *>(ctl);
     a.grad_scale = grad_scale;
     a.max_norm = max_norm;
-    a.beta1 = h->d.beta1;
-    a.beta2 = h->d.beta2;
+    a.log_beta1 = static_cast<float>(std::log(h->d.beta1));  // -infinity for 0: 1 - b^t is 1
+    a.log_beta2 = static_cast<float>(std::log(h->d.beta2));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return h->d.n_tensors <= adam::kSmall ? adam::norm_all<adam::kSmall>(h, a, st) : adam::norm_all<adam::kLarge>(h, a, st);
 }
