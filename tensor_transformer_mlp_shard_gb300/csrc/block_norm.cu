@@ -18,22 +18,31 @@
 
 #include <cmath>
 #include <cstdio>
+#include <mutex>
 #include <new>
 
 #include "device_common.cuh"
 #include "internal.h"
+
+#define TRY(x)                        \
+    do {                              \
+        tp_status _s = (x);           \
+        if (_s != TP_OK) return _s;   \
+    } while (0)
 
 namespace tpmlp {
 namespace bn {
 
 constexpr int kWarps = 8;           // warps of a block in the warp-per-row kernels
 constexpr int kMaxThreads = 512;    // threads of a block in the block-per-row kernels
-constexpr int kMaxH = 16384;        // kMaxThreads * 32 elements a thread
-constexpr int kMaxChunks = 304;     // blocks of the backward, each writing one row of partial sums
+constexpr int kMaxCluster = 4;      // blocks that share a row
+constexpr int kMaxH = 16384;
+constexpr int kMaxChunks = 304;     // workers of the backward, each writing one row of partial sums
 
 struct Plan {
     int M, H, rows_split;
     int post, pre, gate, zero_centered, has_block;
+    int cluster, depth, need_f;     // blocks to a row, rows staged, f is read
     float eps, a, c;
     const void *x[kMaxShards], *f[kMaxShards], *g[kMaxShards];  // g: g[0] for a channel gate
     const void *y_in[kMaxShards], *dy[kMaxShards], *dn[kMaxShards];
@@ -42,56 +51,51 @@ struct Plan {
     const void *post_w, *post_b, *pre_w, *pre_b;
     float4 *stats;                  // [M]: post mean, post rstd, pre mean, pre rstd
     const float4 *stats_in;
-    float *partials;                // [sums][blocks][H]: the sums in use of P1, P0, N1, N0
+    float *partials;                // [sums][workers][H]: the sums in use of P1, P0, N1, N0
     int use[4];
 };
 
 // ---------------------------------------------------------------------------
-// vectors of V elements
+// vectors of V elements, as V / 2 pairs
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+
 template <typename T, int V>
 struct Pack;
 template <>
 struct Pack<__nv_bfloat16, 8> {
     using Raw = uint4;
-    __device__ static void unpack(const Raw &w, float *v) {
-        v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
-        v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
+    __device__ static void unpack(const Raw &w, float2 *v) {
+        v[0] = bf16_pair(w.x); v[1] = bf16_pair(w.y); v[2] = bf16_pair(w.z); v[3] = bf16_pair(w.w);
     }
-    __device__ static Raw pack(const float *v) {
-        return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                          pack_bf16x2(v[6], v[7]));
+    __device__ static Raw pack(const float2 *v) {
+        return make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                          pack_bf16x2(v[3].x, v[3].y));
     }
 };
 template <>
 struct Pack<__nv_bfloat16, 4> {
     using Raw = uint2;
-    __device__ static void unpack(const Raw &w, float *v) {
-        v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
-    }
-    __device__ static Raw pack(const float *v) {
-        return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    __device__ static void unpack(const Raw &w, float2 *v) { v[0] = bf16_pair(w.x); v[1] = bf16_pair(w.y); }
+    __device__ static Raw pack(const float2 *v) {
+        return make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
     }
 };
 template <>
 struct Pack<float, 4> {
     using Raw = float4;
-    __device__ static void unpack(const Raw &w, float *v) { v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w; }
-    __device__ static Raw pack(const float *v) { return make_float4(v[0], v[1], v[2], v[3]); }
+    __device__ static void unpack(const Raw &w, float2 *v) { v[0] = make_float2(w.x, w.y); v[1] = make_float2(w.z, w.w); }
+    __device__ static Raw pack(const float2 *v) { return make_float4(v[0].x, v[0].y, v[1].x, v[1].y); }
 };
 
 template <typename T, int V>
-__device__ __forceinline__ void load(const void *base, long long e, float *v) {
+__device__ __forceinline__ void load(const void *base, long long e, float2 *v) {
     Pack<T, V>::unpack(*reinterpret_cast<const typename Pack<T, V>::Raw *>(static_cast<const T *>(base) + e), v);
 }
 template <typename T, int V>
-__device__ __forceinline__ void store(void *base, long long e, const float *v) {
+__device__ __forceinline__ void store(void *base, long long e, const float2 *v) {
     *reinterpret_cast<typename Pack<T, V>::Raw *>(static_cast<T *>(base) + e) = Pack<T, V>::pack(v);
-}
-// what v reads back as after a store in T
-template <typename T, int V>
-__device__ __forceinline__ void round_to(float *v) {
-    if (sizeof(T) == 2) Pack<T, V>::unpack(Pack<T, V>::pack(v), v);
 }
 template <typename T>
 __device__ __forceinline__ float load1(const void *base, long long e) {
@@ -109,355 +113,581 @@ __device__ __forceinline__ int shard_of(const Plan &p, int row, int &local) {
     return j;
 }
 
-// Sums of N values over the threads of a row, for every one of them: a warp
-// (WARP) or the block.  The block's form alternates between two buffers, so
-// one barrier a call is enough: a buffer is written again only after the
-// barrier of the call in between.
-template <bool WARP, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[32][4], int &phase) {
+// ---------------------------------------------------------------------------
+// Staging.  A worker's next rows are on their way into shared memory while it
+// works on one: a thread copies (cp.async) the very vectors that it will read
+// itself, so its own wait is all the synchronisation, and the bytes in flight
+// do not depend on registers or on how many blocks fit an SM.  A stage holds
+// the arrays one after another, each [K][threads] vectors.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t smem_at(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+template <typename T, int V>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+    if (V * sizeof(T) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the newest n groups have landed
+__device__ __forceinline__ void copies_wait(int n) {
+    if (n >= 3)
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (n == 2)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+}
+constexpr int kMaxDepth = 4;
+
+// a thread's columns: vector k starts at column first + k * step
+template <int K, int V>
+struct Columns {
+    int first, step, lanes;  // lanes: threads of the block (the stride of staged vectors)
+    bool on[K];
+    __device__ __forceinline__ int at(int k) const { return first + k * step; }
+};
+
+template <typename T, int K, int V>
+__device__ __forceinline__ uint32_t stage(uint32_t at, const void *row, const Columns<K, V> &c) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int k = 0; k < K; ++k)
+        if (c.on[k])
+            copy_async<T, V>(at + (k * c.lanes + threadIdx.x) * (V * sizeof(T)), static_cast<const T *>(row) + c.at(k));
+    return at + K * c.lanes * static_cast<uint32_t>(V * sizeof(T));
+}
+// the staged vectors of one array (zero past the row's end); `at` moves to the next array
+template <typename T, int K, int V>
+__device__ __forceinline__ void staged(const uint8_t *&at, const Columns<K, V> &c, float2 (&v)[K][V / 2]) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) v[k][j] = both(0.0f);
+        if (c.on[k]) load<T, V>(at, static_cast<long long>(k * c.lanes + threadIdx.x) * V, v[k]);
+    }
+    at += K * c.lanes * V * sizeof(T);
+}
+
+// ---------------------------------------------------------------------------
+// Sums over a row, for every thread of it: a warp, a block, or a cluster.
+// ---------------------------------------------------------------------------
+struct Reduce {
+    float (*red)[3][16 * kMaxCluster];  // [2][value][block of the cluster x warp]
+    int phase, cluster, rank;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void put(Reduce &r, int value, int warp, float v) {
+    float *mine = &r.red[r.phase][value][r.rank * 16 + warp];
+    if (r.cluster == 1) {
+        *mine = v;
+        return;
+    }
+    for (int b = 0; b < r.cluster; ++b) {
+        uint32_t there;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_at(mine)), "r"(b));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(v) : "memory");
+    }
+}
+
+// Two values: after the first exchange a half of the warp carries one, the
+// other half the other, so they take 5 shuffles and not 10.  A third value (C)
+// takes its own.  Buffers alternate, so one barrier a call is enough: a buffer
+// is written again only after the barrier of the call in between.
+template <bool WARP, bool C>
+__device__ __forceinline__ void row_sum(float &a, float &b, float &c, Reduce &r) {
+    const int lane = threadIdx.x & 31;
+    const bool low = lane < 16;
+    float v = (low ? a : b) + __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (C) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    }
+    if (!WARP) {
+        const int warp = threadIdx.x >> 5;
+        if (lane == 0) {
+            put(r, 0, warp, v);
+            if (C) put(r, 2, warp, c);
+        }
+        if (lane == 16) put(r, 1, warp, v);
+        if (r.cluster == 1)
+            __syncthreads();
+        else
+            cluster_sync();
+        v = r.red[r.phase][low ? 0 : 1][lane & 15];
+        if (C) c = r.red[r.phase][2][lane & 15];
+        for (int k = 1; k < r.cluster; ++k) {
+            v += r.red[r.phase][low ? 0 : 1][k * 16 + (lane & 15)];
+            if (C) c += r.red[r.phase][2][k * 16 + (lane & 15)];
+        }
+        r.phase ^= 1;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (C) c += __shfl_xor_sync(0xffffffffu, c, o);
+        }
+    }
+    a = __shfl_sync(0xffffffffu, v, 0);
+    b = __shfl_sync(0xffffffffu, v, 16);
+}
+template <bool WARP>
+__device__ __forceinline__ void row_sum(float &a, Reduce &r) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     if (WARP) return;
-    const int warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) {
+    if (lane == 0) put(r, 0, threadIdx.x >> 5, a);
+    if (r.cluster == 1)
+        __syncthreads();
+    else
+        cluster_sync();
+    a = r.red[r.phase][0][lane & 15];
+    for (int k = 1; k < r.cluster; ++k) a += r.red[r.phase][0][k * 16 + (lane & 15)];
+    r.phase ^= 1;
 #pragma unroll
-        for (int i = 0; i < N; ++i) red[phase][threadIdx.x >> 5][i] = v[i];
+    for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+}
+
+template <bool WARP>
+__device__ __forceinline__ Reduce make_reduce(float (*red)[3][16 * kMaxCluster], const Plan &p) {
+    Reduce r = {red, 0, WARP ? 1 : p.cluster, 0};
+    if (WARP) return r;
+    // warps that a block does not have add nothing
+    for (int i = threadIdx.x; i < 2 * 3 * 16 * kMaxCluster; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
+    if (r.cluster > 1) {
+        r.rank = cluster_rank();
+        cluster_sync();  // no block writes into one that has not begun
+    } else {
+        __syncthreads();
     }
-    __syncthreads();
+    return r;
+}
+
+template <int K, int V, bool WARP>
+__device__ __forceinline__ Columns<K, V> make_columns(const Plan &p, const Reduce &r) {
+    Columns<K, V> c;
+    const int lanes = WARP ? 32 : blockDim.x;
+    c.lanes = blockDim.x;
+    c.first = r.rank * lanes * K * V + (WARP ? threadIdx.x & 31 : threadIdx.x) * V;
+    c.step = lanes * V;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.0f;
-    for (int w = 0; w < warps; ++w) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += red[phase][w][i];
-    }
-    phase ^= 1;
+    for (int k = 0; k < K; ++k) c.on[k] = c.at(k) < p.H;
+    return c;
 }
 
 // Mean and 1 / spread of a row, and the row less its mean in v.  LayerNorm takes
 // its variance about the mean in a second pass over the registers, and that
 // pass also sums what the fp32 mean left over: subtracting that too, a mean
 // far above the spread costs no digits.
-template <bool WARP, int V, int K>
-__device__ __forceinline__ void centre_row(float (&v)[K][V], const bool (&on)[K], int kind, int H, float eps,
-                                           float (*red)[32][4], int &phase, float &mean, float &rstd) {
+template <bool WARP, bool LN, int V, int K>
+__device__ __forceinline__ void centre_row(float2 (&v)[K][V / 2], const Columns<K, V> &c, int kind, float inv_h,
+                                           float eps, Reduce &r, float &mean, float &rstd) {
     mean = 0.0f;
-    float s[2] = {0.0f, 0.0f};
-    if (kind == TP_NORM_LAYER) {
-        float m[1] = {0.0f};
+    float2 s = both(0.0f), q = both(0.0f);
+    if (LN && kind == TP_NORM_LAYER) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int j = 0; j < V; ++j) m[0] += v[k][j];  // elements past the row are zero
-        row_sum<WARP>(m, red, phase);
-        mean = m[0] / H;
+            for (int j = 0; j < V / 2; ++j) s = __fadd2_rn(s, v[k][j]);  // elements past the row are zero
+        mean = s.x + s.y;
+        row_sum<WARP>(mean, r);
+        mean *= inv_h;
+        s = both(0.0f);
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (on[k]) {
+            if (c.on[k]) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    v[k][j] -= mean;
-                    s[0] += v[k][j];
-                    s[1] = fmaf(v[k][j], v[k][j], s[1]);
+                for (int j = 0; j < V / 2; ++j) {
+                    v[k][j] = __fadd2_rn(v[k][j], both(-mean));
+                    s = __fadd2_rn(s, v[k][j]);
+                    q = __ffma2_rn(v[k][j], v[k][j], q);
                 }
             }
-        row_sum<WARP>(s, red, phase);
-        const float rest = s[0] / H;
-        s[1] = fmaxf(s[1] - s[0] * rest, 0.0f);
+        float a = s.x + s.y, b = q.x + q.y, none;
+        row_sum<WARP, false>(a, b, none, r);
+        const float rest = a * inv_h;
         mean += rest;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[k][j] -= rest;
+            for (int j = 0; j < V / 2; ++j) v[k][j] = __fadd2_rn(v[k][j], both(-rest));
+        rstd = 1.0f / sqrtf(fmaxf(b - a * rest, 0.0f) * inv_h + eps);
     } else {
-        float q[1] = {0.0f};
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int j = 0; j < V; ++j) q[0] = fmaf(v[k][j], v[k][j], q[0]);
-        row_sum<WARP>(q, red, phase);
-        s[1] = q[0];
+            for (int j = 0; j < V / 2; ++j) q = __ffma2_rn(v[k][j], v[k][j], q);
+        float b = q.x + q.y;
+        row_sum<WARP>(b, r);
+        rstd = 1.0f / sqrtf(b * inv_h + eps);
     }
-    rstd = 1.0f / sqrtf(s[1] / H + eps);
 }
 
-// w (1 + w when zero-centred) of the V channels from column c
-template <typename A, int V>
-__device__ __forceinline__ void load_weight(const void *w, int c, int zero_centered, float *v) {
-    load<A, V>(w, c, v);
-    if (zero_centered) {
+// v = w (1 + w when zero-centred) of a thread's columns, `none` without a weight
+template <typename A, int K, int V>
+__device__ __forceinline__ void load_weight(const void *w, const Columns<K, V> &c, float plus, float none,
+                                            float2 (&v)[K][V / 2]) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] += 1.0f;
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) v[k][j] = both(none);
+        if (w && c.on[k]) {
+            load<A, V>(w, c.at(k), v[k]);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) v[k][j] = __fadd2_rn(v[k][j], both(plus));
+        }
+    }
+}
+// v *= c times the channel gate (c alone without one)
+template <typename A, int K, int V>
+__device__ __forceinline__ void times_gate(const Plan &p, const Columns<K, V> &c, float2 (&v)[K][V / 2]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        float2 g[V / 2];
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) g[j] = both(1.0f);
+        if (p.gate == TP_GATE_CHANNEL && c.on[k]) load<A, V>(p.g[0], c.at(k), g);
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) v[k][j] = __fmul2_rn(__fmul2_rn(v[k][j], g[j]), both(p.c));
     }
 }
 
 // ---------------------------------------------------------------------------
 // Forward.  A: type of f, g, n and the weights; R: type of x and y; E elements
-// a thread, in vectors of V.
+// a thread, in vectors of V; LN: one of the norms is a LayerNorm.
 // ---------------------------------------------------------------------------
-template <typename A, typename R, int E, bool WARP>
+template <typename A, typename R, int E, bool WARP, bool LN>
 __global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) fwd_kernel(const __grid_constant__ Plan p) {
-    constexpr int V = sizeof(R) == 2 ? 8 : 4, K = E / V;
-    __shared__ float red[2][32][4];
-    int phase = 0;
-    const int t = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
-    const int stride = WARP ? gridDim.x * kWarps : gridDim.x;
-    bool on[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) on[k] = (t + k * nt) * V < p.H;
-    for (int row = WARP ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x; row < p.M; row += stride) {
+    constexpr int V = sizeof(R) == 2 ? 8 : 4, K = E / V, P = V / 2;
+    __shared__ float red[2][3][16 * kMaxCluster];
+    extern __shared__ __align__(16) uint8_t stages[];
+    Reduce r = make_reduce<WARP>(red, p);
+    const Columns<K, V> c = make_columns<K, V, WARP>(p, r);
+    const int worker = WARP ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x / r.cluster;
+    const int workers = WARP ? gridDim.x * kWarps : gridDim.x / r.cluster;
+    const bool gate_rows = p.gate == TP_GATE_ELEMENT, first = (WARP ? threadIdx.x & 31 : threadIdx.x) == 0 && r.rank == 0;
+    const float inv_h = 1.0f / p.H, plus = p.zero_centered ? 1.0f : 0.0f;
+    const uint32_t stage_bytes =
+        blockDim.x * E * static_cast<uint32_t>(sizeof(R) + (p.has_block ? sizeof(A) : 0) + (gate_rows ? sizeof(A) : 0));
+    const uint32_t base = smem_at(stages);
+    auto fetch = [&](int row, int slot) {
+        if (row < p.M) {
+            int lr;
+            const int js = shard_of(p, row, lr);
+            const long long e = static_cast<long long>(lr) * p.H;
+            uint32_t at = base + slot * stage_bytes;
+            at = stage<R>(at, static_cast<const R *>(p.x[js]) + e, c);
+            if (p.has_block) at = stage<A>(at, static_cast<const A *>(p.f[js]) + e, c);
+            if (gate_rows) stage<A>(at, static_cast<const A *>(p.g[js]) + e, c);
+        }
+        copies_commit();
+    };
+    for (int i = 0; i < p.depth - 1; ++i) fetch(worker + i * workers, i);
+    // weights of this thread's columns, the gate and the block's scale in the post-norm's
+    float2 pw[K][P], nw[K][P], pb[LN ? K : 1][P], nb[LN ? K : 1][P];
+    load_weight<A>(p.post_w, c, plus, 1.0f, pw);
+    times_gate<A>(p, c, pw);
+    load_weight<A>(p.pre_w, c, plus, 1.0f, nw);
+    if constexpr (LN) {
+        load_weight<A>(p.post_b, c, 0.0f, 0.0f, pb);
+        times_gate<A>(p, c, pb);
+        load_weight<A>(p.pre_b, c, 0.0f, 0.0f, nb);
+    }
+    int slot = 0;
+    for (int row = worker; row < p.M; row += workers) {
+        fetch(row + (p.depth - 1) * workers, slot == 0 ? p.depth - 1 : slot - 1);  // the slot of the row before
         int lr;
         const int js = shard_of(p, row, lr);
-        const long long base = static_cast<long long>(lr) * p.H;
-        float y[K][V], f[K][V];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) y[k][j] = f[k][j] = 0.0f;
-            if (on[k]) {
-                load<R, V>(p.x[js], base + (t + k * nt) * V, y[k]);
-                if (p.has_block) load<A, V>(p.f[js], base + (t + k * nt) * V, f[k]);
-            }
-        }
+        const long long e = static_cast<long long>(lr) * p.H;
+        const float gm = p.gate == TP_GATE_TOKEN ? load1<A>(p.g[js], lr) : 1.0f;
+        copies_wait(p.depth - 1);
+        const uint8_t *at = stages + slot * stage_bytes;
+        slot = slot + 1 == p.depth ? 0 : slot + 1;
+        float2 y[K][P];
+        staged<R>(at, c, y);
         float4 st = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
         if (p.has_block) {
-            if (p.post != TP_NORM_NONE)
-                centre_row<WARP, V, K>(f, on, p.post, p.H, p.eps, red, phase, st.x, st.y);
-            const float gm = p.gate == TP_GATE_TOKEN ? p.c * load1<A>(p.g[js], lr) : p.c;
+            float2 f[K][P];
+            staged<A>(at, c, f);
+            if (p.post != TP_NORM_NONE) centre_row<WARP, LN, V, K>(f, c, p.post, inv_h, p.eps, r, st.x, st.y);
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (on[k]) {
-                    const int c = (t + k * nt) * V;
-                    float w[V];
-                    if (p.post != TP_NORM_NONE) {
-                        load_weight<A, V>(p.post_w, c, p.zero_centered, w);
+                if (c.on[k]) {
+                    float2 g[P];
 #pragma unroll
-                        for (int j = 0; j < V; ++j) f[k][j] *= st.y * w[j];
-                        if (p.post == TP_NORM_LAYER) {
-                            load<A, V>(p.post_b, c, w);
-#pragma unroll
-                            for (int j = 0; j < V; ++j) f[k][j] += w[j];
-                        }
+                    for (int j = 0; j < P; ++j) {
+                        f[k][j] = __fmul2_rn(f[k][j], both(st.y));
+                        f[k][j] = LN ? __ffma2_rn(f[k][j], pw[k][j], pb[LN ? k : 0][j]) : __fmul2_rn(f[k][j], pw[k][j]);
+                        y[k][j] = __fmul2_rn(y[k][j], both(p.a));
                     }
-                    if (p.gate == TP_GATE_CHANNEL || p.gate == TP_GATE_ELEMENT) {
-                        load<A, V>(p.gate == TP_GATE_CHANNEL ? p.g[0] : p.g[js],
-                                   p.gate == TP_GATE_CHANNEL ? c : base + c, w);
+                    if (gate_rows) {
+                        load<A, V>(at, static_cast<long long>(k * c.lanes + threadIdx.x) * V, g);
 #pragma unroll
-                        for (int j = 0; j < V; ++j) f[k][j] *= w[j];
+                        for (int j = 0; j < P; ++j) y[k][j] = __ffma2_rn(f[k][j], g[j], y[k][j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < P; ++j) y[k][j] = __ffma2_rn(f[k][j], both(gm), y[k][j]);
                     }
-#pragma unroll
-                    for (int j = 0; j < V; ++j) y[k][j] = fmaf(p.a, y[k][j], gm * f[k][j]);
-                    store<R, V>(p.y[js], base + c, y[k]);
-                    round_to<R, V>(y[k]);
+                    const typename Pack<R, V>::Raw out = Pack<R, V>::pack(y[k]);
+                    *reinterpret_cast<typename Pack<R, V>::Raw *>(static_cast<R *>(p.y[js]) + e + c.at(k)) = out;
+                    Pack<R, V>::unpack(out, y[k]);  // the pre-norm is of y as it is stored
                 }
         }
         if (p.pre != TP_NORM_NONE) {
-            centre_row<WARP, V, K>(y, on, p.pre, p.H, p.eps, red, phase, st.z, st.w);
+            centre_row<WARP, LN, V, K>(y, c, p.pre, inv_h, p.eps, r, st.z, st.w);
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (on[k]) {
-                    const int c = (t + k * nt) * V;
-                    float w[V], o[V];
-                    load_weight<A, V>(p.pre_w, c, p.zero_centered, w);
+                if (c.on[k]) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) o[j] = y[k][j] * st.w * w[j];
-                    if (p.pre == TP_NORM_LAYER) {
-                        load<A, V>(p.pre_b, c, w);
-#pragma unroll
-                        for (int j = 0; j < V; ++j) o[j] += w[j];
+                    for (int j = 0; j < P; ++j) {
+                        y[k][j] = __fmul2_rn(y[k][j], both(st.w));
+                        y[k][j] = LN ? __ffma2_rn(y[k][j], nw[k][j], nb[LN ? k : 0][j]) : __fmul2_rn(y[k][j], nw[k][j]);
                     }
-                    store<A, V>(p.n[js], base + c, o);
+                    store<A, V>(p.n[js], e + c.at(k), y[k]);
                 }
         }
-        if (p.stats && t == 0) p.stats[row] = st;
+        if (p.stats && first) p.stats[row] = st;
     }
+    if (r.cluster > 1) cluster_sync();  // no block leaves while another may write into it
 }
 
 // ---------------------------------------------------------------------------
 // Backward: gradients of x, f and of a token or element gate, row by row, and
-// this block's share of the column sums in registers.
+// this worker's share of the column sums in registers.
 // ---------------------------------------------------------------------------
-template <typename A, typename R, int E, bool WARP>
+template <typename A, typename R, int E, bool WARP, bool LN>
 __global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) bwd_kernel(const __grid_constant__ Plan p) {
-    constexpr int V = sizeof(R) == 2 ? 8 : 4, K = E / V;
-    __shared__ float red[2][32][4];
-    int phase = 0;
-    const int t = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
-    const int stride = WARP ? gridDim.x * kWarps : gridDim.x;
-    const float inv_h = 1.0f / p.H;
-    bool on[K];
-    float acc[4][K][V];
+    constexpr int V = sizeof(R) == 2 ? 8 : 4, K = E / V, P = V / 2, L = LN ? K : 1;
+    __shared__ float red[2][3][16 * kMaxCluster];
+    extern __shared__ __align__(16) uint8_t stages[];
+    Reduce r = make_reduce<WARP>(red, p);
+    const Columns<K, V> c = make_columns<K, V, WARP>(p, r);
+    const int worker = WARP ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x / r.cluster;
+    const int workers = WARP ? gridDim.x * kWarps : gridDim.x / r.cluster;
+    const bool has_pre = p.pre != TP_NORM_NONE, has_dy = p.dy[0] != nullptr, gate_rows = p.gate == TP_GATE_ELEMENT;
+    const bool row_gate = gate_rows || p.gate == TP_GATE_TOKEN;
+    const bool first = (WARP ? threadIdx.x & 31 : threadIdx.x) == 0 && r.rank == 0;
+    const float inv_h = 1.0f / p.H, plus = p.zero_centered ? 1.0f : 0.0f;
+    const uint32_t stage_bytes = blockDim.x * E *
+                                 static_cast<uint32_t>((has_dy ? sizeof(R) : 0) + (has_pre ? sizeof(R) + sizeof(A) : 0) +
+                                                       (p.need_f ? sizeof(A) : 0) + (gate_rows ? sizeof(A) : 0));
+    const uint32_t base = smem_at(stages);
+    auto fetch = [&](int row, int slot) {
+        if (row < p.M) {
+            int lr;
+            const int js = shard_of(p, row, lr);
+            const long long e = static_cast<long long>(lr) * p.H;
+            uint32_t at = base + slot * stage_bytes;
+            if (has_dy) at = stage<R>(at, static_cast<const R *>(p.dy[js]) + e, c);
+            if (has_pre) {
+                at = stage<R>(at, static_cast<const R *>(p.y_in[js]) + e, c);
+                at = stage<A>(at, static_cast<const A *>(p.dn[js]) + e, c);
+            }
+            if (p.need_f) at = stage<A>(at, static_cast<const A *>(p.f[js]) + e, c);
+            if (gate_rows) stage<A>(at, static_cast<const A *>(p.g[js]) + e, c);
+        }
+        copies_commit();
+    };
+    for (int i = 0; i < p.depth - 1; ++i) fetch(worker + i * workers, i);
+    float2 gw[K][P], nw[K][P];  // c times the channel gate times the post-norm's weight; the pre-norm's weight
+    load_weight<A>(p.post_w, c, plus, 1.0f, gw);
+    times_gate<A>(p, c, gw);
+    load_weight<A>(p.pre_w, c, plus, 1.0f, nw);
+    float2 p1[K][P], n1[K][P], p0[L][P], n0[L][P];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        on[k] = (t + k * nt) * V < p.H;
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[0][k][j] = acc[1][k][j] = acc[2][k][j] = acc[3][k][j] = 0.0f;
-    }
-    const bool row_gate = p.gate == TP_GATE_TOKEN || p.gate == TP_GATE_ELEMENT;
-    for (int row = WARP ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x; row < p.M; row += stride) {
+        for (int j = 0; j < P; ++j) p1[k][j] = n1[k][j] = p0[LN ? k : 0][j] = n0[LN ? k : 0][j] = both(0.0f);
+    int slot = 0;
+    float4 st_next = worker < p.M ? p.stats_in[worker] : make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+    for (int row = worker; row < p.M; row += workers) {
+        fetch(row + (p.depth - 1) * workers, slot == 0 ? p.depth - 1 : slot - 1);  // the slot of the row before
         int lr;
         const int js = shard_of(p, row, lr);
-        const long long base = static_cast<long long>(lr) * p.H;
-        const float4 st = p.stats_in[row];
-        float d[K][V];  // dy, then D
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) d[k][j] = 0.0f;
-            if (on[k] && p.dy[js]) load<R, V>(p.dy[js], base + (t + k * nt) * V, d[k]);
-        }
-        if (p.pre != TP_NORM_NONE) {
-            float yh[K][V], h[K][V], s[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) yh[k][j] = h[k][j] = 0.0f;
-                if (on[k]) {
-                    const int c = (t + k * nt) * V;
-                    float w[V];
-                    load<R, V>(p.y_in[js], base + c, yh[k]);
-                    load<A, V>(p.dn[js], base + c, h[k]);
-                    load_weight<A, V>(p.pre_w, c, p.zero_centered, w);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        yh[k][j] = (yh[k][j] - st.z) * st.w;
-                        acc[2][k][j] = fmaf(h[k][j], yh[k][j], acc[2][k][j]);
-                        acc[3][k][j] += h[k][j];
-                        h[k][j] *= w[j];
-                        s[0] += h[k][j];
-                        s[1] = fmaf(h[k][j], yh[k][j], s[1]);
-                    }
-                }
-            }
-            row_sum<WARP>(s, red, phase);
-            const float m0 = p.pre == TP_NORM_LAYER ? s[0] * inv_h : 0.0f, m1 = s[1] * inv_h;
+        const long long e = static_cast<long long>(lr) * p.H;
+        const float4 st = st_next;
+        if (row + workers < p.M) st_next = p.stats_in[row + workers];
+        const float gm = p.gate == TP_GATE_TOKEN ? load1<A>(p.g[js], lr) : 1.0f;
+        copies_wait(p.depth - 1);
+        const uint8_t *at = stages + slot * stage_bytes;
+        slot = slot + 1 == p.depth ? 0 : slot + 1;
+        float2 d[K][P];  // dy, then D
+        if (has_dy) {
+            staged<R>(at, c, d);
+        } else {
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int j = 0; j < V; ++j) d[k][j] += st.w * (h[k][j] - m0 - yh[k][j] * m1);
+                for (int j = 0; j < P; ++j) d[k][j] = both(0.0f);
+        }
+        if (has_pre) {
+            float2 yh[K][P], h[K][P], s0 = both(0.0f), s1 = both(0.0f);
+            staged<R>(at, c, yh);
+            staged<A>(at, c, h);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    if (LN) yh[k][j] = __fadd2_rn(yh[k][j], both(-st.z));
+                    yh[k][j] = __fmul2_rn(yh[k][j], both(st.w));
+                    n1[k][j] = __ffma2_rn(h[k][j], yh[k][j], n1[k][j]);  // h is zero past the row
+                    if (LN) n0[LN ? k : 0][j] = __fadd2_rn(n0[LN ? k : 0][j], h[k][j]);
+                    h[k][j] = __fmul2_rn(h[k][j], nw[k][j]);
+                    if (LN) s0 = __fadd2_rn(s0, h[k][j]);
+                    s1 = __ffma2_rn(h[k][j], yh[k][j], s1);
+                }
+            float m0 = s0.x + s0.y, m1 = s1.x + s1.y, none;
+            if (LN)
+                row_sum<WARP, false>(m0, m1, none, r);
+            else
+                row_sum<WARP>(m1, r);
+            m0 = LN && p.pre == TP_NORM_LAYER ? -st.w * m0 * inv_h : 0.0f;
+            m1 *= -st.w * inv_h;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    if (LN) d[k][j] = __fadd2_rn(d[k][j], both(m0));
+                    d[k][j] = __ffma2_rn(h[k][j], both(st.w), __ffma2_rn(yh[k][j], both(m1), d[k][j]));
+                }
         }
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (on[k]) {
-                float o[V];
+            if (c.on[k]) {
+                float2 o[P];
 #pragma unroll
-                for (int j = 0; j < V; ++j) o[j] = p.a * d[k][j];
-                store<R, V>(p.dx[js], base + (t + k * nt) * V, o);
+                for (int j = 0; j < P; ++j) o[j] = __fmul2_rn(d[k][j], both(p.a));
+                store<R, V>(p.dx[js], e + c.at(k), o);
             }
         if (!p.has_block) continue;
-        const float gm = p.gate == TP_GATE_TOKEN ? load1<A>(p.g[js], lr) : 1.0f;
-        const bool need_f = p.post != TP_NORM_NONE || p.gate != TP_GATE_NONE;
-        float fh[K][V], s[3] = {0.0f, 0.0f, 0.0f};
+        float2 fh[K][P], s0 = both(0.0f), s1 = both(0.0f), s2 = both(0.0f);
+        if (p.need_f) {
+            staged<A>(at, c, fh);
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
+            for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int j = 0; j < V; ++j) fh[k][j] = 0.0f;
-            if (on[k]) {
-                const int c = (t + k * nt) * V;
-                float w[V], pv[V];
-                if (need_f) load<A, V>(p.f[js], base + c, fh[k]);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    fh[k][j] = (fh[k][j] - st.x) * st.y;  // no post-norm: mean 0, rstd 1
-                    w[j] = 1.0f;
-                    pv[j] = fh[k][j];
+                for (int j = 0; j < P; ++j) {
+                    if (LN) fh[k][j] = __fadd2_rn(fh[k][j], both(-st.x));  // no post-norm: mean 0, 1 / spread 1
+                    fh[k][j] = __fmul2_rn(fh[k][j], both(st.y));
                 }
-                if (p.post != TP_NORM_NONE) {
-                    load_weight<A, V>(p.post_w, c, p.zero_centered, w);
-                    if (row_gate) {
+        } else {
 #pragma unroll
-                        for (int j = 0; j < V; ++j) pv[j] = fh[k][j] * w[j];
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j) fh[k][j] = both(0.0f);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (c.on[k]) {
+                if (row_gate) {  // its gradient is D times p = fh w + b
+                    float2 pv[P], w[P];
+#pragma unroll
+                    for (int j = 0; j < P; ++j) pv[j] = fh[k][j];
+                    if (p.post != TP_NORM_NONE) {
+                        load<A, V>(p.post_w, c.at(k), w);
+#pragma unroll
+                        for (int j = 0; j < P; ++j) pv[j] = __fmul2_rn(pv[j], __fadd2_rn(w[j], both(plus)));
                         if (p.post == TP_NORM_LAYER) {
-                            float b[V];
-                            load<A, V>(p.post_b, c, b);
+                            load<A, V>(p.post_b, c.at(k), w);
 #pragma unroll
-                            for (int j = 0; j < V; ++j) pv[j] += b[j];
+                            for (int j = 0; j < P; ++j) pv[j] = __fadd2_rn(pv[j], w[j]);
+                        }
+                    }
+                    if (gate_rows) {
+                        load<A, V>(at, static_cast<long long>(k * c.lanes + threadIdx.x) * V, w);
+#pragma unroll
+                        for (int j = 0; j < P; ++j) {
+                            pv[j] = __fmul2_rn(__fmul2_rn(d[k][j], pv[j]), both(p.c));
+                            d[k][j] = __fmul2_rn(d[k][j], w[j]);
+                        }
+                        store<A, V>(p.dg[js], e + c.at(k), pv);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < P; ++j) {
+                            s2 = __ffma2_rn(d[k][j], pv[j], s2);
+                            d[k][j] = __fmul2_rn(d[k][j], both(gm));
                         }
                     }
                 }
-                if (p.gate == TP_GATE_ELEMENT) {
-                    float g[V], o[V];
-                    load<A, V>(p.g[js], base + c, g);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        o[j] = p.c * d[k][j] * pv[j];
-                        d[k][j] *= g[j];
-                    }
-                    store<A, V>(p.dg[js], base + c, o);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        s[2] = fmaf(d[k][j], pv[j], s[2]);  // the token gate's gradient
-                        d[k][j] *= gm;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    acc[0][k][j] = fmaf(d[k][j], fh[k][j], acc[0][k][j]);
-                    acc[1][k][j] += d[k][j];
-                }
-                if (p.gate == TP_GATE_CHANNEL) {
-                    float g[V];
-                    load<A, V>(p.g[0], c, g);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) d[k][j] *= g[j];
-                }
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    d[k][j] *= p.c * w[j];  // the gradient of fh
-                    s[0] += d[k][j];
-                    s[1] = fmaf(d[k][j], fh[k][j], s[1]);
+                for (int j = 0; j < P; ++j) {
+                    p1[k][j] = __ffma2_rn(d[k][j], fh[k][j], p1[k][j]);
+                    if (LN) p0[LN ? k : 0][j] = __fadd2_rn(p0[LN ? k : 0][j], d[k][j]);
+                    d[k][j] = __fmul2_rn(d[k][j], gw[k][j]);  // the gradient of fh
+                    if (LN) s0 = __fadd2_rn(s0, d[k][j]);
+                    s1 = __ffma2_rn(d[k][j], fh[k][j], s1);
                 }
             }
+        float m0 = s0.x + s0.y, m1 = s1.x + s1.y, dg = s2.x + s2.y;
+        if (p.gate == TP_GATE_TOKEN) {
+            row_sum<WARP, true>(m0, m1, dg, r);
+            if (first) store1<A>(p.dg[js], lr, p.c * dg);
+        } else if (p.post != TP_NORM_NONE) {
+            if (LN)
+                row_sum<WARP, false>(m0, m1, dg, r);
+            else
+                row_sum<WARP>(m1, r);
         }
-        float m0 = 0.0f, m1 = 0.0f;
-        if (p.post != TP_NORM_NONE || p.gate == TP_GATE_TOKEN) {
-            row_sum<WARP>(s, red, phase);
-            if (p.post == TP_NORM_LAYER) m0 = s[0] * inv_h;
-            if (p.post != TP_NORM_NONE) m1 = s[1] * inv_h;
-            if (p.gate == TP_GATE_TOKEN && t == 0) store1<A>(p.dg[js], lr, p.c * s[2]);
-        }
+        m0 = LN && p.post == TP_NORM_LAYER ? -st.y * m0 * inv_h : 0.0f;
+        m1 = p.post != TP_NORM_NONE ? -st.y * m1 * inv_h : 0.0f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (on[k]) {
-                float o[V];
+            if (c.on[k]) {
+                float2 o[P];
 #pragma unroll
-                for (int j = 0; j < V; ++j) o[j] = st.y * (d[k][j] - m0 - fh[k][j] * m1);
-                store<A, V>(p.df[js], base + (t + k * nt) * V, o);
+                for (int j = 0; j < P; ++j) {
+                    o[j] = __ffma2_rn(fh[k][j], both(m1), both(m0));
+                    o[j] = __ffma2_rn(d[k][j], both(st.y), o[j]);
+                }
+                store<A, V>(p.df[js], e + c.at(k), o);
             }
     }
-    // one row of partial sums a block (the warps of a block added in order)
-    __shared__ float comb[WARP ? kWarps * E * 32 : 1];
-    int slot = 0;
+    // one row of partial sums a worker (the warps of a block added in order)
+    const int out_row = WARP ? blockIdx.x : worker, out_rows = WARP ? gridDim.x : workers;
+    int used = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         if (!p.use[q]) continue;
-        float *out = p.partials + (static_cast<long long>(slot++) * gridDim.x + blockIdx.x) * p.H;
+        float *out = p.partials + (static_cast<long long>(used++) * out_rows + out_row) * p.H;
+        float2 (*acc)[P] = q == 0 ? p1 : q == 1 ? p0 : q == 2 ? n1 : n0;
         if (WARP) {
+            // the stages' memory serves again: every row has been read
+            float *comb = reinterpret_cast<float *>(stages);
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    comb[(threadIdx.x >> 5) * E * 32 + (t + k * 32) * V + j] = acc[q][k][j];
+                for (int j = 0; j < P; ++j)
+                    *reinterpret_cast<float2 *>(comb + (threadIdx.x >> 5) * E * 32 + c.at(k) + 2 * j) = acc[LN || !(q & 1) ? k : 0][j];
             __syncthreads();
-            for (int c = threadIdx.x; c < p.H; c += 32 * kWarps) {
+            for (int i = threadIdx.x; i < p.H; i += 32 * kWarps) {
                 float s = 0.0f;
-                for (int w = 0; w < kWarps; ++w) s += comb[w * E * 32 + c];
-                out[c] = s;
+                for (int w = 0; w < kWarps; ++w) s += comb[w * E * 32 + i];
+                out[i] = s;
             }
         } else {
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (on[k]) {
+                if (c.on[k]) {
 #pragma unroll
-                    for (int j = 0; j < V; j += 4)
-                        *reinterpret_cast<float4 *>(out + (t + k * nt) * V + j) =
-                            make_float4(acc[q][k][j], acc[q][k][j + 1], acc[q][k][j + 2], acc[q][k][j + 3]);
+                    for (int j = 0; j < P; j += 2) {
+                        const float2 u = acc[LN || !(q & 1) ? k : 0][j], v = acc[LN || !(q & 1) ? k : 0][j + 1];
+                        *reinterpret_cast<float4 *>(out + c.at(k) + 2 * j) = make_float4(u.x, u.y, v.x, v.y);
+                    }
                 }
         }
     }
+    if (r.cluster > 1) cluster_sync();  // no block leaves while another may write into it
 }
 
 // ---------------------------------------------------------------------------
@@ -513,47 +743,118 @@ __global__ void __launch_bounds__(256) param_grad_kernel(const __grid_constant__
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
-// Elements a thread (8, 16, 32) and whether a warp takes a row: rows of up to
-// 1024 columns go to a warp each, wider ones to a block.
+// How a row is taken, from its width and the bytes an element has in a stage
+// (those that the kernel reads): rows of up to 1024 columns by a warp with 8,
+// 16 or 32 elements a lane, wider ones by a block with 8 or 16 elements a
+// thread, and where a block's threads or its shared memory (two stages at
+// least) do not hold a row, by a cluster of 2 or 4 blocks.
 struct Shape {
     bool warp;
-    int E, threads;
+    int E, threads, cluster, depth;
+    int smem;
 };
-static Shape shape_of(int H) {
+// dynamic shared memory of a block when `blocks` of them share an SM's 228 KB
+// (each also takes 1.5 KB of static buffers and 1 KB of the system's)
+static int smem_share(int blocks) { return (blocks == 1 ? 225 : 228) * 1024 / blocks - 2560; }
+
+static Shape shape_of(int H, int bytes, int blocks_per_sm) {
     Shape s;
-    s.warp = H <= 1024;
-    const int most = s.warp ? 32 : kMaxThreads;
-    s.E = H <= most * 8 ? 8 : H <= most * 16 ? 16 : 32;
-    s.threads = s.warp ? 32 * kWarps : ((H + s.E - 1) / s.E + 31) / 32 * 32;
+    s.cluster = 1;
+    s.E = H <= 256 ? 8 : H <= 512 ? 16 : 32;
+    s.threads = 32 * kWarps;
+    s.warp = H <= 1024 && 2 * s.threads * s.E * bytes <= smem_share(1);
+    if (!s.warp) {
+        while (H > s.cluster * kMaxThreads * 16 || 2 * bytes * ((H + s.cluster - 1) / s.cluster + 512) > smem_share(1))
+            s.cluster *= 2;
+        const int cols = (H + s.cluster - 1) / s.cluster;
+        s.E = cols <= kMaxThreads * 8 ? 8 : 16;
+        s.threads = ((cols + s.E - 1) / s.E + 31) / 32 * 32;
+    }
+    const int stage = s.threads * s.E * bytes;
+    s.depth = smem_share(blocks_per_sm) / stage;
+    s.depth = s.depth < 2 ? 2 : s.depth > kMaxDepth ? kMaxDepth : s.depth;
+    s.smem = s.depth * stage;
+    if (s.warp && s.smem < kWarps * s.E * 32 * 4) s.smem = kWarps * s.E * 32 * 4;  // the warps' sums at the end
     return s;
 }
 
 using Kernel = void (*)(Plan);
-template <typename A, typename R, bool BWD>
+template <typename A, typename R, bool BWD, bool LN>
 static Kernel pick(const Shape &s) {
     if (BWD) {
-        if (s.warp) return s.E == 8 ? bwd_kernel<A, R, 8, true> : s.E == 16 ? bwd_kernel<A, R, 16, true> : bwd_kernel<A, R, 32, true>;
-        return s.E == 8 ? bwd_kernel<A, R, 8, false> : s.E == 16 ? bwd_kernel<A, R, 16, false> : bwd_kernel<A, R, 32, false>;
+        if (s.warp) return s.E == 8 ? bwd_kernel<A, R, 8, true, LN> : s.E == 16 ? bwd_kernel<A, R, 16, true, LN> : bwd_kernel<A, R, 32, true, LN>;
+        return s.E == 8 ? bwd_kernel<A, R, 8, false, LN> : bwd_kernel<A, R, 16, false, LN>;
     }
-    if (s.warp) return s.E == 8 ? fwd_kernel<A, R, 8, true> : s.E == 16 ? fwd_kernel<A, R, 16, true> : fwd_kernel<A, R, 32, true>;
-    return s.E == 8 ? fwd_kernel<A, R, 8, false> : s.E == 16 ? fwd_kernel<A, R, 16, false> : fwd_kernel<A, R, 32, false>;
+    if (s.warp) return s.E == 8 ? fwd_kernel<A, R, 8, true, LN> : s.E == 16 ? fwd_kernel<A, R, 16, true, LN> : fwd_kernel<A, R, 32, true, LN>;
+    return s.E == 8 ? fwd_kernel<A, R, 8, false, LN> : fwd_kernel<A, R, 16, false, LN>;
 }
-
-static Kernel kernel_for(const tp_block_norm_desc &d, bool bwd, const Shape &s) {
+template <bool BWD, bool LN>
+static Kernel pick(const tp_block_norm_desc &d, const Shape &s) {
     using bf = __nv_bfloat16;
-    if (d.dtype == TP_DT_F32) return bwd ? pick<float, float, true>(s) : pick<float, float, false>(s);
-    if (d.residual_f32) return bwd ? pick<bf, float, true>(s) : pick<bf, float, false>(s);
-    return bwd ? pick<bf, bf, true>(s) : pick<bf, bf, false>(s);
+    if (d.dtype == TP_DT_F32) return pick<float, float, BWD, LN>(s);
+    return d.residual_f32 ? pick<bf, float, BWD, LN>(s) : pick<bf, bf, BWD, LN>(s);
 }
 
-static int grid_for(Kernel k, const Shape &s, int M, int cap) {
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, s.threads, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
+// A kernel and how many of its blocks an SM holds; the handle keeps the last
+// device's, so that a call does not ask the runtime again.
+struct Launch {
+    Kernel k = nullptr;
+    Shape s;
+    int per_sm = 0, device = -1;
+};
+static std::mutex g_launch_mutex;
+
+static tp_status prepare(Launch &kept, const tp_block_norm_desc &d, bool bwd, int bytes, Launch &l) {
+    int dev = 0;
+    TRY(cuda_check(cudaGetDevice(&dev), "cudaGetDevice"));
+    std::lock_guard<std::mutex> lock(g_launch_mutex);
+    l = kept;
+    if (l.device == dev) return TP_OK;
+    const bool ln = d.post == TP_NORM_LAYER || d.pre == TP_NORM_LAYER;
+    // the deepest stages that still leave room for the blocks that registers allow
+    int want = 1;
+    for (;;) {
+        l.s = shape_of(d.H, bytes, want);
+        l.k = bwd ? (ln ? pick<true, true>(d, l.s) : pick<true, false>(d, l.s))
+                  : (ln ? pick<false, true>(d, l.s) : pick<false, false>(d, l.s));
+        TRY(cuda_check(cudaFuncSetAttribute(l.k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_share(1)), "block norm"));
+        int by_registers = 0;
+        TRY(cuda_check(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&by_registers, l.k, l.s.threads, 0), "block norm"));
+        if (by_registers <= want || l.s.depth == 2) break;
+        want = by_registers;
+    }
+    TRY(cuda_check(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&l.per_sm, l.k, l.s.threads, l.s.smem), "block norm"));
+    if (l.per_sm < 1) return set_error(TP_ERR_CUDA, "block norm: no block fits an SM");
+    l.device = dev;
+    kept = l;
+    return TP_OK;
+}
+
+static tp_status run(const Launch &l, Plan &p, int most, const char *name, cudaStream_t st, int *workers) {
+    const Shape &s = l.s;
     const int rows = s.warp ? kWarps : 1;
-    int g = per_sm * num_sms();
-    if (g > (M + rows - 1) / rows) g = (M + rows - 1) / rows;
-    if (cap && g > cap) g = cap;
-    return g;
+    int blocks = l.per_sm * num_sms() / s.cluster;
+    if (blocks > (p.M + rows - 1) / rows) blocks = (p.M + rows - 1) / rows;
+    if (most && blocks > most) blocks = most;
+    if (blocks < 1) blocks = 1;
+    p.cluster = s.cluster;
+    p.depth = s.depth;
+    *workers = blocks;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks * s.cluster);
+    cfg.blockDim = dim3(s.threads);
+    cfg.dynamicSmemBytes = s.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = s.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = s.cluster > 1 ? 1 : 0;
+    launch_begin(name, st);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, l.k, p);
+    launch_end(name, st);
+    return cuda_check(e, name);
 }
 
 }  // namespace bn
@@ -565,13 +866,8 @@ struct tp_block_norm {
     tp_block_norm_desc d;
     int M, nx, rows_split;
     int use[4];
+    bn::Launch fwd, bwd;
 };
-
-#define TRY(x)                        \
-    do {                              \
-        tp_status _s = (x);           \
-        if (_s != TP_OK) return _s;   \
-    } while (0)
 
 static tp_status bn_pointer(const void *p, const char *name, int i, int n) {
     char at[16] = "";
@@ -696,14 +992,11 @@ tp_status tp_block_norm_fwd(tp_block_norm *h, const void *const *X, const void *
     if (d.pre == TP_NORM_LAYER) TRY(bn_pointer(p.pre_b = pre_b, "pre_b", 0, 1));
     if (stats) TRY(bn_pointer(p.stats = reinterpret_cast<float4 *>(stats), "stats", 0, 1));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bn::Shape s = bn::shape_of(d.H);
-    const bn::Kernel k = bn::kernel_for(d, false, s);
-    const int grid = bn::grid_for(k, s, h->M, 0);
-    launch_begin("block_norm_fwd", st);
-    k<<<grid, s.threads, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
-    launch_end("block_norm_fwd", st);
-    return cuda_check(e, "block_norm_fwd");
+    const int ea = d.dtype == TP_DT_F32 ? 4 : 2, er = d.residual_f32 ? 4 : ea;
+    bn::Launch l;
+    TRY(bn::prepare(h->fwd, d, false, er + (d.has_block ? ea : 0) + (d.gate == TP_GATE_ELEMENT ? ea : 0), l));
+    int workers;
+    return bn::run(l, p, 0, "block_norm_fwd", st, &workers);
 }
 
 tp_status tp_block_norm_bwd(tp_block_norm *h, const void *const *dY, const void *const *dN, const void *const *Y,
@@ -762,14 +1055,13 @@ tp_status tp_block_norm_bwd(tp_block_norm *h, const void *const *dY, const void 
     p.partials = static_cast<float *>(workspace);
     int grid = 0;
     if (h->M > 0) {
-        const bn::Shape s = bn::shape_of(d.H);
-        const bn::Kernel k = bn::kernel_for(d, true, s);
-        grid = bn::grid_for(k, s, h->M, bn::kMaxChunks);
-        launch_begin("block_norm_bwd", st);
-        k<<<grid, s.threads, 0, st>>>(p);
-        cudaError_t e = cudaGetLastError();
-        launch_end("block_norm_bwd", st);
-        TRY(cuda_check(e, "block_norm_bwd"));
+        const int ea = d.dtype == TP_DT_F32 ? 4 : 2, er = d.residual_f32 ? 4 : ea;
+        p.need_f = d.has_block && (d.post != TP_NORM_NONE || d.gate != TP_GATE_NONE);
+        const bool pre = d.pre != TP_NORM_NONE;
+        bn::Launch l;
+        TRY(bn::prepare(h->bwd, d, true,
+                        er + (pre ? er + ea : 0) + (p.need_f ? ea : 0) + (d.gate == TP_GATE_ELEMENT ? ea : 0), l));
+        TRY(bn::run(l, p, bn::kMaxChunks, "block_norm_bwd", st, &grid));
     }
     if (!h->use[0] && !h->use[2]) return TP_OK;
     fin.partials = p.partials;
