@@ -145,7 +145,7 @@ constexpr int kMaxDepth = 4;
 template <int K, int V>
 struct Columns {
     int first, step, lanes;  // lanes: threads of the block (the stride of staged vectors)
-    bool on[K];
+    bool on[K], ragged;      // ragged: the row ends within this block's (or warp's) columns
     __device__ __forceinline__ int at(int k) const { return first + k * step; }
 };
 
@@ -157,21 +157,27 @@ __device__ __forceinline__ uint32_t stage(uint32_t at, const void *row, const Co
             copy_async<T, V>(at + (k * c.lanes + threadIdx.x) * (V * sizeof(T)), static_cast<const T *>(row) + c.at(k));
     return at + K * c.lanes * static_cast<uint32_t>(V * sizeof(T));
 }
-// the staged vectors of one array (zero past the row's end); `at` moves to the next array
+// the staged vectors of one array; `at` moves to the next array
 template <typename T, int K, int V>
 __device__ __forceinline__ void staged(const uint8_t *&at, const Columns<K, V> &c, float2 (&v)[K][V / 2]) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) v[k][j] = both(0.0f);
-        if (c.on[k]) load<T, V>(at, static_cast<long long>(k * c.lanes + threadIdx.x) * V, v[k]);
-    }
+    for (int k = 0; k < K; ++k) load<T, V>(at, static_cast<int>(k * c.lanes + threadIdx.x) * V, v[k]);
     at += K * c.lanes * V * sizeof(T);
+}
+// Vectors past the row's end are never copied.  Where a block has such, its
+// stages are cleared once, so that they read as zero and the arithmetic on
+// them needs no condition.
+__device__ __forceinline__ void clear_stages(uint8_t *stages, uint32_t bytes) {
+    for (uint32_t i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
+        *reinterpret_cast<uint4 *>(stages + i) = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
 // Sums over a row, for every thread of it: a warp, a block, or a cluster.
 // ---------------------------------------------------------------------------
+// TEAM: kWarp, kBlock or kCluster.
+enum Team { kWarp = 0, kBlock = 1, kCluster = 2 };
 struct Reduce {
     float (*red)[3][16 * kMaxCluster];  // [2][value][block of the cluster x warp]
     int phase, cluster, rank;
@@ -185,9 +191,10 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+template <Team TEAM>
 __device__ __forceinline__ void put(Reduce &r, int value, int warp, float v) {
     float *mine = &r.red[r.phase][value][r.rank * 16 + warp];
-    if (r.cluster == 1) {
+    if (TEAM == kBlock) {
         *mine = v;
         return;
     }
@@ -202,7 +209,14 @@ __device__ __forceinline__ void put(Reduce &r, int value, int warp, float v) {
 // other half the other, so they take 5 shuffles and not 10.  A third value (C)
 // takes its own.  Buffers alternate, so one barrier a call is enough: a buffer
 // is written again only after the barrier of the call in between.
-template <bool WARP, bool C>
+template <Team TEAM>
+__device__ __forceinline__ void team_sync() {
+    if (TEAM == kCluster)
+        cluster_sync();
+    else
+        __syncthreads();
+}
+template <Team TEAM, bool C>
 __device__ __forceinline__ void row_sum(float &a, float &b, float &c, Reduce &r) {
     const int lane = threadIdx.x & 31;
     const bool low = lane < 16;
@@ -213,23 +227,18 @@ __device__ __forceinline__ void row_sum(float &a, float &b, float &c, Reduce &r)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
     }
-    if (!WARP) {
-        const int warp = threadIdx.x >> 5;
-        if (lane == 0) {
-            put(r, 0, warp, v);
-            if (C) put(r, 2, warp, c);
-        }
-        if (lane == 16) put(r, 1, warp, v);
-        if (r.cluster == 1)
-            __syncthreads();
-        else
-            cluster_sync();
-        v = r.red[r.phase][low ? 0 : 1][lane & 15];
-        if (C) c = r.red[r.phase][2][lane & 15];
-        for (int k = 1; k < r.cluster; ++k) {
-            v += r.red[r.phase][low ? 0 : 1][k * 16 + (lane & 15)];
-            if (C) c += r.red[r.phase][2][k * 16 + (lane & 15)];
-        }
+    if (TEAM != kWarp) {
+        if ((lane & 15) == 0) put<TEAM>(r, lane >> 4, threadIdx.x >> 5, v);
+        if (C && lane == 0) put<TEAM>(r, 2, threadIdx.x >> 5, c);
+        team_sync<TEAM>();
+        const float *in = r.red[r.phase][lane >> 4] + (lane & 15), *in_c = r.red[r.phase][2] + (lane & 15);
+        v = in[0];
+        if (C) c = in_c[0];
+        if (TEAM == kCluster)
+            for (int k = 1; k < r.cluster; ++k) {
+                v += in[k * 16];
+                if (C) c += in_c[k * 16];
+            }
         r.phase ^= 1;
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) {
@@ -240,46 +249,43 @@ __device__ __forceinline__ void row_sum(float &a, float &b, float &c, Reduce &r)
     a = __shfl_sync(0xffffffffu, v, 0);
     b = __shfl_sync(0xffffffffu, v, 16);
 }
-template <bool WARP>
+template <Team TEAM>
 __device__ __forceinline__ void row_sum(float &a, Reduce &r) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    if (WARP) return;
-    if (lane == 0) put(r, 0, threadIdx.x >> 5, a);
-    if (r.cluster == 1)
-        __syncthreads();
-    else
-        cluster_sync();
-    a = r.red[r.phase][0][lane & 15];
-    for (int k = 1; k < r.cluster; ++k) a += r.red[r.phase][0][k * 16 + (lane & 15)];
+    if (TEAM == kWarp) return;
+    if (lane == 0) put<TEAM>(r, 0, threadIdx.x >> 5, a);
+    team_sync<TEAM>();
+    const float *in = r.red[r.phase][0] + (lane & 15);
+    a = in[0];
+    if (TEAM == kCluster)
+        for (int k = 1; k < r.cluster; ++k) a += in[k * 16];
     r.phase ^= 1;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
 }
 
-template <bool WARP>
+template <Team TEAM>
 __device__ __forceinline__ Reduce make_reduce(float (*red)[3][16 * kMaxCluster], const Plan &p) {
-    Reduce r = {red, 0, WARP ? 1 : p.cluster, 0};
-    if (WARP) return r;
+    Reduce r = {red, 0, TEAM == kCluster ? p.cluster : 1, 0};
+    if (TEAM == kWarp) return r;
     // warps that a block does not have add nothing
     for (int i = threadIdx.x; i < 2 * 3 * 16 * kMaxCluster; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
-    if (r.cluster > 1) {
-        r.rank = cluster_rank();
-        cluster_sync();  // no block writes into one that has not begun
-    } else {
-        __syncthreads();
-    }
+    if (TEAM == kCluster) r.rank = cluster_rank();
+    team_sync<TEAM>();  // and no block writes into one that has not begun
     return r;
 }
 
-template <int K, int V, bool WARP>
+template <int K, int V, Team TEAM>
 __device__ __forceinline__ Columns<K, V> make_columns(const Plan &p, const Reduce &r) {
+    constexpr bool WARP = TEAM == kWarp;
     Columns<K, V> c;
     const int lanes = WARP ? 32 : blockDim.x;
     c.lanes = blockDim.x;
     c.first = r.rank * lanes * K * V + (WARP ? threadIdx.x & 31 : threadIdx.x) * V;
     c.step = lanes * V;
+    c.ragged = (r.rank + 1) * lanes * K * V > p.H;
 #pragma unroll
     for (int k = 0; k < K; ++k) c.on[k] = c.at(k) < p.H;
     return c;
@@ -289,7 +295,7 @@ __device__ __forceinline__ Columns<K, V> make_columns(const Plan &p, const Reduc
 // its variance about the mean in a second pass over the registers, and that
 // pass also sums what the fp32 mean left over: subtracting that too, a mean
 // far above the spread costs no digits.
-template <bool WARP, bool LN, int V, int K>
+template <Team TEAM, bool LN, int V, int K>
 __device__ __forceinline__ void centre_row(float2 (&v)[K][V / 2], const Columns<K, V> &c, int kind, float inv_h,
                                            float eps, Reduce &r, float &mean, float &rstd) {
     mean = 0.0f;
@@ -298,49 +304,50 @@ __device__ __forceinline__ void centre_row(float2 (&v)[K][V / 2], const Columns<
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int j = 0; j < V / 2; ++j) s = __fadd2_rn(s, v[k][j]);  // elements past the row are zero
+            for (int j = 0; j < V / 2; ++j) s = __fadd2_rn(s, v[k][j]);
         mean = s.x + s.y;
-        row_sum<WARP>(mean, r);
+        row_sum<TEAM>(mean, r);
         mean *= inv_h;
         s = both(0.0f);
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (c.on[k]) {
+        for (int k = 0; k < K; ++k) {
+            const float2 less = both(c.on[k] ? -mean : 0.0f);  // past the row's end zeros stay zeros
 #pragma unroll
-                for (int j = 0; j < V / 2; ++j) {
-                    v[k][j] = __fadd2_rn(v[k][j], both(-mean));
-                    s = __fadd2_rn(s, v[k][j]);
-                    q = __ffma2_rn(v[k][j], v[k][j], q);
-                }
+            for (int j = 0; j < V / 2; ++j) {
+                v[k][j] = __fadd2_rn(v[k][j], less);
+                s = __fadd2_rn(s, v[k][j]);
+                q = __ffma2_rn(v[k][j], v[k][j], q);
             }
+        }
         float a = s.x + s.y, b = q.x + q.y, none;
-        row_sum<WARP, false>(a, b, none, r);
+        row_sum<TEAM, false>(a, b, none, r);
         const float rest = a * inv_h;
         mean += rest;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) v[k][j] = __fadd2_rn(v[k][j], both(-rest));
-        rstd = 1.0f / sqrtf(fmaxf(b - a * rest, 0.0f) * inv_h + eps);
+        rstd = rsqrtf(fmaxf(b - a * rest, 0.0f) * inv_h + eps);
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) q = __ffma2_rn(v[k][j], v[k][j], q);
         float b = q.x + q.y;
-        row_sum<WARP>(b, r);
-        rstd = 1.0f / sqrtf(b * inv_h + eps);
+        row_sum<TEAM>(b, r);
+        rstd = rsqrtf(b * inv_h + eps);
     }
 }
 
-// v = w (1 + w when zero-centred) of a thread's columns, `none` without a weight
+// v = w (1 + w when zero-centred) of a thread's columns, `none` without a weight;
+// zero past the row's end, where what it multiplies may be anything finite
 template <typename A, int K, int V>
 __device__ __forceinline__ void load_weight(const void *w, const Columns<K, V> &c, float plus, float none,
                                             float2 (&v)[K][V / 2]) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) v[k][j] = both(none);
+        for (int j = 0; j < V / 2; ++j) v[k][j] = both(c.on[k] ? none : 0.0f);
         if (w && c.on[k]) {
             load<A, V>(w, c.at(k), v[k]);
 #pragma unroll
@@ -366,13 +373,14 @@ __device__ __forceinline__ void times_gate(const Plan &p, const Columns<K, V> &c
 // Forward.  A: type of f, g, n and the weights; R: type of x and y; E elements
 // a thread, in vectors of V; LN: one of the norms is a LayerNorm.
 // ---------------------------------------------------------------------------
-template <typename A, typename R, int E, bool WARP, bool LN>
-__global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) fwd_kernel(const __grid_constant__ Plan p) {
+template <typename A, typename R, int E, Team TEAM, bool LN>
+__global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd_kernel(const __grid_constant__ Plan p) {
+    constexpr bool WARP = TEAM == kWarp;
     constexpr int V = sizeof(R) == 2 ? 8 : 4, K = E / V, P = V / 2;
     __shared__ float red[2][3][16 * kMaxCluster];
     extern __shared__ __align__(16) uint8_t stages[];
-    Reduce r = make_reduce<WARP>(red, p);
-    const Columns<K, V> c = make_columns<K, V, WARP>(p, r);
+    Reduce r = make_reduce<TEAM>(red, p);
+    const Columns<K, V> c = make_columns<K, V, TEAM>(p, r);
     const int worker = WARP ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x / r.cluster;
     const int workers = WARP ? gridDim.x * kWarps : gridDim.x / r.cluster;
     const bool gate_rows = p.gate == TP_GATE_ELEMENT, first = (WARP ? threadIdx.x & 31 : threadIdx.x) == 0 && r.rank == 0;
@@ -392,6 +400,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) fwd_kernel(c
         }
         copies_commit();
     };
+    if (c.ragged) clear_stages(stages, p.depth * stage_bytes);
     for (int i = 0; i < p.depth - 1; ++i) fetch(worker + i * workers, i);
     // weights of this thread's columns, the gate and the block's scale in the post-norm's
     float2 pw[K][P], nw[K][P], pb[LN ? K : 1][P], nb[LN ? K : 1][P];
@@ -419,59 +428,60 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) fwd_kernel(c
         if (p.has_block) {
             float2 f[K][P];
             staged<A>(at, c, f);
-            if (p.post != TP_NORM_NONE) centre_row<WARP, LN, V, K>(f, c, p.post, inv_h, p.eps, r, st.x, st.y);
+            if (p.post != TP_NORM_NONE) centre_row<TEAM, LN, V, K>(f, c, p.post, inv_h, p.eps, r, st.x, st.y);
+            // y = a x + g (P(f) scaled): the row's factors first, then the channel's
+            const float2 row_scale = both(LN ? st.y : st.y * gm);
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (c.on[k]) {
-                    float2 g[P];
+            for (int k = 0; k < K; ++k) {
 #pragma unroll
-                    for (int j = 0; j < P; ++j) {
-                        f[k][j] = __fmul2_rn(f[k][j], both(st.y));
-                        f[k][j] = LN ? __ffma2_rn(f[k][j], pw[k][j], pb[LN ? k : 0][j]) : __fmul2_rn(f[k][j], pw[k][j]);
-                        y[k][j] = __fmul2_rn(y[k][j], both(p.a));
-                    }
-                    if (gate_rows) {
-                        load<A, V>(at, static_cast<long long>(k * c.lanes + threadIdx.x) * V, g);
-#pragma unroll
-                        for (int j = 0; j < P; ++j) y[k][j] = __ffma2_rn(f[k][j], g[j], y[k][j]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < P; ++j) y[k][j] = __ffma2_rn(f[k][j], both(gm), y[k][j]);
-                    }
-                    const typename Pack<R, V>::Raw out = Pack<R, V>::pack(y[k]);
-                    *reinterpret_cast<typename Pack<R, V>::Raw *>(static_cast<R *>(p.y[js]) + e + c.at(k)) = out;
-                    Pack<R, V>::unpack(out, y[k]);  // the pre-norm is of y as it is stored
+                for (int j = 0; j < P; ++j) {
+                    f[k][j] = __fmul2_rn(f[k][j], row_scale);
+                    if (LN) f[k][j] = __fmul2_rn(__ffma2_rn(f[k][j], pw[k][j], pb[LN ? k : 0][j]), both(gm));
+                    y[k][j] = __fmul2_rn(y[k][j], both(p.a));
                 }
+                if (gate_rows) {
+                    float2 g[P];
+                    load<A, V>(at, static_cast<int>(k * c.lanes + threadIdx.x) * V, g);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) f[k][j] = __fmul2_rn(f[k][j], g[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < P; ++j)
+                    y[k][j] = LN ? __fadd2_rn(f[k][j], y[k][j]) : __ffma2_rn(f[k][j], pw[k][j], y[k][j]);
+                const typename Pack<R, V>::Raw out = Pack<R, V>::pack(y[k]);
+                if (c.on[k]) *reinterpret_cast<typename Pack<R, V>::Raw *>(static_cast<R *>(p.y[js]) + e + c.at(k)) = out;
+                Pack<R, V>::unpack(out, y[k]);  // the pre-norm is of y as it is stored
+            }
         }
         if (p.pre != TP_NORM_NONE) {
-            centre_row<WARP, LN, V, K>(y, c, p.pre, inv_h, p.eps, r, st.z, st.w);
+            centre_row<TEAM, LN, V, K>(y, c, p.pre, inv_h, p.eps, r, st.z, st.w);
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (c.on[k]) {
+            for (int k = 0; k < K; ++k) {
 #pragma unroll
-                    for (int j = 0; j < P; ++j) {
-                        y[k][j] = __fmul2_rn(y[k][j], both(st.w));
-                        y[k][j] = LN ? __ffma2_rn(y[k][j], nw[k][j], nb[LN ? k : 0][j]) : __fmul2_rn(y[k][j], nw[k][j]);
-                    }
-                    store<A, V>(p.n[js], e + c.at(k), y[k]);
+                for (int j = 0; j < P; ++j) {
+                    y[k][j] = __fmul2_rn(y[k][j], both(st.w));
+                    y[k][j] = LN ? __ffma2_rn(y[k][j], nw[k][j], nb[LN ? k : 0][j]) : __fmul2_rn(y[k][j], nw[k][j]);
                 }
+                if (c.on[k]) store<A, V>(p.n[js], e + c.at(k), y[k]);
+            }
         }
         if (p.stats && first) p.stats[row] = st;
     }
-    if (r.cluster > 1) cluster_sync();  // no block leaves while another may write into it
+    if (TEAM == kCluster) cluster_sync();  // no block leaves while another may write into it
 }
 
 // ---------------------------------------------------------------------------
 // Backward: gradients of x, f and of a token or element gate, row by row, and
 // this worker's share of the column sums in registers.
 // ---------------------------------------------------------------------------
-template <typename A, typename R, int E, bool WARP, bool LN>
-__global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) bwd_kernel(const __grid_constant__ Plan p) {
+template <typename A, typename R, int E, Team TEAM, bool LN>
+__global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) bwd_kernel(const __grid_constant__ Plan p) {
+    constexpr bool WARP = TEAM == kWarp;
     constexpr int V = sizeof(R) == 2 ? 8 : 4, K = E / V, P = V / 2, L = LN ? K : 1;
     __shared__ float red[2][3][16 * kMaxCluster];
     extern __shared__ __align__(16) uint8_t stages[];
-    Reduce r = make_reduce<WARP>(red, p);
-    const Columns<K, V> c = make_columns<K, V, WARP>(p, r);
+    Reduce r = make_reduce<TEAM>(red, p);
+    const Columns<K, V> c = make_columns<K, V, TEAM>(p, r);
     const int worker = WARP ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x / r.cluster;
     const int workers = WARP ? gridDim.x * kWarps : gridDim.x / r.cluster;
     const bool has_pre = p.pre != TP_NORM_NONE, has_dy = p.dy[0] != nullptr, gate_rows = p.gate == TP_GATE_ELEMENT;
@@ -498,6 +508,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) bwd_kernel(c
         }
         copies_commit();
     };
+    if (c.ragged) clear_stages(stages, p.depth * stage_bytes);
     for (int i = 0; i < p.depth - 1; ++i) fetch(worker + i * workers, i);
     float2 gw[K][P], nw[K][P];  // c times the channel gate times the post-norm's weight; the pre-norm's weight
     load_weight<A>(p.post_w, c, plus, 1.0f, gw);
@@ -548,9 +559,9 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) bwd_kernel(c
                 }
             float m0 = s0.x + s0.y, m1 = s1.x + s1.y, none;
             if (LN)
-                row_sum<WARP, false>(m0, m1, none, r);
+                row_sum<TEAM, false>(m0, m1, none, r);
             else
-                row_sum<WARP>(m1, r);
+                row_sum<TEAM>(m1, r);
             m0 = LN && p.pre == TP_NORM_LAYER ? -st.w * m0 * inv_h : 0.0f;
             m1 *= -st.w * inv_h;
 #pragma unroll
@@ -587,9 +598,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) bwd_kernel(c
                 for (int j = 0; j < P; ++j) fh[k][j] = both(0.0f);
         }
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (c.on[k]) {
-                if (row_gate) {  // its gradient is D times p = fh w + b
+        for (int k = 0; k < K; ++k) {
+                if (row_gate && c.on[k]) {  // its gradient is D times p = fh w + b
                     float2 pv[P], w[P];
 #pragma unroll
                     for (int j = 0; j < P; ++j) pv[j] = fh[k][j];
@@ -604,7 +614,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) bwd_kernel(c
                         }
                     }
                     if (gate_rows) {
-                        load<A, V>(at, static_cast<long long>(k * c.lanes + threadIdx.x) * V, w);
+                        load<A, V>(at, static_cast<int>(k * c.lanes + threadIdx.x) * V, w);
 #pragma unroll
                         for (int j = 0; j < P; ++j) {
                             pv[j] = __fmul2_rn(__fmul2_rn(d[k][j], pv[j]), both(p.c));
@@ -630,13 +640,13 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) bwd_kernel(c
             }
         float m0 = s0.x + s0.y, m1 = s1.x + s1.y, dg = s2.x + s2.y;
         if (p.gate == TP_GATE_TOKEN) {
-            row_sum<WARP, true>(m0, m1, dg, r);
+            row_sum<TEAM, true>(m0, m1, dg, r);
             if (first) store1<A>(p.dg[js], lr, p.c * dg);
         } else if (p.post != TP_NORM_NONE) {
             if (LN)
-                row_sum<WARP, false>(m0, m1, dg, r);
+                row_sum<TEAM, false>(m0, m1, dg, r);
             else
-                row_sum<WARP>(m1, r);
+                row_sum<TEAM>(m1, r);
         }
         m0 = LN && p.post == TP_NORM_LAYER ? -st.y * m0 * inv_h : 0.0f;
         m1 = p.post != TP_NORM_NONE ? -st.y * m1 * inv_h : 0.0f;
@@ -652,6 +662,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) bwd_kernel(c
                 store<A, V>(p.df[js], e + c.at(k), o);
             }
     }
+    // the parameter gradients' blocks may take the SMs that are done; they wait for the whole grid
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // one row of partial sums a worker (the warps of a block added in order)
     const int out_row = WARP ? blockIdx.x : worker, out_rows = WARP ? gridDim.x : workers;
     int used = 0;
@@ -687,12 +699,11 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : kMaxThreads) bwd_kernel(c
                 }
         }
     }
-    if (r.cluster > 1) cluster_sync();  // no block leaves while another may write into it
+    if (TEAM == kCluster) cluster_sync();  // no block leaves while another may write into it
 }
 
-// ---------------------------------------------------------------------------
-// Parameter gradients from the partial rows: 32 columns a block, 8 threads a
-// column, the rows in a fixed order.
+// Parameter gradients from the partial rows: 32 columns a block, 32 threads a
+// column quadruple, the rows in a fixed order.
 // ---------------------------------------------------------------------------
 struct FinalPlan {
     const float *partials;
@@ -704,37 +715,52 @@ struct FinalPlan {
 
 template <typename A>
 __global__ void __launch_bounds__(256) param_grad_kernel(const __grid_constant__ FinalPlan p) {
-    __shared__ float part[4][8][32];
-    const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;
+    __shared__ float part[4][32][33];
+    const int quad = threadIdx.x & 7, r = threadIdx.x >> 3;
+    const int c0 = blockIdx.x * 32 + quad * 4;  // H is a multiple of 8: a quadruple is whole or absent
+    float4 s[4];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     int slot = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        float s = 0.0f;
-        if (p.use[q]) {
-            const float *in = p.partials + static_cast<long long>(slot++) * p.chunks * p.H + col;
-            if (col < p.H)
-                for (int i = r; i < p.chunks; i += 8) s += in[static_cast<long long>(i) * p.H];
-        }
-        part[q][r][lane] = s;
+        s[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (!p.use[q]) continue;
+        const float *in = p.partials + static_cast<long long>(slot++) * p.chunks * p.H + c0;
+        if (c0 < p.H)
+#pragma unroll 5
+            for (int i = r; i < p.chunks; i += 32) {
+                const float4 v = *reinterpret_cast<const float4 *>(in + static_cast<long long>(i) * p.H);
+                s[q].x += v.x; s[q].y += v.y; s[q].z += v.z; s[q].w += v.w;
+            }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        part[q][r][quad * 4] = s[q].x;
+        part[q][r][quad * 4 + 1] = s[q].y;
+        part[q][r][quad * 4 + 2] = s[q].z;
+        part[q][r][quad * 4 + 3] = s[q].w;
     }
     __syncthreads();
-    if (r || col >= p.H) return;
+    // 8 lanes a column: 4 rows each, then over the lanes
+    const int own = threadIdx.x >> 3, eighth = threadIdx.x & 7, col = blockIdx.x * 32 + own;
     float v[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         v[q] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[q] += part[q][i][lane];
+        for (int i = 0; i < 4; ++i) v[q] += part[q][eighth * 4 + i][own];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) v[q] += __shfl_xor_sync(0xffffffffu, v[q], o);
     }
+    if (eighth || col >= p.H) return;
     const float g = p.gate ? load1<A>(p.gate, col) : 1.0f;
     if (p.dpost_w) p.dpost_w[col] = p.c * g * v[0];
     if (p.dpost_b) p.dpost_b[col] = p.c * g * v[1];
     if (p.dgate) {
-        float s = v[0];
-        if (p.post_w) s *= load1<A>(p.post_w, col) + (p.zero_centered ? 1.0f : 0.0f);
-        if (p.post_b) s = fmaf(load1<A>(p.post_b, col), v[1], s);
-        p.dgate[col] = p.c * s;
+        float t = v[0];
+        if (p.post_w) t *= load1<A>(p.post_w, col) + (p.zero_centered ? 1.0f : 0.0f);
+        if (p.post_b) t = fmaf(load1<A>(p.post_b, col), v[1], t);
+        p.dgate[col] = p.c * t;
     }
     if (p.dpre_w) p.dpre_w[col] = v[2];
     if (p.dpre_b) p.dpre_b[col] = v[3];
@@ -782,11 +808,13 @@ using Kernel = void (*)(Plan);
 template <typename A, typename R, bool BWD, bool LN>
 static Kernel pick(const Shape &s) {
     if (BWD) {
-        if (s.warp) return s.E == 8 ? bwd_kernel<A, R, 8, true, LN> : s.E == 16 ? bwd_kernel<A, R, 16, true, LN> : bwd_kernel<A, R, 32, true, LN>;
-        return s.E == 8 ? bwd_kernel<A, R, 8, false, LN> : bwd_kernel<A, R, 16, false, LN>;
+        if (s.warp) return s.E == 8 ? bwd_kernel<A, R, 8, kWarp, LN> : s.E == 16 ? bwd_kernel<A, R, 16, kWarp, LN> : bwd_kernel<A, R, 32, kWarp, LN>;
+        if (s.cluster > 1) return s.E == 8 ? bwd_kernel<A, R, 8, kCluster, LN> : bwd_kernel<A, R, 16, kCluster, LN>;
+        return s.E == 8 ? bwd_kernel<A, R, 8, kBlock, LN> : bwd_kernel<A, R, 16, kBlock, LN>;
     }
-    if (s.warp) return s.E == 8 ? fwd_kernel<A, R, 8, true, LN> : s.E == 16 ? fwd_kernel<A, R, 16, true, LN> : fwd_kernel<A, R, 32, true, LN>;
-    return s.E == 8 ? fwd_kernel<A, R, 8, false, LN> : fwd_kernel<A, R, 16, false, LN>;
+    if (s.warp) return s.E == 8 ? fwd_kernel<A, R, 8, kWarp, LN> : s.E == 16 ? fwd_kernel<A, R, 16, kWarp, LN> : fwd_kernel<A, R, 32, kWarp, LN>;
+    if (s.cluster > 1) return s.E == 8 ? fwd_kernel<A, R, 8, kCluster, LN> : fwd_kernel<A, R, 16, kCluster, LN>;
+    return s.E == 8 ? fwd_kernel<A, R, 8, kBlock, LN> : fwd_kernel<A, R, 16, kBlock, LN>;
 }
 template <bool BWD, bool LN>
 static Kernel pick(const tp_block_norm_desc &d, const Shape &s) {
@@ -1073,12 +1101,18 @@ tp_status tp_block_norm_bwd(tp_block_norm *h, const void *const *dY, const void 
     fin.post_w = p.post_w;
     fin.post_b = p.post_b;
     fin.gate = d.gate == TP_GATE_CHANNEL ? p.g[0] : nullptr;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((d.H + 31) / 32);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_on() && grid ? 1 : 0;
     launch_begin("block_norm_param_grads", st);
-    if (d.dtype == TP_DT_F32)
-        bn::param_grad_kernel<float><<<(d.H + 31) / 32, 256, 0, st>>>(fin);
-    else
-        bn::param_grad_kernel<__nv_bfloat16><<<(d.H + 31) / 32, 256, 0, st>>>(fin);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = d.dtype == TP_DT_F32 ? cudaLaunchKernelEx(&cfg, bn::param_grad_kernel<float>, fin)
+                                         : cudaLaunchKernelEx(&cfg, bn::param_grad_kernel<__nv_bfloat16>, fin);
     launch_end("block_norm_param_grads", st);
     return cuda_check(e, "block_norm_param_grads");
 }
