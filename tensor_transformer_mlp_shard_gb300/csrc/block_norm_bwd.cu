@@ -1,0 +1,268 @@
+// The backward kernels of the block norm (see block_norm.cu for the mathematics).
+#include "block_norm.cuh"
+
+namespace tpmlp {
+namespace bn {
+
+// ---------------------------------------------------------------------------
+// Gradients of x, f and of a token or element gate, row by row, and this
+// worker's share of the column sums in registers.  LP, LN: the post- and the
+// pre-norm is a LayerNorm.
+// ---------------------------------------------------------------------------
+template <typename A, typename R, int E, Team TEAM, bool LP, bool LN>
+__global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) bwd_kernel(const __grid_constant__ Plan p) {
+    constexpr bool WARP = TEAM == kWarp;
+    constexpr int V = sizeof(R) == 2 ? 8 : 4, K = E / V, P = V / 2;
+    __shared__ float red[2][3][kSlots];
+    extern __shared__ __align__(16) uint8_t stages[];
+    Reduce r = make_reduce<TEAM>(red, p);
+    const Columns<K, V> c = make_columns<K, V, TEAM>(p, r);
+    const int worker = WARP ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x / r.cluster;
+    const int workers = WARP ? gridDim.x * kWarps : gridDim.x / r.cluster;
+    const bool has_pre = p.pre != TP_NORM_NONE, has_dy = p.dy[0] != nullptr, gate_rows = p.gate == TP_GATE_ELEMENT;
+    const bool row_gate = gate_rows || p.gate == TP_GATE_TOKEN;
+    const bool first = (WARP ? threadIdx.x & 31 : threadIdx.x) == 0 && r.rank == 0;
+    const float inv_h = 1.0f / p.H, plus = p.zero_centered ? 1.0f : 0.0f;
+    const uint32_t row_bytes = blockDim.x * E *
+                               static_cast<uint32_t>((has_dy ? sizeof(R) : 0) + (has_pre ? sizeof(R) + sizeof(A) : 0) +
+                                                     (p.need_f ? sizeof(A) : 0) + (gate_rows ? sizeof(A) : 0));
+    const uint32_t base = smem_at(stages);
+    Cursor next(p, worker, workers);
+    auto fetch = [&](int slot) {
+        if (next.row < p.M) {
+            const int js = next.shard;
+            const long long e = static_cast<long long>(next.local) * p.H;
+            uint32_t at = base + slot * row_bytes;
+            if (has_dy) at = stage<R>(at, static_cast<const R *>(p.dy[js]) + e, c);
+            if (has_pre) {
+                at = stage<R>(at, static_cast<const R *>(p.y_in[js]) + e, c);
+                at = stage<A>(at, static_cast<const A *>(p.dn[js]) + e, c);
+            }
+            if (p.need_f) at = stage<A>(at, static_cast<const A *>(p.f[js]) + e, c);
+            if (gate_rows) stage<A>(at, static_cast<const A *>(p.g[js]) + e, c);
+            next.advance(p);
+        }
+        copies_commit();
+    };
+    if (c.ragged) clear_stages(stages, p.depth * row_bytes);
+    for (int i = 0; i < p.depth - 1; ++i) fetch(i);
+    float2 gw[K][P], nw[K][P];  // c times the channel gate times the post-norm's weight; the pre-norm's weight
+    load_weight<A>(p.post_w, c, plus, 1.0f, gw);
+    times_gate<A>(p, c, gw);
+    load_weight<A>(p.pre_w, c, plus, 1.0f, nw);
+    float2 p1[K][P], n1[K][P], p0[LP ? K : 1][P], n0[LN ? K : 1][P];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < P; ++j) p1[k][j] = n1[k][j] = p0[LP ? k : 0][j] = n0[LN ? k : 0][j] = both(0.0f);
+    int slot = 0;
+    float4 st_next = worker < p.M ? p.stats_in[worker] : make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+    for (Cursor at_row(p, worker, workers); at_row.row < p.M; at_row.advance(p)) {
+        fetch(slot == 0 ? p.depth - 1 : slot - 1);  // into the slot of the row before
+        const int js = at_row.shard;
+        const long long e = static_cast<long long>(at_row.local) * p.H;
+        const float4 st = st_next;
+        if (at_row.row + workers < p.M) st_next = p.stats_in[at_row.row + workers];
+        const float gm = p.gate == TP_GATE_TOKEN ? load1<A>(p.g[js], at_row.local) : 1.0f;
+        copies_wait(p.depth - 1);
+        const uint8_t *at = stages + slot * row_bytes;
+        slot = slot + 1 == p.depth ? 0 : slot + 1;
+        float2 d[K][P];  // dy, then D
+        if (has_dy) {
+            staged<R>(at, c, d);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j) d[k][j] = both(0.0f);
+        }
+        if (has_pre) {
+            float2 yh[K][P], h[K][P];
+            float m0, m1, none;
+            float2 s0 = both(0.0f), s1 = both(0.0f);
+            staged<R>(at, c, yh);
+            staged<A>(at, c, h);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    if (LN) yh[k][j] = __fadd2_rn(yh[k][j], both(-st.z));
+                    yh[k][j] = __fmul2_rn(yh[k][j], both(st.w));
+                    n1[k][j] = __ffma2_rn(h[k][j], yh[k][j], n1[k][j]);  // h is zero past the row
+                    if (LN) n0[LN ? k : 0][j] = __fadd2_rn(n0[LN ? k : 0][j], h[k][j]);
+                    h[k][j] = __fmul2_rn(h[k][j], nw[k][j]);
+                    if (LN) s0 = __fadd2_rn(s0, h[k][j]);
+                    s1 = __ffma2_rn(h[k][j], yh[k][j], s1);
+                }
+            m0 = s0.x + s0.y;
+            m1 = s1.x + s1.y;
+            if (LN)
+                row_sum<TEAM, false>(m0, m1, none, r);
+            else
+                row_sum<TEAM>(m1, r);
+            m0 *= -st.w * inv_h;
+            m1 *= -st.w * inv_h;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    if (LN) d[k][j] = __fadd2_rn(d[k][j], both(m0));
+                    d[k][j] = __ffma2_rn(h[k][j], both(st.w), __ffma2_rn(yh[k][j], both(m1), d[k][j]));
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (c.on[k]) {
+                float2 o[P];
+#pragma unroll
+                for (int j = 0; j < P; ++j) o[j] = __fmul2_rn(d[k][j], both(p.a));
+                store<R, V>(p.dx[js], e + c.at(k), o);
+            }
+        if (!p.has_block) continue;
+        float2 fh[K][P];
+        float m0, m1, dg;
+        float2 s0 = both(0.0f), s1 = both(0.0f), s2 = both(0.0f);
+        if (p.need_f) {
+            staged<A>(at, c, fh);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    if (LP) fh[k][j] = __fadd2_rn(fh[k][j], both(-st.x));
+                    fh[k][j] = __fmul2_rn(fh[k][j], both(st.y));  // no post-norm: 1
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j) fh[k][j] = both(0.0f);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (row_gate && c.on[k]) {  // its gradient is D times p = fh w + b
+                float2 pv[P], w[P];
+#pragma unroll
+                for (int j = 0; j < P; ++j) pv[j] = fh[k][j];
+                if (p.post != TP_NORM_NONE) {
+                    load<A, V>(p.post_w, c.at(k), w);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) pv[j] = __fmul2_rn(pv[j], __fadd2_rn(w[j], both(plus)));
+                    if (LP) {
+                        load<A, V>(p.post_b, c.at(k), w);
+#pragma unroll
+                        for (int j = 0; j < P; ++j) pv[j] = __fadd2_rn(pv[j], w[j]);
+                    }
+                }
+                if (gate_rows) {
+                    load<A, V>(at, static_cast<int>(k * c.lanes + threadIdx.x) * V, w);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        pv[j] = __fmul2_rn(__fmul2_rn(d[k][j], pv[j]), both(p.c));
+                        d[k][j] = __fmul2_rn(d[k][j], w[j]);
+                    }
+                    store<A, V>(p.dg[js], e + c.at(k), pv);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        s2 = __ffma2_rn(d[k][j], pv[j], s2);
+                        d[k][j] = __fmul2_rn(d[k][j], both(gm));
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                p1[k][j] = __ffma2_rn(d[k][j], fh[k][j], p1[k][j]);
+                if (LP) p0[LP ? k : 0][j] = __fadd2_rn(p0[LP ? k : 0][j], d[k][j]);
+                d[k][j] = __fmul2_rn(d[k][j], gw[k][j]);  // the gradient of fh
+                if (LP) s0 = __fadd2_rn(s0, d[k][j]);
+                s1 = __ffma2_rn(d[k][j], fh[k][j], s1);
+            }
+        }
+        m0 = s0.x + s0.y;
+        m1 = s1.x + s1.y;
+        dg = s2.x + s2.y;
+        float none;
+        const bool token = p.gate == TP_GATE_TOKEN;
+        if (token)
+            row_sum<TEAM, true>(m0, m1, dg, r);
+        else if (LP)
+            row_sum<TEAM, false>(m0, m1, none, r);
+        else if (p.post != TP_NORM_NONE)
+            row_sum<TEAM>(m1, r);
+        if (token && first) store1<A>(p.dg[js], at_row.local, p.c * dg);
+        m0 *= -st.y * inv_h;
+        m1 = p.post != TP_NORM_NONE ? -st.y * m1 * inv_h : 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (c.on[k]) {
+                float2 o[P];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    o[j] = __fmul2_rn(d[k][j], both(st.y));
+                    if (LP) o[j] = __fadd2_rn(o[j], both(m0));
+                    o[j] = __ffma2_rn(fh[k][j], both(m1), o[j]);
+                }
+                store<A, V>(p.df[js], e + c.at(k), o);
+            }
+    }
+    // the parameter gradients' blocks may take the SMs that are done; they wait for the whole grid
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // one row of partial sums a worker (the warps of a block added in order)
+    const int out_row = WARP ? blockIdx.x : worker, out_rows = WARP ? gridDim.x : workers;
+    int used = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (!p.use[q]) continue;
+        float *out = p.partials + (static_cast<long long>(used++) * out_rows + out_row) * p.H;
+        float2 (*acc)[P] = q == 0 ? p1 : q == 1 ? p0 : q == 2 ? n1 : n0;
+        const bool whole = q == 0 || q == 2 || (q == 1 ? LP : LN);
+        if (WARP) {
+            // the stages' memory serves again: every row has been read
+            float *comb = reinterpret_cast<float *>(stages);
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j)
+                    *reinterpret_cast<float2 *>(comb + (threadIdx.x >> 5) * E * 32 + c.at(k) + 2 * j) = acc[whole ? k : 0][j];
+            __syncthreads();
+            for (int i = threadIdx.x; i < p.H; i += 32 * kWarps) {
+                float s = 0.0f;
+                for (int w = 0; w < kWarps; ++w) s += comb[w * E * 32 + i];
+                out[i] = s;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (c.on[k]) {
+#pragma unroll
+                    for (int j = 0; j < P; j += 2) {
+                        const float2 u = acc[whole ? k : 0][j], v = acc[whole ? k : 0][j + 1];
+                        *reinterpret_cast<float4 *>(out + c.at(k) + 2 * j) = make_float4(u.x, u.y, v.x, v.y);
+                    }
+                }
+        }
+    }
+    if (TEAM == kCluster) cluster_sync();  // no block leaves while another may write into it
+}
+
+template <typename A, typename R, bool LP, bool LN>
+static Kernel pick(const Shape &s) {
+    if (s.team == kWarp) return s.E == 8 ? bwd_kernel<A, R, 8, kWarp, LP, LN> : bwd_kernel<A, R, 16, kWarp, LP, LN>;
+    if (s.team == kCluster) return bwd_kernel<A, R, 16, kCluster, LP, LN>;
+    return s.E == 8 ? bwd_kernel<A, R, 8, kBlock, LP, LN> : bwd_kernel<A, R, 16, kBlock, LP, LN>;
+}
+template <bool LP, bool LN>
+static Kernel pick(const tp_block_norm_desc &d, const Shape &s) {
+    using bf = __nv_bfloat16;
+    if (d.dtype == TP_DT_F32) return pick<float, float, LP, LN>(s);
+    return d.residual_f32 ? pick<bf, float, LP, LN>(s) : pick<bf, bf, LP, LN>(s);
+}
+Kernel bwd_kernel_for(const tp_block_norm_desc &d, const Shape &s) {
+    const bool lp = d.post == TP_NORM_LAYER, ln = d.pre == TP_NORM_LAYER;
+    return lp ? (ln ? pick<true, true>(d, s) : pick<true, false>(d, s))
+              : (ln ? pick<false, true>(d, s) : pick<false, false>(d, s));
+}
+
+}  // namespace bn
+}  // namespace tpmlp

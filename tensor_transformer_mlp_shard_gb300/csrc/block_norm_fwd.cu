@@ -1,0 +1,127 @@
+// The forward kernels of the block norm (see block_norm.cu for the mathematics).
+#include "block_norm.cuh"
+
+namespace tpmlp {
+namespace bn {
+
+// ---------------------------------------------------------------------------
+// Forward.  A: type of f, g, n and the weights; R: type of x and y; E elements
+// a thread, in vectors of V; LP, LN: the post- and the pre-norm is a LayerNorm.
+// ---------------------------------------------------------------------------
+template <typename A, typename R, int E, Team TEAM, bool LP, bool LN>
+__global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd_kernel(const __grid_constant__ Plan p) {
+    constexpr bool WARP = TEAM == kWarp;
+    constexpr int V = sizeof(R) == 2 ? 8 : 4, K = E / V, P = V / 2;
+    __shared__ float red[2][3][kSlots];
+    extern __shared__ __align__(16) uint8_t stages[];
+    Reduce r = make_reduce<TEAM>(red, p);
+    const Columns<K, V> c = make_columns<K, V, TEAM>(p, r);
+    const int worker = WARP ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x / r.cluster;
+    const int workers = WARP ? gridDim.x * kWarps : gridDim.x / r.cluster;
+    const bool gate_rows = p.gate == TP_GATE_ELEMENT, first = (WARP ? threadIdx.x & 31 : threadIdx.x) == 0 && r.rank == 0;
+    const float inv_h = 1.0f / p.H, plus = p.zero_centered ? 1.0f : 0.0f;
+    const uint32_t stage_bytes =
+        blockDim.x * E * static_cast<uint32_t>(sizeof(R) + (p.has_block ? sizeof(A) : 0) + (gate_rows ? sizeof(A) : 0));
+    const uint32_t base = smem_at(stages);
+    Cursor next(p, worker, workers);
+    auto fetch = [&](int slot) {
+        if (next.row < p.M) {
+            const int js = next.shard;
+            const long long e = static_cast<long long>(next.local) * p.H;
+            uint32_t at = base + slot * stage_bytes;
+            at = stage<R>(at, static_cast<const R *>(p.x[js]) + e, c);
+            if (p.has_block) at = stage<A>(at, static_cast<const A *>(p.f[js]) + e, c);
+            if (gate_rows) stage<A>(at, static_cast<const A *>(p.g[js]) + e, c);
+            next.advance(p);
+        }
+        copies_commit();
+    };
+    if (c.ragged) clear_stages(stages, p.depth * stage_bytes);
+    for (int i = 0; i < p.depth - 1; ++i) fetch(i);
+    // weights of this thread's columns, the gate and the block's scale in the post-norm's
+    float2 pw[K][P], nw[K][P], pb[LP ? K : 1][P], nb[LN ? K : 1][P];
+    load_weight<A>(p.post_w, c, plus, 1.0f, pw);
+    times_gate<A>(p, c, pw);
+    load_weight<A>(p.pre_w, c, plus, 1.0f, nw);
+    if constexpr (LP) {
+        load_weight<A>(p.post_b, c, 0.0f, 0.0f, pb);
+        times_gate<A>(p, c, pb);
+    }
+    if constexpr (LN) load_weight<A>(p.pre_b, c, 0.0f, 0.0f, nb);
+    int slot = 0;
+    for (Cursor at_row(p, worker, workers); at_row.row < p.M; at_row.advance(p)) {
+        fetch(slot == 0 ? p.depth - 1 : slot - 1);  // into the slot of the row before
+        const int js = at_row.shard;
+        const long long e = static_cast<long long>(at_row.local) * p.H;
+        const float gm = p.gate == TP_GATE_TOKEN ? load1<A>(p.g[js], at_row.local) : 1.0f;
+        copies_wait(p.depth - 1);
+        const uint8_t *at = stages + slot * stage_bytes;
+        slot = slot + 1 == p.depth ? 0 : slot + 1;
+        float2 y[K][P];
+        staged<R>(at, c, y);
+        float4 st = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+        if (p.has_block) {
+            float2 f[K][P];
+            staged<A>(at, c, f);
+            if (p.post != TP_NORM_NONE) centre_row<TEAM, LP, V, K>(f, c, p.post, inv_h, p.eps, r, st.x, st.y);
+            // y = a x + g (P(f) scaled): the row's factors first, then the channel's
+            const float2 row_scale = both(LP ? st.y : st.y * gm);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    f[k][j] = __fmul2_rn(f[k][j], row_scale);
+                    if (LP) f[k][j] = __fmul2_rn(__ffma2_rn(f[k][j], pw[k][j], pb[LP ? k : 0][j]), both(gm));
+                    y[k][j] = __fmul2_rn(y[k][j], both(p.a));
+                }
+                if (gate_rows) {
+                    float2 g[P];
+                    load<A, V>(at, static_cast<int>(k * c.lanes + threadIdx.x) * V, g);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) f[k][j] = __fmul2_rn(f[k][j], g[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < P; ++j)
+                    y[k][j] = LP ? __fadd2_rn(f[k][j], y[k][j]) : __ffma2_rn(f[k][j], pw[k][j], y[k][j]);
+                const typename Pack<R, V>::Raw out = Pack<R, V>::pack(y[k]);
+                if (c.on[k]) *reinterpret_cast<typename Pack<R, V>::Raw *>(static_cast<R *>(p.y[js]) + e + c.at(k)) = out;
+                Pack<R, V>::unpack(out, y[k]);  // the pre-norm is of y as it is stored
+            }
+        }
+        if (p.pre != TP_NORM_NONE) {
+            centre_row<TEAM, LN, V, K>(y, c, p.pre, inv_h, p.eps, r, st.z, st.w);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    y[k][j] = __fmul2_rn(y[k][j], both(st.w));
+                    y[k][j] = LN ? __ffma2_rn(y[k][j], nw[k][j], nb[LN ? k : 0][j]) : __fmul2_rn(y[k][j], nw[k][j]);
+                }
+                if (c.on[k]) store<A, V>(p.n[js], e + c.at(k), y[k]);
+            }
+        }
+        if (p.stats && first) p.stats[at_row.row] = st;
+    }
+    if (TEAM == kCluster) cluster_sync();  // no block leaves while another may write into it
+}
+
+template <typename A, typename R, bool LP, bool LN>
+static Kernel pick(const Shape &s) {
+    if (s.team == kWarp) return s.E == 8 ? fwd_kernel<A, R, 8, kWarp, LP, LN> : fwd_kernel<A, R, 16, kWarp, LP, LN>;
+    if (s.team == kCluster) return fwd_kernel<A, R, 16, kCluster, LP, LN>;
+    return s.E == 8 ? fwd_kernel<A, R, 8, kBlock, LP, LN> : fwd_kernel<A, R, 16, kBlock, LP, LN>;
+}
+template <bool LP, bool LN>
+static Kernel pick(const tp_block_norm_desc &d, const Shape &s) {
+    using bf = __nv_bfloat16;
+    if (d.dtype == TP_DT_F32) return pick<float, float, LP, LN>(s);
+    return d.residual_f32 ? pick<bf, float, LP, LN>(s) : pick<bf, bf, LP, LN>(s);
+}
+Kernel fwd_kernel_for(const tp_block_norm_desc &d, const Shape &s) {
+    const bool lp = d.post == TP_NORM_LAYER, ln = d.pre == TP_NORM_LAYER;
+    return lp ? (ln ? pick<true, true>(d, s) : pick<true, false>(d, s))
+              : (ln ? pick<false, true>(d, s) : pick<false, false>(d, s));
+}
+
+}  // namespace bn
+}  // namespace tpmlp
