@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -104,9 +105,9 @@ SIGNATURES = {
     "tp_block_norm_create": (ctypes.c_int, [ctypes.POINTER(BlockNormDesc), ctypes.POINTER(VP)]),
     "tp_block_norm_destroy": (None, [VP]),
     "tp_block_norm_workspace_bytes": (ctypes.c_size_t, [VP]),
-    "tp_block_norm_fwd": (ctypes.c_int, [VP, PP, PP, PP, VP, VP, VP, VP, PP, PP, VP, VP]),
-    "tp_block_norm_bwd": (ctypes.c_int, [VP, PP, PP, PP, PP, PP, VP, VP, VP, VP, PP, PP, PP, VP, VP, VP, VP, VP,
-                                         ctypes.c_size_t, VP]),
+    # (their pointer arrays go as packed bytes, cheaper to make than ctypes arrays)
+    "tp_block_norm_fwd": (ctypes.c_int, [VP] * 12),
+    "tp_block_norm_bwd": (ctypes.c_int, [VP] * 18 + [ctypes.c_size_t, VP]),
     "tp_adamw_create": (ctypes.c_int, [ctypes.POINTER(AdamWDesc), ctypes.POINTER(AdamWTensor), ctypes.POINTER(VP)]),
     "tp_adamw_destroy": (None, [VP]),
     "tp_adamw_set_grads": (ctypes.c_int, [VP, PP]),
@@ -161,8 +162,14 @@ def _check(status: int):
         raise TpError(status, lib().tp_last_error().decode(errors="replace"))
 
 
+# the current stream's handle without a torch.cuda.Stream object around it (0.4 us against 3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         return VP(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, torch.cuda.Stream):
         return VP(stream.cuda_stream)
@@ -556,6 +563,40 @@ NORM = {"none": 0, "rms": 1, "layer": 2}
 GATE = {"none": 0, "channel": 1, "token": 2, "element": 3}
 
 
+def _pointer(name, t, n, dtype):
+    """Address of a contiguous CUDA tensor of n elements of a type."""
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() == n:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    raise ValueError(f"{name}: {tuple(t.shape)} has {t.numel()} elements, expected {n}")
+
+
+_pack1 = struct.Struct("P").pack
+
+
+def _pointers(name, ts, count, n, dtype):
+    """The addresses of `count` shards (one tensor, or a list), as a C array."""
+    if count == 1 and isinstance(ts, torch.Tensor):
+        return _pack1(_pointer(name, ts, n, dtype))
+    if ts is None:
+        raise ValueError(f"{name}: required")
+    if isinstance(ts, torch.Tensor):
+        ts = (ts,)
+    if len(ts) != count:
+        raise ValueError(f"{name}: expected {count} tensors, got {len(ts)}")
+    if count == 1:
+        return _pack1(_pointer(name, ts[0], n, dtype))
+    return struct.pack("%dP" % count, *[_pointer(f"{name}[{i}]", t, n, dtype) for i, t in enumerate(ts)])
+
+
 class TPBlockNorm:
     """Handle for the residual stream between one block and the next
     (tp_block_norm_create):
@@ -589,7 +630,9 @@ class TPBlockNorm:
         # elements and type of a gate's gradient are those of the gate, but a channel gate's is fp32
         self._gate_n = {"none": 0, "channel": self.H, "token": rows, "element": self._n}[gate]
         self._gate_nx = 1 if gate == "channel" else self.nx
-        self._array = VP * self.nx
+        self._has_post, self._has_pre = post != "none", pre != "none"
+        self._post_layer, self._pre_layer = post == "layer", pre == "layer"
+        self._fwd, self._bwd = lib().tp_block_norm_fwd, lib().tp_block_norm_bwd
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -600,77 +643,60 @@ class TPBlockNorm:
     def workspace_bytes(self) -> int:
         return int(lib().tp_block_norm_workspace_bytes(self._h))
 
-    @staticmethod
-    def _ptr(name, t, n, dtype):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{name}: must be a CUDA tensor")
-        if t.dtype != dtype:
-            raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
-        if t.numel() != n:
-            raise ValueError(f"{name}: {tuple(t.shape)} has {t.numel()} elements, expected {n}")
-        return t.data_ptr()
-
-    def _shards(self, name, ts, n, dtype, count=None):
-        if isinstance(ts, torch.Tensor):
-            ts = (ts,)
-        elif ts is None:
-            raise ValueError(f"{name}: required")
-        count = self.nx if count is None else count
-        if len(ts) != count:
-            raise ValueError(f"{name}: expected {count} tensors, got {len(ts)}")
-        if count == 1:
-            return self._array(self._ptr(name, ts[0], n, dtype))
-        return self._array(*[self._ptr(f"{name}[{i}]", t, n, dtype) for i, t in enumerate(ts)])
-
     def fwd(self, X, F=None, gate=None, post_w=None, post_b=None, pre_w=None, pre_b=None, Y=None, N=None, stats=None,
             stream=None):
         """Forward into Y and N (Y may be X).  stats: an fp32 [M, 4] tensor that
         keeps what the backward needs, or None."""
-        n, H, act, ptr = self._n, self.H, self._act, self._ptr
-        x = self._shards("X", X, n, self._res)
-        f = y = g = None
+        n, nx, H, act, res = self._n, self.nx, self.H, self._act, self._res
+        x, f, g, y, out = _pointers("X", X, nx, n, res), None, None, None, None
         if self.block:
-            f, y = self._shards("F", F, n, act), self._shards("Y", Y, n, self._res)
+            f, y = _pointers("F", F, nx, n, act), _pointers("Y", Y, nx, n, res)
             if self._gate_n:
-                g = self._shards("gate", gate, self._gate_n, act, self._gate_nx)
-        out = None if self.pre == "none" else self._shards("N", N, n, act)
-        _check(lib().tp_block_norm_fwd(
+                g = _pointers("gate", gate, self._gate_nx, self._gate_n, act)
+        if self._has_pre:
+            out = _pointers("N", N, nx, n, act)
+        status = self._fwd(
             self._h, x, f, g,
-            None if self.post == "none" else ptr("post_w", post_w, H, act),
-            ptr("post_b", post_b, H, act) if self.post == "layer" else None,
-            None if self.pre == "none" else ptr("pre_w", pre_w, H, act),
-            ptr("pre_b", pre_b, H, act) if self.pre == "layer" else None,
-            y, out, None if stats is None else ptr("stats", stats, 4 * self.M, torch.float32), _stream(stream)))
+            _pointer("post_w", post_w, H, act) if self._has_post else None,
+            _pointer("post_b", post_b, H, act) if self._post_layer else None,
+            _pointer("pre_w", pre_w, H, act) if self._has_pre else None,
+            _pointer("pre_b", pre_b, H, act) if self._pre_layer else None,
+            y, out, None if stats is None else _pointer("stats", stats, 4 * self.M, torch.float32), _stream(stream))
+        if status:
+            _check(status)
 
     def bwd(self, dY, dN, Y, F, gate, post_w, post_b, pre_w, stats, dX, dF, dgate, dpost_w, dpost_b, dpre_w, dpre_b,
             workspace=None, stream=None):
         """Backward from dY (None: zero) and dN, with the forward's Y (X without
         a block), F and stats.  dX may be dY.  Parameter gradients are fp32 and
         overwritten; a token or element gate's gradient has the gate's type."""
-        n, H, act, f32, ptr = self._n, self.H, self._act, torch.float32, self._ptr
-        has_pre, has_post = self.pre != "none", self.post != "none"
-        need_f = has_post or self.gate != "none"
-        dy = None if dY is None else self._shards("dY", dY, n, self._res)
-        dn = self._shards("dN", dN, n, act) if has_pre else None
-        y = self._shards("Y", Y, n, self._res) if has_pre else None
-        dx = self._shards("dX", dX, n, self._res)
-        f = self._shards("F", F, n, act) if need_f else None
-        df = self._shards("dF", dF, n, act) if self.block else None
+        n, nx, H, act, res, f32 = self._n, self.nx, self.H, self._act, self._res, torch.float32
+        pre, post, pre_l, post_l = self._has_pre, self._has_post, self._pre_layer, self._post_layer
         g = dg = None
         if self._gate_n:
-            g = self._shards("gate", gate, self._gate_n, act, self._gate_nx)
-            dg = self._shards("dgate", dgate, self._gate_n, f32 if self.gate == "channel" else act, self._gate_nx)
+            g = _pointers("gate", gate, self._gate_nx, self._gate_n, act)
+            dg = _pointers("dgate", dgate, self._gate_nx, self._gate_n, f32 if self.gate == "channel" else act)
         ws, nws = (None, 0) if workspace is None else _workspace(workspace)
-        _check(lib().tp_block_norm_bwd(
-            self._h, dy, dn, y, f, g, ptr("post_w", post_w, H, act) if has_post else None,
-            ptr("post_b", post_b, H, act) if self.post == "layer" else None,
-            ptr("pre_w", pre_w, H, act) if has_pre else None, ptr("stats", stats, 4 * self.M, f32), dx, df, dg,
-            ptr("dpost_w", dpost_w, H, f32) if has_post else None,
-            ptr("dpost_b", dpost_b, H, f32) if self.post == "layer" else None,
-            ptr("dpre_w", dpre_w, H, f32) if has_pre else None,
-            ptr("dpre_b", dpre_b, H, f32) if self.pre == "layer" else None, ws, nws, _stream(stream)))
+        status = self._bwd(
+            self._h,
+            None if dY is None else _pointers("dY", dY, nx, n, res),
+            _pointers("dN", dN, nx, n, act) if pre else None,
+            _pointers("Y", Y, nx, n, res) if pre else None,
+            _pointers("F", F, nx, n, act) if post or g is not None else None,
+            g,
+            _pointer("post_w", post_w, H, act) if post else None,
+            _pointer("post_b", post_b, H, act) if post_l else None,
+            _pointer("pre_w", pre_w, H, act) if pre else None,
+            _pointer("stats", stats, 4 * self.M, f32),
+            _pointers("dX", dX, nx, n, res),
+            _pointers("dF", dF, nx, n, act) if self.block else None,
+            dg,
+            _pointer("dpost_w", dpost_w, H, f32) if post else None,
+            _pointer("dpost_b", dpost_b, H, f32) if post_l else None,
+            _pointer("dpre_w", dpre_w, H, f32) if pre else None,
+            _pointer("dpre_b", dpre_b, H, f32) if pre_l else None, ws, nws, _stream(stream))
+        if status:
+            _check(status)
 
 
 # ---------------------------------------------------------------------------
@@ -747,7 +773,8 @@ class TPAdamW:
         self._h = h
         self.ctl = torch.empty(self.CTL_BYTES // 4, dtype=f32, device=dev)
         _check(lib().tp_adamw_ctl_init(self.ctl.data_ptr(), int(steps_done), _stream(None)))
-        self._ctl = VP(self.ctl.data_ptr())
+        self._ctl = self.ctl.data_ptr()
+        self._norm, self._step = lib().tp_adamw_grad_norm, lib().tp_adamw_step
         self.norm, self.scale = self.ctl[0:1], self.ctl[1:2]
         self.finite, self.steps = self.ctl.view(torch.int32)[2:3], self.ctl.view(torch.int32)[3:4]
 
@@ -788,16 +815,20 @@ class TPAdamW:
         from it: the clip factor, the step count and whether the norm is finite
         (if not, that step changes nothing).  Returns the norm as a one-element
         CUDA tensor that the next call overwrites."""
-        _check(lib().tp_adamw_grad_norm(self._h, grad_scale, max_norm, self._ctl, _stream(stream)))
+        status = self._norm(self._h, grad_scale, max_norm, self._ctl, _stream(stream))
+        if status:
+            _check(status)
         return self.norm
 
     def step(self, lr, step=None, grad_scale=1.0, stream=None):
         """Enqueue one step: number `step` (from 1) on grad_scale * grads, or,
         with step=None, as the last grad_norm() call left it."""
         if step is None:
-            _check(lib().tp_adamw_step(self._h, lr, 1.0, 0, self._ctl, _stream(stream)))
+            status = self._step(self._h, lr, 1.0, 0, self._ctl, _stream(stream))
         else:
-            _check(lib().tp_adamw_step(self._h, lr, grad_scale, step, None, _stream(stream)))
+            status = self._step(self._h, lr, grad_scale, step, None, _stream(stream))
+        if status:
+            _check(status)
 
 
 # ---------------------------------------------------------------------------
