@@ -528,7 +528,7 @@ TP_API tp_status tp_block_norm_bwd(tp_block_norm *h, const void *const *dY, cons
  *   float norm; float scale; int32 finite; int32 steps;
  * and lets a step be clipped, skipped and counted without the host, so that a
  * captured graph can be replayed step after step. */
-#define TP_ADAMW_CTL_BYTES 8192
+#define TP_ADAMW_CTL_BYTES 32768
 #define TP_ADAMW_MAX_TENSORS 65536
 typedef struct {
     int n_tensors;             /* 1..TP_ADAMW_MAX_TENSORS */
@@ -536,7 +536,7 @@ typedef struct {
     int grad_dtype;            /* TP_DT_F32 or TP_DT_BF16 */
     int state_bits;            /* 32 or 8 */
     double beta1, beta2;       /* in [0, 1) */
-    float eps;                 /* > 0 */
+    float eps;                 /* > 0, not subnormal */
     uint32_t seed;             /* of the 8-bit states' rounding */
 } tp_adamw_desc;
 typedef struct {

@@ -715,7 +715,7 @@ class TPAdamW:
     for each tensor.  steps_done: steps taken before, as grad_norm counts them.
     """
 
-    QBLOCK, CTL_BYTES = 256, 8192
+    QBLOCK, CTL_BYTES = 256, 32768
 
     def __init__(self, params, grads, master=None, m=None, v=None, m_scale=None, v_scale=None, state_bits=32,
                  beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, lr_scale=1.0, seed=0, steps_done=0):

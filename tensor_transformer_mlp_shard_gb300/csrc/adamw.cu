@@ -31,7 +31,7 @@ constexpr int kThreads = 256;
 constexpr int kBlock = 256;                     // elements that share a scale: a warp's, 8 a lane
 constexpr int kChunk = kThreads / 32 * kBlock;  // elements a thread block takes at a time
 constexpr int kNormChunk = 8 * 4 * kThreads;    // the gradient norm's chunk: 8 loads of 4 a thread in flight
-constexpr int kNormBlocks = 912;
+constexpr int kNormBlocks = 3648;
 constexpr uint32_t kMix1 = 0x9E3779B9u, kMix2 = 0xB504F333u;  // fractions of the golden ratio and of sqrt(2)
 
 // The control block in device memory: what the gradient norm leaves for the step.
@@ -56,11 +56,18 @@ struct Entry {
     long long n;
 };
 
+// Entries of the index over a table: a search of its few hundred chunk numbers
+// from the middle is a chain of reads past the constant cache, this leaves a
+// step or two of it.
+constexpr int kCoarse = 64;
+
 // Tensors of one launch, in the kernel's parameters: no copy to the device, no
 // allocation, and a launch captured into a graph carries its own table.
 template <int CAP>
 struct Table {
     int count, base;    // tensors here, and the index of the first of them in the list
+    int shift;          // chunk c lies in one of the tensors coarse[c >> shift] .. coarse[(c >> shift) + 1]
+    unsigned short coarse[kCoarse + 1];
     int chunk0[CAP + 1];
     float lr_scale[CAP], decay[CAP];
     Entry t[CAP];
@@ -75,7 +82,7 @@ struct Hyper {
 // tensor that holds chunk c: the last whose first chunk is at most c
 template <int CAP>
 __device__ __forceinline__ int tensor_of(const Table<CAP> &tab, int c) {
-    int lo = 0, hi = tab.count - 1;
+    int lo = tab.coarse[c >> tab.shift], hi = tab.coarse[(c >> tab.shift) + 1];
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (tab.chunk0[mid] <= c)
@@ -86,9 +93,11 @@ __device__ __forceinline__ int tensor_of(const Table<CAP> &tab, int c) {
     return lo;
 }
 
-// 4 elements from e, as two pairs; unless FULL, those past n read as zero
+// Elements are addressed as (a chunk's start, the same for the whole block; an
+// offset of 32 bits within the chunk, a thread's own and the same in every
+// chunk).  4 of them from e, as two pairs; unless FULL, those past n read as zero.
 template <bool FULL>
-__device__ __forceinline__ void load4(const float *p, long long e, long long n, float2 *v) {
+__device__ __forceinline__ void load4(const float *p, uint32_t e, uint32_t n, float2 *v) {
     if (FULL || e + 4 <= n) {
         const float4 w = *reinterpret_cast<const float4 *>(p + e);
         v[0] = make_float2(w.x, w.y);
@@ -102,7 +111,7 @@ __device__ __forceinline__ void load4(const float *p, long long e, long long n, 
     }
 }
 template <bool FULL>
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, long long e, long long n, float2 *v) {
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, uint32_t e, uint32_t n, float2 *v) {
     uint2 w = make_uint2(0u, 0u);
     if (FULL || e + 4 <= n) {
         w = *reinterpret_cast<const uint2 *>(p + e);
@@ -116,7 +125,7 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *p, long long e, long 
     v[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
 }
 template <bool FULL>
-__device__ __forceinline__ void store4(float *p, long long e, long long n, const float2 *v) {
+__device__ __forceinline__ void store4(float *p, uint32_t e, uint32_t n, const float2 *v) {
     if (FULL || e + 4 <= n) {
         *reinterpret_cast<float4 *>(p + e) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
     } else {
@@ -126,7 +135,7 @@ __device__ __forceinline__ void store4(float *p, long long e, long long n, const
     }
 }
 template <bool FULL>
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, long long e, long long n, const float2 *v) {
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, uint32_t e, uint32_t n, const float2 *v) {
     const uint2 w = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
     if (FULL || e + 4 <= n) {
         *reinterpret_cast<uint2 *>(p + e) = w;
@@ -140,7 +149,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, long long e, long long 
 
 // e4m3 codes, 4 in a word
 template <bool FULL>
-__device__ __forceinline__ uint32_t load4_codes(const uint8_t *p, long long e, long long n) {
+__device__ __forceinline__ uint32_t load4_codes(const uint8_t *p, uint32_t e, uint32_t n) {
     if (FULL || e + 4 <= n) return *reinterpret_cast<const uint32_t *>(p + e);
     uint32_t w = 0;
 #pragma unroll
@@ -149,7 +158,7 @@ __device__ __forceinline__ uint32_t load4_codes(const uint8_t *p, long long e, l
     return w;
 }
 template <bool FULL>
-__device__ __forceinline__ void store4_codes(uint8_t *p, long long e, long long n, uint32_t w) {
+__device__ __forceinline__ void store4_codes(uint8_t *p, uint32_t e, uint32_t n, uint32_t w) {
     if (FULL || e + 4 <= n) {
         *reinterpret_cast<uint32_t *>(p + e) = w;
     } else {
@@ -168,6 +177,27 @@ __device__ __forceinline__ void decode4(uint32_t w, float2 *v) {
 }
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// 1 / x to one unit in the last place, for a normal x (eps is one, and a root
+// is below 2^64); past 2^126 it is zero
+__device__ __forceinline__ float reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Square roots, rounded correctly for v from 2^-100 up: one Newton step from
+// the approximate reciprocal root, its residual s^2 - v exact in a fused
+// operation (Markstein, IBM J. Res. Dev. 34, 1990).  Compared with sqrtf for
+// all 2^24 values of two binades at ten exponents: none differs.  sqrtf itself
+// branches for its small arguments, at each of 8 values, and cost a quarter of
+// the kernel's instructions.
+constexpr float kRootMin = 7.8886091e-31f;  // 2^-100
+__device__ __forceinline__ float2 roots(float2 v) {
+    float2 y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(v.x));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(v.y));
+    const float2 s = __fmul2_rn(v, y), rest = __ffma2_rn(s, s, make_float2(-v.x, -v.y));
+    return __ffma2_rn(rest, __fmul2_rn(y, both(-0.5f)), s);
+}
 // two products that no addition is fused with
 __device__ __forceinline__ float2 mul(float a, float2 x) { return make_float2(__fmul_rn(a, x.x), __fmul_rn(a, x.y)); }
 
@@ -199,10 +229,11 @@ __device__ __forceinline__ void random_bits(uint32_t shifted_key, uint32_t eleme
 // probability of its nearness (16 random bits of it).  At that scale e4m3's
 // smallest normal value, 2^-6, is fp32's, 2^-126, so the formats' subnormal
 // values coincide too: a code's 7 bits are bits 20..26 of the fp32 value, and
-// one integer addition rounds in both ranges.  Largest code 0x7E (448): 0x7F
-// is NaN.
+// one integer addition rounds in both ranges.  448 plus the most random bits
+// that there are, 0x7EFFFF00, stays below 0x7F000000 (the code of NaN), and so
+// do the few units in the last place that 448 |x| / max |x| may exceed it by.
 __device__ __forceinline__ uint32_t round_e4m3(float x, uint32_t bits) {
-    return min((__float_as_uint(x) << 4) + bits, 0x7EFFFFFFu);  // the shift drops the sign
+    return (__float_as_uint(x) << 4) + bits;  // the shift drops the sign
 }
 __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
@@ -233,41 +264,64 @@ struct Values {
     float ms, vs;
 };
 
+// A chunk of a tensor: where its arrays start, and the elements that are left
+// of the tensor from there on (at most a chunk's count).
+template <typename G>
+struct Chunk {
+    float *w;
+    __nv_bfloat16 *p;
+    const G *g;
+    void *m, *v;
+    float *ms, *vs;
+    uint32_t left;
+};
+template <typename G, int BITS>
+__device__ __forceinline__ Chunk<G> chunk_of(const Entry &t, int index) {
+    const long long e = static_cast<long long>(index) * kChunk, blk = static_cast<long long>(index) * (kChunk / kBlock);
+    Chunk<G> k;
+    k.w = static_cast<float *>(t.w) + e;
+    k.p = static_cast<__nv_bfloat16 *>(t.p) + e;
+    k.g = static_cast<const G *>(t.g) + e;
+    k.m = static_cast<char *>(t.m) + e * (BITS / 8);
+    k.v = static_cast<char *>(t.v) + e * (BITS / 8);
+    k.ms = t.ms + blk;
+    k.vs = t.vs + blk;
+    const long long left = t.n - e;
+    k.left = left < kChunk ? static_cast<uint32_t>(left) : kChunk;
+    return k;
+}
+
 template <bool FULL, typename G, int BITS>
-__device__ __forceinline__ void read_block(const Entry &t, long long blk, Values<G, BITS> &x) {
-    const long long n = t.n;
+__device__ __forceinline__ void read_block(const Chunk<G> &t, uint32_t e0, Values<G, BITS> &x) {
     if (BITS == 8) {
-        x.ms = t.ms[blk];
-        x.vs = t.vs[blk];
+        x.ms = t.ms[threadIdx.x >> 5];
+        x.vs = t.vs[threadIdx.x >> 5];
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const long long e = blk * kBlock + (threadIdx.x & 31) * 4 + j * 128;
-        load4<FULL>(static_cast<const float *>(t.w), e, n, x.w[j]);
-        load4<FULL>(static_cast<const G *>(t.g), e, n, x.g[j]);
+        const uint32_t e = e0 + j * 128;
+        load4<FULL>(static_cast<const float *>(t.w), e, t.left, x.w[j]);
+        load4<FULL>(t.g, e, t.left, x.g[j]);
         if (BITS == 32) {
-            load4<FULL>(static_cast<const float *>(t.m), e, n, x.m[j]);
-            load4<FULL>(static_cast<const float *>(t.v), e, n, x.v[j]);
+            load4<FULL>(static_cast<const float *>(t.m), e, t.left, x.m[j]);
+            load4<FULL>(static_cast<const float *>(t.v), e, t.left, x.v[j]);
         } else {
-            x.mc[j] = load4_codes<FULL>(static_cast<const uint8_t *>(t.m), e, n);
-            x.vc[j] = load4_codes<FULL>(static_cast<const uint8_t *>(t.v), e, n);
+            x.mc[j] = load4_codes<FULL>(static_cast<const uint8_t *>(t.m), e, t.left);
+            x.vc[j] = load4_codes<FULL>(static_cast<const uint8_t *>(t.v), e, t.left);
         }
     }
 }
 
 template <bool FULL, bool HALF, typename G, int BITS>
-__device__ __forceinline__ void step_block(const Entry &t, long long blk, Values<G, BITS> &x, uint32_t key,
-                                           const uint32_t (&elem)[2][4], const Hyper &hy, float scale,
-                                           float decay, float rate, float inv_root_bc2) {
-    const int lane = threadIdx.x & 31;
-    const long long n = t.n, e0 = blk * kBlock + lane * 4;
+__device__ __forceinline__ void step_block(const Chunk<G> &t, uint32_t e0, Values<G, BITS> &x, uint32_t key,
+                                           const uint32_t (&elem)[2][4], const Hyper &hy, float scale, float decay,
+                                           float rate, float inv_root_bc2) {
+    const uint32_t n = t.left;
     float2 (&w)[2][2] = x.w, (&g)[2][2] = x.g, (&m)[2][2] = x.m, (&v)[2][2] = x.v;
     uint32_t (&mc)[2] = x.mc, (&vc)[2] = x.vc;
     float &ms = x.ms, &vs = x.vs;
-    uint32_t top_m = 0, top_r = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const long long e = e0 + j * 128;
         if (BITS == 8) {
             decode4(mc[j], m[j]);
             decode4(vc[j], v[j]);
@@ -286,19 +340,46 @@ __device__ __forceinline__ void step_block(const Entry &t, long long blk, Values
             const float2 gi = __fmul2_rn(g[j][i], both(scale)), cg = __fmul2_rn(both(hy.c2), gi);
             m[j][i] = __fadd2_rn(mul(hy.b1, m[j][i]), mul(hy.c1, gi));
             v[j][i] = __fadd2_rn(mul(hy.b2, v[j][i]), make_float2(__fmul_rn(cg.x, gi.x), __fmul_rn(cg.y, gi.y)));
-            const float2 root = make_float2(sqrtf(v[j][i].x), sqrtf(v[j][i].y));
-            const float2 d = __ffma2_rn(root, both(inv_root_bc2), both(hy.eps));
-            const float2 q = __fmul2_rn(m[j][i], both(-rate));
-            w[j][i] = __fadd2_rn(__ffma2_rn(both(-decay), w[j][i], w[j][i]),
-                                 make_float2(__fdividef(q.x, d.x), __fdividef(q.y, d.y)));
-            if (BITS == 8) {
-                v[j][i] = root;
-                top_m = max(top_m, max(__float_as_uint(m[j][i].x) & 0x7FFFFFFFu, __float_as_uint(m[j][i].y) & 0x7FFFFFFFu));
-                top_r = max(top_r, max(__float_as_uint(root.x) & 0x7FFFFFFFu, __float_as_uint(root.y) & 0x7FFFFFFFu));
-            }
         }
-        store4<FULL>(static_cast<float *>(t.w), e, n, w[j]);
-        if (HALF) store4<FULL>(static_cast<__nv_bfloat16 *>(t.p), e, n, w[j]);
+    }
+    float2 root[2][2];
+    uint32_t top_m = 0, top_r = 0;
+    if (BITS == 8) {
+        float least = 3.4e38f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                root[j][i] = roots(v[j][i]);
+                least = fminf(least, fminf(v[j][i].x, v[j][i].y));
+                top_m = max(top_m, max(__float_as_uint(m[j][i].x) & 0x7FFFFFFFu, __float_as_uint(m[j][i].y) & 0x7FFFFFFFu));
+                top_r = max(top_r, max(__float_as_uint(root[j][i].x), __float_as_uint(root[j][i].y)));  // not negative
+            }
+        // outside what roots() takes (zeros above all), where it may have left a NaN
+        if (least < kRootMin || top_r >= 0x7F800000u) {
+            top_r = 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    root[j][i] = make_float2(sqrtf(v[j][i].x), sqrtf(v[j][i].y));
+                    top_r = max(top_r, max(__float_as_uint(root[j][i].x) & 0x7FFFFFFFu, __float_as_uint(root[j][i].y) & 0x7FFFFFFFu));
+                }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t e = e0 + j * 128;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (BITS == 32) root[j][i] = make_float2(sqrtf(v[j][i].x), sqrtf(v[j][i].y));
+            const float2 d = __ffma2_rn(root[j][i], both(inv_root_bc2), both(hy.eps));
+            const float2 q = __fmul2_rn(m[j][i], both(-rate));
+            w[j][i] = __ffma2_rn(q, make_float2(reciprocal(d.x), reciprocal(d.y)),
+                                 __ffma2_rn(both(-decay), w[j][i], w[j][i]));
+        }
+        store4<FULL>(t.w, e, n, w[j]);
+        if (HALF) store4<FULL>(t.p, e, n, w[j]);
         if (BITS == 32) {
             store4<FULL>(static_cast<float *>(t.m), e, n, m[j]);
             store4<FULL>(static_cast<float *>(t.v), e, n, v[j]);
@@ -317,15 +398,15 @@ __device__ __forceinline__ void step_block(const Entry &t, long long blk, Values
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float2 a = __fmul2_rn(__fmul2_rn(m[j][i], both(inv_m)), down);
-            const float2 b = __fmul2_rn(__fmul2_rn(v[j][i], both(inv_r)), down);
+            const float2 b = __fmul2_rn(__fmul2_rn(root[j][i], both(inv_r)), down);
             uint32_t of_m, of_r;
             random_bits(shifted_key, elem[j][2 * i], of_m, of_r);
             cm[2 * i] = round_e4m3(a.x, of_m);
             // a root above zero (at least 2^-75, the root of fp32's smallest value) keeps a code above zero
-            cr[2 * i] = max(round_e4m3(b.x, of_r), min(__float_as_uint(v[j][i].x), 0x01000000u));
+            cr[2 * i] = max(round_e4m3(b.x, of_r), min(__float_as_uint(root[j][i].x), 0x01000000u));
             random_bits(shifted_key, elem[j][2 * i + 1], of_m, of_r);
             cm[2 * i + 1] = round_e4m3(a.y, of_m);
-            cr[2 * i + 1] = max(round_e4m3(b.y, of_r), min(__float_as_uint(v[j][i].y), 0x01000000u));
+            cr[2 * i + 1] = max(round_e4m3(b.y, of_r), min(__float_as_uint(root[j][i].y), 0x01000000u));
         }
         const uint32_t sign = top_bytes(__float_as_uint(m[j][0].x), __float_as_uint(m[j][0].y),
                                         __float_as_uint(m[j][1].x), __float_as_uint(m[j][1].y)) & 0x80808080u;
@@ -334,9 +415,9 @@ __device__ __forceinline__ void step_block(const Entry &t, long long blk, Values
         store4_codes<FULL>(static_cast<uint8_t *>(t.m), e0 + j * 128, n, mc[j]);
         store4_codes<FULL>(static_cast<uint8_t *>(t.v), e0 + j * 128, n, vc[j]);
     }
-    if (lane == 0) {
-        t.ms[blk] = ms;
-        t.vs[blk] = vs;
+    if ((threadIdx.x & 31) == 0) {
+        t.ms[threadIdx.x >> 5] = ms;
+        t.vs[threadIdx.x >> 5] = vs;
     }
 }
 
@@ -378,26 +459,24 @@ __device__ __forceinline__ void copy_async4(uint32_t dst, const void *src) {
 }
 
 template <typename G>
-__device__ __forceinline__ void stage_block(const Entry &t, long long blk, uint32_t at) {
+__device__ __forceinline__ void stage_block(const Chunk<G> &t, uint32_t e, uint32_t at) {
     at += threadIdx.x * 16;
-    const long long e = blk * kBlock + (threadIdx.x & 31) * 4;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        copy_async16(at + j * kThreads * 16, static_cast<const float *>(t.w) + e + j * 128);
+        copy_async16(at + j * kThreads * 16, t.w + (e + j * 128));
         if (sizeof(G) == 4)
-            copy_async16(at + (2 + j) * kThreads * 16, static_cast<const G *>(t.g) + e + j * 128);
+            copy_async16(at + (2 + j) * kThreads * 16, t.g + (e + j * 128));
         else
-            copy_async8(at + 2 * kThreads * 16 + (j * kThreads - static_cast<int>(threadIdx.x)) * 8,
-                        static_cast<const G *>(t.g) + e + j * 128);
+            copy_async8(at + 2 * kThreads * 16 + (j * kThreads - static_cast<int>(threadIdx.x)) * 8, t.g + (e + j * 128));
     }
     at += kThreads * (32 + 8 * sizeof(G)) - threadIdx.x * 12;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        copy_async4(at + j * kThreads * 4, static_cast<const uint8_t *>(t.m) + e + j * 128);
-        copy_async4(at + (2 + j) * kThreads * 4, static_cast<const uint8_t *>(t.v) + e + j * 128);
+        copy_async4(at + j * kThreads * 4, static_cast<const uint8_t *>(t.m) + (e + j * 128));
+        copy_async4(at + (2 + j) * kThreads * 4, static_cast<const uint8_t *>(t.v) + (e + j * 128));
     }
-    copy_async4(at + 4 * kThreads * 4, t.ms + blk);  // every lane its own copy of the scales
-    copy_async4(at + 5 * kThreads * 4, t.vs + blk);
+    copy_async4(at + 4 * kThreads * 4, t.ms + (threadIdx.x >> 5));  // every lane its own copy of the scales
+    copy_async4(at + 5 * kThreads * 4, t.vs + (threadIdx.x >> 5));
 }
 template <typename G>
 __device__ __forceinline__ void staged_block(const uint8_t *at, Values<G, 8> &x) {
@@ -420,13 +499,14 @@ __global__ void __launch_bounds__(kThreads, 4) step_kernel(const __grid_constant
     float scale = hy.scale, inv_bc1 = hy.inv_bc1, inv_root_bc2 = hy.inv_root_bc2;
     uint32_t step = hy.step;
     if (hy.ctl) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the gradient norm, whose end this launch overlaps
         if (!hy.ctl->finite) return;
         scale = hy.ctl->scale;
         inv_bc1 = hy.ctl->inv_bc1;
         inv_root_bc2 = hy.ctl->inv_root_bc2;
         step = static_cast<uint32_t>(hy.ctl->steps);
     }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t at_step = mix(hy.seed + kMix1 * step);
     uint32_t elem[2][4];
 #pragma unroll
@@ -434,13 +514,13 @@ __global__ void __launch_bounds__(kThreads, 4) step_kernel(const __grid_constant
 #pragma unroll
         for (int i = 0; i < 4; ++i) elem[j][i] = BITS == 8 ? hash_of_element(j * 128 + lane * 4 + i) : 0u;
     const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(stages));
+    const uint32_t e0 = warp * kBlock + lane * 4;
     Walk<CAP> now(tab), ahead = now;
     // stages the next whole block of this warp; a group is committed in any case, so that the count of groups is that of chunks
     auto fetch = [&](int slot) {
         if (ahead.c < ahead.end) {
-            const Entry &t = tab.t[ahead.ti];
-            const long long blk = static_cast<long long>(ahead.c - tab.chunk0[ahead.ti]) * (kThreads / 32) + warp;
-            if ((blk + 1) * kBlock <= t.n) stage_block<G>(t, blk, smem + slot * stage_bytes<G>());
+            const Chunk<G> t = chunk_of<G, BITS>(tab.t[ahead.ti], ahead.c - tab.chunk0[ahead.ti]);
+            if ((warp + 1) * kBlock <= t.left) stage_block<G>(t, e0, smem + slot * stage_bytes<G>());
             ahead.next(tab);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -449,32 +529,35 @@ __global__ void __launch_bounds__(kThreads, 4) step_kernel(const __grid_constant
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) fetch(i);
     }
-    int slot = 0;
+    int slot = 0, of = -1;
+    uint32_t of_tensor = 0;
+    float decay = 0.0f, rate = 0.0f;
     for (; now.c < now.end; now.next(tab)) {
-        const int ti = now.ti;
-        const Entry &t = tab.t[ti];
-        const long long blk = static_cast<long long>(now.c - tab.chunk0[ti]) * (kThreads / 32) + warp;
-        const float lr = hy.lr * tab.lr_scale[ti];
-        const float decay = lr * tab.decay[ti], rate = lr * inv_bc1;
-        const bool full = (blk + 1) * kBlock <= t.n, some = blk * kBlock < t.n;
-        uint32_t key = 0;
-        if (BITS == 8) {
-            key = mix(mix(at_step ^ (static_cast<uint32_t>(tab.base + ti) * kMix2 + 1u)) + static_cast<uint32_t>(blk));
+        const int ti = now.ti, index = now.c - tab.chunk0[ti];
+        const Chunk<G> t = chunk_of<G, BITS>(tab.t[ti], index);
+        if (ti != of) {
+            of = ti;
+            const float lr = hy.lr * tab.lr_scale[ti];
+            decay = lr * tab.decay[ti];
+            rate = lr * inv_bc1;
+            of_tensor = mix(at_step ^ (static_cast<uint32_t>(tab.base + ti) * kMix2 + 1u));
         }
+        uint32_t key = 0;
+        if (BITS == 8) key = mix(of_tensor + static_cast<uint32_t>(index * (kChunk / kBlock) + warp));
         Values<G, BITS> x;
         if (BITS == 8) {
             fetch(slot == 0 ? kStages - 1 : slot - 1);  // the slot read in the last round
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         }
-        if (full) {
+        if ((warp + 1) * kBlock <= t.left) {
             if constexpr (BITS == 8)
                 staged_block<G>(stages + slot * stage_bytes<G>(), x);
             else
-                read_block<true, G, BITS>(t, blk, x);
-            step_block<true, HALF, G, BITS>(t, blk, x, key, elem, hy, scale, decay, rate, inv_root_bc2);
-        } else if (some) {
-            read_block<false, G, BITS>(t, blk, x);
-            step_block<false, HALF, G, BITS>(t, blk, x, key, elem, hy, scale, decay, rate, inv_root_bc2);
+                read_block<true, G, BITS>(t, e0, x);
+            step_block<true, HALF, G, BITS>(t, e0, x, key, elem, hy, scale, decay, rate, inv_root_bc2);
+        } else if (warp * kBlock < t.left) {
+            read_block<false, G, BITS>(t, e0, x);
+            step_block<false, HALF, G, BITS>(t, e0, x, key, elem, hy, scale, decay, rate, inv_root_bc2);
         }
         slot = slot + 1 == kStages ? 0 : slot + 1;
     }
@@ -526,12 +609,12 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     __shared__ int is_last;
     float2 s = both(0.0f), rest = both(0.0f);
     for (Walk<CAP> now(tab); now.c < now.end; now.next(tab)) {
-        const long long n = tab.t[now.ti].n;
-        const long long e = static_cast<long long>(now.c - tab.chunk0[now.ti]) * kNormChunk + threadIdx.x * 4;
-        const G *in = static_cast<const G *>(tab.t[now.ti].g);
+        const long long e0 = static_cast<long long>(now.c - tab.chunk0[now.ti]) * kNormChunk, left = tab.t[now.ti].n - e0;
+        const G *in = static_cast<const G *>(tab.t[now.ti].g) + e0;
+        const uint32_t e = threadIdx.x * 4, n = left < kNormChunk ? static_cast<uint32_t>(left) : kNormChunk;
         constexpr int L = kNormChunk / (4 * kThreads);
         float2 g[L][2];
-        if (e - threadIdx.x * 4 + kNormChunk <= n) {
+        if (n == kNormChunk) {
 #pragma unroll
             for (int j = 0; j < L; ++j) load4<true>(in, e + j * 4 * kThreads, n, g[j]);
         } else {
@@ -548,6 +631,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
                 s = z;
             }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     add_pair(s.x, rest.x, s.y, rest.y);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -633,7 +717,8 @@ static tp_status aw_validate(const tp_adamw_desc *d, const tp_adamw_tensor *t) {
         return set_error(TP_ERR_ARG, "state_bits=%d is neither 8 nor 32", d->state_bits);
     if (!(d->beta1 >= 0.0 && d->beta1 < 1.0) || !(d->beta2 >= 0.0 && d->beta2 < 1.0))
         return set_error(TP_ERR_ARG, "beta1 and beta2 must be in [0, 1)");
-    if (!(d->eps > 0.0f) || !std::isfinite(d->eps)) return set_error(TP_ERR_ARG, "eps must be positive and finite");
+    if (!(d->eps >= 1.17549435e-38f) || !std::isfinite(d->eps))
+        return set_error(TP_ERR_ARG, "eps must be a positive normal number");
     if (!t) return set_error(TP_ERR_ARG, "tensors is NULL");
     long long chunks = 0;
     for (int i = 0; i < d->n_tensors; ++i) {
@@ -683,7 +768,27 @@ static int fill(const tp_adamw *h, int i, int chunk, Table<CAP> &tab) {
         tab.chunk0[tab.count + 1] = tab.chunk0[tab.count] + static_cast<int>((s.n + chunk - 1) / chunk);
         ++tab.count;
     }
+    const int chunks = tab.chunk0[tab.count];
+    for (tab.shift = 0; (chunks >> tab.shift) >= kCoarse; ++tab.shift) {
+    }
+    for (int k = 0, t = 0; k <= kCoarse; ++k) {
+        const long long c = static_cast<long long>(k) << tab.shift;
+        while (t + 1 < tab.count && tab.chunk0[t + 1] <= c) ++t;
+        tab.coarse[k] = static_cast<unsigned short>(t);
+    }
     return i;
+}
+
+// Thread blocks for a number of chunks.  The SMs do not run at one speed (an
+// SM's distance to the memory that it happens to read differs), so even runs
+// for just the resident blocks leave the fast ones idle at the end; runs of
+// kRun chunks are short enough for the hardware to deal them out as blocks
+// finish, and long enough to pay for a block's start.
+constexpr int kRun = 2, kNormRun = 8;
+static int blocks_for(int chunks, int run, int resident) {
+    if (chunks <= resident) return chunks;
+    const int runs = (chunks + run - 1) / run;
+    return runs > resident ? runs : resident;
 }
 
 template <int CAP>
@@ -698,13 +803,24 @@ static tp_status step_launch(const Table<CAP> &tab, const tp_adamw_desc &d, cons
     else
         k = half ? (gh ? step_kernel<CAP, true, bf, 8> : step_kernel<CAP, true, float, 8>)
                  : (gh ? step_kernel<CAP, false, bf, 8> : step_kernel<CAP, false, float, 8>);
-    const int chunks = tab.chunk0[tab.count], most = 4 * num_sms();
+    const int chunks = tab.chunk0[tab.count];
     if (!chunks) return TP_OK;
+    const int grid = blocks_for(chunks, kRun, 4 * num_sms());
     const int smem = d.state_bits == 8 ? kStages * (gh ? stage_bytes<bf>() : stage_bytes<float>()) : 0;
     if (smem) TRY(cuda_check(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), "adamw_step"));
+    // after the gradient norm, the blocks' starts overlap its end
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = hy.ctl && pdl_on() ? 1 : 0;
     launch_begin("adamw_step", st);
-    k<<<chunks < most ? chunks : most, kThreads, smem, st>>>(tab, hy);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k, tab, hy);
     launch_end("adamw_step", st);
     return cuda_check(e, "adamw_step");
 }
@@ -737,8 +853,8 @@ static tp_status norm_all(const tp_adamw *h, NormArgs a, cudaStream_t st) {
     Table<CAP> tab;
     long long chunks = 0;
     for (int i = 0; i < h->d.n_tensors; ++i) chunks += (h->t[i].n + kNormChunk - 1) / kNormChunk;
-    int grid = kNormBlocks < 6 * num_sms() ? kNormBlocks : 6 * num_sms();
-    if (chunks < grid) grid = chunks > 0 ? static_cast<int>(chunks) : 1;
+    int grid = blocks_for(static_cast<int>(chunks), kNormRun, 4 * num_sms());
+    grid = grid < 1 ? 1 : grid > kNormBlocks ? kNormBlocks : grid;
     for (int i = 0; i < h->d.n_tensors;) {
         a.first = i == 0;
         i = fill(h, i, kNormChunk, tab);
