@@ -140,7 +140,7 @@ struct Launch {
 };
 static std::mutex g_launch_mutex;
 
-static tp_status prepare(Launch &kept, const tp_block_norm_desc &d, bool bwd, int bytes, Launch &l) {
+static tp_status prepare(Launch &kept, const tp_block_norm_desc &d, bool bwd, bool has_dy, int bytes, Launch &l) {
     int dev = 0;
     TRY(cuda_check(cudaGetDevice(&dev), "cudaGetDevice"));
     std::lock_guard<std::mutex> lock(g_launch_mutex);
@@ -150,7 +150,11 @@ static tp_status prepare(Launch &kept, const tp_block_norm_desc &d, bool bwd, in
     int want = 1;
     for (;;) {
         l.s = shape_of(d.H, bytes, want);
-        l.k = bwd ? bwd_kernel_for(d, l.s) : fwd_kernel_for(d, l.s);
+        l.s.common = !d.seq_parallel && d.has_block && d.pre != TP_NORM_NONE && d.gate <= TP_GATE_CHANNEL &&
+                     (!bwd || (has_dy && (d.post != TP_NORM_NONE || d.gate == TP_GATE_CHANNEL)));
+        l.k = d.dtype == TP_DT_F32  ? (bwd ? bwd_kernel_f32(d, l.s) : fwd_kernel_f32(d, l.s))
+              : d.residual_f32      ? (bwd ? bwd_kernel_mixed(d, l.s) : fwd_kernel_mixed(d, l.s))
+                                    : (bwd ? bwd_kernel_bf16(d, l.s) : fwd_kernel_bf16(d, l.s));
         TRY(cuda_check(cudaFuncSetAttribute(l.k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_share(1)), "block norm"));
         int by_registers = 0;
         TRY(cuda_check(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&by_registers, l.k, l.s.threads, 0), "block norm"));
@@ -200,7 +204,7 @@ struct tp_block_norm {
     tp_block_norm_desc d;
     int M, nx, rows_split;
     int use[4];
-    bn::Launch fwd, bwd;
+    bn::Launch fwd, bwd, bwd_alone;  // bwd_alone: without dY
 };
 
 static tp_status bn_pointer(const void *p, const char *name, int i, int n) {
@@ -328,7 +332,7 @@ tp_status tp_block_norm_fwd(tp_block_norm *h, const void *const *X, const void *
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int ea = d.dtype == TP_DT_F32 ? 4 : 2, er = d.residual_f32 ? 4 : ea;
     bn::Launch l;
-    TRY(bn::prepare(h->fwd, d, false, er + (d.has_block ? ea : 0) + (d.gate == TP_GATE_ELEMENT ? ea : 0), l));
+    TRY(bn::prepare(h->fwd, d, false, false, er + (d.has_block ? ea : 0) + (d.gate == TP_GATE_ELEMENT ? ea : 0), l));
     int workers;
     return bn::run(l, p, 0, "block_norm_fwd", st, &workers);
 }
@@ -393,7 +397,7 @@ tp_status tp_block_norm_bwd(tp_block_norm *h, const void *const *dY, const void 
         p.need_f = d.has_block && (d.post != TP_NORM_NONE || d.gate != TP_GATE_NONE);
         const bool pre = d.pre != TP_NORM_NONE;
         bn::Launch l;
-        TRY(bn::prepare(h->bwd, d, true,
+        TRY(bn::prepare(dY ? h->bwd : h->bwd_alone, d, true, dY != nullptr,
                         er + (pre ? er + ea : 0) + (p.need_f ? ea : 0) + (d.gate == TP_GATE_ELEMENT ? ea : 0), l));
         TRY(bn::run(l, p, bn::kMaxChunks, "block_norm_bwd", st, &grid));
     }

@@ -67,12 +67,14 @@ struct Pack<float, 4> {
     __device__ static Raw pack(const float2 *v) { return make_float4(v[0].x, v[0].y, v[1].x, v[1].y); }
 };
 
+// (a row's start is the same for the whole block: a thread's own part of an
+// address is 32 bits and the same in every row)
 template <typename T, int V>
-__device__ __forceinline__ void load(const void *base, long long e, float2 *v) {
+__device__ __forceinline__ void load(const void *base, uint32_t e, float2 *v) {
     Pack<T, V>::unpack(*reinterpret_cast<const typename Pack<T, V>::Raw *>(static_cast<const T *>(base) + e), v);
 }
 template <typename T, int V>
-__device__ __forceinline__ void store(void *base, long long e, const float2 *v) {
+__device__ __forceinline__ void store(void *base, uint32_t e, const float2 *v) {
     *reinterpret_cast<typename Pack<T, V>::Raw *>(static_cast<T *>(base) + e) = Pack<T, V>::pack(v);
 }
 template <typename T>
@@ -134,9 +136,9 @@ constexpr int kMaxDepth = 4;
 // a thread's columns: vector k starts at column first + k * step
 template <int K, int V>
 struct Columns {
-    int first, step, lanes;  // lanes: threads of the block (the stride of staged vectors)
-    bool on[K], ragged;      // ragged: the row ends within this block's (or warp's) columns
-    __device__ __forceinline__ int at(int k) const { return first + k * step; }
+    uint32_t first, step, lanes;  // lanes: threads of the block (the stride of staged vectors)
+    bool on[K], ragged;           // ragged: the row ends within this block's (or warp's) columns
+    __device__ __forceinline__ uint32_t at(int k) const { return first + k * step; }
 };
 
 template <typename T, int K, int V>
@@ -144,14 +146,14 @@ __device__ __forceinline__ uint32_t stage(uint32_t at, const void *row, const Co
 #pragma unroll
     for (int k = 0; k < K; ++k)
         if (c.on[k])
-            copy_async<T, V>(at + (k * c.lanes + threadIdx.x) * (V * sizeof(T)), static_cast<const T *>(row) + c.at(k));
+            copy_async<T, V>(at + (k * c.lanes + threadIdx.x) * static_cast<uint32_t>(V * sizeof(T)), static_cast<const T *>(row) + c.at(k));
     return at + K * c.lanes * static_cast<uint32_t>(V * sizeof(T));
 }
 // the staged vectors of one array; `at` moves to the next array
 template <typename T, int K, int V>
 __device__ __forceinline__ void staged(const uint8_t *&at, const Columns<K, V> &c, float2 (&v)[K][V / 2]) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) load<T, V>(at, static_cast<int>(k * c.lanes + threadIdx.x) * V, v[k]);
+    for (int k = 0; k < K; ++k) load<T, V>(at, (k * c.lanes + threadIdx.x) * V, v[k]);
     at += K * c.lanes * V * sizeof(T);
 }
 // Vectors past the row's end are never copied.  Where a block has such, its
@@ -277,7 +279,7 @@ __device__ __forceinline__ Columns<K, V> make_columns(const Plan &p, const Reduc
     c.step = lanes * V;
     c.ragged = (r.rank + 1) * lanes * K * V > p.H;
 #pragma unroll
-    for (int k = 0; k < K; ++k) c.on[k] = c.at(k) < p.H;
+    for (int k = 0; k < K; ++k) c.on[k] = c.at(k) < static_cast<uint32_t>(p.H);
     return c;
 }
 
@@ -362,10 +364,15 @@ __device__ __forceinline__ void times_gate(const Plan &p, const Columns<K, V> &c
 // Which kernel a row takes (chosen in block_norm.cu).
 struct Shape {
     int team, E, threads, cluster, depth, smem;
+    bool common;  // what almost every call has; see the kernels
 };
 using Kernel = void (*)(Plan);
-Kernel fwd_kernel_for(const tp_block_norm_desc &d, const Shape &s);
-Kernel bwd_kernel_for(const tp_block_norm_desc &d, const Shape &s);
+Kernel fwd_kernel_bf16(const tp_block_norm_desc &d, const Shape &s);
+Kernel fwd_kernel_mixed(const tp_block_norm_desc &d, const Shape &s);
+Kernel fwd_kernel_f32(const tp_block_norm_desc &d, const Shape &s);
+Kernel bwd_kernel_bf16(const tp_block_norm_desc &d, const Shape &s);
+Kernel bwd_kernel_mixed(const tp_block_norm_desc &d, const Shape &s);
+Kernel bwd_kernel_f32(const tp_block_norm_desc &d, const Shape &s);
 
 }  // namespace bn
 }  // namespace tpmlp

@@ -1,4 +1,7 @@
-// The forward kernels of the block norm (see block_norm.cu for the mathematics).
+// The forward kernels of the block norm (see block_norm.cu for the mathematics);
+// each pair of types is compiled in a unit of its own (block_norm_fwd_*.cu).
+#pragma once
+
 #include "block_norm.cuh"
 
 namespace tpmlp {
@@ -6,9 +9,11 @@ namespace bn {
 
 // ---------------------------------------------------------------------------
 // Forward.  A: type of f, g, n and the weights; R: type of x and y; E elements
-// a thread, in vectors of V; LP, LN: the post- and the pre-norm is a LayerNorm.
+// a thread, in vectors of V; LP, LN: the post- and the pre-norm is a LayerNorm;
+// COMMON: there are a block and a pre-norm, no token or element gate and no
+// token shards.
 // ---------------------------------------------------------------------------
-template <typename A, typename R, int E, Team TEAM, bool LP, bool LN>
+template <typename A, typename R, int E, Team TEAM, bool LP, bool LN, bool COMMON>
 __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd_kernel(const __grid_constant__ Plan p) {
     constexpr bool WARP = TEAM == kWarp;
     constexpr int V = sizeof(R) == 2 ? 8 : 4, K = E / V, P = V / 2;
@@ -18,19 +23,21 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
     const Columns<K, V> c = make_columns<K, V, TEAM>(p, r);
     const int worker = WARP ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x / r.cluster;
     const int workers = WARP ? gridDim.x * kWarps : gridDim.x / r.cluster;
-    const bool gate_rows = p.gate == TP_GATE_ELEMENT, first = (WARP ? threadIdx.x & 31 : threadIdx.x) == 0 && r.rank == 0;
+    const bool has_block = COMMON || p.has_block, has_pre = COMMON || p.pre != TP_NORM_NONE;
+    const bool gate_rows = !COMMON && p.gate == TP_GATE_ELEMENT, token = !COMMON && p.gate == TP_GATE_TOKEN;
+    const bool first = (WARP ? threadIdx.x & 31 : threadIdx.x) == 0 && r.rank == 0;
     const float inv_h = 1.0f / p.H, plus = p.zero_centered ? 1.0f : 0.0f;
     const uint32_t stage_bytes =
-        blockDim.x * E * static_cast<uint32_t>(sizeof(R) + (p.has_block ? sizeof(A) : 0) + (gate_rows ? sizeof(A) : 0));
+        blockDim.x * E * static_cast<uint32_t>(sizeof(R) + (has_block ? sizeof(A) : 0) + (gate_rows ? sizeof(A) : 0));
     const uint32_t base = smem_at(stages);
     Cursor next(p, worker, workers);
     auto fetch = [&](int slot) {
         if (next.row < p.M) {
-            const int js = next.shard;
+            const int js = COMMON ? 0 : next.shard;
             const long long e = static_cast<long long>(next.local) * p.H;
             uint32_t at = base + slot * stage_bytes;
             at = stage<R>(at, static_cast<const R *>(p.x[js]) + e, c);
-            if (p.has_block) at = stage<A>(at, static_cast<const A *>(p.f[js]) + e, c);
+            if (has_block) at = stage<A>(at, static_cast<const A *>(p.f[js]) + e, c);
             if (gate_rows) stage<A>(at, static_cast<const A *>(p.g[js]) + e, c);
             next.advance(p);
         }
@@ -51,16 +58,16 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
     int slot = 0;
     for (Cursor at_row(p, worker, workers); at_row.row < p.M; at_row.advance(p)) {
         fetch(slot == 0 ? p.depth - 1 : slot - 1);  // into the slot of the row before
-        const int js = at_row.shard;
+        const int js = COMMON ? 0 : at_row.shard;
         const long long e = static_cast<long long>(at_row.local) * p.H;
-        const float gm = p.gate == TP_GATE_TOKEN ? load1<A>(p.g[js], at_row.local) : 1.0f;
+        const float gm = token ? load1<A>(p.g[js], at_row.local) : 1.0f;
         copies_wait(p.depth - 1);
         const uint8_t *at = stages + slot * stage_bytes;
         slot = slot + 1 == p.depth ? 0 : slot + 1;
         float2 y[K][P];
         staged<R>(at, c, y);
         float4 st = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
-        if (p.has_block) {
+        if (has_block) {
             float2 f[K][P];
             staged<A>(at, c, f);
             if (p.post != TP_NORM_NONE) centre_row<TEAM, LP, V, K>(f, c, p.post, inv_h, p.eps, r, st.x, st.y);
@@ -76,7 +83,7 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
                 }
                 if (gate_rows) {
                     float2 g[P];
-                    load<A, V>(at, static_cast<int>(k * c.lanes + threadIdx.x) * V, g);
+                    load<A, V>(at, (k * c.lanes + threadIdx.x) * V, g);
 #pragma unroll
                     for (int j = 0; j < P; ++j) f[k][j] = __fmul2_rn(f[k][j], g[j]);
                 }
@@ -88,7 +95,7 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
                 Pack<R, V>::unpack(out, y[k]);  // the pre-norm is of y as it is stored
             }
         }
-        if (p.pre != TP_NORM_NONE) {
+        if (has_pre) {
             centre_row<TEAM, LN, V, K>(y, c, p.pre, inv_h, p.eps, r, st.z, st.w);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -97,7 +104,7 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
                     y[k][j] = __fmul2_rn(y[k][j], both(st.w));
                     y[k][j] = LN ? __ffma2_rn(y[k][j], nw[k][j], nb[LN ? k : 0][j]) : __fmul2_rn(y[k][j], nw[k][j]);
                 }
-                if (c.on[k]) store<A, V>(p.n[js], e + c.at(k), y[k]);
+                if (c.on[k]) store<A, V>(static_cast<A *>(p.n[js]) + e, c.at(k), y[k]);
             }
         }
         if (p.stats && first) p.stats[at_row.row] = st;
@@ -105,22 +112,17 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
     if (TEAM == kCluster) cluster_sync();  // no block leaves while another may write into it
 }
 
-template <typename A, typename R, bool LP, bool LN>
+template <typename A, typename R, bool LP, bool LN, bool COMMON>
 static Kernel pick(const Shape &s) {
-    if (s.team == kWarp) return s.E == 8 ? fwd_kernel<A, R, 8, kWarp, LP, LN> : fwd_kernel<A, R, 16, kWarp, LP, LN>;
-    if (s.team == kCluster) return fwd_kernel<A, R, 16, kCluster, LP, LN>;
-    return s.E == 8 ? fwd_kernel<A, R, 8, kBlock, LP, LN> : fwd_kernel<A, R, 16, kBlock, LP, LN>;
+    if (s.team == kWarp) return s.E == 8 ? fwd_kernel<A, R, 8, kWarp, LP, LN, COMMON> : fwd_kernel<A, R, 16, kWarp, LP, LN, COMMON>;
+    if (s.team == kCluster) return fwd_kernel<A, R, 16, kCluster, LP, LN, COMMON>;
+    return s.E == 8 ? fwd_kernel<A, R, 8, kBlock, LP, LN, COMMON> : fwd_kernel<A, R, 16, kBlock, LP, LN, COMMON>;
 }
-template <bool LP, bool LN>
-static Kernel pick(const tp_block_norm_desc &d, const Shape &s) {
-    using bf = __nv_bfloat16;
-    if (d.dtype == TP_DT_F32) return pick<float, float, LP, LN>(s);
-    return d.residual_f32 ? pick<bf, float, LP, LN>(s) : pick<bf, bf, LP, LN>(s);
-}
-Kernel fwd_kernel_for(const tp_block_norm_desc &d, const Shape &s) {
+template <typename A, typename R, bool COMMON>
+static Kernel of_types(const tp_block_norm_desc &d, const Shape &s) {
     const bool lp = d.post == TP_NORM_LAYER, ln = d.pre == TP_NORM_LAYER;
-    return lp ? (ln ? pick<true, true>(d, s) : pick<true, false>(d, s))
-              : (ln ? pick<false, true>(d, s) : pick<false, false>(d, s));
+    return lp ? (ln ? pick<A, R, true, true, COMMON>(s) : pick<A, R, true, false, COMMON>(s))
+              : (ln ? pick<A, R, false, true, COMMON>(s) : pick<A, R, false, false, COMMON>(s));
 }
 
 }  // namespace bn
