@@ -103,30 +103,27 @@ __global__ void __launch_bounds__(256) param_grad_kernel(const __grid_constant__
 // How a row is taken, from its width and the bytes an element has in a stage
 // (those that the kernel reads): rows of up to 512 columns by a warp with 8 or
 // 16 elements a lane, wider ones by a block with 8 or 16 elements a thread, and
-// where a block's threads or its shared memory (two stages at least) do not
-// hold a row, by a cluster of 2 or 4 blocks.
-// dynamic shared memory of a block when `blocks` of them share an SM's 228 KB
-// (each also takes 1.5 KB of static buffers and 1 KB of the system's)
-static int smem_share(int blocks) { return (blocks == 1 ? 225 : 228) * 1024 / blocks - 2560; }
+// where a block's threads or its shared memory do not hold a row, by a cluster
+// of 2 or 4 blocks.  A row shared by a cluster costs its barriers dear (8192 x
+// 4096 bf16 forward: 84 us with 2 blocks, 48 us with one), so it is the last
+// resort.
+constexpr int kSmemMost = 225 * 1024 - 2560;  // dynamic; the static buffers and the system take the rest
 
-static Shape shape_of(int H, int bytes, int blocks_per_sm) {
+static Shape shape_of(int H, int bytes) {
     Shape s = {};
     s.cluster = 1;
     s.E = H <= 256 ? 8 : 16;
     s.threads = 32 * kWarps;
-    s.team = H <= 512 && 2 * s.threads * s.E * bytes <= smem_share(1) ? kWarp : kBlock;
+    s.team = H <= 512 && kStages * s.threads * s.E * bytes <= kSmemMost ? kWarp : kBlock;
     if (s.team != kWarp) {
-        while (H > s.cluster * kMaxThreads * 16 || 2 * bytes * ((H + s.cluster - 1) / s.cluster + 512) > smem_share(1))
+        while (H > s.cluster * kMaxThreads * 16 || kStages * bytes * ((H + s.cluster - 1) / s.cluster + 512) > kSmemMost)
             s.cluster *= 2;
         if (s.cluster > 1) s.team = kCluster;
         const int cols = (H + s.cluster - 1) / s.cluster;
         s.E = s.team == kBlock && cols <= kMaxThreads * 8 ? 8 : 16;
         s.threads = ((cols + s.E - 1) / s.E + 31) / 32 * 32;
     }
-    const int stage = s.threads * s.E * bytes;
-    s.depth = smem_share(blocks_per_sm) / stage;
-    s.depth = s.depth < 2 ? 2 : s.depth > kMaxDepth ? kMaxDepth : s.depth;
-    s.smem = s.depth * stage;
+    s.smem = kStages * s.threads * s.E * bytes;
     if (s.team == kWarp && s.smem < kWarps * s.E * 32 * 4) s.smem = kWarps * s.E * 32 * 4;  // the warps' sums at the end
     return s;
 }
@@ -146,21 +143,13 @@ static tp_status prepare(Launch &kept, const tp_block_norm_desc &d, bool bwd, bo
     std::lock_guard<std::mutex> lock(g_launch_mutex);
     l = kept;
     if (l.device == dev) return TP_OK;
-    // the deepest stages that still leave room for the blocks that registers allow
-    int want = 1;
-    for (;;) {
-        l.s = shape_of(d.H, bytes, want);
-        l.s.common = !d.seq_parallel && d.has_block && d.pre != TP_NORM_NONE && d.gate <= TP_GATE_CHANNEL &&
-                     (!bwd || (has_dy && (d.post != TP_NORM_NONE || d.gate == TP_GATE_CHANNEL)));
-        l.k = d.dtype == TP_DT_F32  ? (bwd ? bwd_kernel_f32(d, l.s) : fwd_kernel_f32(d, l.s))
-              : d.residual_f32      ? (bwd ? bwd_kernel_mixed(d, l.s) : fwd_kernel_mixed(d, l.s))
-                                    : (bwd ? bwd_kernel_bf16(d, l.s) : fwd_kernel_bf16(d, l.s));
-        TRY(cuda_check(cudaFuncSetAttribute(l.k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_share(1)), "block norm"));
-        int by_registers = 0;
-        TRY(cuda_check(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&by_registers, l.k, l.s.threads, 0), "block norm"));
-        if (by_registers <= want || l.s.depth == 2) break;
-        want = by_registers;
-    }
+    l.s = shape_of(d.H, bytes);
+    l.s.common = !d.seq_parallel && d.has_block && d.pre != TP_NORM_NONE && d.gate <= TP_GATE_CHANNEL &&
+                 (!bwd || (has_dy && (d.post != TP_NORM_NONE || d.gate == TP_GATE_CHANNEL)));
+    l.k = d.dtype == TP_DT_F32  ? (bwd ? bwd_kernel_f32(d, l.s) : fwd_kernel_f32(d, l.s))
+          : d.residual_f32      ? (bwd ? bwd_kernel_mixed(d, l.s) : fwd_kernel_mixed(d, l.s))
+                                : (bwd ? bwd_kernel_bf16(d, l.s) : fwd_kernel_bf16(d, l.s));
+    TRY(cuda_check(cudaFuncSetAttribute(l.k, cudaFuncAttributeMaxDynamicSharedMemorySize, l.s.smem), "block norm"));
     TRY(cuda_check(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&l.per_sm, l.k, l.s.threads, l.s.smem), "block norm"));
     if (l.per_sm < 1) return set_error(TP_ERR_CUDA, "block norm: no block fits an SM");
     l.device = dev;
@@ -176,7 +165,6 @@ static tp_status run(const Launch &l, Plan &p, int most, const char *name, cudaS
     if (most && blocks > most) blocks = most;
     if (blocks < 1) blocks = 1;
     p.cluster = s.cluster;
-    p.depth = s.depth;
     *workers = blocks;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks * s.cluster);

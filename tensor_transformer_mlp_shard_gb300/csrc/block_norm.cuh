@@ -20,7 +20,7 @@ constexpr int kMaxChunks = 304;     // workers of the backward, each writing one
 struct Plan {
     int M, H, rows_split;
     int post, pre, gate, zero_centered, has_block;
-    int cluster, depth, need_f;     // blocks to a row, rows staged, f is read
+    int cluster, need_f;            // blocks to a row; f is read
     float eps, a, c;
     const void *x[kMaxShards], *f[kMaxShards], *g[kMaxShards];  // g: g[0] for a channel gate
     const void *y_in[kMaxShards], *dy[kMaxShards], *dn[kMaxShards];
@@ -122,16 +122,9 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// all but the newest n groups have landed
-__device__ __forceinline__ void copies_wait(int n) {
-    if (n >= 3)
-        asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else if (n == 2)
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-}
-constexpr int kMaxDepth = 4;
+// all but the newest group have landed
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+constexpr int kStages = 2;  // a row being worked on and the next (3 and 4 measured no faster)
 
 // a thread's columns: vector k starts at column first + k * step
 template <int K, int V>
@@ -363,7 +356,7 @@ __device__ __forceinline__ void times_gate(const Plan &p, const Columns<K, V> &c
 
 // Which kernel a row takes (chosen in block_norm.cu).
 struct Shape {
-    int team, E, threads, cluster, depth, smem;
+    int team, E, threads, cluster, smem;
     bool common;  // what almost every call has; see the kernels
 };
 using Kernel = void (*)(Plan);

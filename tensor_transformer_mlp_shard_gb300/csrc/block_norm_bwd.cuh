@@ -52,8 +52,8 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
         }
         copies_commit();
     };
-    if (c.ragged) clear_stages(stages, p.depth * row_bytes);
-    for (int i = 0; i < p.depth - 1; ++i) fetch(i);
+    if (c.ragged) clear_stages(stages, kStages * row_bytes);
+    fetch(0);
     float2 gw[K][P], nw[K][P];  // c times the channel gate times the post-norm's weight; the pre-norm's weight
     load_weight<A>(p.post_w, c, plus, 1.0f, gw);
     times_gate<A>(p, c, gw);
@@ -66,15 +66,15 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
     int slot = 0;
     float4 st_next = worker < p.M ? p.stats_in[worker] : make_float4(0.0f, 1.0f, 0.0f, 1.0f);
     for (Cursor at_row(p, worker, workers); at_row.row < p.M; at_row.advance(p)) {
-        fetch(slot == 0 ? p.depth - 1 : slot - 1);  // into the slot of the row before
+        fetch(slot ^ 1);  // into the slot of the row before
         const int js = COMMON ? 0 : at_row.shard;
         const long long e = static_cast<long long>(at_row.local) * p.H;
         const float4 st = st_next;
         if (at_row.row + workers < p.M) st_next = p.stats_in[at_row.row + workers];
         const float gm = token ? load1<A>(p.g[js], at_row.local) : 1.0f;
-        copies_wait(p.depth - 1);
+        copies_wait();
         const uint8_t *at = stages + slot * row_bytes;
-        slot = slot + 1 == p.depth ? 0 : slot + 1;
+        slot ^= 1;
         float2 d[K][P];  // dy, then D
         if (has_dy) {
             staged<R>(at, c, d);

@@ -43,8 +43,8 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
         }
         copies_commit();
     };
-    if (c.ragged) clear_stages(stages, p.depth * stage_bytes);
-    for (int i = 0; i < p.depth - 1; ++i) fetch(i);
+    if (c.ragged) clear_stages(stages, kStages * stage_bytes);
+    fetch(0);
     // weights of this thread's columns, the gate and the block's scale in the post-norm's
     float2 pw[K][P], nw[K][P], pb[LP ? K : 1][P], nb[LN ? K : 1][P];
     load_weight<A>(p.post_w, c, plus, 1.0f, pw);
@@ -57,13 +57,13 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
     if constexpr (LN) load_weight<A>(p.pre_b, c, 0.0f, 0.0f, nb);
     int slot = 0;
     for (Cursor at_row(p, worker, workers); at_row.row < p.M; at_row.advance(p)) {
-        fetch(slot == 0 ? p.depth - 1 : slot - 1);  // into the slot of the row before
+        fetch(slot ^ 1);  // into the slot of the row before
         const int js = COMMON ? 0 : at_row.shard;
         const long long e = static_cast<long long>(at_row.local) * p.H;
         const float gm = token ? load1<A>(p.g[js], at_row.local) : 1.0f;
-        copies_wait(p.depth - 1);
+        copies_wait();
         const uint8_t *at = stages + slot * stage_bytes;
-        slot = slot + 1 == p.depth ? 0 : slot + 1;
+        slot ^= 1;
         float2 y[K][P];
         staged<R>(at, c, y);
         float4 st = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
