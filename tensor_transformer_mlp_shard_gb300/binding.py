@@ -168,7 +168,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(stream):
     if stream is None:
-        if _raw_stream is not None and torch.cuda.is_initialized():
+        if _raw_stream is not None:
             return _raw_stream(torch.cuda.current_device())
         return VP(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, torch.cuda.Stream):
@@ -584,8 +584,13 @@ _pack1 = struct.Struct("P").pack
 
 def _pointers(name, ts, count, n, dtype):
     """The addresses of `count` shards (one tensor, or a list), as a C array."""
-    if count == 1 and isinstance(ts, torch.Tensor):
-        return _pack1(_pointer(name, ts, n, dtype))
+    if count == 1:
+        t = ts[0] if type(ts) is list and len(ts) == 1 else ts
+        try:
+            if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() == n:
+                return _pack1(t.data_ptr())
+        except AttributeError:
+            pass
     if ts is None:
         raise ValueError(f"{name}: required")
     if isinstance(ts, torch.Tensor):

@@ -102,14 +102,16 @@ __global__ void __launch_bounds__(256) param_grad_kernel(const __grid_constant__
 // ---------------------------------------------------------------------------
 // How a row is taken, from its width and the bytes an element has in a stage
 // (those that the kernel reads): rows of up to 512 columns by a warp with 8 or
-// 16 elements a lane, wider ones by a block with 8 or 16 elements a thread, and
-// where a block's threads or its shared memory do not hold a row, by a cluster
+// 16 elements a lane, wider ones by a block, with 16 elements a thread in the
+// forward (8192 x 4096 bf16 with two LayerNorms: 56 us, 64 us with 8) and with
+// 8 in the backward while its threads suffice (its column sums take as many
+// registers again: 85 us, 116 us with 16), and where a block's threads or its shared memory do not hold a row, by a cluster
 // of 2 or 4 blocks.  A row shared by a cluster costs its barriers dear (8192 x
 // 4096 bf16 forward: 84 us with 2 blocks, 48 us with one), so it is the last
 // resort.
 constexpr int kSmemMost = 225 * 1024 - 2560;  // dynamic; the static buffers and the system take the rest
 
-static Shape shape_of(int H, int bytes) {
+static Shape shape_of(int H, int bytes, bool bwd) {
     Shape s = {};
     s.cluster = 1;
     s.E = H <= 256 ? 8 : 16;
@@ -120,7 +122,7 @@ static Shape shape_of(int H, int bytes) {
             s.cluster *= 2;
         if (s.cluster > 1) s.team = kCluster;
         const int cols = (H + s.cluster - 1) / s.cluster;
-        s.E = s.team == kBlock && cols <= kMaxThreads * 8 ? 8 : 16;
+        s.E = bwd && s.team == kBlock && cols <= kMaxThreads * 8 ? 8 : 16;
         s.threads = ((cols + s.E - 1) / s.E + 31) / 32 * 32;
     }
     s.smem = kStages * s.threads * s.E * bytes;
@@ -143,9 +145,9 @@ static tp_status prepare(Launch &kept, const tp_block_norm_desc &d, bool bwd, bo
     std::lock_guard<std::mutex> lock(g_launch_mutex);
     l = kept;
     if (l.device == dev) return TP_OK;
-    l.s = shape_of(d.H, bytes);
+    l.s = shape_of(d.H, bytes, bwd);
     l.s.common = !d.seq_parallel && d.has_block && d.pre != TP_NORM_NONE && d.gate <= TP_GATE_CHANNEL &&
-                 (!bwd || (has_dy && (d.post != TP_NORM_NONE || d.gate == TP_GATE_CHANNEL)));
+                 (!bwd || has_dy);
     l.k = d.dtype == TP_DT_F32  ? (bwd ? bwd_kernel_f32(d, l.s) : fwd_kernel_f32(d, l.s))
           : d.residual_f32      ? (bwd ? bwd_kernel_mixed(d, l.s) : fwd_kernel_mixed(d, l.s))
                                 : (bwd ? bwd_kernel_bf16(d, l.s) : fwd_kernel_bf16(d, l.s));
@@ -292,7 +294,7 @@ void tp_block_norm_destroy(tp_block_norm *h) { delete h; }
 size_t tp_block_norm_workspace_bytes(const tp_block_norm *h) {
     if (!h) return 0;
     const int sums = h->use[0] + h->use[1] + h->use[2] + h->use[3];
-    const int chunks = h->M < bn::kMaxChunks ? h->M : bn::kMaxChunks;
+    const int most = bn::max_chunks(h->d.H), chunks = h->M < most ? h->M : most;
     return sizeof(float) * sums * chunks * static_cast<size_t>(h->d.H);
 }
 
@@ -387,7 +389,7 @@ tp_status tp_block_norm_bwd(tp_block_norm *h, const void *const *dY, const void 
         bn::Launch l;
         TRY(bn::prepare(dY ? h->bwd : h->bwd_alone, d, true, dY != nullptr,
                         er + (pre ? er + ea : 0) + (p.need_f ? ea : 0) + (d.gate == TP_GATE_ELEMENT ? ea : 0), l));
-        TRY(bn::run(l, p, bn::kMaxChunks, "block_norm_bwd", st, &grid));
+        TRY(bn::run(l, p, bn::max_chunks(d.H), "block_norm_bwd", st, &grid));
     }
     if (!h->use[0] && !h->use[2]) return TP_OK;
     fin.partials = p.partials;

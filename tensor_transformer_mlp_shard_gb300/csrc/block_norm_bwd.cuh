@@ -10,9 +10,9 @@ namespace bn {
 // ---------------------------------------------------------------------------
 // Gradients of x, f and of a token or element gate, row by row, and this
 // worker's share of the column sums in registers.  LP, LN: the post- and the
-// pre-norm is a LayerNorm.  COMMON: there are dy, a pre-norm, a block whose f
-// is read, no token or element gate and no token shards; without the branches
-// and the pointer lookups for the rest a row takes a fifth fewer instructions.
+// pre-norm is a LayerNorm.  COMMON: there are dy, a pre-norm and a block, no
+// token or element gate and no token shards; without the branches and the
+// pointer lookups for the rest a row takes a fifth fewer instructions.
 // ---------------------------------------------------------------------------
 template <typename A, typename R, int E, Team TEAM, bool LP, bool LN, bool COMMON>
 __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
     const int worker = WARP ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x / r.cluster;
     const int workers = WARP ? gridDim.x * kWarps : gridDim.x / r.cluster;
     const bool has_pre = COMMON || p.pre != TP_NORM_NONE, has_dy = COMMON || p.dy[0] != nullptr;
-    const bool has_block = COMMON || p.has_block, need_f = COMMON || p.need_f;
+    const bool has_block = COMMON || p.has_block, need_f = p.need_f;
     const bool gate_rows = !COMMON && p.gate == TP_GATE_ELEMENT, token = !COMMON && p.gate == TP_GATE_TOKEN;
     const bool row_gate = gate_rows || token;
     const bool first = (WARP ? threadIdx.x & 31 : threadIdx.x) == 0 && r.rank == 0;

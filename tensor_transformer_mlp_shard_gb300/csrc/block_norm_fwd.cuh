@@ -116,7 +116,7 @@ template <typename A, typename R, bool LP, bool LN, bool COMMON>
 static Kernel pick(const Shape &s) {
     if (s.team == kWarp) return s.E == 8 ? fwd_kernel<A, R, 8, kWarp, LP, LN, COMMON> : fwd_kernel<A, R, 16, kWarp, LP, LN, COMMON>;
     if (s.team == kCluster) return fwd_kernel<A, R, 16, kCluster, LP, LN, COMMON>;
-    return s.E == 8 ? fwd_kernel<A, R, 8, kBlock, LP, LN, COMMON> : fwd_kernel<A, R, 16, kBlock, LP, LN, COMMON>;
+    return fwd_kernel<A, R, 16, kBlock, LP, LN, COMMON>;
 }
 template <typename A, typename R, bool COMMON>
 static Kernel of_types(const tp_block_norm_desc &d, const Shape &s) {

@@ -119,9 +119,11 @@ def test_block_norm_bwd_pointers(tp, drop):
 
 
 def test_block_norm_workspace(tp):
-    """One row of partial sums a block (at most 304, at most one a token) for
-    each of the sums the parameters need."""
-    assert tp.TPBlockNorm(**{**NORM_BASE, "S": 1000}).workspace_bytes() == 4 * 3 * 304 * 64
+    """One row of partial sums a block (at most 304 from 4096 columns on, 1216 up
+    to 1024, and at most one a token) for each of the sums the parameters need."""
+    assert tp.TPBlockNorm(**{**NORM_BASE, "S": 1000}).workspace_bytes() == 4 * 3 * 1216 * 64
+    assert tp.TPBlockNorm(**{**NORM_BASE, "S": 1000, "H": 4096}).workspace_bytes() == 4 * 3 * 304 * 4096
+    assert tp.TPBlockNorm(**{**NORM_BASE, "S": 1000, "H": 2048}).workspace_bytes() == 4 * 3 * 608 * 2048
     assert tp.TPBlockNorm(**{**NORM_BASE, "S": 3}).workspace_bytes() == 4 * 3 * 6 * 64
     assert tp.TPBlockNorm(16, 2, 64, post="none", pre="none", gate="element").workspace_bytes() == 0
 
