@@ -443,7 +443,8 @@ TP_API tp_status tp_fp8_quantize(const void *const *in, void *const *out, const 
  *     with residual_f32.  Parameter gradients are fp32.
  *   Shards.  X, F, Y, N, token and element gates and their gradients are
  *     1-entry pointer arrays, or T token shards under seq_parallel (any M/T).
- *     stats is one [M, 4] fp32 buffer in token order.
+ *     stats is one [M, 4] fp32 buffer in token order.  A token gate and its
+ *     gradient need only the alignment of their type.
  *   Overlap.  Y may be X, and dX may be dY (the same buffers); no other output
  *     may overlap an input.
  * Results are deterministic (no atomics).  The handle holds host state only

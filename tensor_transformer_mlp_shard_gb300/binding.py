@@ -579,7 +579,8 @@ def _pointer(name, t, n, dtype):
     raise ValueError(f"{name}: {tuple(t.shape)} has {t.numel()} elements, expected {n}")
 
 
-_pack1 = struct.Struct("P").pack
+_pack = [struct.Struct("%dP" % k).pack for k in range(MAX_SHARDS + 1)]
+_pack1 = _pack[1]
 
 
 def _pointers(name, ts, count, n, dtype):
@@ -599,7 +600,14 @@ def _pointers(name, ts, count, n, dtype):
         raise ValueError(f"{name}: expected {count} tensors, got {len(ts)}")
     if count == 1:
         return _pack1(_pointer(name, ts[0], n, dtype))
-    return struct.pack("%dP" % count, *[_pointer(f"{name}[{i}]", t, n, dtype) for i, t in enumerate(ts)])
+    try:
+        ptrs = [t.data_ptr() for t in ts
+                if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() == n]
+        if len(ptrs) == count:
+            return _pack[count](*ptrs)
+    except AttributeError:
+        pass
+    return _pack[count](*[_pointer(f"{name}[{i}]", t, n, dtype) for i, t in enumerate(ts)])
 
 
 class TPBlockNorm:

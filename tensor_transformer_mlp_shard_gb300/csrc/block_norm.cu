@@ -197,20 +197,21 @@ struct tp_block_norm {
     bn::Launch fwd, bwd, bwd_alone;  // bwd_alone: without dY
 };
 
-static tp_status bn_pointer(const void *p, const char *name, int i, int n) {
+static tp_status bn_pointer(const void *p, const char *name, int i, int n, unsigned align = 16) {
     char at[16] = "";
     if (n > 1) snprintf(at, sizeof(at), "[%d]", i);
     if (!p) return set_error(TP_ERR_ARG, "%s%s is NULL", name, at);
-    if (reinterpret_cast<uintptr_t>(p) & 15u) return set_error(TP_ERR_ARG, "%s%s is not 16-byte aligned", name, at);
+    if (reinterpret_cast<uintptr_t>(p) & (align - 1))
+        return set_error(TP_ERR_ARG, "%s%s is not %u-byte aligned", name, at, align);
     return TP_OK;
 }
 
 // copies an array of n pointers into a plan after checking them
 template <typename P>
-static tp_status bn_array(P *const *in, int n, const char *name, P **out) {
+static tp_status bn_array(P *const *in, int n, const char *name, P **out, unsigned align = 16) {
     if (!in) return set_error(TP_ERR_ARG, "%s: pointer array is NULL", name);
     for (int i = 0; i < n; ++i) {
-        TRY(bn_pointer(in[i], name, i, n));
+        TRY(bn_pointer(in[i], name, i, n, align));
         out[i] = in[i];
     }
     return TP_OK;
@@ -264,9 +265,14 @@ static bn::Plan bn_plan(const tp_block_norm *h) {
     return p;
 }
 
+// a token gate is read value by value: its shards need no more than a value's alignment
+static unsigned bn_gate_align(const tp_block_norm *h) {
+    return h->d.gate != TP_GATE_TOKEN ? 16 : h->d.dtype == TP_DT_F32 ? 4 : 2;
+}
+
 static tp_status bn_gate(const tp_block_norm *h, const void *const *gate, bn::Plan &p) {
     if (h->d.gate == TP_GATE_NONE) return TP_OK;
-    return bn_array(gate, h->d.gate == TP_GATE_CHANNEL ? 1 : h->nx, "gate", p.g);
+    return bn_array(gate, h->d.gate == TP_GATE_CHANNEL ? 1 : h->nx, "gate", p.g, bn_gate_align(h));
 }
 
 extern "C" {
@@ -368,7 +374,7 @@ tp_status tp_block_norm_bwd(tp_block_norm *h, const void *const *dY, const void 
         }
         if (d.gate == TP_GATE_TOKEN || d.gate == TP_GATE_ELEMENT) {
             TRY(bn_gate(h, gate, p));
-            TRY(bn_array(dgate, h->nx, "dgate", p.dg));
+            TRY(bn_array(dgate, h->nx, "dgate", p.dg, bn_gate_align(h)));
         }
         TRY(bn_pointer(p.stats_in = reinterpret_cast<const float4 *>(stats), "stats", 0, 1));
     }

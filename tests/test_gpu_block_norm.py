@@ -225,6 +225,17 @@ def test_token_shards(tp, gate, H):
     c.check_bwd()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_token_gate_shards_need_no_vector_alignment(tp, dtype):
+    """7 tokens a shard: a shard's gates start at any multiple of their type's size."""
+    c = Case(35, 264, dtype, "rms", "layer", "token", T=5)
+    h = c.handle(tp)
+    c.run_fwd(h)
+    c.check_fwd()
+    c.run_bwd(h, tp)
+    c.check_bwd()
+
+
 def test_norm_without_a_block(tp):
     for kind in ("rms", "layer"):
         c = Case(19, 776, "bf16", "none", kind, block=False)
