@@ -807,7 +807,7 @@ static tp_status step_launch(const Table<CAP> &tab, const tp_adamw_desc &d, cons
     if (!chunks) return TP_OK;
     const int grid = blocks_for(chunks, kRun, 4 * num_sms());
     const int smem = d.state_bits == 8 ? kStages * (gh ? stage_bytes<bf>() : stage_bytes<float>()) : 0;
-    if (smem) TRY(cuda_check(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), "adamw_step"));
+    static_assert(kStages * stage_bytes<float>() <= 48 * 1024, "within what a launch may ask for without an attribute");
     // after the gradient norm, the blocks' starts overlap its end
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);

@@ -151,7 +151,8 @@ static tp_status prepare(Launch &kept, const tp_block_norm_desc &d, bool bwd, bo
     l.k = d.dtype == TP_DT_F32  ? (bwd ? bwd_kernel_f32(d, l.s) : fwd_kernel_f32(d, l.s))
           : d.residual_f32      ? (bwd ? bwd_kernel_mixed(d, l.s) : fwd_kernel_mixed(d, l.s))
                                 : (bwd ? bwd_kernel_bf16(d, l.s) : fwd_kernel_bf16(d, l.s));
-    TRY(cuda_check(cudaFuncSetAttribute(l.k, cudaFuncAttributeMaxDynamicSharedMemorySize, l.s.smem), "block norm"));
+    // the most any configuration takes: the attribute is the kernel's, and another handle's may need more
+    TRY(cuda_check(cudaFuncSetAttribute(l.k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost), "block norm"));
     TRY(cuda_check(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&l.per_sm, l.k, l.s.threads, l.s.smem), "block norm"));
     if (l.per_sm < 1) return set_error(TP_ERR_CUDA, "block norm: no block fits an SM");
     l.device = dev;

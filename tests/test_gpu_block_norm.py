@@ -236,6 +236,21 @@ def test_token_gate_shards_need_no_vector_alignment(tp, dtype):
     c.check_bwd()
 
 
+def test_handles_of_one_kernel_take_turns(tp):
+    """Configurations that stage more and less of a row run the same kernels:
+    neither may keep the other from its shared memory."""
+    cases = [Case(9, 4096, "bf16", "rms", "rms", "channel"), Case(9, 4096, "bf16", "none", "rms", "none"),
+             Case(9, 2056, "bf16", "rms", "rms", "element"), Case(9, 2056, "bf16", "none", "rms", "none", block=False)]
+    handles = [c.handle(tp) for c in cases]
+    for _ in range(2):
+        for dy in (True, False):
+            for c, h in zip(cases, handles):
+                c.run_fwd(h)
+                c.check_fwd()
+                c.run_bwd(h, tp, dy=dy)
+                c.check_bwd()
+
+
 def test_norm_without_a_block(tp):
     for kind in ("rms", "layer"):
         c = Case(19, 776, "bf16", "none", kind, block=False)
