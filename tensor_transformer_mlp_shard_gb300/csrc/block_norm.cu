@@ -33,9 +33,11 @@ namespace tpmlp {
 namespace bn {
 
 // ---------------------------------------------------------------------------
-// Parameter gradients from the partial rows: 32 columns a block, 32 threads a
-// column quadruple, the rows in a fixed order.
+// Parameter gradients from the partial rows, which are still in L2: 16 columns a
+// block, so that there are blocks for all SMs, and 64 threads down the rows of
+// a column quadruple, the rows in a fixed order.
 // ---------------------------------------------------------------------------
+constexpr int kFinalCols = 16;
 struct FinalPlan {
     const float *partials;
     int chunks, H, use[4], zero_centered;
@@ -46,24 +48,29 @@ struct FinalPlan {
 
 template <typename A>
 __global__ void __launch_bounds__(256) param_grad_kernel(const __grid_constant__ FinalPlan p) {
-    __shared__ float part[4][32][33];
-    const int quad = threadIdx.x & 7, r = threadIdx.x >> 3;
-    const int c0 = blockIdx.x * 32 + quad * 4;  // H is a multiple of 8: a quadruple is whole or absent
+    __shared__ float part[4][64][kFinalCols + 1];
+    const int quad = threadIdx.x & 3, r = threadIdx.x >> 2;
+    const int c0 = blockIdx.x * kFinalCols + quad * 4;  // H is a multiple of 8: a quadruple is whole or absent
     float4 s[4];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float *in[4];
     int slot = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         s[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (!p.use[q]) continue;
-        const float *in = p.partials + static_cast<long long>(slot++) * p.chunks * p.H + c0;
-        if (c0 < p.H)
-#pragma unroll 5
-            for (int i = r; i < p.chunks; i += 32) {
-                const float4 v = *reinterpret_cast<const float4 *>(in + static_cast<long long>(i) * p.H);
-                s[q].x += v.x; s[q].y += v.y; s[q].z += v.z; s[q].w += v.w;
-            }
+        in[q] = p.partials + static_cast<long long>(slot) * p.chunks * p.H + c0;
+        slot += p.use[q];
     }
+    wait_for_stream();
+    let_next_start();
+    if (c0 < p.H)
+#pragma unroll 2
+        for (int i = r; i < p.chunks; i += 64)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (p.use[q]) {
+                    const float4 v = *reinterpret_cast<const float4 *>(in[q] + static_cast<long long>(i) * p.H);
+                    s[q].x += v.x; s[q].y += v.y; s[q].z += v.z; s[q].w += v.w;
+                }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         part[q][r][quad * 4] = s[q].x;
@@ -72,18 +79,18 @@ __global__ void __launch_bounds__(256) param_grad_kernel(const __grid_constant__
         part[q][r][quad * 4 + 3] = s[q].w;
     }
     __syncthreads();
-    // 8 lanes a column: 4 rows each, then over the lanes
-    const int own = threadIdx.x >> 3, eighth = threadIdx.x & 7, col = blockIdx.x * 32 + own;
+    // 16 lanes a column: 4 rows each, then over the lanes
+    const int own = threadIdx.x >> 4, part_of = threadIdx.x & 15, col = blockIdx.x * kFinalCols + own;
     float v[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         v[q] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[q] += part[q][eighth * 4 + i][own];
+        for (int i = 0; i < 4; ++i) v[q] += part[q][part_of * 4 + i][own];
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) v[q] += __shfl_xor_sync(0xffffffffu, v[q], o);
+        for (int o = 8; o > 0; o >>= 1) v[q] += __shfl_xor_sync(0xffffffffu, v[q], o);
     }
-    if (eighth || col >= p.H) return;
+    if (part_of || col >= p.H) return;
     const float g = p.gate ? load1<A>(p.gate, col) : 1.0f;
     if (p.dpost_w) p.dpost_w[col] = p.c * g * v[0];
     if (p.dpost_b) p.dpost_b[col] = p.c * g * v[1];
@@ -174,12 +181,18 @@ static tp_status run(const Launch &l, Plan &p, int most, const char *name, cudaS
     cfg.blockDim = dim3(s.threads);
     cfg.dynamicSmemBytes = s.smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = s.cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
-    cfg.numAttrs = s.cluster > 1 ? 1 : 0;
+    if (pdl_on()) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (s.cluster > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = s.cluster;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
     launch_begin(name, st);
     cudaError_t e = cudaLaunchKernelEx(&cfg, l.k, p);
     launch_end(name, st);
@@ -409,7 +422,7 @@ tp_status tp_block_norm_bwd(tp_block_norm *h, const void *const *dY, const void 
     fin.post_b = p.post_b;
     fin.gate = d.gate == TP_GATE_CHANNEL ? p.g[0] : nullptr;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((d.H + 31) / 32);
+    cfg.gridDim = dim3((d.H + bn::kFinalCols - 1) / bn::kFinalCols);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

@@ -126,6 +126,10 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // all but the newest group have landed
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+// Programmatic dependent launch: a kernel may start while the one before it in
+// the stream ends, sets up what is its own, and waits before it touches memory.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 constexpr int kStages = 2;  // a row being worked on and the next (3 and 4 measured no faster)
 
 // a thread's columns: vector k starts at column first + k * step

@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
         copies_commit();
     };
     if (c.ragged) clear_stages(stages, kStages * row_bytes);
+    wait_for_stream();
     fetch(0);
     float2 gw[K][P], nw[K][P];  // c times the channel gate times the post-norm's weight; the pre-norm's weight
     load_weight<A>(p.post_w, c, plus, 1.0f, gw);
@@ -212,8 +213,7 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
                 store<A, V>(static_cast<A *>(p.df[js]) + e, c.at(k), o);
             }
     }
-    // the parameter gradients' blocks may take the SMs that are done; they wait for the whole grid
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();  // the parameter gradients' blocks, on the SMs that are done
     // one row of partial sums a worker (the warps of a block added in order)
     const int out_row = WARP ? blockIdx.x : worker, out_rows = WARP ? gridDim.x : workers;
     int used = 0;

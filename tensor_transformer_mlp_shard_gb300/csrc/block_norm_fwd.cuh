@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
         copies_commit();
     };
     if (c.ragged) clear_stages(stages, kStages * stage_bytes);
+    wait_for_stream();
     fetch(0);
     // weights of this thread's columns, the gate and the block's scale in the post-norm's
     float2 pw[K][P], nw[K][P], pb[LP ? K : 1][P], nb[LN ? K : 1][P];
@@ -109,6 +110,7 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
         }
         if (p.stats && first) p.stats[at_row.row] = st;
     }
+    let_next_start();
     if (TEAM == kCluster) cluster_sync();  // no block leaves while another may write into it
 }
 
