@@ -498,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 4) step_kernel(const __grid_constant
     extern __shared__ __align__(16) uint8_t stages[];
     float scale = hy.scale, inv_bc1 = hy.inv_bc1, inv_root_bc2 = hy.inv_root_bc2;
     uint32_t step = hy.step;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before, whose end this launch overlaps
     if (hy.ctl) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // the gradient norm, whose end this launch overlaps
         if (!hy.ctl->finite) return;
         scale = hy.ctl->scale;
         inv_bc1 = hy.ctl->inv_bc1;
@@ -561,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 4) step_kernel(const __grid_constant
         }
         slot = slot + 1 == kStages ? 0 : slot + 1;
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -608,7 +609,9 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     __shared__ double red[kThreads / 32];
     __shared__ int is_last;
     float2 s = both(0.0f), rest = both(0.0f);
-    for (Walk<CAP> now(tab); now.c < now.end; now.next(tab)) {
+    Walk<CAP> now(tab);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (; now.c < now.end; now.next(tab)) {
         const long long e0 = static_cast<long long>(now.c - tab.chunk0[now.ti]) * kNormChunk, left = tab.t[now.ti].n - e0;
         const G *in = static_cast<const G *>(tab.t[now.ti].g) + e0;
         const uint32_t e = threadIdx.x * 4, n = left < kNormChunk ? static_cast<uint32_t>(left) : kNormChunk;
@@ -791,6 +794,20 @@ static int blocks_for(int chunks, int run, int resident) {
     return runs > resident ? runs : resident;
 }
 
+// A launch whose start may overlap the end of the kernel before it.
+static cudaLaunchConfig_t launch_config(int grid, int smem, cudaStream_t st, cudaLaunchAttribute *attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_on() ? 1 : 0;
+    return cfg;
+}
+
 template <int CAP>
 static tp_status step_launch(const Table<CAP> &tab, const tp_adamw_desc &d, const Hyper &hy, cudaStream_t st) {
     using bf = __nv_bfloat16;
@@ -808,18 +825,9 @@ static tp_status step_launch(const Table<CAP> &tab, const tp_adamw_desc &d, cons
     const int grid = blocks_for(chunks, kRun, 4 * num_sms());
     const int smem = d.state_bits == 8 ? kStages * (gh ? stage_bytes<bf>() : stage_bytes<float>()) : 0;
     static_assert(kStages * stage_bytes<float>() <= 48 * 1024, "within what a launch may ask for without an attribute");
-    // after the gradient norm, the blocks' starts overlap its end
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = hy.ctl && pdl_on() ? 1 : 0;
     launch_begin("adamw_step", st);
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = launch_config(grid, smem, st, attr);
     cudaError_t e = cudaLaunchKernelEx(&cfg, k, tab, hy);
     launch_end("adamw_step", st);
     return cuda_check(e, "adamw_step");
@@ -829,11 +837,10 @@ template <int CAP>
 static tp_status norm_launch(const Table<CAP> &tab, const tp_adamw_desc &d, const NormArgs &a, int grid,
                              cudaStream_t st) {
     launch_begin("adamw_grad_norm", st);
-    if (d.grad_dtype == TP_DT_BF16)
-        norm_kernel<CAP, __nv_bfloat16><<<grid, kThreads, 0, st>>>(tab, a);
-    else
-        norm_kernel<CAP, float><<<grid, kThreads, 0, st>>>(tab, a);
-    cudaError_t e = cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = launch_config(grid, 0, st, attr);
+    cudaError_t e = d.grad_dtype == TP_DT_BF16 ? cudaLaunchKernelEx(&cfg, norm_kernel<CAP, __nv_bfloat16>, tab, a)
+                                               : cudaLaunchKernelEx(&cfg, norm_kernel<CAP, float>, tab, a);
     launch_end("adamw_grad_norm", st);
     return cuda_check(e, "adamw_grad_norm");
 }
