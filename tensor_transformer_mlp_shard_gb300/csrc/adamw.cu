@@ -254,7 +254,16 @@ __device__ __forceinline__ void block_scale(uint32_t top, float &inv, float &sca
 
 // ---------------------------------------------------------------------------
 // The step.  A warp takes 256 consecutive elements (a block of the 8-bit
-// states), 8 a lane in two runs of 4.
+// states), 8 a lane in two runs of 4, so that every load and store of a warp
+// is contiguous and a block's largest value is one warp reduction.
+//
+// Bound by HBM.  134M bf16 parameters with fp32 master copies and gradients:
+// 30 bytes an element with 32-bit states, 580 us (6.9 TB/s), and 18 bytes with
+// 8-bit states, 360 us (6.7 TB/s, a plain copy's rate; 76 instructions an
+// element at 73 % of the issue slots).  With 8 bits the arithmetic is nearly as
+// long as the memory's time: hence the loads staged a chunk ahead, the rounding
+// in three integer instructions, one hash for both states, the roots without
+// branches and the paired products (558 us with none of them and even runs).
 // ---------------------------------------------------------------------------
 // What a lane reads of a block.
 template <typename G, int BITS>
@@ -571,9 +580,10 @@ __global__ void __launch_bounds__(kThreads, 4) step_kernel(const __grid_constant
 // the error of every addition kept beside the sum (Knuth's two-sum), 7
 // additions an element, in pairs; fp64, which this machine has few units for,
 // comes once at the end (one fp64 addition for 8 elements was the bound before:
-// 157 us for 134M fp32 gradients).  The norm is then the rounded norm of the rounded
-// squares, whatever the order, and the clip factor that scales every gradient
-// does not move with the list's grouping.
+// 157 us for 134M fp32 gradients; now 85 us, 6.3 TB/s, and 101 us right after
+// a step, whose last writes still leave L2).  The norm is then the rounded norm
+// of the rounded squares, whatever the order, and the clip factor that scales
+// every gradient does not move with the list's grouping.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return __fadd2_rn(a, make_float2(-b.x, -b.y)); }
 
@@ -782,11 +792,14 @@ static int fill(const tp_adamw *h, int i, int chunk, Table<CAP> &tab) {
     return i;
 }
 
-// Thread blocks for a number of chunks.  The SMs do not run at one speed (an
-// SM's distance to the memory that it happens to read differs), so even runs
-// for just the resident blocks leave the fast ones idle at the end; runs of
-// kRun chunks are short enough for the hardware to deal them out as blocks
-// finish, and long enough to pay for a block's start.
+// Thread blocks for a number of chunks.  Even runs for just the resident blocks
+// end unevenly (SMs were busy 0.9 of the time) and spread what is read and
+// written at one time over the whole list; short runs are dealt out by the
+// hardware, in order, as blocks finish.  134M elements in 8 bits: 494 us with
+// one run a resident block, 417 with runs of 6 or 7 chunks, 364 with 2, 416
+// with single ones, which stage nothing ahead.  The norm's blocks end with a
+// reduction and an atomic, so its runs are longer (8 chunks and 2: 23 and 25 us
+// for 24M elements in 300 tensors, the same for one large one).
 constexpr int kRun = 2, kNormRun = 8;
 static int blocks_for(int chunks, int run, int resident) {
     if (chunks <= resident) return chunks;

@@ -35,7 +35,8 @@ namespace bn {
 // ---------------------------------------------------------------------------
 // Parameter gradients from the partial rows, which are still in L2: 16 columns a
 // block, so that there are blocks for all SMs, and 64 threads down the rows of
-// a column quadruple, the rows in a fixed order.
+// a column quadruple, the rows in a fixed order.  304 rows of two sums over 4096
+// columns: 4 to 5 us after the backward, whose end its start overlaps.
 // ---------------------------------------------------------------------------
 constexpr int kFinalCols = 16;
 struct FinalPlan {
@@ -115,7 +116,8 @@ __global__ void __launch_bounds__(256) param_grad_kernel(const __grid_constant__
 // registers again: 85 us, 116 us with 16), and where a block's threads or its shared memory do not hold a row, by a cluster
 // of 2 or 4 blocks.  A row shared by a cluster costs its barriers dear (8192 x
 // 4096 bf16 forward: 84 us with 2 blocks, 48 us with one), so it is the last
-// resort.
+// resort: above 8192 columns, and in fp32 where two rows of all arrays exceed
+// an SM's shared memory.
 constexpr int kSmemMost = 225 * 1024 - 2560;  // dynamic; the static buffers and the system take the rest
 
 static Shape shape_of(int H, int bytes, bool bwd) {

@@ -13,6 +13,15 @@ namespace bn {
 // pre-norm is a LayerNorm.  COMMON: there are dy, a pre-norm and a block, no
 // token or element gate and no token shards; without the branches and the
 // pointer lookups for the rest a row takes a fifth fewer instructions.
+//
+// Bound by HBM as the forward is: dy, y, dn and f are read once and dx and df
+// written once.  8192 x 4096 bf16 (RMS, channel gate, RMS) takes 67 us in this
+// kernel and 74 us with the parameter gradients, 5.4 TB/s of 403 MB (0.81 of a
+// plain copy's rate); 4096 x 8192 with an fp32 stream and a LayerNorm 96 and
+// 101 us (6.0 TB/s, 0.89).  Two blocks of 64 registers an SM, where both norms
+// are RMS: one block of 73 took 118 us, its two barriers a row idle the SM.
+// The column sums stay in registers over all rows of a worker: 304 rows of
+// partial sums for 4096 columns and more, 10 MB that do not leave L2.
 // ---------------------------------------------------------------------------
 template <typename A, typename R, int E, Team TEAM, bool LP, bool LN, bool COMMON>
 __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
