@@ -109,15 +109,19 @@ __global__ void __launch_bounds__(256) param_grad_kernel(const __grid_constant__
 // launchers
 // ---------------------------------------------------------------------------
 // How a row is taken, from its width and the bytes an element has in a stage
-// (those that the kernel reads): rows of up to 512 columns by a warp with 8 or
-// 16 elements a lane, wider ones by a block, with 16 elements a thread in the
-// forward (8192 x 4096 bf16 with two LayerNorms: 56 us, 64 us with 8) and with
-// 8 in the backward while its threads suffice (its column sums take as many
-// registers again: 85 us, 116 us with 16), and where a block's threads or its shared memory do not hold a row, by a cluster
-// of 2 or 4 blocks.  A row shared by a cluster costs its barriers dear (8192 x
-// 4096 bf16 forward: 84 us with 2 blocks, 48 us with one), so it is the last
-// resort: above 8192 columns, and in fp32 where two rows of all arrays exceed
-// an SM's shared memory.
+// (those that the kernel reads).
+//   Up to 512 columns: by a warp, 8 or 16 elements a lane.
+//   Wider, forward: by a block, 16 elements a thread (8192 x 4096 bf16 with two
+//   LayerNorms: 56 us, 64 us with 8), above 8192 columns 32 (2048 x 16384 with
+//   one RMS norm: 46 us, 86 us by a cluster).
+//   Wider, backward: by a block, 8 elements a thread while its threads suffice
+//   (its column sums take as many registers again: 8192 x 4096 with two
+//   LayerNorms 85 us, 116 us with 16), else 16.
+//   Where a block's threads or its shared memory do not hold a row: by a
+//   cluster of 2 or 4 blocks.  Its barriers cost dear (8192 x 4096 bf16 forward:
+//   84 us with 2 blocks, 48 us with one), so it is the last resort: above 8192
+//   columns in the backward, and wherever two rows of all arrays exceed an SM's
+//   shared memory.
 constexpr int kSmemMost = 225 * 1024 - 2560;  // dynamic; the static buffers and the system take the rest
 
 static Shape shape_of(int H, int bytes, bool bwd) {
@@ -127,11 +131,12 @@ static Shape shape_of(int H, int bytes, bool bwd) {
     s.threads = 32 * kWarps;
     s.team = H <= 512 && kStages * s.threads * s.E * bytes <= kSmemMost ? kWarp : kBlock;
     if (s.team != kWarp) {
-        while (H > s.cluster * kMaxThreads * 16 || kStages * bytes * ((H + s.cluster - 1) / s.cluster + 512) > kSmemMost)
+        const int most = bwd ? 16 : 32;  // elements a thread
+        while (H > s.cluster * kMaxThreads * most || kStages * bytes * ((H + s.cluster - 1) / s.cluster + 32 * most) > kSmemMost)
             s.cluster *= 2;
         if (s.cluster > 1) s.team = kCluster;
         const int cols = (H + s.cluster - 1) / s.cluster;
-        s.E = bwd && s.team == kBlock && cols <= kMaxThreads * 8 ? 8 : 16;
+        s.E = bwd && s.team == kBlock && cols <= kMaxThreads * 8 ? 8 : cols <= kMaxThreads * 16 ? 16 : 32;
         s.threads = ((cols + s.E - 1) / s.E + 31) / 32 * 32;
     }
     s.smem = kStages * s.threads * s.E * bytes;

@@ -330,35 +330,51 @@ __device__ __forceinline__ void centre_row(float2 (&v)[K][V / 2], const Columns<
     }
 }
 
-// v = w (1 + w when zero-centred) of a thread's columns, `none` without a weight;
-// zero past the row's end, where what it multiplies may be anything finite
-template <typename A, int K, int V>
-__device__ __forceinline__ void load_weight(const void *w, const Columns<K, V> &c, float plus, float none,
-                                            float2 (&v)[K][V / 2]) {
+// A vector of per-channel factors of a thread's columns: zero past the row's
+// end, where what it multiplies may be anything finite.  KEEP: read once and
+// kept in registers; otherwise read again (from L1 or L2) at every row, where
+// the registers are worth more.
+//   weight: w (1 + w when zero-centred), `none` without one; gated: times the
+//   channel gate and the block's scale.
+template <typename A, int K, int V, bool KEEP>
+struct Factors {
+    float2 kept[KEEP ? K : 1][V / 2];
+    __device__ __forceinline__ static void read(const Plan &p, const Columns<K, V> &c, int k, const void *w, float plus,
+                                                float none, bool gated, float2 *v) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) v[k][j] = both(c.on[k] ? none : 0.0f);
+        for (int j = 0; j < V / 2; ++j) v[j] = both(c.on[k] ? none : 0.0f);
         if (w && c.on[k]) {
-            load<A, V>(w, c.at(k), v[k]);
+            load<A, V>(w, c.at(k), v);
 #pragma unroll
-            for (int j = 0; j < V / 2; ++j) v[k][j] = __fadd2_rn(v[k][j], both(plus));
+            for (int j = 0; j < V / 2; ++j) v[j] = __fadd2_rn(v[j], both(plus));
+        }
+        if (!gated) return;
+        if (p.gate == TP_GATE_CHANNEL && c.on[k]) {
+            float2 g[V / 2];
+            load<A, V>(p.g[0], c.at(k), g);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) v[j] = __fmul2_rn(v[j], g[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) v[j] = __fmul2_rn(v[j], both(p.c));
+    }
+    __device__ __forceinline__ void keep(const Plan &p, const Columns<K, V> &c, const void *w, float plus, float none,
+                                         bool gated) {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) read(p, c, k, w, plus, none, gated, kept[k]);
         }
     }
-}
-// v *= c times the channel gate (c alone without one)
-template <typename A, int K, int V>
-__device__ __forceinline__ void times_gate(const Plan &p, const Columns<K, V> &c, float2 (&v)[K][V / 2]) {
+    __device__ __forceinline__ void get(const Plan &p, const Columns<K, V> &c, int k, const void *w, float plus,
+                                        float none, bool gated, float2 *v) const {
+        if constexpr (KEEP) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        float2 g[V / 2];
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) g[j] = both(1.0f);
-        if (p.gate == TP_GATE_CHANNEL && c.on[k]) load<A, V>(p.g[0], c.at(k), g);
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) v[k][j] = __fmul2_rn(__fmul2_rn(v[k][j], g[j]), both(p.c));
+            for (int j = 0; j < V / 2; ++j) v[j] = kept[k][j];
+        } else {
+            read(p, c, k, w, plus, none, gated, v);
+        }
     }
-}
+};
 
 // Which kernel a row takes (chosen in block_norm.cu).
 struct Shape {

@@ -64,10 +64,12 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
     if (c.ragged) clear_stages(stages, kStages * row_bytes);
     wait_for_stream();
     fetch(0);
-    float2 gw[K][P], nw[K][P];  // c times the channel gate times the post-norm's weight; the pre-norm's weight
-    load_weight<A>(p.post_w, c, plus, 1.0f, gw);
-    times_gate<A>(p, c, gw);
-    load_weight<A>(p.pre_w, c, plus, 1.0f, nw);
+    // kept unless four column sums of 16 fill the registers (8192 x 4096 with two LayerNorms: 105 us, kept 118 us;
+    // with one, 101 us, not kept 145 us)
+    constexpr bool KEEP = E == 8 || !LP || !LN || sizeof(A) == 4;
+    Factors<A, K, V, KEEP> gw, nw;  // the post-norm's weight, gate and block scale in it, and the pre-norm's
+    gw.keep(p, c, p.post_w, plus, 1.0f, true);
+    nw.keep(p, c, p.pre_w, plus, 1.0f, false);
     float2 p1[K][P], n1[K][P], p0[LP ? K : 1][P], n0[LN ? K : 1][P];
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -101,17 +103,20 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
             staged<R>(at, c, yh);
             staged<A>(at, c, h);
 #pragma unroll
-            for (int k = 0; k < K; ++k)
+            for (int k = 0; k < K; ++k) {
+                float2 w[P];
+                nw.get(p, c, k, p.pre_w, plus, 1.0f, false, w);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     if (LN) yh[k][j] = __fadd2_rn(yh[k][j], both(-st.z));
                     yh[k][j] = __fmul2_rn(yh[k][j], both(st.w));
                     n1[k][j] = __ffma2_rn(h[k][j], yh[k][j], n1[k][j]);  // h is zero past the row
                     if (LN) n0[LN ? k : 0][j] = __fadd2_rn(n0[LN ? k : 0][j], h[k][j]);
-                    h[k][j] = __fmul2_rn(h[k][j], nw[k][j]);
+                    h[k][j] = __fmul2_rn(h[k][j], w[j]);
                     if (LN) s0 = __fadd2_rn(s0, h[k][j]);
                     s1 = __ffma2_rn(h[k][j], yh[k][j], s1);
                 }
+            }
             m0 = s0.x + s0.y;
             m1 = s1.x + s1.y;
             if (LN)
@@ -187,11 +192,13 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
                     }
                 }
             }
+            float2 w[P];
+            gw.get(p, c, k, p.post_w, plus, 1.0f, true, w);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 p1[k][j] = __ffma2_rn(d[k][j], fh[k][j], p1[k][j]);
                 if (LP) p0[LP ? k : 0][j] = __fadd2_rn(p0[LP ? k : 0][j], d[k][j]);
-                d[k][j] = __fmul2_rn(d[k][j], gw[k][j]);  // the gradient of fh
+                d[k][j] = __fmul2_rn(d[k][j], w[j]);  // the gradient of fh
                 if (LP) s0 = __fadd2_rn(s0, d[k][j]);
                 s1 = __ffma2_rn(d[k][j], fh[k][j], s1);
             }

@@ -57,16 +57,14 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
     if (c.ragged) clear_stages(stages, kStages * stage_bytes);
     wait_for_stream();
     fetch(0);
-    // weights of this thread's columns, the gate and the block's scale in the post-norm's
-    float2 pw[K][P], nw[K][P], pb[LP ? K : 1][P], nb[LN ? K : 1][P];
-    load_weight<A>(p.post_w, c, plus, 1.0f, pw);
-    times_gate<A>(p, c, pw);
-    load_weight<A>(p.pre_w, c, plus, 1.0f, nw);
-    if constexpr (LP) {
-        load_weight<A>(p.post_b, c, 0.0f, 0.0f, pb);
-        times_gate<A>(p, c, pb);
-    }
-    if constexpr (LN) load_weight<A>(p.pre_b, c, 0.0f, 0.0f, nb);
+    constexpr bool KEEP = E <= 16;  // 32 elements a thread leave no registers for them
+    Factors<A, K, V, KEEP> pw, nw;       // the post-norm's, gate and block scale in it, and the pre-norm's
+    Factors<A, K, V, KEEP && LP> pb;
+    Factors<A, K, V, KEEP && LN> nb;
+    pw.keep(p, c, p.post_w, plus, 1.0f, true);
+    nw.keep(p, c, p.pre_w, plus, 1.0f, false);
+    if (LP) pb.keep(p, c, p.post_b, 0.0f, 0.0f, true);
+    if (LN) nb.keep(p, c, p.pre_b, 0.0f, 0.0f, false);
     int slot = 0;
     for (Cursor at_row(p, worker, workers); at_row.row < p.M; at_row.advance(p)) {
         fetch(slot ^ 1);  // into the slot of the row before
@@ -87,10 +85,13 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
             const float2 row_scale = both(LP ? st.y : st.y * gm);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
+                float2 w[P], b[P];
+                pw.get(p, c, k, p.post_w, plus, 1.0f, true, w);
+                if (LP) pb.get(p, c, k, p.post_b, 0.0f, 0.0f, true, b);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     f[k][j] = __fmul2_rn(f[k][j], row_scale);
-                    if (LP) f[k][j] = __fmul2_rn(__ffma2_rn(f[k][j], pw[k][j], pb[LP ? k : 0][j]), both(gm));
+                    if (LP) f[k][j] = __fmul2_rn(__ffma2_rn(f[k][j], w[j], b[j]), both(gm));
                     y[k][j] = __fmul2_rn(y[k][j], both(p.a));
                 }
                 if (gate_rows) {
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
                 }
 #pragma unroll
                 for (int j = 0; j < P; ++j)
-                    y[k][j] = LP ? __fadd2_rn(f[k][j], y[k][j]) : __ffma2_rn(f[k][j], pw[k][j], y[k][j]);
+                    y[k][j] = LP ? __fadd2_rn(f[k][j], y[k][j]) : __ffma2_rn(f[k][j], w[j], y[k][j]);
                 const typename Pack<R, V>::Raw out = Pack<R, V>::pack(y[k]);
                 if (c.on[k]) *reinterpret_cast<typename Pack<R, V>::Raw *>(static_cast<R *>(p.y[js]) + e + c.at(k)) = out;
                 Pack<R, V>::unpack(out, y[k]);  // the pre-norm is of y as it is stored
@@ -111,10 +112,13 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
             centre_row<TEAM, LN, V, K>(y, c, p.pre, inv_h, p.eps, r, st.z, st.w);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
+                float2 w[P], b[P];
+                nw.get(p, c, k, p.pre_w, plus, 1.0f, false, w);
+                if (LN) nb.get(p, c, k, p.pre_b, 0.0f, 0.0f, false, b);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     y[k][j] = __fmul2_rn(y[k][j], both(st.w));
-                    y[k][j] = LN ? __ffma2_rn(y[k][j], nw[k][j], nb[LN ? k : 0][j]) : __fmul2_rn(y[k][j], nw[k][j]);
+                    y[k][j] = LN ? __ffma2_rn(y[k][j], w[j], b[j]) : __fmul2_rn(y[k][j], w[j]);
                 }
                 if (c.on[k]) store<A, V>(static_cast<A *>(p.n[js]) + e, c.at(k), y[k]);
             }
@@ -129,7 +133,7 @@ template <typename A, typename R, bool LP, bool LN, bool COMMON>
 static Kernel pick(const Shape &s) {
     if (s.team == kWarp) return s.E == 8 ? fwd_kernel<A, R, 8, kWarp, LP, LN, COMMON> : fwd_kernel<A, R, 16, kWarp, LP, LN, COMMON>;
     if (s.team == kCluster) return fwd_kernel<A, R, 16, kCluster, LP, LN, COMMON>;
-    return fwd_kernel<A, R, 16, kBlock, LP, LN, COMMON>;
+    return s.E == 32 ? fwd_kernel<A, R, 32, kBlock, LP, LN, COMMON> : fwd_kernel<A, R, 16, kBlock, LP, LN, COMMON>;
 }
 template <typename A, typename R, bool COMMON>
 static Kernel of_types(const tp_block_norm_desc &d, const Shape &s) {
