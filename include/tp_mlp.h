@@ -670,8 +670,9 @@ TP_API tp_status tp_set_band_rows(int rows);
  * SMs the previous kernel in the stream has left, set up their barriers and
  * tensor memory there, and wait in griddepcontrol.wait until that kernel
  * has completed and its writes are visible before they read an operand or
- * write an output, so stream order and results are unchanged.  on = 0
- * launches them in plain stream order.  TP_ERR_ARG unless on is 0 or 1. */
+ * write an output, so stream order and results are unchanged.  The block norm
+ * and AdamW kernels are launched the same way.  on = 0 launches all of them in
+ * plain stream order.  TP_ERR_ARG unless on is 0 or 1. */
 TP_API tp_status tp_set_launch_overlap(int on);
 
 /* Upper bound on the CTA pairs of the persistent pair-tile GEMMs, for all

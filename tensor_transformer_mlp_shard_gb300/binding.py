@@ -885,8 +885,8 @@ def set_k_order(alternate: bool):
 
 
 def set_launch_overlap(on: bool):
-    """Programmatic dependent launch of the pair GEMMs (on by default): a
-    GEMM's CTAs set up while the previous kernel finishes and wait for it
+    """Programmatic dependent launch of the pair GEMMs, the block norm and
+    AdamW (on by default): a kernel's CTAs set up while the previous kernel finishes and wait for it
     before touching memory; False: plain stream order."""
     _check(lib().tp_set_launch_overlap(1 if on else 0))
 

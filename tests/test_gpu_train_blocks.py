@@ -92,3 +92,21 @@ def test_training_reduces_the_loss(ex, bits):
         graph.replay()
     torch.cuda.synchronize()
     assert int(s.opt.finite) == 1 and float(s.loss) < 0.8 * start, (start, float(s.loss))
+
+
+def test_launch_overlap_changes_nothing(ex):
+    """Kernels that start while the one before them ends give the results of
+    plain stream order."""
+    import tensor_transformer_mlp_shard_gb300 as tp
+    a, b = (ex.BlockStack(blocks=3, seed=2) for _ in range(2))
+    try:
+        for on, s in ((False, a), (True, b)):
+            tp.set_launch_overlap(on)
+            for _ in range(6):
+                s.step()
+            torch.cuda.synchronize()
+    finally:
+        tp.set_launch_overlap(True)
+    for p, q in zip(a.opt.params, b.opt.params):
+        assert torch.equal(p, q)
+    assert torch.equal(a.out, b.out)
