@@ -198,6 +198,17 @@ __device__ __forceinline__ float2 roots(float2 v) {
     const float2 s = __fmul2_rn(v, y), rest = __ffma2_rn(s, s, make_float2(-v.x, -v.y));
     return __ffma2_rn(rest, __fmul2_rn(y, both(-0.5f)), s);
 }
+// Largest magnitude of three, NaN if one is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // two products that no addition is fused with
 __device__ __forceinline__ float2 mul(float a, float2 x) { return make_float2(__fmul_rn(a, x.x), __fmul_rn(a, x.y)); }
 
@@ -210,14 +221,11 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 
 // The hash of element e of a block is mix(key ^ e kMix1), its low half the
 // random bits of m and its high half those of the root.  The first xor-shift
-// is linear: taken of the key and of e kMix1 apart, it costs one xor an
-// element.  Both halves come out where round_e4m3 adds them, at bits 8..23.
-__device__ __forceinline__ uint32_t hash_of_element(uint32_t e) {
-    e *= kMix1;
-    return e ^ (e >> 16);
-}
-__device__ __forceinline__ void random_bits(uint32_t shifted_key, uint32_t element, uint32_t &of_m, uint32_t &of_r) {
-    uint32_t x = (shifted_key ^ element) * kMix1;
+// is linear: taken of the key and of e kMix1 apart, the element's part is the
+// same for every block.  Both halves come out where round_e4m3 adds them, at
+// bits 8..23.
+__device__ __forceinline__ void random_bits(uint32_t shifted_key, uint32_t e_mix1, uint32_t &of_m, uint32_t &of_r) {
+    uint32_t x = (shifted_key ^ e_mix1 ^ (e_mix1 >> 16)) * kMix1;
     x = (x ^ (x >> 15)) * kMix2;
     const uint32_t t = x >> 8;
     of_m = ((x << 8) ^ t) & 0x00FFFF00u;
@@ -239,17 +247,38 @@ __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c
     return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
-// Scale of a block from its largest magnitude's bits, and what multiplies its
-// values before rounding.  Below 2^-100 (where 448 / t nears the range of
-// fp32) a block is kept as zero.  `poison` is all ones where the block holds a
-// NaN or an infinity (as integers the magnitudes' bits order NaN above all):
-// its codes are then NaN.
-__device__ __forceinline__ void block_scale(uint32_t top, float &inv, float &scale, uint32_t &poison) {
-    const float t = __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+// Scale of a block from its lanes' largest magnitudes, and the factor that its
+// values take before rounding, 2^-120 448 / t.  Below 2^-100 (where 448 / t
+// nears the range of fp32) a block is kept as zero.  Above 2^12 the factor would
+// leave that range: the values take 2^-64 first, and `large` says so.  `poison`
+// marks a block that holds a NaN or an infinity (as integers the magnitudes'
+// bits order NaN above all): its codes are then NaN.
+struct Scale {
+    float factor, scale;
+    bool large;
+    uint32_t poison;
+};
+__device__ __forceinline__ Scale block_scale(float lane_top) {
+    const float t = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(lane_top) & 0x7FFFFFFFu));
     const bool zero = t < 7.888609e-31f;
-    inv = zero ? 0.0f : __fmul_rn(__frcp_rn(t), 448.0f);
-    scale = zero ? 0.0f : __fmul_rn(t, 1.0f / 448.0f);
-    poison = t < __uint_as_float(0x7F800000u) ? 0u : 0x7F7F7F7Fu;
+    Scale s;
+    s.large = t > 4096.0f;
+    s.factor = zero ? 0.0f : __fmul_rn(__frcp_rn(t), 448.0f) * (s.large ? 1.38777878e-17f : 7.52316385e-37f);  // 2^-56, 2^-120
+    s.scale = zero ? 0.0f : __fmul_rn(t, 1.0f / 448.0f);
+    s.poison = t < __uint_as_float(0x7F800000u) ? 0u : 0x7F7F7F7Fu;
+    return s;
+}
+__device__ __forceinline__ void scale_values(const Scale &s, float2 (&x)[2][2]) {
+    if (s.large) {  // the whole warp
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x[j][i] = __fmul2_rn(x[j][i], both(5.42101086e-20f));  // 2^-64
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x[j][i] = __fmul2_rn(x[j][i], both(s.factor));
 }
 
 // ---------------------------------------------------------------------------
@@ -259,11 +288,13 @@ __device__ __forceinline__ void block_scale(uint32_t top, float &inv, float &sca
 //
 // Bound by HBM.  134M bf16 parameters with fp32 master copies and gradients:
 // 30 bytes an element with 32-bit states, 580 us (6.9 TB/s), and 18 bytes with
-// 8-bit states, 360 us (6.7 TB/s, a plain copy's rate; 76 instructions an
-// element at 73 % of the issue slots).  With 8 bits the arithmetic is nearly as
-// long as the memory's time: hence the loads staged a chunk ahead, the rounding
-// in three integer instructions, one hash for both states, the roots without
-// branches and the paired products (558 us with none of them and even runs).
+// 8-bit states, 352 us (6.9 TB/s, above a plain copy's rate).  With 8 bits the
+// arithmetic is nearly as long as the memory's time, and with bf16 gradients
+// and fp32 parameters (14 bytes) it is longer: 349 us.  Hence the loads staged a
+// chunk ahead, the rounding in two integer operations, one hash for both
+// states, the roots without branches, the paired products and the extremes of
+// three (558 us with none of them and even runs of chunks), and 64 registers
+// without spills: 390 us with 16 bytes of them.
 // ---------------------------------------------------------------------------
 // What a lane reads of a block.
 template <typename G, int BITS>
@@ -321,9 +352,10 @@ __device__ __forceinline__ void read_block(const Chunk<G> &t, uint32_t e0, Value
     }
 }
 
+// `staged`: where the weights are staged (8 bits, whole blocks), else null.
 template <bool FULL, bool HALF, typename G, int BITS>
-__device__ __forceinline__ void step_block(const Chunk<G> &t, uint32_t e0, Values<G, BITS> &x, uint32_t key,
-                                           const uint32_t (&elem)[2][4], const Hyper &hy, float scale, float decay,
+__device__ __forceinline__ void step_block(const Chunk<G> &t, uint32_t e0, Values<G, BITS> &x, const float *staged, uint32_t key,
+                                           uint32_t e_mix1, const Hyper &hy, float scale, float decay,
                                            float rate, float inv_root_bc2) {
     const uint32_t n = t.left;
     float2 (&w)[2][2] = x.w, (&g)[2][2] = x.g, (&m)[2][2] = x.m, (&v)[2][2] = x.v;
@@ -352,7 +384,8 @@ __device__ __forceinline__ void step_block(const Chunk<G> &t, uint32_t e0, Value
         }
     }
     float2 root[2][2];
-    uint32_t top_m = 0, top_r = 0;
+    float top_m = 0.0f, top_r = 0.0f;
+    uint32_t some[2] = {0x01010101u, 0x01010101u};  // a byte for each element: its root is above zero
     if (BITS == 8) {
         float least = 3.4e38f;
 #pragma unroll
@@ -360,25 +393,29 @@ __device__ __forceinline__ void step_block(const Chunk<G> &t, uint32_t e0, Value
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 root[j][i] = roots(v[j][i]);
-                least = fminf(least, fminf(v[j][i].x, v[j][i].y));
-                top_m = max(top_m, max(__float_as_uint(m[j][i].x) & 0x7FFFFFFFu, __float_as_uint(m[j][i].y) & 0x7FFFFFFFu));
-                top_r = max(top_r, max(__float_as_uint(root[j][i].x), __float_as_uint(root[j][i].y)));  // not negative
+                least = min3(least, v[j][i].x, v[j][i].y);
+                top_m = max_abs3(top_m, m[j][i].x, m[j][i].y);
+                top_r = max_abs3(top_r, root[j][i].x, root[j][i].y);
             }
         // outside what roots() takes (zeros above all), where it may have left a NaN
-        if (least < kRootMin || top_r >= 0x7F800000u) {
-            top_r = 0;
+        if (!(least >= kRootMin && top_r < __uint_as_float(0x7F800000u))) {
+            top_r = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j) {
+                some[j] = 0u;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     root[j][i] = make_float2(sqrtf(v[j][i].x), sqrtf(v[j][i].y));
-                    top_r = max(top_r, max(__float_as_uint(root[j][i].x) & 0x7FFFFFFFu, __float_as_uint(root[j][i].y) & 0x7FFFFFFFu));
+                    top_r = max_abs3(top_r, root[j][i].x, root[j][i].y);
+                    some[j] |= (root[j][i].x > 0.0f ? 1u << (16 * i) : 0u) | (root[j][i].y > 0.0f ? 256u << (16 * i) : 0u);
                 }
+            }
         }
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const uint32_t e = e0 + j * 128;
+        if (BITS == 8 && FULL) load4<true>(staged, (j * kThreads + threadIdx.x) * 4, 0, w[j]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (BITS == 32) root[j][i] = make_float2(sqrtf(v[j][i].x), sqrtf(v[j][i].y));
@@ -395,35 +432,35 @@ __device__ __forceinline__ void step_block(const Chunk<G> &t, uint32_t e0, Value
         }
     }
     if (BITS == 32) return;
-    float inv_m, inv_r;
-    uint32_t bad_m, bad_r;
-    block_scale(top_m, inv_m, ms, bad_m);
-    block_scale(top_r, inv_r, vs, bad_r);
-    const float2 down = both(7.52316385e-37f);  // 2^-120
+    const Scale sm = block_scale(top_m), sr = block_scale(top_r);
     const uint32_t shifted_key = key ^ (key >> 16);
+    scale_values(sm, m);
+    scale_values(sr, root);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         uint32_t cm[4], cr[4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float2 a = __fmul2_rn(__fmul2_rn(m[j][i], both(inv_m)), down);
-            const float2 b = __fmul2_rn(__fmul2_rn(root[j][i], both(inv_r)), down);
             uint32_t of_m, of_r;
-            random_bits(shifted_key, elem[j][2 * i], of_m, of_r);
-            cm[2 * i] = round_e4m3(a.x, of_m);
-            // a root above zero (at least 2^-75, the root of fp32's smallest value) keeps a code above zero
-            cr[2 * i] = max(round_e4m3(b.x, of_r), min(__float_as_uint(root[j][i].x), 0x01000000u));
-            random_bits(shifted_key, elem[j][2 * i + 1], of_m, of_r);
-            cm[2 * i + 1] = round_e4m3(a.y, of_m);
-            cr[2 * i + 1] = max(round_e4m3(b.y, of_r), min(__float_as_uint(root[j][i].y), 0x01000000u));
+            random_bits(shifted_key, e_mix1 + (j * 128 + 2 * i) * kMix1, of_m, of_r);
+            cm[2 * i] = round_e4m3(m[j][i].x, of_m);
+            cr[2 * i] = round_e4m3(root[j][i].x, of_r);
+            random_bits(shifted_key, e_mix1 + (j * 128 + 2 * i + 1) * kMix1, of_m, of_r);
+            cm[2 * i + 1] = round_e4m3(m[j][i].y, of_m);
+            cr[2 * i + 1] = round_e4m3(root[j][i].y, of_r);
         }
         const uint32_t sign = top_bytes(__float_as_uint(m[j][0].x), __float_as_uint(m[j][0].y),
                                         __float_as_uint(m[j][1].x), __float_as_uint(m[j][1].y)) & 0x80808080u;
-        mc[j] = top_bytes(cm[0], cm[1], cm[2], cm[3]) | sign | bad_m;
-        vc[j] = top_bytes(cr[0], cr[1], cr[2], cr[3]) | bad_r;
+        mc[j] = top_bytes(cm[0], cm[1], cm[2], cm[3]) | sign | sm.poison;
+        vc[j] = top_bytes(cr[0], cr[1], cr[2], cr[3]) | sr.poison;
+        // bit 7 of each byte: whether it is zero; a root above zero keeps a code above zero
+        const uint32_t none = ~(((vc[j] & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | vc[j]);
+        vc[j] |= (none >> 7) & some[j];
         store4_codes<FULL>(static_cast<uint8_t *>(t.m), e0 + j * 128, n, mc[j]);
         store4_codes<FULL>(static_cast<uint8_t *>(t.v), e0 + j * 128, n, vc[j]);
     }
+    ms = sm.scale;
+    vs = sr.scale;
     if ((threadIdx.x & 31) == 0) {
         t.ms[threadIdx.x >> 5] = ms;
         t.vs[threadIdx.x >> 5] = vs;
@@ -492,7 +529,6 @@ __device__ __forceinline__ void staged_block(const uint8_t *at, Values<G, 8> &x)
     const uint32_t *codes = reinterpret_cast<const uint32_t *>(at + kThreads * (32 + 8 * sizeof(G)));
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        load4<true>(reinterpret_cast<const float *>(at), (j * kThreads + threadIdx.x) * 4, 0, x.w[j]);
         load4<true>(reinterpret_cast<const G *>(at + 2 * kThreads * 16), (j * kThreads + threadIdx.x) * 4, 0, x.g[j]);
         x.mc[j] = codes[j * kThreads + threadIdx.x];
         x.vc[j] = codes[(2 + j) * kThreads + threadIdx.x];
@@ -517,11 +553,7 @@ __global__ void __launch_bounds__(kThreads, 4) step_kernel(const __grid_constant
     }
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t at_step = mix(hy.seed + kMix1 * step);
-    uint32_t elem[2][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) elem[j][i] = BITS == 8 ? hash_of_element(j * 128 + lane * 4 + i) : 0u;
+    const uint32_t e_mix1 = lane * 4 * kMix1;
     const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(stages));
     const uint32_t e0 = warp * kBlock + lane * 4;
     Walk<CAP> now(tab), ahead = now;
@@ -563,10 +595,10 @@ __global__ void __launch_bounds__(kThreads, 4) step_kernel(const __grid_constant
                 staged_block<G>(stages + slot * stage_bytes<G>(), x);
             else
                 read_block<true, G, BITS>(t, e0, x);
-            step_block<true, HALF, G, BITS>(t, e0, x, key, elem, hy, scale, decay, rate, inv_root_bc2);
+            step_block<true, HALF, G, BITS>(t, e0, x, reinterpret_cast<const float *>(stages + slot * stage_bytes<G>()), key, e_mix1, hy, scale, decay, rate, inv_root_bc2);
         } else if (warp * kBlock < t.left) {
             read_block<false, G, BITS>(t, e0, x);
-            step_block<false, HALF, G, BITS>(t, e0, x, key, elem, hy, scale, decay, rate, inv_root_bc2);
+            step_block<false, HALF, G, BITS>(t, e0, x, nullptr, key, e_mix1, hy, scale, decay, rate, inv_root_bc2);
         }
         slot = slot + 1 == kStages ? 0 : slot + 1;
     }

@@ -228,6 +228,29 @@ def test_blocks_of_zeros_and_tiny_values(tp):
     assert (s.v[0][768:] > 0).all() and s.v[0][769] == 1
 
 
+@pytest.mark.parametrize("g_scale", [3e3, 1e6, 1e12, 1e-6, 1e-12])
+def test_states_of_any_size(tp, g_scale):
+    """Block scales far from 1 on either side, up to squares near fp32's largest."""
+    s = Setup(tp, sizes=[5000, 257], bits=8, g_scale=g_scale)
+    s.opt.step(1e-2, step=3)
+    s.check(3, 1e-2, 1.0)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_bad_gradient_without_the_norm_stays_in_its_block(tp, value):
+    """Its block's states become NaN, which no later step hides; the others are as without it."""
+    s, clean = (Setup(tp, sizes=[1024], bits=8) for _ in range(2))
+    s.g[0][300] = value
+    s.opt.step(1e-2, step=1)
+    clean.opt.step(1e-2, step=1)
+    assert not torch.isfinite(s.w[0][300])
+    rest = torch.arange(1024, device="cuda") != 300
+    assert torch.equal(s.w[0][rest], clean.w[0][rest])
+    far = torch.arange(1024, device="cuda") // 256 != 1
+    for a, b in ((s.m, clean.m), (s.v, clean.v)):
+        assert torch.equal(a[0][far], b[0][far]) and ((a[0][~far] & 0x7F) == 0x7F).all()
+
+
 def test_set_grads(tp):
     s, ref = Setup(tp), Setup(tp)
     other = [g * -2 for g in s.g]
