@@ -73,6 +73,17 @@ struct Table {
     Entry t[CAP];
 };
 
+// The table's size is a launch's parameter bytes, at most 32764 with the rest: a
+// short list takes the small one.
+constexpr int kSmall = 40, kLarge = 420;
+
+// The tables of a list's launches, made when the list or its gradients change.
+template <int CAP>
+struct Plans {
+    Table<CAP> *step = nullptr, *norm = nullptr;
+    int launches = 0;
+};
+
 struct Hyper {
     float lr, b1, b2, c1, c2, eps, scale, inv_bc1, inv_root_bc2;  // c: 1 - b, rounded once
     uint32_t seed, step;
@@ -735,6 +746,9 @@ using namespace tpmlp;
 struct tp_adamw {
     tp_adamw_desc d;
     tp_adamw_tensor *t;
+    long long norm_chunks;
+    adam::Plans<adam::kSmall> few;   // the launches' tables: these for a short list,
+    adam::Plans<adam::kLarge> many;  // these for a long one
 };
 
 #define TRY(x)                        \
@@ -790,9 +804,9 @@ static tp_status aw_validate(const tp_adamw_desc *d, const tp_adamw_tensor *t) {
 namespace tpmlp {
 namespace adam {
 
-// tensors [i, i + tab.count) of the list; returns the index after the last
+// the table of tensors [i, i + CAP) of the list, or what it has of them
 template <int CAP>
-static int fill(const tp_adamw *h, int i, int chunk, Table<CAP> &tab) {
+static void fill(const tp_adamw *h, int i, int chunk, Table<CAP> &tab) {
     tab.base = i;
     tab.count = 0;
     tab.chunk0[0] = 0;
@@ -821,7 +835,6 @@ static int fill(const tp_adamw *h, int i, int chunk, Table<CAP> &tab) {
         while (t + 1 < tab.count && tab.chunk0[t + 1] <= c) ++t;
         tab.coarse[k] = static_cast<unsigned short>(t);
     }
-    return i;
 }
 
 // Thread blocks for a number of chunks.  Even runs for just the resident blocks
@@ -873,7 +886,8 @@ static tp_status step_launch(const Table<CAP> &tab, const tp_adamw_desc &d, cons
     launch_begin("adamw_step", st);
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = launch_config(grid, smem, st, attr);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k, tab, hy);
+    void *args[] = {const_cast<Table<CAP> *>(&tab), const_cast<Hyper *>(&hy)};  // no copies of the table on the way
+    cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(k), args);
     launch_end("adamw_step", st);
     return cuda_check(e, "adamw_step");
 }
@@ -884,40 +898,54 @@ static tp_status norm_launch(const Table<CAP> &tab, const tp_adamw_desc &d, cons
     launch_begin("adamw_grad_norm", st);
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = launch_config(grid, 0, st, attr);
-    cudaError_t e = d.grad_dtype == TP_DT_BF16 ? cudaLaunchKernelEx(&cfg, norm_kernel<CAP, __nv_bfloat16>, tab, a)
-                                               : cudaLaunchKernelEx(&cfg, norm_kernel<CAP, float>, tab, a);
+    using K = void (*)(Table<CAP>, NormArgs);
+    const K k = d.grad_dtype == TP_DT_BF16 ? norm_kernel<CAP, __nv_bfloat16> : norm_kernel<CAP, float>;
+    void *args[] = {const_cast<Table<CAP> *>(&tab), const_cast<NormArgs *>(&a)};
+    cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(k), args);
     launch_end("adamw_grad_norm", st);
     return cuda_check(e, "adamw_grad_norm");
 }
 
+static_assert(sizeof(Table<kLarge>) + sizeof(Hyper) <= 32764, "a launch's parameters");
+static_assert(sizeof(Table<kLarge>) + sizeof(NormArgs) <= 32764, "a launch's parameters");
+
+// (re)makes the tables of a handle; false without memory for them
 template <int CAP>
-static tp_status step_all(const tp_adamw *h, const Hyper &hy, cudaStream_t st) {
-    Table<CAP> tab;
-    for (int i = 0; i < h->d.n_tensors;) {
-        i = fill(h, i, kChunk, tab);
-        TRY(step_launch(tab, h->d, hy, st));
+static bool make_plans(tp_adamw *h, Plans<CAP> &p) {
+    const int launches = (h->d.n_tensors + CAP - 1) / CAP;
+    if (!p.step) p.step = new (std::nothrow) Table<CAP>[launches];
+    if (!p.norm) p.norm = new (std::nothrow) Table<CAP>[launches];
+    if (!p.step || !p.norm) return false;
+    p.launches = launches;
+    for (int k = 0; k < launches; ++k) {
+        fill(h, k * CAP, kChunk, p.step[k]);
+        fill(h, k * CAP, kNormChunk, p.norm[k]);
     }
+    return true;
+}
+static bool make_plans(tp_adamw *h) {
+    h->norm_chunks = 0;
+    for (int i = 0; i < h->d.n_tensors; ++i) h->norm_chunks += (h->t[i].n + kNormChunk - 1) / kNormChunk;
+    return h->d.n_tensors <= kSmall ? make_plans(h, h->few) : make_plans(h, h->many);
+}
+
+template <int CAP>
+static tp_status step_all(const Plans<CAP> &p, const tp_adamw_desc &d, const Hyper &hy, cudaStream_t st) {
+    for (int k = 0; k < p.launches; ++k) TRY(step_launch(p.step[k], d, hy, st));
     return TP_OK;
 }
 
 template <int CAP>
-static tp_status norm_all(const tp_adamw *h, NormArgs a, cudaStream_t st) {
-    Table<CAP> tab;
-    long long chunks = 0;
-    for (int i = 0; i < h->d.n_tensors; ++i) chunks += (h->t[i].n + kNormChunk - 1) / kNormChunk;
-    int grid = blocks_for(static_cast<int>(chunks), kNormRun, 4 * num_sms());
+static tp_status norm_all(const Plans<CAP> &p, const tp_adamw *h, NormArgs a, cudaStream_t st) {
+    int grid = blocks_for(static_cast<int>(h->norm_chunks), kNormRun, 4 * num_sms());
     grid = grid < 1 ? 1 : grid > kNormBlocks ? kNormBlocks : grid;
-    for (int i = 0; i < h->d.n_tensors;) {
-        a.first = i == 0;
-        i = fill(h, i, kNormChunk, tab);
-        a.last = i == h->d.n_tensors;
-        TRY(norm_launch(tab, h->d, a, grid, st));
+    for (int k = 0; k < p.launches; ++k) {
+        a.first = k == 0;
+        a.last = k == p.launches - 1;
+        TRY(norm_launch(p.norm[k], h->d, a, grid, st));
     }
     return TP_OK;
 }
-
-// The table's size is a launch's parameter bytes: a short list takes the small one.
-constexpr int kSmall = 40, kLarge = 360;
 
 }  // namespace adam
 }  // namespace tpmlp
@@ -944,12 +972,20 @@ tp_status tp_adamw_create(const tp_adamw_desc *desc, const tp_adamw_tensor *tens
     h->d = *desc;
     h->t = t;
     for (int i = 0; i < desc->n_tensors; ++i) t[i] = tensors[i];
+    if (!adam::make_plans(h)) {
+        tp_adamw_destroy(h);
+        return set_error(TP_ERR_ARG, "out of host memory");
+    }
     *out = h;
     return TP_OK;
 }
 
 void tp_adamw_destroy(tp_adamw *h) {
     if (!h) return;
+    delete[] h->few.step;
+    delete[] h->few.norm;
+    delete[] h->many.step;
+    delete[] h->many.norm;
     delete[] h->t;
     delete h;
 }
@@ -960,6 +996,7 @@ tp_status tp_adamw_set_grads(tp_adamw *h, const void *const *grads) {
     for (int i = 0; i < h->d.n_tensors; ++i)
         if (h->t[i].n) TRY(aw_pointer(grads[i], "grad", i));
     for (int i = 0; i < h->d.n_tensors; ++i) h->t[i].grad = grads[i];
+    adam::make_plans(h);  // in the memory it has
     return TP_OK;
 }
 
@@ -987,7 +1024,7 @@ tp_status tp_adamw_grad_norm(tp_adamw *h, float grad_scale, float max_norm, void
     a.log_beta1 = static_cast<float>(std::log(h->d.beta1));  // -infinity for 0: 1 - b^t is 1
     a.log_beta2 = static_cast<float>(std::log(h->d.beta2));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return h->d.n_tensors <= adam::kSmall ? adam::norm_all<adam::kSmall>(h, a, st) : adam::norm_all<adam::kLarge>(h, a, st);
+    return h->few.launches ? adam::norm_all(h->few, h, a, st) : adam::norm_all(h->many, h, a, st);
 }
 
 tp_status tp_adamw_step(tp_adamw *h, float lr, float grad_scale, int step, const void *ctl, void *stream) {
@@ -1013,7 +1050,7 @@ tp_status tp_adamw_step(tp_adamw *h, float lr, float grad_scale, int step, const
         hy.inv_root_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(h->d.beta2, step)));
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return h->d.n_tensors <= adam::kSmall ? adam::step_all<adam::kSmall>(h, hy, st) : adam::step_all<adam::kLarge>(h, hy, st);
+    return h->few.launches ? adam::step_all(h->few, h->d, hy, st) : adam::step_all(h->many, h->d, hy, st);
 }
 
 }  // extern "C"

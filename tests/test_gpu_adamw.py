@@ -201,7 +201,7 @@ def test_a_step_before_any_norm_changes_nothing(tp):
     assert all(torch.equal(a, b) for a, b in zip(was, s.tensors()))
 
 
-@pytest.mark.parametrize("count", [40, 41, 360, 361, 800])
+@pytest.mark.parametrize("count", [40, 41, 360, 361, 420, 421, 860])
 @pytest.mark.parametrize("bits", [32, 8])
 def test_many_tensors(tp, count, bits):
     """Lists around the sizes of one launch's tables; the norm is of all of them."""
