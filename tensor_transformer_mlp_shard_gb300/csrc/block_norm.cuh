@@ -330,6 +330,32 @@ __device__ __forceinline__ void centre_row(float2 (&v)[K][V / 2], const Columns<
     }
 }
 
+// The backward's normalised row, v = (x - mean) / spread, less its own mean.
+// The statistics hold the mean rounded to fp32, so v is off by up to 2^-24
+// |mean| / spread, the same for the whole row: a bias, which a sum over tokens
+// does not average out.  Up to a mean of one spread that is within v's own
+// rounding; rows with a larger one take this further sum (the condition is one
+// row's, the same for all threads that work on it).
+template <Team TEAM, int V, int K>
+__device__ __forceinline__ void recentre_row(float2 (&v)[K][V / 2], const Columns<K, V> &c, float mean, float rstd,
+                                             float inv_h, Reduce &r) {
+    if (!(fabsf(mean) * rstd > 1.0f)) return;
+    float2 s = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (c.on[k]) {
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) s = __fadd2_rn(s, v[k][j]);
+        }
+    float rest = s.x + s.y;
+    row_sum<TEAM>(rest, r);
+    rest *= inv_h;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) v[k][j] = __fadd2_rn(v[k][j], both(-rest));
+}
+
 // A vector of per-channel factors of a thread's columns: zero past the row's
 // end, where what it multiplies may be anything finite.  KEEP: read once and
 // kept in registers; otherwise read again (from L1 or L2) at every row, where

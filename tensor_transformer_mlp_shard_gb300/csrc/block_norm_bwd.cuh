@@ -101,6 +101,14 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
             float m0, m1, none;
             float2 s0 = both(0.0f), s1 = both(0.0f);
             staged<R>(at, c, yh);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    if (LN) yh[k][j] = __fadd2_rn(yh[k][j], both(-st.z));
+                    yh[k][j] = __fmul2_rn(yh[k][j], both(st.w));
+                }
+            if (LN) recentre_row<TEAM, V, K>(yh, c, st.z, st.w, inv_h, r);
             staged<A>(at, c, h);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -108,8 +116,6 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
                 nw.get(p, c, k, p.pre_w, plus, 1.0f, false, w);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
-                    if (LN) yh[k][j] = __fadd2_rn(yh[k][j], both(-st.z));
-                    yh[k][j] = __fmul2_rn(yh[k][j], both(st.w));
                     n1[k][j] = __ffma2_rn(h[k][j], yh[k][j], n1[k][j]);  // h is zero past the row
                     if (LN) n0[LN ? k : 0][j] = __fadd2_rn(n0[LN ? k : 0][j], h[k][j]);
                     h[k][j] = __fmul2_rn(h[k][j], w[j]);
@@ -154,6 +160,7 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
                     if (LP) fh[k][j] = __fadd2_rn(fh[k][j], both(-st.x));
                     fh[k][j] = __fmul2_rn(fh[k][j], both(st.y));  // no post-norm: 1
                 }
+            if (LP) recentre_row<TEAM, V, K>(fh, c, st.x, st.y, inv_h, r);
         } else {
 #pragma unroll
             for (int k = 0; k < K; ++k)
