@@ -330,16 +330,15 @@ __device__ __forceinline__ void centre_row(float2 (&v)[K][V / 2], const Columns<
     }
 }
 
-// The backward's normalised row, v = (x - mean) / spread, less its own mean.
-// The statistics hold the mean rounded to fp32, so v is off by up to 2^-24
-// |mean| / spread, the same for the whole row: a bias, which a sum over tokens
+// Mean of a normalised row, v = (x - mean) / spread, for every thread of it.
+// The statistics hold the mean rounded to fp32, so it is not zero but up to 2^-24
+// |mean| / spread, the same for all columns: a bias, which a sum over tokens
 // does not average out.  Up to a mean of one spread that is within v's own
-// rounding; rows with a larger one take this further sum (the condition is one
-// row's, the same for all threads that work on it).
+// rounding; the backward takes it off the rows whose mean is larger (one row's
+// condition, the same for all threads that work on it).
+__device__ __forceinline__ bool far_from_zero(float mean, float rstd) { return fabsf(mean) * rstd > 1.0f; }
 template <Team TEAM, int V, int K>
-__device__ __forceinline__ void recentre_row(float2 (&v)[K][V / 2], const Columns<K, V> &c, float mean, float rstd,
-                                             float inv_h, Reduce &r) {
-    if (!(fabsf(mean) * rstd > 1.0f)) return;
+__device__ __forceinline__ float mean_left(const float2 (&v)[K][V / 2], const Columns<K, V> &c, float inv_h, Reduce &r) {
     float2 s = both(0.0f);
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -349,11 +348,7 @@ __device__ __forceinline__ void recentre_row(float2 (&v)[K][V / 2], const Column
         }
     float rest = s.x + s.y;
     row_sum<TEAM>(rest, r);
-    rest *= inv_h;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) v[k][j] = __fadd2_rn(v[k][j], both(-rest));
+    return rest * inv_h;
 }
 
 // A vector of per-channel factors of a thread's columns: zero past the row's

@@ -17,8 +17,8 @@ namespace bn {
 // Bound by HBM as the forward is: dy, y, dn and f are read once and dx and df
 // written once.  8192 x 4096 bf16 (RMS, channel gate, RMS) takes 67 us in this
 // kernel and 74 us with the parameter gradients, 5.4 TB/s of 403 MB (0.81 of a
-// plain copy's rate); 4096 x 8192 with an fp32 stream and a LayerNorm 96 and
-// 101 us (6.0 TB/s, 0.89).  Two blocks of 64 registers an SM, where both norms
+// plain copy's rate); 4096 x 8192 with an fp32 stream and a LayerNorm 102 us with
+// them (5.9 TB/s, 0.88).  Two blocks of 64 registers an SM, where both norms
 // are RMS: one block of 73 took 118 us, its two barriers a row idle the SM.
 // The column sums stay in registers over all rows of a worker: 304 rows of
 // partial sums for 4096 columns and more, 10 MB that do not leave L2.
@@ -88,27 +88,30 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
         const uint8_t *at = stages + slot * row_bytes;
         slot ^= 1;
         float2 d[K][P];  // dy, then D
-        if (has_dy) {
-            staged<R>(at, c, d);
+        auto read_dy = [&](const uint8_t *&from) {
+            if (has_dy) {
+                staged<R>(from, c, d);
+            } else {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int j = 0; j < P; ++j) d[k][j] = both(0.0f);
+            }
+        };
+        // Under a pre-LayerNorm dy stays staged until the row's sums are known: with it in
+        // registers the branch for rows far from zero spills (4096 x 8192 bf16: 79 us, 72 so)
+        const uint8_t *at_dy = at;
+        if (LN) {
+            if (has_dy) at += K * c.lanes * V * sizeof(R);
         } else {
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-#pragma unroll
-                for (int j = 0; j < P; ++j) d[k][j] = both(0.0f);
+            read_dy(at);
         }
         if (has_pre) {
             float2 yh[K][P], h[K][P];
             float m0, m1, none;
             float2 s0 = both(0.0f), s1 = both(0.0f);
             staged<R>(at, c, yh);
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    if (LN) yh[k][j] = __fadd2_rn(yh[k][j], both(-st.z));
-                    yh[k][j] = __fmul2_rn(yh[k][j], both(st.w));
-                }
-            if (LN) recentre_row<TEAM, V, K>(yh, c, st.z, st.w, inv_h, r);
+            const uint8_t *at_dn = at;
             staged<A>(at, c, h);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -116,6 +119,8 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
                 nw.get(p, c, k, p.pre_w, plus, 1.0f, false, w);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
+                    if (LN) yh[k][j] = __fadd2_rn(yh[k][j], both(-st.z));
+                    yh[k][j] = __fmul2_rn(yh[k][j], both(st.w));
                     n1[k][j] = __ffma2_rn(h[k][j], yh[k][j], n1[k][j]);  // h is zero past the row
                     if (LN) n0[LN ? k : 0][j] = __fadd2_rn(n0[LN ? k : 0][j], h[k][j]);
                     h[k][j] = __fmul2_rn(h[k][j], w[j]);
@@ -131,6 +136,21 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
                 row_sum<TEAM>(m1, r);
             m0 *= -st.w * inv_h;
             m1 *= -st.w * inv_h;
+            if (LN && far_from_zero(st.z, st.w)) {
+                // yh - rest in the place of yh: in the sum, in D below (its part that
+                // the columns share joins m0) and in the column sums
+                const float rest = mean_left<TEAM, V, K>(yh, c, inv_h, r);
+                m1 = fmaf(-rest, m0, m1);
+                m0 = fmaf(-rest, m1, m0);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    float2 dn[P];
+                    load<A, V>(at_dn, (k * c.lanes + threadIdx.x) * V, dn);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) n1[k][j] = __ffma2_rn(dn[j], both(-rest), n1[k][j]);
+                }
+            }
+            if (LN) read_dy(at_dy);
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -160,7 +180,13 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
                     if (LP) fh[k][j] = __fadd2_rn(fh[k][j], both(-st.x));
                     fh[k][j] = __fmul2_rn(fh[k][j], both(st.y));  // no post-norm: 1
                 }
-            if (LP) recentre_row<TEAM, V, K>(fh, c, st.x, st.y, inv_h, r);
+            if (LP && far_from_zero(st.x, st.y)) {
+                const float rest = mean_left<TEAM, V, K>(fh, c, inv_h, r);
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int j = 0; j < P; ++j) fh[k][j] = __fadd2_rn(fh[k][j], both(-rest));
+            }
         } else {
 #pragma unroll
             for (int k = 0; k < K; ++k)
