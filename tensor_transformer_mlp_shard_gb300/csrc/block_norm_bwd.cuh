@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
             row_sum<TEAM>(m1, r);
         if (token && first) store1<A>(p.dg[js], at_row.local, p.c * dg);
         m0 *= -st.y * inv_h;
-        m1 = p.post != TP_NORM_NONE ? -st.y * m1 * inv_h : 0.0f;
+        m1 *= -st.y * inv_h;
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (c.on[k]) {
@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
                 for (int j = 0; j < P; ++j) {
                     o[j] = __fmul2_rn(d[k][j], both(st.y));
                     if (LP) o[j] = __fadd2_rn(o[j], both(m0));
-                    o[j] = __ffma2_rn(fh[k][j], both(m1), o[j]);
+                    // without a post-norm df has no part of f, whatever f holds
+                    if (LP || p.post != TP_NORM_NONE) o[j] = __ffma2_rn(fh[k][j], both(m1), o[j]);
                 }
                 store<A, V>(static_cast<A *>(p.df[js]) + e, c.at(k), o);
             }

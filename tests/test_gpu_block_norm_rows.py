@@ -97,3 +97,23 @@ def test_odd_rows_backward(tp, kind, H):
     c.run_bwd(h, tp)
     c.check_bwd()
     assert all(torch.isfinite(t).all() for k, t in c.out.items() if kind == "layer" or not k.endswith("_b"))
+
+
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "element"])
+@pytest.mark.parametrize("H", [256, 2056, 16384])
+def test_without_a_post_norm_df_does_not_depend_on_f(tp, H, gate):
+    """y = a x + c g f: the gradient of f is c g dy, also where f is NaN or
+    infinite (an expert's output that a token's gate of zero leaves out)."""
+    def edit(c):
+        c.f[3, 5], c.f[4, H - 1], c.f[5] = float("nan"), float("inf"), -float("inf")
+
+    bad, clean = (Case(9, H, "bf16", "none", "none", gate, c=0.5, edit=e) for e in (edit, None))
+    for c in (bad, clean):
+        if gate != "none":
+            c.g[..., 0] = 0.0
+        h = c.handle(tp)
+        c.run_fwd(h)
+        c.run_bwd(h, tp)
+    for k in ("dx", "df"):
+        assert torch.equal(bad.out[k], clean.out[k]), k
+    assert torch.isfinite(bad.out["df"]).all()
