@@ -570,9 +570,11 @@ TP_API tp_status tp_adamw_ctl_init(void *ctl, int steps_done, void *stream);
 /* The norm of all gradients of the list, sqrt(sum g^2) * grad_scale, in the
  * control block, with what the next step takes from it: scale = grad_scale *
  * min(1, max_norm / norm), the step count (one more) and its bias corrections.
- * A norm that is not finite (a gradient is NaN or infinite, or its square
- * overflows fp32) clears `finite` and counts no step: the step then changes
- * nothing.  max_norm: > 0, infinity for no clipping.  Summed in a fixed order.
+ * A norm that is not finite (a gradient is NaN or infinite), or whose square
+ * after clipping is not (min(norm, max_norm) above 1.8e19: the states hold
+ * squares), clears `finite` and counts no step: the step then changes nothing.
+ * max_norm: > 0, infinity for no clipping.  Summed in a fixed order; any finite
+ * gradients, subnormal ones among them, have their norm to fp32's rounding.
  * Two calls on one control block must not overlap. */
 TP_API tp_status tp_adamw_grad_norm(tp_adamw *h, float grad_scale, float max_norm, void *ctl, void *stream);
 

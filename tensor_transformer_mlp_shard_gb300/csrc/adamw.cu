@@ -627,6 +627,12 @@ __global__ void __launch_bounds__(kThreads, 4) step_kernel(const __grid_constant
 // a step, whose last writes still leave L2).  The norm is then the rounded norm
 // of the rounded squares, whatever the order, and the clip factor that scales
 // every gradient does not move with the list's grouping.
+//
+// That needs squares that fp32 holds.  A thread's sum tells: between 2^-90 and
+// 2^90 none overflowed, and what underflowed was less than 2^-38 of it (a thread
+// has at most 2^21 elements, and loses up to 2^-150 of each).  A thread whose sum
+// lies outside reads its gradients again, scaled, and joins in fp64: any finite
+// gradients have their norm.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return __fadd2_rn(a, make_float2(-b.x, -b.y)); }
 
@@ -636,6 +642,39 @@ struct NormArgs {
     float log_beta1, log_beta2;
     int first, last;  // of the launches over one list
 };
+
+// (s, rest) += the squares of g, or of k g
+template <bool SCALED, int L>
+__device__ __forceinline__ void add_squares(const float2 (&g)[L][2], float k, float2 &s, float2 &rest) {
+#pragma unroll
+    for (int j = 0; j < L; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float x = SCALED ? __fmul_rn(g[j][i].x, k) : g[j][i].x, y = SCALED ? __fmul_rn(g[j][i].y, k) : g[j][i].y;
+            const float2 q = make_float2(__fmul_rn(x, x), __fmul_rn(y, y));
+            const float2 z = __fadd2_rn(s, q), d = sub2(z, s);
+            rest = __fadd2_rn(rest, __fadd2_rn(sub2(s, sub2(z, d)), sub2(q, d)));
+            s = z;
+        }
+}
+constexpr float kSumMin = 8.077935669463161e-28f, kSumMax = 1.2379400392853803e+27f;  // 2^-90, 2^90
+// A thread's sum where fp32 does not hold its squares, all its gradients read
+// again (a NaN or an infinity among them: NaN).  Not inlined, for the registers.
+template <int CAP, typename G>
+__device__ __noinline__ double scaled_squares(const Table<CAP> &tab, bool large) {
+    constexpr int L = kNormChunk / (4 * kThreads);
+    float2 s = both(0.0f), rest = both(0.0f);
+    for (Walk<CAP> now(tab); now.c < now.end; now.next(tab)) {
+        const long long e0 = static_cast<long long>(now.c - tab.chunk0[now.ti]) * kNormChunk, left = tab.t[now.ti].n - e0;
+        const G *in = static_cast<const G *>(tab.t[now.ti].g) + e0;
+        const uint32_t n = left < kNormChunk ? static_cast<uint32_t>(left) : kNormChunk;
+        float2 g[L][2];
+#pragma unroll
+        for (int j = 0; j < L; ++j) load4<false>(in, threadIdx.x * 4 + j * 4 * kThreads, n, g[j]);
+        add_squares<true>(g, large ? 8.271806125530277e-25f : 1.2676506002282294e+30f, s, rest);  // 2^-80, 2^100
+    }
+    return (static_cast<double>(s.x) + s.y + rest.x + rest.y) * (large ? 1.461501637330903e+48 : 6.223015277861142e-61);  // 2^160, 2^-200
+}
 
 // (s, rest) += (a, b): the error of s + a joins the rests
 __device__ __forceinline__ void add_pair(float &s, float &rest, float a, float b) {
@@ -656,9 +695,10 @@ __device__ __forceinline__ double block_sum(double s, double *red) {
     return s;
 }
 
+// (five blocks an SM for bf16, whose loads are half as large: 40M gradients in 97 tensors 4 us longer with four)
 template <int CAP, typename G>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<CAP> tab,
-                                                        const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(G) == 2 ? 5 : 4) norm_kernel(const __grid_constant__ Table<CAP> tab,
+                                                                                const __grid_constant__ NormArgs a) {
     __shared__ double red[kThreads / 32];
     __shared__ int is_last;
     float2 s = both(0.0f), rest = both(0.0f);
@@ -677,22 +717,24 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 #pragma unroll
             for (int j = 0; j < L; ++j) load4<false>(in, e + j * 4 * kThreads, n, g[j]);
         }
-#pragma unroll
-        for (int j = 0; j < L; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 q = make_float2(__fmul_rn(g[j][i].x, g[j][i].x), __fmul_rn(g[j][i].y, g[j][i].y));
-                const float2 z = __fadd2_rn(s, q), d = sub2(z, s);
-                rest = __fadd2_rn(rest, __fadd2_rn(sub2(s, sub2(z, d)), sub2(q, d)));
-                s = z;
-            }
+        add_squares<false>(g, 1.0f, s, rest);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    double beyond = 0.0;
+    const float size = s.x + s.y;
+    if (!(size >= kSumMin && size <= kSumMax)) {
+        beyond = scaled_squares<CAP, G>(tab, !(size < kSumMin));
+        s = rest = both(0.0f);
+    }
     add_pair(s.x, rest.x, s.y, rest.y);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         add_pair(s.x, rest.x, __shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, rest.x, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = static_cast<double>(s.x) + rest.x;
+    if (__any_sync(0xffffffffu, beyond != 0.0)) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) beyond += __shfl_xor_sync(0xffffffffu, beyond, o);
+    }
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = static_cast<double>(s.x) + rest.x + beyond;
     __syncthreads();
     double sum = 0.0;
     if (threadIdx.x == 0) {
@@ -714,7 +756,9 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     sum = block_sum(sum, red);
     if (threadIdx.x) return;
     const float norm = static_cast<float>(sqrt(sum) * a.grad_scale);
-    const bool finite = norm <= 3.402823466e38f;
+    // the states hold squares of scaled gradients: the clipped norm, which bounds these, has to have one
+    const float most = fminf(norm, a.max_norm);
+    const bool finite = norm <= 3.402823466e38f && most * most <= 3.402823466e38f;
     a.ctl->ticket = 0;
     a.ctl->norm = norm;
     a.ctl->finite = finite;
