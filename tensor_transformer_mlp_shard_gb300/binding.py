@@ -724,7 +724,8 @@ class TPAdamW:
     where they are at every step (set_grads changes the gradients).  m, v (and
     m_scale, v_scale with state_bits=8) are the states, zeros when not given:
     fp32, or one byte an element (E4M3 codes of m and sqrt(v)) and one fp32
-    scale for every 256 elements.  weight_decay and lr_scale: a number, or one
+    scale for every 256 elements.  States that are not zero come whole: m with v,
+    codes with their scales.  weight_decay and lr_scale: a number, or one
     for each tensor.  steps_done: steps taken before, as grad_norm counts them.
     """
 
@@ -751,6 +752,11 @@ class TPAdamW:
         if half and master is None:
             master = [p.detach().float().contiguous() for p in params]
         self.master = self._each("master", list(master), sizes, f32) if half else None
+        m, v, m_scale, v_scale = (None if ts is None else list(ts) for ts in (m, v, m_scale, v_scale))
+        if state_bits == 8:
+            self._whole("m", m, "m_scale", m_scale)
+            self._whole("v", v, "v_scale", v_scale)
+        self._whole("m", m, "v", v)
         state = f32 if state_bits == 32 else torch.uint8
         self.m = self._each("m", own(m, sizes, state), sizes, state)
         self.v = self._each("v", own(v, sizes, state), sizes, state)
@@ -811,6 +817,16 @@ class TPAdamW:
             if t.numel() != n:
                 raise ValueError(f"{name}[{i}]: {tuple(t.shape)} has {t.numel()} elements, expected {n}")
         return ts
+
+    @staticmethod
+    def _whole(name, ts, other, others):
+        """Refuses one part of a state whose other part is missing, unless it is zero."""
+        if (ts is None) == (others is None):
+            return
+        if ts is None:
+            name, ts, other = other, others, name
+        if any(bool(t.any()) for t in ts):
+            raise ValueError(f"{other}: required with {name}")
 
     def _grads(self, grads, dtype):
         if dtype not in (torch.float32, torch.bfloat16):

@@ -91,6 +91,16 @@ def test_no_step_whose_squares_overflow(tp, scale, max_norm, steps):
     assert torch.isfinite(opt.v[0]).all() and bool((w[0] != 0).all()) == bool(steps)
 
 
+def test_no_step_whose_squares_overflow_once_scaled(tp):
+    """Gradients with a norm of 3e16 and a scale of 1e10 above it."""
+    w, opt = optimizer(tp, [torch.full((1000,), 1e15, device="cuda")])
+    norm = opt.grad_norm(grad_scale=1e10)
+    opt.step(1e-2)
+    total = 1e15 * 1000 ** 0.5 * 1e10
+    assert abs(float(norm) - total) <= 32 * U * total
+    assert int(opt.finite) == 0 and (opt.v[0] == 0).all() and (w[0] == 0).all()
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("beside", [0.0, 1e-30, 1.0, 1e30])
 def test_not_finite_whatever_lies_beside(tp, value, beside):
