@@ -15,6 +15,7 @@ constexpr int kMaxThreads = 512;    // threads of a block in the block-per-row k
 constexpr int kMaxCluster = 4;      // blocks that share a row
 constexpr int kSlots = 16 * kMaxCluster;  // partial sums of a row: one a warp
 constexpr int kMaxH = 16384;
+constexpr int kSmemMost = 225 * 1024 - 2560;  // dynamic shared memory; the static buffers and the system take the rest
 // workers of the backward, each writing one row of partial sums: two blocks an
 // SM for rows of 4096 columns and more, up to eight for narrower ones
 constexpr int max_chunks(int H) { return H >= 4096 ? 304 : H <= 1024 ? 1216 : 304 * 4096 / H; }

@@ -132,7 +132,9 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads) fwd
 template <typename A, typename R, bool LP, bool LN, bool COMMON>
 static Kernel pick(const Shape &s) {
     if (s.team == kWarp) return s.E == 8 ? fwd_kernel<A, R, 8, kWarp, LP, LN, COMMON> : fwd_kernel<A, R, 16, kWarp, LP, LN, COMMON>;
-    if (s.team == kCluster) return fwd_kernel<A, R, 16, kCluster, LP, LN, COMMON>;
+    // types whose widest row fits a block have no cluster
+    if constexpr (kStages * (sizeof(R) + (COMMON ? 1 : 2) * sizeof(A)) * (kMaxH + 32 * 32) > kSmemMost)
+        if (s.team == kCluster) return fwd_kernel<A, R, 16, kCluster, LP, LN, COMMON>;
     return s.E == 32 ? fwd_kernel<A, R, 32, kBlock, LP, LN, COMMON> : fwd_kernel<A, R, 16, kBlock, LP, LN, COMMON>;
 }
 template <typename A, typename R, bool COMMON>
