@@ -197,10 +197,9 @@ __device__ __forceinline__ float reciprocal(float x) {
 }
 // Square roots, rounded correctly for v from 2^-100 up: one Newton step from
 // the approximate reciprocal root, its residual s^2 - v exact in a fused
-// operation (Markstein, IBM J. Res. Dev. 34, 1990).  Compared with sqrtf for
-// all 2^24 values of two binades at ten exponents: none differs.  sqrtf itself
-// branches for its small arguments, at each of 8 values, and cost a quarter of
-// the kernel's instructions.
+// operation (Markstein, IBM J. Res. Dev. 34, 1990).  test_gpu_adamw_roots.py
+// compares 2^17 of them with IEEE roots.  With sqrtf the profile counted ten
+// branch instructions an element more.
 constexpr float kRootMin = 7.8886091e-31f;  // 2^-100
 __device__ __forceinline__ float2 roots(float2 v) {
     float2 y;
@@ -304,8 +303,9 @@ __device__ __forceinline__ void scale_values(const Scale &s, float2 (&x)[2][2]) 
 // and fp32 parameters (14 bytes) it is longer: 349 us.  Hence the loads staged a
 // chunk ahead, the rounding in two integer operations, one hash for both
 // states, the roots without branches, the paired products and the extremes of
-// three (558 us with none of them and even runs of chunks), and 64 registers
-// without spills: 390 us with 16 bytes of them.
+// three (558 us with none of them and even runs of chunks), and four blocks of 64
+// registers.  bf16 parameters fit these; fp32 parameters spill 8 bytes (16 with
+// bf16 gradients).
 // ---------------------------------------------------------------------------
 // What a lane reads of a block.
 template <typename G, int BITS>
