@@ -528,7 +528,9 @@ TP_API tp_status tp_block_norm_bwd(tp_block_norm *h, const void *const *dY, cons
  * (256-byte aligned), initialised once by tp_adamw_ctl_init.  It begins with
  *   float norm; float scale; int32 finite; int32 steps;
  * and lets a step be clipped, skipped and counted without the host, so that a
- * captured graph can be replayed step after step. */
+ * captured graph can be replayed step after step.  The learning rate is an
+ * argument: a graph replays the one it was captured with, so a schedule that
+ * changes it captures again. */
 #define TP_ADAMW_CTL_BYTES 32768
 #define TP_ADAMW_MAX_TENSORS 65536
 typedef struct {
@@ -560,7 +562,7 @@ TP_API tp_status tp_adamw_create(const tp_adamw_desc *desc, const tp_adamw_tenso
 TP_API void tp_adamw_destroy(tp_adamw *h);
 
 /* Replace the gradients' addresses (n_tensors pointers) for the calls made
- * after this one.  Host only. */
+ * after this one.  Host only; makes the launches' tables anew. */
 TP_API tp_status tp_adamw_set_grads(tp_adamw *h, const void *const *grads);
 
 /* Initialise a control block: `steps_done` steps taken so far, nothing
@@ -575,6 +577,8 @@ TP_API tp_status tp_adamw_ctl_init(void *ctl, int steps_done, void *stream);
  * squares), clears `finite` and counts no step: the step then changes nothing.
  * max_norm: > 0, infinity for no clipping.  Summed in a fixed order; any finite
  * gradients, subnormal ones among them, have their norm to fp32's rounding.
+ * Every call counts a step, whether or not one follows: a norm that is only to
+ * be looked at takes a control block of its own.
  * Two calls on one control block must not overlap. */
 TP_API tp_status tp_adamw_grad_norm(tp_adamw *h, float grad_scale, float max_norm, void *ctl, void *stream);
 

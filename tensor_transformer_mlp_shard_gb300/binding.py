@@ -841,9 +841,10 @@ class TPAdamW:
 
     def grad_norm(self, grad_scale=1.0, max_norm=float("inf"), stream=None):
         """Enqueue the norm of grad_scale * grads and what the next step() takes
-        from it: the clip factor, the step count and whether the norm is finite
-        (if not, that step changes nothing).  Returns the norm as a one-element
-        CUDA tensor that the next call overwrites."""
+        from it: the clip factor, the step count (each call counts one) and
+        whether the norm, and its square once clipped, are finite (if not, that
+        step changes nothing and none is counted).  Returns the norm as a
+        one-element CUDA tensor that the next call overwrites."""
         status = self._norm(self._h, grad_scale, max_norm, self._ctl, _stream(stream))
         if status:
             _check(status)
@@ -851,7 +852,8 @@ class TPAdamW:
 
     def step(self, lr, step=None, grad_scale=1.0, stream=None):
         """Enqueue one step: number `step` (from 1) on grad_scale * grads, or,
-        with step=None, as the last grad_norm() call left it."""
+        with step=None, as the last grad_norm() call left it.  A captured step
+        keeps the lr of its capture."""
         if step is None:
             status = self._step(self._h, lr, 1.0, 0, self._ctl, _stream(stream))
         else:

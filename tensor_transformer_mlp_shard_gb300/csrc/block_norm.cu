@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256) param_grad_kernel(const __grid_constant__
 //   one RMS norm: 46 us, 86 us by a cluster).
 //   Wider, backward: by a block, 8 elements a thread while its threads suffice
 //   (its column sums take as many registers again: 8192 x 4096 with two
-//   LayerNorms 85 us, 116 us with 16), else 16.
+//   LayerNorms 78 us, 90 us with 16; fp32 126 us, 196 us with 16), else 16.
 //   Where a block's threads or its shared memory do not hold a row: by a
 //   cluster of 2 or 4 blocks.  Its barriers cost dear (8192 x 4096 bf16 forward:
 //   84 us with 2 blocks, 48 us with one), so it is the last resort: above 8192

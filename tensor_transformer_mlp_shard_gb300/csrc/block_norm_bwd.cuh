@@ -17,8 +17,8 @@ namespace bn {
 // Bound by HBM as the forward is: dy, y, dn and f are read once and dx and df
 // written once.  8192 x 4096 bf16 (RMS, channel gate, RMS) takes 67 us in this
 // kernel and 74 us with the parameter gradients, 5.4 TB/s of 403 MB (0.81 of a
-// plain copy's rate); 4096 x 8192 with an fp32 stream and a LayerNorm 102 us with
-// them (5.9 TB/s, 0.88).  Two blocks of 64 registers an SM, where both norms
+// plain copy's rate); 4096 x 8192 with an fp32 stream and a LayerNorm 98 and
+// 102 us (5.9 TB/s, 0.88).  Two blocks of 64 registers an SM, where both norms
 // are RMS: one block of 73 took 118 us, its two barriers a row idle the SM.
 // The column sums stay in registers over all rows of a worker: 304 rows of
 // partial sums for 4096 columns and more, 10 MB that do not leave L2.
@@ -64,8 +64,8 @@ __global__ void __launch_bounds__(TEAM == kWarp ? 32 * kWarps : kMaxThreads,
     if (c.ragged) clear_stages(stages, kStages * row_bytes);
     wait_for_stream();
     fetch(0);
-    // kept unless four column sums of 16 fill the registers (8192 x 4096 with two LayerNorms: 105 us, kept 118 us;
-    // with one, 101 us, not kept 145 us)
+    // kept unless four column sums of 16 fill the registers (4096 x 8192 bf16 with two LayerNorms: 94 us, kept 117 us;
+    // with one, 72 us, not kept 80 us, and with an fp32 stream 102 us, not kept 131 us)
     constexpr bool KEEP = E == 8 || !LP || !LN || sizeof(A) == 4;
     Factors<A, K, V, KEEP> gw, nw;  // the post-norm's weight, gate and block scale in it, and the pre-norm's
     gw.keep(p, c, p.post_w, plus, 1.0f, true);
