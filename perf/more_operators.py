@@ -97,8 +97,8 @@ def draw(rng):
         M = _log_int(rng, 1, most)
         B = min(M, rng.randint(1, 5))
         case.update(S=M // B, B=B, place=rng.random() < 0.5, positions=rng.random() < 0.5)
-        if case["place"]:
-            case["scaling"] = "none" if case["scaling"] == "parts" else case["scaling"]
+        if case["place"] and case["scaling"] == "parts":  # its factor would grow from pass to pass
+            case.update(scaling="none", factor=1.0)
         return case
     case["page"] = rng.choice([16, 16, 32, 64, 128, 16 * rng.randint(1, 20)])
     row = 2 * kv * D * (1 if dtype == "fp8" else size)  # a position's bytes
@@ -254,7 +254,6 @@ def prepare(case, seed):
             which = torch.repeat_interleave(torch.arange(len(lengths), device="cuda"), lengths)
             at = torch.arange(M, device="cuda") - start[which] + torch.where(which == 0, 1717, 0)
             s["positions"] = s["at"] = at.int()
-        shared = ("x", "y")
     elif case["op"] == "append":
         new, past = _append_plan(case)
         s["x"] = _qkv(case, gen, case["tokens"] + case["pad"])
@@ -267,7 +266,6 @@ def prepare(case, seed):
         s["table"], s["pages"] = _table(case, gen, [a + b for a, b in zip(new, past)])
         s["k"], s["v"] = _cache(case, gen, s["pages"])
         s["q"] = torch.zeros(T, case["tokens"] + case["pad"], heads // T * D, dtype=act, device="cuda")
-        shared = ("x", "k", "v", "q")
     else:
         lengths = _decode_lengths(case)
         s["positions"] = torch.tensor(lengths, dtype=torch.int32, device="cuda") - 1
@@ -276,12 +274,10 @@ def prepare(case, seed):
         sharp = 0.5 + 2.0 * torch.rand(T, 1, heads // T, 1, generator=gen, device="cuda")
         s["q"] = (_normal(gen, T, len(lengths), heads // T, D) * sharp).to(act).view(T, len(lengths), -1)
         s["o"] = torch.empty_like(s["q"])
-        shared = ("q", "k", "v", "o")
     for key, top in (("k_amax", 6.0), ("v_amax", 5.0)):  # what calibration found for each key head
         s[key] = None
         if case["dtype"] == "fp8":
             s[key] = top * (0.8 + 0.4 * torch.rand(kv, generator=gen, device="cuda"))
-    s["shards"] = {key: list(s[key].unbind(0)) for key in shared}
     return s
 
 
@@ -303,12 +299,12 @@ def _own_rope(c):
 
 def _own_rotary(s):
     import tensor_transformer_mlp_shard_gb300 as tp
-    c, t = s["case"], s["shards"]
+    c = s["case"]
     if "rotary" not in s:  # one object for a shape, as a program keeps it
         s["rotary"] = tp.TPRotary(S=c["S"], B=c["B"], heads=c["heads"], kv_heads=c["kv_heads"], head_dim=c["D"],
                                   T=c["T"], dtype=c["dtype"], grouped=c["grouped"], rope=_own_rope(c))
     call = s["rotary"].fwd if c["op"] == "rotary_fwd" else s["rotary"].bwd
-    call(t["x"], t["y"], positions=s["positions"])
+    call(s["x"], None if c["place"] else s["y"], positions=s["positions"])
     return s["y"]
 
 
@@ -324,15 +320,13 @@ def _own_attention(s):
 
 
 def _own_append(s):
-    t = s["shards"]
-    _own_attention(s).append(t["x"], s["positions"], s["table"], t["k"], t["v"], t["q"], sequences=s["sequences"],
+    _own_attention(s).append(s["x"], s["positions"], s["table"], s["k"], s["v"], s["q"], sequences=s["sequences"],
                              k_amax=s["k_amax"], v_amax=s["v_amax"])
     return _append_out(s)
 
 
 def _own_decode(s):
-    t = s["shards"]
-    _own_attention(s).decode(t["q"], s["positions"], s["table"], t["k"], t["v"], t["o"], workspace=s["ws"],
+    _own_attention(s).decode(s["q"], s["positions"], s["table"], s["k"], s["v"], s["o"], workspace=s["ws"],
                              k_amax=s["k_amax"], v_amax=s["v_amax"])
     return s["o"]
 
