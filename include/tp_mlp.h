@@ -75,7 +75,8 @@ typedef enum {
     TP_ERR_SHAPE = 2,        /* F % T, S % T under SP, width % 8, T range, ... */
     TP_ERR_UNSUPPORTED = 3,  /* valid request this library does not implement */
     TP_ERR_CUDA = 4,         /* a CUDA runtime/driver call failed */
-    TP_ERR_TIMEOUT = 5       /* a kernel's bounded wait ran out (device status) */
+    TP_ERR_TIMEOUT = 5,      /* a kernel's bounded wait ran out (device status) */
+    TP_ERR_INDEX = 6         /* a kernel met a page, sequence or position out of range (tp_paged_sync_status) */
 } tp_status;
 
 typedef enum { TP_ACT_NONE = 0, TP_ACT_GELU_TANH = 1, TP_ACT_SWIGLU = 2 } tp_act;
@@ -587,6 +588,153 @@ TP_API tp_status tp_adamw_grad_norm(tp_adamw *h, float grad_scale, float max_nor
  * grad_scale and t = step >= 1; a gradient that is not finite then spreads
  * into its weight and states. */
 TP_API tp_status tp_adamw_step(tp_adamw *h, float lr, float grad_scale, int step, const void *ctl, void *stream);
+
+/* ---- attention around the projections --------------------------------------
+ * What stands between the QKV column layer and the output row layer
+ * ("Megatron-LM 源码精读" s3.3: attention's column and row layers; the heads are
+ * split over the T shards).  Shard i of the QKV tensor is the column layer's
+ * output out_i, [tokens, (heads + 2 kv_heads) / T * head_dim], its columns
+ *   grouped = 0: the shard's query heads, then its key heads, then its values;
+ *   grouped = 1: for each of the shard's key heads its heads / kv_heads query
+ *                heads, the key, the value.
+ * Query head h uses key head h / (heads / kv_heads); shard i holds the query
+ * heads from i * heads / T and the key heads from i * kv_heads / T.
+ *
+ * Rotary positions.  The first `dim` elements of every query and key head are
+ * pairs, (x[i], x[i + dim/2]) or interleaved (x[2i], x[2i+1]), and a pair at
+ * position p turns by the angle p * f_i:
+ *   y1 = a (x1 cos - x2 sin),   y2 = a (x2 cos + x1 sin).
+ * f_i = base^(-2i/dim), or, for contexts `factor` = s times longer,
+ *   TP_ROPE_LINEAR  f_i / s (position interpolation, Chen et al. 2023);
+ *   TP_ROPE_NTK     base replaced by base * s^(dim/(dim-2));
+ *   TP_ROPE_PARTS   k f_i + (1-k) f_i / s, k = clamp((r - slow) / (fast - slow),
+ *                   0, 1), r = original * f_i / 2 pi the turns of the pair over
+ *                   the length trained on (YaRN's interpolation by parts, Peng
+ *                   et al. 2023).
+ * a is attention_factor; 0 stands for the default, 0.1 ln(s) + 1 for
+ * TP_ROPE_PARTS and 1 otherwise.  Angles are exact to 2^-32 of a turn at any
+ * position; sines and products are fp32, rounded once when stored. */
+typedef enum { TP_ROPE_HALVES = 0, TP_ROPE_INTERLEAVED = 1 } tp_rope_pairs;
+typedef enum { TP_ROPE_NONE = 0, TP_ROPE_LINEAR = 1, TP_ROPE_NTK = 2, TP_ROPE_PARTS = 3 } tp_rope_scaling;
+typedef struct {
+    int dim;                 /* rotated elements of a head: even, 0 (no rotation)..head_dim */
+    int pairs;               /* tp_rope_pairs */
+    int scaling;             /* tp_rope_scaling */
+    double base;             /* >= 1 */
+    double factor;           /* s >= 1 (1 with TP_ROPE_NONE) */
+    double original;         /* TP_ROPE_PARTS: positions trained on, > 0 */
+    double fast, slow;       /* TP_ROPE_PARTS: turns, fast > slow >= 0 (32 and 1) */
+    double attention_factor; /* a > 0, or 0 */
+} tp_rope_desc;
+
+/* Rotation of a QKV tensor's queries and keys in training: M = S*B tokens. */
+typedef struct {
+    int S, B;
+    int T;                /* shards, 1..TP_MAX_SHARDS */
+    int heads;            /* query heads of all shards, a multiple of T and of kv_heads */
+    int kv_heads;         /* key (and value) heads of all shards, a multiple of T */
+    int head_dim;         /* a multiple of 8, 8..256 */
+    int dtype;            /* TP_DT_BF16 or TP_DT_F32 */
+    int grouped;          /* 0 or 1 */
+    tp_rope_desc rope;
+} tp_rotary_desc;
+
+typedef struct tp_rotary tp_rotary;
+
+/* Validate and create (host only, no CUDA call).  TP_ERR_ARG for bad enums,
+ * flags or rotation constants, TP_ERR_SHAPE for sizes that do not divide or
+ * M above 2^24, TP_ERR_UNSUPPORTED for head_dim above 256. */
+TP_API tp_status tp_rotary_create(const tp_rotary_desc *desc, tp_rotary **out);
+TP_API void tp_rotary_destroy(tp_rotary *h);
+
+/* Y = rotation of X; T pointers each.  Y_i may be X_i (then the values and the
+ * elements behind `dim` are not touched); otherwise the two do not overlap and
+ * they are copied.  positions: int32 [M] on the device (4-byte aligned), or
+ * NULL: token m = s*B + b is at position s.  A token at a negative position is
+ * not rotated. */
+TP_API tp_status tp_rotary_fwd(tp_rotary *h, const void *const *X, const int32_t *positions, void *const *Y,
+                               void *stream);
+
+/* dX = the gradient of X from that of Y (the transposed rotation); dX_i may be
+ * dY_i.  positions as in the forward; nothing else is kept. */
+TP_API tp_status tp_rotary_bwd(tp_rotary *h, const void *const *dY, const int32_t *positions, void *const *dX,
+                               void *stream);
+
+/* Paged key-value cache and the attention of single tokens over it.
+ * Cache: K_i and V_i of shard i, [pages, kv_heads / T, page_size, head_dim]
+ * each, of the handle's type, or bytes with TP_DT_FP8: E4M3 codes, code =
+ * fp8(x * scale) saturating, scale = 448 / amax of the key head (1 when amax is
+ * not in [2^-100, 3e38]) from k_amax and v_amax, fp32 [kv_heads] on the device
+ * (4-byte aligned; NULL otherwise).  A cache is read with the amax it was
+ * written with.
+ * Table: int32 [sequences, table_cols] on the device; position p of sequence s
+ * is slot p % page_size of page table[s][p / page_size].  Entries that no
+ * position of a call needs are not read as pages (-1, say).
+ * Tokens (rows): `positions` and `sequences` are int32 [n] on the device;
+ * sequences may be NULL: row j belongs to sequence j.  A row at a negative
+ * position is padding. */
+typedef struct {
+    int T, heads, kv_heads, head_dim; /* as tp_rotary_desc; TP_DT_FP8: head_dim a multiple of 16 */
+    int dtype;                        /* TP_DT_F32, TP_DT_BF16, or TP_DT_FP8: bf16 and a cache of E4M3 codes */
+    int grouped;                      /* columns of X in tp_paged_append */
+    int page_size;                    /* positions a page: a multiple of 16 */
+    int pages;                        /* pages of the cache, >= 1 */
+    int window;                       /* positions that a token sees, its own among them; 0: all */
+    float scale;                      /* of the scores, finite; 0: 1 / sqrt(head_dim) */
+    tp_rope_desc rope;                /* dim 0: keys and queries as they are */
+} tp_paged_desc;
+
+typedef struct tp_paged tp_paged;
+
+/* Validate and create (host only; takes one of 1024 index words, released by
+ * tp_paged_destroy).  Errors as tp_rotary_create; TP_ERR_SHAPE for a page size
+ * that is not a multiple of 16 or pages < 1; TP_ERR_UNSUPPORTED when 1024 such
+ * handles are live. */
+TP_API tp_status tp_paged_create(const tp_paged_desc *desc, tp_paged **out);
+TP_API void tp_paged_destroy(tp_paged *h);
+
+/* Bytes of device workspace for tp_paged_decode (256-byte aligned start): the
+ * partial results of rows whose pages are read by several blocks.  A function
+ * of the descriptor alone.  Calls that may overlap take one each. */
+TP_API size_t tp_paged_workspace_bytes(const tp_paged *h);
+
+/* n new tokens: X (T pointers, QKV shards of n rows) -> Q (T pointers, [n,
+ * heads / T * head_dim], the rotated queries) and the slots of K and V that
+ * (sequences, positions) name.  Padding rows, whose sequence is not looked at,
+ * leave Q and the cache as they were.  A row whose sequence is outside
+ * [0, sequences), whose position is behind the table's last column or whose
+ * page is outside [0, pages) is left out in the same way and sets the handle's
+ * index word.  No two rows of a call name the same slot.
+ * n, the table's rows and its columns are at most 2^20, n = 0 enqueues nothing. */
+TP_API tp_status tp_paged_append(tp_paged *h, const void *const *X, const int32_t *positions,
+                                 const int32_t *sequences, int n, const int32_t *table, int table_rows,
+                                 int table_cols, const float *k_amax, const float *v_amax, void *const *Q,
+                                 void *const *K, void *const *V, void *stream);
+
+/* n rows of queries Q (T pointers, as tp_paged_append leaves them) over the
+ * cache: O (T pointers, [n, heads / T * head_dim]; O_i may be Q_i) =
+ *   sum_j w_j V_j,   w = softmax_j(scale * q . K_j),
+ * j over the positions max(0, p - window + 1)..p of the row's sequence.  Rows
+ * may share a sequence.  Whatever the other slots hold (NaN, infinities) is not
+ * read.  A padding row's output is zero, and so is that of a row that sees
+ * only scores of -infinity.  A row whose sequence or position is out of range
+ * (as above) gives zero, a page out of range is left out of the sum; both set
+ * the handle's index word.
+ * Scores, softmax and sums are fp32; bf16 and FP8 weights enter the products as
+ * the sum of two 16-bit numbers.  The long axis is split over blocks, whose
+ * results are joined in a fixed order: outputs are deterministic.
+ * workspace: >= tp_paged_workspace_bytes, 256-byte aligned; contents on entry
+ * are ignored. */
+TP_API tp_status tp_paged_decode(tp_paged *h, const void *const *Q, const int32_t *positions,
+                                 const int32_t *sequences, int n, const int32_t *table, int table_rows,
+                                 int table_cols, const float *k_amax, const float *v_amax, const void *const *K,
+                                 const void *const *V, void *const *O, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* Synchronise `stream`, then read and clear the handle's index word (of the
+ * current device): TP_ERR_INDEX iff a call of h met an index out of range since
+ * the last read, TP_ERR_CUDA when the synchronisation or the read fails. */
+TP_API tp_status tp_paged_sync_status(tp_paged *h, void *stream);
 
 /* ---- status, limits, diagnostics ---------------------------------------- */
 

@@ -22,7 +22,7 @@ ACT = {"none": 0, "gelu_tanh": 1, "swiglu": 2}
 DTYPE = {"f32": 0, "bf16": 1, "fp8": 2}
 TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.bfloat16}  # fp8: bf16 buffers
 STATUS = {0: "TP_OK", 1: "TP_ERR_ARG", 2: "TP_ERR_SHAPE", 3: "TP_ERR_UNSUPPORTED", 4: "TP_ERR_CUDA",
-          5: "TP_ERR_TIMEOUT"}
+          5: "TP_ERR_TIMEOUT", 6: "TP_ERR_INDEX"}
 MAX_SHARDS = 16
 
 
@@ -61,6 +61,24 @@ class AdamWTensor(ctypes.Structure):
                 ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("lr_scale", ctypes.c_float),
                 ("weight_decay", ctypes.c_float)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int), ("pairs", ctypes.c_int), ("scaling", ctypes.c_int), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original", ctypes.c_double), ("fast", ctypes.c_double),
+                ("slow", ctypes.c_double), ("attention_factor", ctypes.c_double)]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int), ("B", ctypes.c_int), ("T", ctypes.c_int), ("heads", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("grouped", ctypes.c_int), ("rope", RopeDesc)]
+
+
+class PagedDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("grouped", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("pages", ctypes.c_int), ("window", ctypes.c_int), ("scale", ctypes.c_float), ("rope", RopeDesc)]
 
 
 class ProfEntry(ctypes.Structure):
@@ -114,6 +132,17 @@ SIGNATURES = {
     "tp_adamw_ctl_init": (ctypes.c_int, [VP, ctypes.c_int, VP]),
     "tp_adamw_grad_norm": (ctypes.c_int, [VP, ctypes.c_float, ctypes.c_float, VP, VP]),
     "tp_adamw_step": (ctypes.c_int, [VP, ctypes.c_float, ctypes.c_float, ctypes.c_int, VP, VP]),
+    "tp_rotary_create": (ctypes.c_int, [ctypes.POINTER(RotaryDesc), ctypes.POINTER(VP)]),
+    "tp_rotary_destroy": (None, [VP]),
+    "tp_rotary_fwd": (ctypes.c_int, [VP] * 5),
+    "tp_rotary_bwd": (ctypes.c_int, [VP] * 5),
+    "tp_paged_create": (ctypes.c_int, [ctypes.POINTER(PagedDesc), ctypes.POINTER(VP)]),
+    "tp_paged_destroy": (None, [VP]),
+    "tp_paged_workspace_bytes": (ctypes.c_size_t, [VP]),
+    "tp_paged_append": (ctypes.c_int, [VP] * 4 + [ctypes.c_int, VP, ctypes.c_int, ctypes.c_int] + [VP] * 6),
+    "tp_paged_decode": (ctypes.c_int, [VP] * 4 + [ctypes.c_int, VP, ctypes.c_int, ctypes.c_int] + [VP] * 6 +
+                        [ctypes.c_size_t, VP]),
+    "tp_paged_sync_status": (ctypes.c_int, [VP, VP]),
     "tp_fp8_quantize": (ctypes.c_int, [PP, PP, ctypes.POINTER(ctypes.c_int64), ctypes.c_int, ctypes.c_int, VP, VP]),
     "tp_sync_status": (ctypes.c_int, [VP]),
     "tp_mlp_sync_status": (ctypes.c_int, [VP, VP]),
@@ -858,6 +887,200 @@ class TPAdamW:
             status = self._step(self._h, lr, 1.0, 0, self._ctl, _stream(stream))
         else:
             status = self._step(self._h, lr, grad_scale, step, None, _stream(stream))
+        if status:
+            _check(status)
+
+
+# ---------------------------------------------------------------------------
+# attention around the projections
+# ---------------------------------------------------------------------------
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+class Rope:
+    """How queries and keys turn with their position (tp_rope_desc).
+
+    dim: rotated elements at the start of each head (None: the whole head; 0:
+    no rotation); interleaved: pairs (2i, 2i+1) instead of (i, i + dim/2);
+    scaling: "none", "linear", "ntk" or "parts" for contexts `factor` times
+    longer ("parts" with the length `original` trained on and the turns `fast`
+    and `slow` over it); attention_factor: of cosines and sines, None for the
+    default (0.1 ln(factor) + 1 with "parts", else 1)."""
+
+    def __init__(self, dim=None, base=10000.0, interleaved=False, scaling="none", factor=1.0, original=0, fast=32.0,
+                 slow=1.0, attention_factor=None):
+        self.dim, self.base, self.interleaved, self.scaling = dim, base, interleaved, scaling
+        self.factor, self.original, self.fast, self.slow = factor, original, fast, slow
+        self.attention_factor = attention_factor
+
+    def desc(self, head_dim: int) -> RopeDesc:
+        return RopeDesc(int(head_dim) if self.dim is None else int(self.dim), int(bool(self.interleaved)),
+                        ROPE_SCALING[self.scaling], float(self.base), float(self.factor), float(self.original),
+                        float(self.fast), float(self.slow),
+                        0.0 if self.attention_factor is None else float(self.attention_factor))
+
+
+def _shards(name, ts, count, n, dtype, dev):
+    """The addresses of `count` shards of n elements, a list of tensors or one
+    tensor whose equal parts they are, as a C array; all on device `dev`."""
+    if type(ts) is torch.Tensor and ts.dtype is dtype and ts.numel() == count * n and ts.get_device() == dev \
+            and ts.is_contiguous():
+        at, step = ts.data_ptr(), n * dtype.itemsize
+        return _pack[count](*range(at, at + count * step, step)) if n else _pack[count](*[at] * count)
+    if isinstance(ts, torch.Tensor):
+        ts, count, n = [ts], 1, count * n
+    out = _pointers(name, ts, count, n, dtype)
+    for t in ts:
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+    return out
+
+
+def _vector(name, t, n, dtype, dev):
+    """Address of a contiguous tensor of n elements on device `dev`."""
+    at = _pointer(name, t, n, dtype)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+    return at
+
+
+class TPRotary:
+    """Handle for the rotation of a QKV tensor's queries and keys
+    (tp_rotary_create), in training: M = S*B tokens, T shards [M, (heads + 2
+    kv_heads) / T * head_dim] as the QKV column layer leaves them, each a list
+    of T tensors or one [T, ...] tensor.  grouped: a shard's columns are, key
+    head by key head, its queries, the key and the value; otherwise all
+    queries, all keys, all values."""
+
+    def __init__(self, S, B, heads, kv_heads, head_dim, T=1, dtype="bf16", grouped=False, rope=None):
+        rope = rope or Rope()
+        self._d = RotaryDesc(int(S), int(B), int(T), int(heads), int(kv_heads), int(head_dim), DTYPE[dtype],
+                             int(bool(grouped)), rope.desc(head_dim))
+        h = VP()
+        _check(lib().tp_rotary_create(ctypes.byref(self._d), ctypes.byref(h)))
+        self._h = h
+        self.M, self.T, self.dtype = int(S) * int(B), int(T), dtype
+        self._act = TORCH_DTYPE[dtype]
+        self._n = self.M * (int(heads) + 2 * int(kv_heads)) // self.T * int(head_dim)
+        self._fwd, self._bwd = lib().tp_rotary_fwd, lib().tp_rotary_bwd
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and _lib is not None:
+            _lib.tp_rotary_destroy(h)
+            self._h = None
+
+    def _run(self, call, x, x_name, y, y_name, positions, stream):
+        dev = torch.cuda.current_device() if self.M else 0
+        px = _shards(x_name, x, self.T, self._n, self._act, dev)
+        py = px if y is None else _shards(y_name, y, self.T, self._n, self._act, dev)
+        at = None if positions is None else _vector("positions", positions, self.M, torch.int32, dev)
+        status = call(self._h, px, at, py, _stream(stream))
+        if status:
+            _check(status)
+
+    def fwd(self, X, Y=None, positions=None, stream=None):
+        """Y = X with its queries and keys turned (None: in place).  positions:
+        int32 [M], or None: token m = s*B + b is at position s; a token at a
+        negative position is not turned."""
+        self._run(self._fwd, X, "X", Y, "Y", positions, stream)
+
+    def bwd(self, dY, dX=None, positions=None, stream=None):
+        """dX = the gradient of X from dY (None: in place)."""
+        self._run(self._bwd, dY, "dY", dX, "dX", positions, stream)
+
+
+class TPPagedAttention:
+    """Handle for a paged key-value cache and the attention of single tokens
+    over it (tp_paged_create).
+
+    The cache of shard i is K_i, V_i: [pages, kv_heads / T, page_size,
+    head_dim], of the handle's type, or uint8 with dtype "fp8" (E4M3 codes of
+    x * 448 / amax of the key head, from k_amax and v_amax, fp32 [kv_heads];
+    everything else is bf16).  X, Q, K, V and O are lists of T tensors or one
+    [T, ...] tensor each.  table: int32 [sequences, columns] of pages;
+    positions and sequences: int32 [n], a row at a negative position is padding;
+    sequences=None: row j is sequence j's.  window: positions that a token sees,
+    its own among them (0: all); scale: of the scores (None: head_dim ** -0.5).
+    rope: see Rope (None: the whole head, base 10000; Rope(dim=0): none)."""
+
+    def __init__(self, heads, kv_heads, head_dim, page_size, pages, T=1, dtype="bf16", grouped=False, rope=None,
+                 window=0, scale=None):
+        rope = rope or Rope()
+        if scale is not None and not scale:
+            raise ValueError("scale: 0 leaves no attention")
+        self._d = PagedDesc(int(T), int(heads), int(kv_heads), int(head_dim), DTYPE[dtype], int(bool(grouped)),
+                            int(page_size), int(pages), int(window), 0.0 if scale is None else float(scale),
+                            rope.desc(head_dim))
+        h = VP()
+        _check(lib().tp_paged_create(ctypes.byref(self._d), ctypes.byref(h)))
+        self._h = h
+        self.T, self.heads, self.kv_heads, self.head_dim, self.dtype = (int(T), int(heads), int(kv_heads),
+                                                                        int(head_dim), dtype)
+        self.cache_shape = (int(pages), self.kv_heads // self.T, int(page_size), self.head_dim)
+        self.cache_dtype = torch.uint8 if dtype == "fp8" else TORCH_DTYPE[dtype]
+        self._act = TORCH_DTYPE[dtype]
+        self._cache_n = _prod(self.cache_shape)
+        self._q_n = self.heads // self.T * self.head_dim
+        self._x_n = (self.heads + 2 * self.kv_heads) // self.T * self.head_dim
+        self._append, self._decode = lib().tp_paged_append, lib().tp_paged_decode
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and _lib is not None:
+            _lib.tp_paged_destroy(h)
+            self._h = None
+
+    def workspace_bytes(self) -> int:
+        return int(lib().tp_paged_workspace_bytes(self._h))
+
+    def sync_status(self, stream=None) -> int:
+        """Synchronise the stream and return (and clear) this handle's index
+        word: TP_ERR_INDEX when a call met a page, sequence or position out of
+        range."""
+        return int(lib().tp_paged_sync_status(self._h, _stream(stream)))
+
+    def _rows(self, positions, sequences, table, k_amax, v_amax, dev):
+        if not isinstance(positions, torch.Tensor) or positions.dim() != 1:
+            raise ValueError("positions: must be a CUDA tensor [n]")
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table: must be a CUDA tensor [sequences, columns]")
+        n, (rows, cols) = positions.shape[0], table.shape
+        at = (_vector("positions", positions, n, torch.int32, dev),
+              None if sequences is None else _vector("sequences", sequences, n, torch.int32, dev), n,
+              _vector("table", table, rows * cols, torch.int32, dev), rows, cols)
+        if self.dtype != "fp8":
+            return at + (None, None)
+        return at + (_vector("k_amax", k_amax, self.kv_heads, torch.float32, dev),
+                     _vector("v_amax", v_amax, self.kv_heads, torch.float32, dev))
+
+    def append(self, X, positions, table, K, V, Q, sequences=None, k_amax=None, v_amax=None, stream=None):
+        """New tokens X [n, (heads + 2 kv_heads) / T * head_dim] a shard: turned
+        queries to Q [n, heads / T * head_dim], turned keys and values to the
+        slots of their positions.  No two rows name the same slot."""
+        dev, T, act = torch.cuda.current_device(), self.T, self._act
+        rows = self._rows(positions, sequences, table, k_amax, v_amax, dev)
+        n = rows[2]
+        status = self._append(self._h, _shards("X", X, T, n * self._x_n, act, dev), *rows,
+                              _shards("Q", Q, T, n * self._q_n, act, dev),
+                              _shards("K", K, T, self._cache_n, self.cache_dtype, dev),
+                              _shards("V", V, T, self._cache_n, self.cache_dtype, dev), _stream(stream))
+        if status:
+            _check(status)
+
+    def decode(self, Q, positions, table, K, V, O, workspace, sequences=None, k_amax=None, v_amax=None, stream=None):
+        """O [n, heads / T * head_dim] a shard (it may be Q) = attention of each
+        row's queries over positions max(0, p - window + 1)..p of its sequence;
+        zero for padding.  workspace: see alloc_workspace, one for each of the
+        calls that may overlap."""
+        dev, T, act = torch.cuda.current_device(), self.T, self._act
+        rows = self._rows(positions, sequences, table, k_amax, v_amax, dev)
+        n = rows[2]
+        ws, nws = _workspace(workspace)
+        status = self._decode(self._h, _shards("Q", Q, T, n * self._q_n, act, dev), *rows,
+                              _shards("K", K, T, self._cache_n, self.cache_dtype, dev),
+                              _shards("V", V, T, self._cache_n, self.cache_dtype, dev),
+                              _shards("O", O, T, n * self._q_n, act, dev), ws, nws, _stream(stream))
         if status:
             _check(status)
 

@@ -934,6 +934,7 @@ const char *tp_status_str(tp_status s) {
         case TP_ERR_UNSUPPORTED: return "TP_ERR_UNSUPPORTED";
         case TP_ERR_CUDA: return "TP_ERR_CUDA";
         case TP_ERR_TIMEOUT: return "TP_ERR_TIMEOUT";
+        case TP_ERR_INDEX: return "TP_ERR_INDEX";
     }
     return "TP_ERR_UNKNOWN";
 }

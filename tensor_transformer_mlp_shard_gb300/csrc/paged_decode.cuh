@@ -1,0 +1,934 @@
+// Decode attention over a paged cache: o = sum_j w_j v_j, w = softmax(scale q.k_j).
+//
+// Bound by HBM: each key and value is read once, for all queries of its head.
+// The positions of all rows and key heads are one list of units (64 positions),
+// in order of row, head, position; every block takes an equal stretch of it
+// (as many blocks as are resident), so that uneven lengths load the SMs
+// evenly and one long row is split over all of them.  Within a stretch, the
+// units of one (row, head) are a segment; a segment that ends in another block
+// leaves its running maximum, sum and unnormalised output in the workspace, at
+// most two a block, and a second kernel joins them, in the blocks' order.
+//
+// Four warps share a unit, 16 positions each, and keep softmax states of their
+// own until the segment ends: no barrier in the loop.  Keys and values go from
+// memory into registers, already in the layout of the matrix instructions: the
+// contraction over the head's elements may take them in any order, so a
+// lane loads 16 contiguous bytes and its elements stand for whichever the
+// instruction calls k; the same holds for the rows of V^T, which only name
+// output elements.  Positions are the 16 rows of K and of P^T, the queries of a
+// head its 8 columns, so that one query wastes tensor work (which is cheap
+// here) and no bytes.  While a step's scores and products are computed, the
+// next step's keys are on their way, and then its values.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <mutex>
+#include <type_traits>
+
+#include "attention.cuh"
+
+namespace tpmlp {
+namespace attn {
+
+constexpr int kWarps = 4;
+constexpr int kBlock = 32 * kWarps;
+constexpr int kUnit = 16 * kWarps;      // positions
+constexpr int kMostBlocks = 1024;       // of a launch, and so of the workspace
+
+enum CacheKind : int { CACHE_BF16 = 0, CACHE_FP8 = 1, CACHE_F32 = 2 };
+
+// 16 positions of a row for one warp
+struct Step {
+    long long off;  // elements from the cache's start to its first position
+    int lo, hi;     // the positions [lo, hi) of the 16 that the row sees
+};
+
+// A segment of a row: what the warps need to walk it.
+struct Segment {
+    const int32_t *pages;       // the row's table
+    int head, t0, t1;           // key head of the shard; units [t0, t1)
+    int first, last;            // positions that the row sees
+};
+
+__device__ __forceinline__ Step step_at(const DecodePlan &p, const Segment &s, int unit, int warp) {
+    Step r;
+    const int base = unit * kUnit + warp * 16;
+    r.lo = max(s.first - base, 0);
+    r.hi = min(s.last + 1 - base, 16);
+    r.off = 0;
+    if (r.hi <= r.lo) {
+        r.lo = r.hi = 0;
+        return r;
+    }
+    uint32_t in_page;
+    const int page = s.pages[p.at.page.divmod(base, in_page)];
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.at.pages)) {
+        bad_index(p.at);
+        r.lo = r.hi = 0;
+        return r;
+    }
+    r.off = ((static_cast<long long>(page) * p.hk + s.head) * p.at.page_size + in_page) * p.D;
+    return r;
+}
+
+// keys and values pass through once: they need no place in L1
+__device__ __forceinline__ uint4 stream16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 stream8(const void *p) {
+    uint2 v;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 8x8 matrix of 16-bit elements, a row to four lanes, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int KIND>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    if constexpr (KIND == CACHE_BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// two E4M3 codes (the low and high byte) as two fp16 numbers, exactly
+__device__ __forceinline__ uint32_t half2_of_codes(uint32_t two) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+// ---------------------------------------------------------------------------
+// 16-bit products: bf16 caches as they are, E4M3 codes as fp16
+// ---------------------------------------------------------------------------
+// Lane l = 4g + t.  Score tile: C[position][query], position g or g + 8, queries
+// 2t, 2t + 1 of each 8.  Output tile: C[element][query], elements 2i and 2i + 1
+// of the VD that the lane holds of every value row, the same two queries.
+template <int KIND, int DP, int NT>
+struct TensorCore {
+    static constexpr bool k8 = KIND == CACHE_FP8;
+    using Cache = typename std::conditional<k8, uint8_t, __nv_bfloat16>::type;
+    using Act = __nv_bfloat16;
+    static constexpr int kHeads = 8 * NT;
+    static constexpr int kTileElems = DP;
+    static constexpr int kBlocksPerSm = DP == 256 ? 2 : DP == 128 ? (NT == 2 ? 2 : k8 ? 4 : 3) : NT == 2 ? 4 : 5;
+    static constexpr int KC = k8 ? DP / 64 : DP / 32;       // 16-byte loads of a lane's key row
+    static constexpr int KE = k8 ? 16 : 8;                  // elements of one
+    static constexpr int VD = k8 && DP % 128 == 0 ? 16 : 8; // elements of a lane's value load
+    static constexpr int VB = DP / (8 * VD);
+    static constexpr int VW = VD * (k8 ? 1 : 2) / 4;        // 32-bit words of one
+
+    uint32_t q[NT][DP / 16][2];
+    float sc[NT][2];     // score to log2 units, of the lane's queries
+    float m[NT][2], l[NT][2];
+    float acc[VB][VD / 2][NT][4];
+    uint32_t kr[2][KC][4];
+    uint32_t vr[4][VB][VW];
+    int g, t;
+
+    // the group's nq queries, from the row of its first
+    __device__ __forceinline__ void begin(const DecodePlan &p, const Act *qrow, int kv_head, int nq, float *) {
+        const int lane = threadIdx.x & 31;
+        g = lane >> 2;
+        t = lane & 3;
+        float kscale = 1.0f;
+        if (k8) kscale = 1.0f / cache_scale(p.k_amax, kv_head);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int h = 8 * n + g;
+            const Act *src = qrow + static_cast<long long>(h) * p.D;
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+                // bf16: lane's 8 elements 32c + 8t; codes: its 16 elements 64(c/2) + 16t, 8 at a time
+                const int e = k8 ? 64 * (c / 2) + 16 * t + 8 * (c % 2) : 32 * c + 8 * t;
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (h < nq && e < p.D) w = *reinterpret_cast<const uint4 *>(src + e);
+                q[n][2 * c][0] = w.x;
+                q[n][2 * c][1] = w.y;
+                q[n][2 * c + 1][0] = w.z;
+                q[n][2 * c + 1][1] = w.w;
+            }
+            float unit = p.scale_log2;
+            if constexpr (k8) {
+                // fp16 holds a bf16 number's bits but not its range: the query times a power of two
+                // that brings its largest element to [2^14, 2^15); what falls below fp16's smallest
+                // is 2^-38 of that
+                float top = 0.0f;
+#pragma unroll
+                for (int c = 0; c < DP / 16; ++c)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        top = fmaxf(top, fmaxf(fabsf(bf16_lo(q[n][c][r])), fabsf(bf16_hi(q[n][c][r]))));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // exponent of the power of two, within what two normal factors can make
+                int e = 0;
+                if (top > 0.0f && top <= 3.4e38f) e = min(max(14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), -113), 126);
+                const float up = __int_as_float((e + 127) << 23);
+#pragma unroll
+                for (int c = 0; c < DP / 16; ++c)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const __half2 x = __floats2half2_rn(bf16_lo(q[n][c][r]) * up, bf16_hi(q[n][c][r]) * up);
+                        q[n][c][r] = *reinterpret_cast<const uint32_t *>(&x);
+                    }
+                // the lanes hold query g here, queries 2t and 2t + 1 in the scores
+                unit = unit * kscale;
+                const int e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
+                // finite, so that a score of zero stays zero
+                sc[n][0] = fminf(fmaxf(unit * __int_as_float((127 - e0) << 23), -3.0e38f), 3.0e38f);
+                sc[n][1] = fminf(fmaxf(unit * __int_as_float((127 - e1) << 23), -3.0e38f), 3.0e38f);
+            } else {
+                sc[n][0] = sc[n][1] = unit;
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                m[n][r] = -INFINITY;
+                l[n][r] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < VB; ++b)
+#pragma unroll
+            for (int i = 0; i < VD / 2; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[b][i][n][r] = 0.0f;
+    }
+
+    __device__ __forceinline__ void load_k(const DecodePlan &p, const void *base, const Step &s) {
+        const Cache *k = static_cast<const Cache *>(base) + s.off;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = g + 8 * r;
+            const bool in = row >= s.lo && row < s.hi;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const int e = 4 * KE * c + KE * t;
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (in && e < p.D) w = stream16(k + row * p.D + e);
+                kr[r][c][0] = w.x;
+                kr[r][c][1] = w.y;
+                kr[r][c][2] = w.z;
+                kr[r][c][3] = w.w;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void load_v(const DecodePlan &p, const void *base, const Step &s) {
+        const Cache *v = static_cast<const Cache *>(base) + s.off;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 2 * t + (r & 1) + 8 * (r >> 1);
+            const bool in = row >= s.lo && row < s.hi;
+#pragma unroll
+            for (int b = 0; b < VB; ++b) {
+                const int e = 8 * VD * b + VD * g;
+                if constexpr (VW == 4) {
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (in && e < p.D) w = stream16(v + row * p.D + e);
+                    vr[r][b][0] = w.x;
+                    vr[r][b][1] = w.y;
+                    vr[r][b][2] = w.z;
+                    vr[r][b][3] = w.w;
+                } else {
+                    uint2 w = make_uint2(0u, 0u);
+                    if (in && e < p.D) w = stream8(v + row * p.D + e);
+                    vr[r][b][0] = w.x;
+                    vr[r][b][1] = w.y;
+                }
+            }
+        }
+    }
+
+    float s[NT][4];
+
+    __device__ __forceinline__ void scores(const Step &st) {
+        float c2[NT][2][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) c2[n][x][r] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {  // word pairs of the load
+                if constexpr (k8) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t x0 = kr[0][c][2 * w + u], x1 = kr[1][c][2 * w + u];
+                        const uint32_t a0 = half2_of_codes(x0 & 0xffffu), a2 = half2_of_codes(x0 >> 16);
+                        const uint32_t a1 = half2_of_codes(x1 & 0xffffu), a3 = half2_of_codes(x1 >> 16);
+                        const int k = 4 * c + 2 * w + u;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16816<KIND>(c2[n][u], a0, a1, a2, a3, q[n][k][0], q[n][k][1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma16816<KIND>(c2[n][w], kr[0][c][2 * w], kr[1][c][2 * w], kr[0][c][2 * w + 1], kr[1][c][2 * w + 1],
+                                       q[n][2 * c + w][0], q[n][2 * c + w][1]);
+                }
+            }
+        }
+        const bool in0 = g >= st.lo && g < st.hi, in1 = g + 8 >= st.lo && g + 8 < st.hi;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                s[n][r] = (r < 2 ? in0 : in1) ? (c2[n][0][r] + c2[n][1][r]) * sc[n][r & 1] : -INFINITY;
+    }
+
+    uint32_t ph[NT][2], pl[NT][2];  // weights as the sum of two 16-bit numbers
+
+    __device__ __forceinline__ void softmax() {
+        float top[NT][2];
+        bool rise = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float x = fmaxf(s[n][r], s[n][r + 2]);
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                top[n][r] = x;
+                rise |= x > m[n][r];
+            }
+        if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float now = fmaxf(m[n][r], top[n][r]);
+                    const float f = now == -INFINITY ? 1.0f : exp2_fast(m[n][r] - now);
+                    m[n][r] = now;
+                    l[n][r] *= f;
+#pragma unroll
+                    for (int b = 0; b < VB; ++b)
+#pragma unroll
+                        for (int i = 0; i < VD / 2; ++i) {
+                            acc[b][i][n][r] *= f;
+                            acc[b][i][n][r + 2] *= f;
+                        }
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float w[4], rest[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float top_of = m[n][r & 1] == -INFINITY ? 0.0f : m[n][r & 1];
+                w[r] = exp2_fast(s[n][r] - top_of);
+            }
+            l[n][0] += w[0] + w[2];
+            l[n][1] += w[1] + w[3];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                uint32_t hi;
+                if constexpr (k8) {
+                    const __half2 x = __floats2half2_rn(w[2 * r], w[2 * r + 1]);
+                    hi = *reinterpret_cast<const uint32_t *>(&x);
+                    rest[2 * r] = w[2 * r] - __low2float(x);
+                    rest[2 * r + 1] = w[2 * r + 1] - __high2float(x);
+                    const __half2 y = __floats2half2_rn(rest[2 * r], rest[2 * r + 1]);
+                    pl[n][r] = transpose8(*reinterpret_cast<const uint32_t *>(&y));
+                } else {
+                    hi = pack_bf16x2(w[2 * r], w[2 * r + 1]);
+                    rest[2 * r] = w[2 * r] - bf16_lo(hi);
+                    rest[2 * r + 1] = w[2 * r + 1] - bf16_hi(hi);
+                    pl[n][r] = transpose8(pack_bf16x2(rest[2 * r], rest[2 * r + 1]));
+                }
+                ph[n][r] = transpose8(hi);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void values() {
+#pragma unroll
+        for (int b = 0; b < VB; ++b) {
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+                // the same element of two neighbouring positions to one register
+#pragma unroll
+                for (int u = 0; u < (k8 ? 2 : 1); ++u) {
+                    uint32_t a0, a1, a2, a3;
+                    if constexpr (k8) {
+                        const uint32_t x = __byte_perm(vr[0][b][w], vr[1][b][w], u ? 0x7362 : 0x5140);
+                        const uint32_t y = __byte_perm(vr[2][b][w], vr[3][b][w], u ? 0x7362 : 0x5140);
+                        a0 = half2_of_codes(x & 0xffffu);
+                        a1 = half2_of_codes(x >> 16);
+                        a2 = half2_of_codes(y & 0xffffu);
+                        a3 = half2_of_codes(y >> 16);
+                    } else {
+                        a0 = __byte_perm(vr[0][b][w], vr[1][b][w], 0x5410);
+                        a1 = __byte_perm(vr[0][b][w], vr[1][b][w], 0x7632);
+                        a2 = __byte_perm(vr[2][b][w], vr[3][b][w], 0x5410);
+                        a3 = __byte_perm(vr[2][b][w], vr[3][b][w], 0x7632);
+                    }
+                    const int i = k8 ? 2 * w + u : w;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma16816<KIND>(acc[b][i][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
+                        mma16816<KIND>(acc[b][i][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+                    }
+                }
+            }
+        }
+    }
+
+    // the whole step: next is loaded as registers become free
+    __device__ __forceinline__ void step(const DecodePlan &p, const void *k, const void *v, const Step &now, const Step &next) {
+        scores(now);
+        load_k(p, k, next);
+        softmax();
+        values();
+        load_v(p, v, next);
+    }
+    __device__ __forceinline__ void first(const DecodePlan &p, const void *k, const void *v, const Step &now) {
+        load_k(p, k, now);
+        load_v(p, v, now);
+    }
+
+    // the warp's state to shared memory: out [kHeads][DP], top and sum [kHeads]
+    __device__ __forceinline__ void finish(const DecodePlan &p, float *out, float *top, float *sum) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float x = l[n][r];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                const int h = 8 * n + 2 * t + r;
+                if (g == 0) {
+                    top[h] = m[n][r];
+                    sum[h] = x;
+                }
+#pragma unroll
+                for (int b = 0; b < VB; ++b)
+#pragma unroll
+                    for (int i = 0; i < VD / 2; i += 2)
+                        *reinterpret_cast<float4 *>(out + h * DP + 8 * VD * b + VD * g + 2 * i) =
+                            make_float4(acc[b][i][n][r], acc[b][i][n][r + 2], acc[b][i + 1][n][r], acc[b][i + 1][n][r + 2]);
+            }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// fp32 products
+// ---------------------------------------------------------------------------
+// Eight lanes share a position, DP / 8 elements each; the four groups of lanes
+// keep softmax states of their own.  Queries lie in shared memory, scaled.
+template <int DP, int NH>
+struct FloatCore {
+    using Cache = float;
+    using Act = float;
+    static constexpr int kHeads = NH;
+    static constexpr int kTileElems = DP;
+    static constexpr int kBlocksPerSm = NH * DP >= 1024 ? 2 : NH * DP >= 512 ? 3 : 4;
+    static constexpr int J = DP / 32;        // 16-byte loads of a lane's row
+    static constexpr int I = 8 / J;          // positions of a lane at a time
+    static constexpr int kSub = 16 / (4 * I);
+
+    const float *q;   // [NH][DP]
+    float m[NH], l[NH];
+    float acc[NH][J][4];
+    float4 kr[I][J], vr[I][J];
+    int tg, sub;
+
+    __device__ __forceinline__ void begin(const DecodePlan &p, const Act *qrow, int, int nq, float *smem_q) {
+        const int lane = threadIdx.x & 31;
+        tg = lane >> 3;
+        sub = lane & 7;
+        q = smem_q;
+        __syncthreads();  // nobody reads the segment before's queries any more
+        for (int i = threadIdx.x; i < NH * DP; i += kBlock) {
+            const int h = i / DP, e = i - h * DP;
+            smem_q[i] = h < nq && e < p.D ? qrow[static_cast<long long>(h) * p.D + e] * p.scale_log2 : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            m[h] = -INFINITY;
+            l[h] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[h][j][r] = 0.0f;
+        }
+    }
+
+    __device__ __forceinline__ void load(const DecodePlan &p, float4 (&to)[I][J], const void *base, const Step &s, int part) {
+        const float *x = static_cast<const float *>(base) + s.off;
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            const int row = part * 4 * I + 4 * i + tg;
+            const bool in = row >= s.lo && row < s.hi;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int e = 32 * j + 4 * sub;
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (in && e < p.D) w = stream16(x + row * p.D + e);
+                to[i][j] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+            }
+        }
+    }
+
+    __device__ __forceinline__ void step(const DecodePlan &p, const void *k, const void *v, const Step &now, const Step &next) {
+#pragma unroll
+        for (int part = 0; part < kSub; ++part) {
+            const Step &then = part + 1 < kSub ? now : next;
+            const int then_part = part + 1 < kSub ? part + 1 : 0;
+            float s[I][NH];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+#pragma unroll
+                for (int i = 0; i < I; ++i) s[i][h] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const float4 x = *reinterpret_cast<const float4 *>(q + h * DP + 32 * j + 4 * sub);
+#pragma unroll
+                    for (int i = 0; i < I; ++i)
+                        s[i][h] = fmaf(x.x, kr[i][j].x, fmaf(x.y, kr[i][j].y, fmaf(x.z, kr[i][j].z, fmaf(x.w, kr[i][j].w, s[i][h]))));
+                }
+            }
+            load(p, kr, k, then, then_part);
+            float w[I][NH];
+            bool rise = false;
+            float top[NH];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                top[h] = m[h];
+#pragma unroll
+                for (int i = 0; i < I; ++i) {
+                    float x = s[i][h];
+                    x += __shfl_xor_sync(0xffffffffu, x, 1);
+                    x += __shfl_xor_sync(0xffffffffu, x, 2);
+                    x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    const int row = part * 4 * I + 4 * i + tg;
+                    s[i][h] = row >= now.lo && row < now.hi ? x : -INFINITY;
+                    top[h] = fmaxf(top[h], s[i][h]);
+                }
+                rise |= top[h] > m[h];
+            }
+            if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    const float f = top[h] == -INFINITY ? 1.0f : exp2_fast(m[h] - top[h]);
+                    m[h] = top[h];
+                    l[h] *= f;
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[h][j][r] *= f;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                const float top_of = m[h] == -INFINITY ? 0.0f : m[h];
+#pragma unroll
+                for (int i = 0; i < I; ++i) {
+                    w[i][h] = exp2_fast(s[i][h] - top_of);
+                    l[h] += w[i][h];
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        acc[h][j][0] = fmaf(w[i][h], vr[i][j].x, acc[h][j][0]);
+                        acc[h][j][1] = fmaf(w[i][h], vr[i][j].y, acc[h][j][1]);
+                        acc[h][j][2] = fmaf(w[i][h], vr[i][j].z, acc[h][j][2]);
+                        acc[h][j][3] = fmaf(w[i][h], vr[i][j].w, acc[h][j][3]);
+                    }
+                }
+            }
+            load(p, vr, v, then, then_part);
+        }
+    }
+    __device__ __forceinline__ void first(const DecodePlan &p, const void *k, const void *v, const Step &now) {
+        load(p, kr, k, now, 0);
+        load(p, vr, v, now, 0);
+    }
+
+    __device__ __forceinline__ void finish(const DecodePlan &p, float *out, float *top, float *sum) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            float now = m[h];
+            now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 8));
+            now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 16));
+            const float f = m[h] == -INFINITY ? 0.0f : exp2_fast(m[h] - now);
+            float x = l[h] * f;
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            if ((threadIdx.x & 31) == 0) {
+                top[h] = now;
+                sum[h] = x;
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                float r[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    r[k] = acc[h][j][k] * f;
+                    r[k] += __shfl_xor_sync(0xffffffffu, r[k], 8);
+                    r[k] += __shfl_xor_sync(0xffffffffu, r[k], 16);
+                }
+                if (tg == 0) *reinterpret_cast<float4 *>(out + h * DP + 32 * j + 4 * sub) = make_float4(r[0], r[1], r[2], r[3]);
+            }
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// the blocks' stretches
+// ---------------------------------------------------------------------------
+// Where a row's positions lie, and how many units a key head of it has (at
+// least one, so that every row has an output).
+struct Row {
+    int first, last, t0, units;
+};
+__device__ __forceinline__ Row row_at(const DecodePlan &p, int r, bool *bad) {
+    Row x;
+    const int pos = p.at.positions[r];
+    const int seq = p.at.sequences ? p.at.sequences[r] : r;
+    // a position in the table's columns: pos / page_size < table_cols
+    const bool ok = pos < 0 || (static_cast<unsigned>(seq) < static_cast<unsigned>(p.at.table_rows) &&
+                                static_cast<int>(p.at.page.div(max(pos, 0))) < p.at.table_cols);
+    if (bad) *bad = !ok;
+    x.last = ok ? pos : -1;
+    x.first = p.window > 0 ? max(0, x.last - p.window + 1) : 0;
+    x.t0 = x.first / kUnit;
+    x.units = x.last < 0 ? 1 : x.last / kUnit - x.t0 + 1;
+    return x;
+}
+
+template <typename Act>
+__device__ __forceinline__ void store8(Act *to, const float *f) {
+    if constexpr (sizeof(Act) == 2)
+        *reinterpret_cast<uint4 *>(to) =
+            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    else {
+        reinterpret_cast<float4 *>(to)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4 *>(to)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+}
+
+// row-head index rh of a row -> shard, key head of the shard, first query
+struct HeadAt {
+    int shard, kv, query;
+};
+__device__ __forceinline__ HeadAt head_at(const DecodePlan &p, int rh) {
+    HeadAt h;
+    uint32_t group, kv;
+    const uint32_t k = p.by_groups.divmod(rh, group);
+    h.shard = p.by_hk.divmod(k, kv);
+    h.kv = kv;
+    h.query = kv * p.per + group * p.nh;
+    return h;
+}
+// queries of a group: the last group of a head may have fewer
+__device__ __forceinline__ int queries_of(const DecodePlan &p, int rh) {
+    uint32_t group;
+    p.by_groups.divmod(rh, group);
+    return min(p.nh, p.per - static_cast<int>(group) * p.nh);
+}
+
+// A group's outputs [nh][D], maxima [nh] and sums [nh], in whole 16 bytes.
+inline __host__ __device__ int part_floats(int nh, int D) { return (nh * (D + 2) + 3) & ~3; }
+
+template <class Core>
+__global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(const __grid_constant__ DecodePlan p) {
+    using Act = typename Core::Act;
+    constexpr int DP = Core::kTileElems, NH = Core::kHeads;
+    extern __shared__ __align__(16) float smem[];
+    float *out = smem;                       // [kWarps][NH][DP]
+    float *top = out + kWarps * NH * DP;     // [kWarps][NH]
+    float *sum = top + kWarps * NH;          // [kWarps][NH]
+    float *q_smem = sum + kWarps * NH;       // fp32: [NH][DP]
+    __shared__ long long scan[kWarps], start_unit;
+    __shared__ int start_row;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    wait_for_stream();
+    let_next_start();
+
+    // units of all rows, and the row that this block's stretch starts in
+    const int each = (p.at.n + kBlock - 1) / kBlock, r0 = min(threadIdx.x * each, p.at.n), r1 = min(r0 + each, p.at.n);
+    long long mine = 0;
+    for (int r = r0; r < r1; ++r) {
+        bool bad;
+        mine += row_at(p, r, &bad).units;
+        if (bad && blockIdx.x == 0) bad_index(p.at);
+    }
+    mine *= p.row_heads;
+    long long before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += x;
+    }
+    if (lane == 31) scan[warp] = before;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    before -= mine;
+    const long long blocks = total < gridDim.x ? total : gridDim.x;
+    const int c = blockIdx.x;
+    if (c >= blocks) {
+        if (!p.by_segment && threadIdx.x == 0) p.joins[c] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    const long long u0 = total * c / blocks, u1 = total * (c + 1) / blocks;
+    if (u0 >= before && u0 < before + mine) {
+        long long u = before;
+        int r = r0;
+        for (;; ++r) {
+            const long long n = static_cast<long long>(row_at(p, r, nullptr).units) * p.row_heads;
+            if (u0 < u + n) break;
+            u += n;
+        }
+        start_row = r;
+        start_unit = u;
+    }
+    __syncthreads();
+
+    Core core;
+    int r = start_row;
+    long long row_begin = start_unit;  // unit of the row's first head
+    Row row = row_at(p, r, nullptr);
+    int rh = static_cast<int>((u0 - row_begin) / row.units);
+    bool listed = false;
+    for (long long u = u0; u < u1;) {
+        const long long seg_begin = row_begin + static_cast<long long>(rh) * row.units, seg_end = seg_begin + row.units;
+        const HeadAt at = head_at(p, rh);
+        const int nq = queries_of(p, rh);
+        Segment s;
+        s.head = at.kv;
+        s.first = row.first;
+        s.last = row.last;
+        s.t0 = row.t0 + static_cast<int>(u - seg_begin);
+        s.t1 = row.t0 + static_cast<int>((seg_end < u1 ? seg_end : u1) - seg_begin);
+        s.pages = p.at.table + static_cast<long long>(p.at.sequences && row.last >= 0 ? p.at.sequences[r] : row.last >= 0 ? r : 0) * p.at.table_cols;
+        const long long q_at = (static_cast<long long>(r) * p.hq + at.query) * p.D;
+        const void *k = p.k[at.shard], *v = p.v[at.shard];
+
+        Step now = step_at(p, s, s.t0, warp);
+        core.begin(p, static_cast<const Act *>(p.q[at.shard]) + q_at, at.shard * p.hk + at.kv, nq, q_smem);
+        core.first(p, k, v, now);
+        Step next = {0, 0, 0};
+        if (s.t0 + 1 < s.t1) next = step_at(p, s, s.t0 + 1, warp);
+        for (int unit = s.t0; unit < s.t1; ++unit) {
+            Step after = {0, 0, 0};
+            if (unit + 2 < s.t1) after = step_at(p, s, unit + 2, warp);
+            if (now.hi) core.step(p, k, v, now, next);
+            else core.first(p, k, v, next);
+            now = next;
+            next = after;
+        }
+        __syncthreads();  // the segment before has been read from shared memory
+        core.finish(p, out + warp * NH * DP, top + warp * NH, sum + warp * NH);
+        __syncthreads();
+
+        const bool whole = u == seg_begin && seg_end <= u1;
+        // slot 0: began in an earlier block; 1: ends in a later one
+        float *part = p.partial + (static_cast<long long>(c) * 2 + (u == seg_begin ? 1 : 0)) * part_floats(p.nh, p.D);
+        const float vscale = p.v_amax ? 1.0f / cache_scale(p.v_amax, at.shard * p.hk + at.kv) : 1.0f;
+        const int chunks = p.D / 8;
+        for (int i = threadIdx.x; i < nq * chunks; i += kBlock) {
+            const int h = i / chunks, e = (i - h * chunks) * 8;
+            float most = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) most = fmaxf(most, top[w * NH + h]);
+            float all = 0.0f, f[8] = {};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float x = top[w * NH + h], by = x == -INFINITY ? 0.0f : exp2_fast(x - most);
+                all = fmaf(sum[w * NH + h], by, all);
+                const float4 *o = reinterpret_cast<const float4 *>(out + (w * NH + h) * DP + e);
+                const float4 a = o[0], b = o[1];
+                f[0] = fmaf(a.x, by, f[0]); f[1] = fmaf(a.y, by, f[1]); f[2] = fmaf(a.z, by, f[2]); f[3] = fmaf(a.w, by, f[3]);
+                f[4] = fmaf(b.x, by, f[4]); f[5] = fmaf(b.y, by, f[5]); f[6] = fmaf(b.z, by, f[6]); f[7] = fmaf(b.w, by, f[7]);
+            }
+            if (whole) {
+                const float by = all == 0.0f ? 0.0f : vscale / all;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = all == 0.0f ? 0.0f : f[j] * by;
+                store8(static_cast<Act *>(p.o[at.shard]) + q_at + static_cast<long long>(h) * p.D + e, f);
+            } else {
+                store8(part + h * p.D + e, f);
+                if (e == 0) {
+                    part[p.nh * p.D + h] = most;
+                    part[p.nh * (p.D + 1) + h] = all;
+                }
+            }
+        }
+        if (u == seg_begin && threadIdx.x == 0) {
+            // the block that holds the segment's last unit
+            const int last = static_cast<int>((seg_end * blocks + total - 1) / total) - 1;
+            if (p.by_segment)
+                p.joins[r * p.row_heads + rh] = make_int4(r, rh, c, last);
+            else if (!whole)
+                p.joins[c] = make_int4(r, rh, c, last);
+        }
+        listed |= u == seg_begin && !whole;
+        u = seg_end < u1 ? seg_end : u1;
+        if (u == seg_end && ++rh == p.row_heads && u < u1) {
+            rh = 0;
+            ++r;
+            row_begin = seg_end;
+            row = row_at(p, r, nullptr);
+        }
+    }
+    if (!p.by_segment && !listed && threadIdx.x == 0) p.joins[c] = make_int4(0, 0, 0, 0);
+}
+
+// Joins the parts of the segments that several blocks read: W warps a query,
+// each a part in turn, 4 elements a lane.
+template <typename Act, int W>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) join_kernel(const __grid_constant__ DecodePlan p) {
+    constexpr int kQueries = W == 1 ? 4 : 1;  // queries of a block
+    __shared__ float tops[W], sums[W];
+    __shared__ __align__(16) float4 outs[W == 1 ? 1 : W][64];
+    wait_for_stream();
+    let_next_start();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.y * kQueries + (W == 1 ? warp : 0);
+    const int4 j = p.joins[blockIdx.x];
+    if (j.z == j.w) return;  // one block has done it all (or there is none)
+    const int nq = queries_of(p, j.y);
+    if (h >= nq) return;
+    const long long stride = part_floats(p.nh, p.D);
+    // the part of block c: its second slot where the segment begins, else the first
+    const float *base = p.partial + static_cast<long long>(j.z) * 2 * stride + stride;
+    const int n = j.w - j.z + 1;
+    auto part = [&](int i) { return i == 0 ? base : base + (2 * i - 1) * stride; };
+    const int e0 = 4 * lane, e1 = 128 + 4 * lane;
+    float most = -INFINITY, all = 0.0f;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+    for (int i = W == 1 ? 0 : warp; i < n; i += W) most = fmaxf(most, part(i)[p.nh * p.D + h]);
+#pragma unroll 4
+    for (int i = W == 1 ? 0 : warp; i < n; i += W) {
+        const float *x = part(i);
+        const float top = x[p.nh * p.D + h], by = top == -INFINITY ? 0.0f : exp2_fast(top - most);
+        all = fmaf(x[p.nh * (p.D + 1) + h], by, all);
+        if (e0 < p.D) {
+            const float4 v = *reinterpret_cast<const float4 *>(x + h * p.D + e0);
+            a.x = fmaf(v.x, by, a.x); a.y = fmaf(v.y, by, a.y); a.z = fmaf(v.z, by, a.z); a.w = fmaf(v.w, by, a.w);
+        }
+        if (e1 < p.D) {
+            const float4 v = *reinterpret_cast<const float4 *>(x + h * p.D + e1);
+            b.x = fmaf(v.x, by, b.x); b.y = fmaf(v.y, by, b.y); b.z = fmaf(v.z, by, b.z); b.w = fmaf(v.w, by, b.w);
+        }
+    }
+    if constexpr (W > 1) {
+        if (lane == 0) {
+            tops[warp] = most;
+            sums[warp] = all;
+        }
+        outs[warp][lane] = a;
+        outs[warp][32 + lane] = b;
+        __syncthreads();
+        if (threadIdx.x >= 64) return;
+        most = -INFINITY;
+        for (int w = 0; w < W; ++w) most = fmaxf(most, tops[w]);
+        all = 0.0f;
+        a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w = 0; w < W; ++w) {
+            const float by = tops[w] == -INFINITY ? 0.0f : exp2_fast(tops[w] - most);
+            all = fmaf(sums[w], by, all);
+            const float4 v = outs[w][threadIdx.x];
+            a.x = fmaf(v.x, by, a.x); a.y = fmaf(v.y, by, a.y); a.z = fmaf(v.z, by, a.z); a.w = fmaf(v.w, by, a.w);
+        }
+    }
+    const HeadAt at = head_at(p, j.y);
+    const float vscale = p.v_amax ? 1.0f / cache_scale(p.v_amax, at.shard * p.hk + at.kv) : 1.0f;
+    const float by = all == 0.0f ? 0.0f : vscale / all;
+    Act *o = static_cast<Act *>(p.o[at.shard]) + (static_cast<long long>(j.x) * p.hq + at.query + h) * p.D;
+    auto put = [&](int e, const float4 &v) {
+        if (e >= p.D) return;
+        const float4 r = all == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(v.x * by, v.y * by, v.z * by, v.w * by);
+        if constexpr (sizeof(Act) == 2)
+            *reinterpret_cast<uint2 *>(o + e) = make_uint2(pack_bf16x2(r.x, r.y), pack_bf16x2(r.z, r.w));
+        else
+            *reinterpret_cast<float4 *>(o + e) = r;
+    };
+    if constexpr (W == 1) {
+        put(e0, a);
+        put(e1, b);
+    } else {
+        put(4 * threadIdx.x, a);
+    }
+}
+
+// Launches the kernel of a core: as many blocks as are resident (or as there
+// is room for in the workspace).
+template <class Core>
+tp_status launch_core(DecodePlan &p, int *grid, cudaStream_t st) {
+    constexpr int kSmem = sizeof(float) * (kWarps * Core::kHeads * (Core::kTileElems + 2) +
+                                           (sizeof(typename Core::Act) == 4 ? Core::kHeads * Core::kTileElems : 0));
+    static int per_sm[64] = {};  // by device
+    static std::mutex mu;
+    int dev = 0, resident;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_check(e, "cudaGetDevice");
+    if (dev < 0 || dev >= 64) return set_error(TP_ERR_UNSUPPORTED, "device ordinal %d above 63", dev);
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!per_sm[dev]) {
+            e = cudaFuncSetAttribute(decode_kernel<Core>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            if (e == cudaSuccess)
+                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm[dev], decode_kernel<Core>, kBlock, kSmem);
+            if (e != cudaSuccess) return cuda_check(e, "paged_decode");
+            if (per_sm[dev] < 1) return set_error(TP_ERR_CUDA, "paged_decode: no block fits an SM");
+        }
+        resident = per_sm[dev] * num_sms();
+    }
+    *grid = resident < kMostBlocks ? resident : kMostBlocks;
+    const long long segments = static_cast<long long>(p.at.n) * p.row_heads;
+    p.by_segment = segments <= *grid;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(*grid);
+    cfg.blockDim = dim3(kBlock);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_on() ? 1 : 0;
+    launch_begin("paged_decode", st);
+    e = cudaLaunchKernelEx(&cfg, decode_kernel<Core>, p);
+    launch_end("paged_decode", st);
+    return cuda_check(e, "paged_decode");
+}
+
+// by the padded width (64, 128, 256) and the queries of a group
+tp_status launch_decode_bf16(DecodePlan &p, int *grid, cudaStream_t st);
+tp_status launch_decode_fp8(DecodePlan &p, int *grid, cudaStream_t st);
+tp_status launch_decode_f32(DecodePlan &p, int *grid, cudaStream_t st);
+
+}  // namespace attn
+}  // namespace tpmlp

@@ -1,0 +1,648 @@
+// Rotary positions of the QKV shards, in training (tp_rotary_*) and on the way
+// into a paged key-value cache (tp_paged_append).
+//
+// One kernel serves both: it reads the QKV tensor once, 16 bytes a load, turns
+// the pairs of the queries and keys in fp32 and writes them once, to where the
+// mode says (the same columns; or the query tensor and the cache's slots).  It
+// is bound by HBM.  A block takes a few tokens: their cosines and sines, which
+// all heads share, are computed once, by one thread a pair, while the first
+// loads are on their way, and kept in shared memory; a table in memory would
+// cost as many bytes as a head.  An item is two chunks of a head: with pairs
+// (i, i + dim/2) a chunk and its partner, else neighbours.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdio>
+#include <mutex>
+#include <new>
+#include <type_traits>
+
+#include "attention.cuh"
+
+#define TRY(x)                        \
+    do {                              \
+        tp_status _s = (x);           \
+        if (_s != TP_OK) return _s;   \
+    } while (0)
+
+namespace tpmlp {
+namespace attn {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 4;  // tokens of a block
+
+enum Mode : int { ROTATE = 0, APPEND = 1, APPEND8 = 2 };
+
+struct QkvPlan {
+    const void *x[kMaxShards];
+    void *y[kMaxShards];                      // ROTATE: like x; APPEND: Q
+    void *k[kMaxShards], *v[kMaxShards];      // APPEND: the cache
+    Pages at;                                 // ROTATE: positions (or null), n and no table
+    const float *k_amax, *v_amax;             // APPEND8
+    Divisor batch;                            // ROTATE: position of token m without positions: m / B
+    int hq, hk, per, grouped, columns;        // columns: heads of a row, hq + 2 hk
+    int D, half, interleaved;                 // half: pairs of a head
+    int pair_items;                           // items of a head whose chunks are partners
+    int in_place;
+    int tokens;                               // of a block
+    int block_items;                          // tokens * T * slots * items
+    Divisor by_items, by_slots, by_shards, by_group;
+    float sign;                               // -1: the transposed rotation
+    Turns turns;
+};
+
+template <typename E, int VE>
+struct Chunk {  // VE elements as they are stored
+    static constexpr int kBytes = VE * sizeof(E);
+    using Word = typename std::conditional<kBytes == 16, uint4,
+                 typename std::conditional<kBytes == 8, uint2,
+                 typename std::conditional<kBytes == 4, uint32_t, uint16_t>::type>::type>::type;
+    Word w;
+    __device__ __forceinline__ void load(const E *p) { w = *reinterpret_cast<const Word *>(p); }
+    __device__ __forceinline__ void store(E *p) const { *reinterpret_cast<Word *>(p) = w; }
+    __device__ __forceinline__ void unpack(float *f) const {
+        const E *e = reinterpret_cast<const E *>(&w);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) f[i] = static_cast<float>(e[i]);
+    }
+    __device__ __forceinline__ void pack(const float *f) {
+        E *e = reinterpret_cast<E *>(&w);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) e[i] = static_cast<E>(f[i]);
+    }
+};
+
+template <int VE>
+__device__ __forceinline__ void store_codes(uint8_t *p, const float *f, float scale) {
+    uint8_t c[VE];
+#pragma unroll
+    for (int i = 0; i < VE; ++i) c[i] = __nv_cvt_float_to_fp8(f[i] * scale, __NV_SATFINITE, __NV_E4M3);
+    if constexpr (VE == 8)
+        *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(c);
+    else if constexpr (VE == 4)
+        *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(c);
+    else
+        *p = c[0];
+}
+
+enum Kind : int { QUERY = 0, KEY = 1, VALUE = 2 };
+
+// Where a thread's item is.
+struct Item {
+    int token;        // of the block; -1: none
+    int shard, kind, head, column, a, b;  // a, b: the chunks' first elements (b = -1: none)
+};
+
+template <int VE>
+__device__ __forceinline__ Item item_at(const QkvPlan &p, int i) {
+    Item it;
+    if (i >= p.block_items) {
+        it.token = -1;
+        return it;
+    }
+    uint32_t item, slot, shard;
+    const uint32_t rest = p.by_items.divmod(i, item), row = p.by_slots.divmod(rest, slot);
+    it.token = p.by_shards.divmod(row, shard);
+    it.shard = shard;
+    if (p.grouped) {
+        uint32_t r;
+        const int j = p.by_group.divmod(slot, r);  // a group: its queries, the key and, out of place, the value
+        it.column = j * (p.per + 2) + r;
+        it.kind = static_cast<int>(r) < p.per ? QUERY : static_cast<int>(r) == p.per ? KEY : VALUE;
+        it.head = it.kind == QUERY ? j * p.per + r : j;
+    } else {
+        it.column = slot;
+        const int s = slot;
+        it.kind = s < p.hq ? QUERY : s < p.hq + p.hk ? KEY : VALUE;
+        it.head = it.kind == QUERY ? s : it.kind == KEY ? s - p.hq : s - p.hq - p.hk;
+    }
+    const int n = item;
+    if (n < p.pair_items) {
+        it.a = n * VE;
+        it.b = it.a + p.half;
+    } else {
+        it.a = 2 * (p.pair_items * VE + (n - p.pair_items) * VE);
+        it.b = it.a + VE < (p.in_place ? 2 * p.half : p.D) ? it.a + VE : -1;
+    }
+    return it;
+}
+
+// the pairs (first + 2i, first + 2i + 1) of a chunk, those that turn
+template <int VE>
+__device__ __forceinline__ void turn_neighbours(float *f, int first, int half, const float *cs, const float *sn) {
+#pragma unroll
+    for (int e = 0; e + 1 < VE; e += 2) {
+        const int i = (first + e) / 2;
+        if (i < half) {
+            const float c = cs[i], s = sn[i], x = f[e], y = f[e + 1];
+            f[e] = x * c - y * s;
+            f[e + 1] = y * c + x * s;
+        }
+    }
+}
+
+template <typename E, int VE, int MODE>
+__global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ QkvPlan p) {
+    constexpr int U = 2;  // items of a thread in flight
+    // cosines and sines by token
+    __shared__ __align__(16) float cs[kMaxTokens][kMaxPairs], sn[kMaxTokens][kMaxPairs];
+    __shared__ long long slot_of[kMaxTokens];  // APPEND: the slot's row of the cache, of key head 0
+    __shared__ int active[kMaxTokens];
+    wait_for_stream();
+    let_next_start();
+    const int token0 = blockIdx.x * p.tokens;
+    const int step = kThreads * gridDim.y;
+    int i = blockIdx.y * kThreads + threadIdx.x;
+    Item it[U];
+    Chunk<E, VE> a[U], b[U];
+    const long long width = static_cast<long long>(p.columns) * p.D;
+    auto load = [&](int from) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            it[u] = item_at<VE>(p, from + u * step);
+            if (it[u].token < 0 || token0 + it[u].token >= p.at.n) {
+                it[u].token = -1;
+                continue;
+            }
+            const E *x = static_cast<const E *>(p.x[it[u].shard]) + (token0 + it[u].token) * width + it[u].column * p.D;
+            a[u].load(x + it[u].a);
+            if (it[u].b >= 0) b[u].load(x + it[u].b);
+        }
+    };
+    load(i);
+    const int pairs = p.half > 0 ? p.half : 1;
+    for (int k = threadIdx.x; k < p.tokens * pairs; k += kThreads) {
+        const int t = k / pairs, pair = k - t * pairs, m = token0 + t;
+        if (m >= p.at.n) break;
+        const int pos = MODE == ROTATE && !p.at.positions ? static_cast<int>(p.batch.div(m)) : p.at.positions[m];
+        if (pair == 0) {
+            int ok = pos >= 0;
+            if (MODE != ROTATE && ok) {
+                const int seq = p.at.sequences ? p.at.sequences[m] : m;
+                uint32_t off;
+                const int col = p.at.page.divmod(pos, off);
+                ok = static_cast<unsigned>(seq) < static_cast<unsigned>(p.at.table_rows) && col < p.at.table_cols;
+                const int page = ok ? p.at.table[static_cast<long long>(seq) * p.at.table_cols + col] : -1;
+                ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.at.pages);
+                if (!ok && blockIdx.y == 0) bad_index(p.at);
+                // the heads of a page lie page_size rows apart
+                slot_of[t] = static_cast<long long>(page) * p.hk * p.at.page_size + off;
+            }
+            active[t] = ok;
+        }
+        const float2 r = turn(p.turns, pair, pos);
+        cs[t][pair] = r.x;
+        sn[t][pair] = r.y * p.sign;
+    }
+    __syncthreads();
+    while (true) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (it[u].token < 0) continue;
+            const int t = it[u].token;
+            if (!active[t] && (MODE != ROTATE || p.in_place)) continue;  // padding stays as it was
+            const bool two = it[u].b >= 0;
+            float fa[VE], fb[VE];
+            a[u].unpack(fa);
+            if (two) b[u].unpack(fb);
+            if (it[u].kind != VALUE && active[t]) {
+                if (p.interleaved) {
+                    turn_neighbours<VE>(fa, it[u].a, p.half, cs[t], sn[t]);
+                    a[u].pack(fa);
+                    if (two) {
+                        turn_neighbours<VE>(fb, it[u].b, p.half, cs[t], sn[t]);
+                        b[u].pack(fb);
+                    }
+                } else if (it[u].a < p.half) {
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        const float c = cs[t][it[u].a + e], s = sn[t][it[u].a + e], x = fa[e], y = fb[e];
+                        fa[e] = x * c - y * s;
+                        fb[e] = y * c + x * s;
+                    }
+                    a[u].pack(fa);
+                    b[u].pack(fb);
+                }
+            }
+            const long long m = token0 + t;
+            if (MODE == ROTATE) {
+                E *y = static_cast<E *>(p.y[it[u].shard]) + m * width + it[u].column * p.D;
+                a[u].store(y + it[u].a);
+                if (two) b[u].store(y + it[u].b);
+            } else if (it[u].kind == QUERY) {
+                E *y = static_cast<E *>(p.y[it[u].shard]) + (m * p.hq + it[u].head) * p.D;
+                a[u].store(y + it[u].a);
+                if (two) b[u].store(y + it[u].b);
+            } else {
+                void *to = it[u].kind == KEY ? p.k[it[u].shard] : p.v[it[u].shard];
+                const long long row = (slot_of[t] + static_cast<long long>(it[u].head) * p.at.page_size) * p.D;
+                if (MODE == APPEND) {
+                    E *y = static_cast<E *>(to) + row;
+                    a[u].store(y + it[u].a);
+                    if (two) b[u].store(y + it[u].b);
+                } else {
+                    // fp32 goes to the code in one rounding
+                    const float scale = cache_scale(it[u].kind == KEY ? p.k_amax : p.v_amax, it[u].shard * p.hk + it[u].head);
+                    uint8_t *y = static_cast<uint8_t *>(to) + row;
+                    store_codes<VE>(y + it[u].a, fa, scale);
+                    if (two) store_codes<VE>(y + it[u].b, fb, scale);
+                }
+            }
+        }
+        i += U * step;
+        if (i >= p.block_items) break;
+        load(i);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+tp_status rope_validate(const tp_rope_desc *r, int head_dim) {
+    if (r->dim < 0 || r->dim > head_dim || r->dim % 2)
+        return set_error(TP_ERR_ARG, "rope.dim=%d is not an even number up to head_dim=%d", r->dim, head_dim);
+    if (r->pairs != TP_ROPE_HALVES && r->pairs != TP_ROPE_INTERLEAVED) return set_error(TP_ERR_ARG, "bad rope.pairs %d", r->pairs);
+    if (r->scaling < TP_ROPE_NONE || r->scaling > TP_ROPE_PARTS) return set_error(TP_ERR_ARG, "bad rope.scaling %d", r->scaling);
+    if (!(r->base >= 1.0) || !std::isfinite(r->base)) return set_error(TP_ERR_ARG, "rope.base must be finite and at least 1");
+    if (!(r->factor >= 1.0) || !std::isfinite(r->factor)) return set_error(TP_ERR_ARG, "rope.factor must be finite and at least 1");
+    if (r->scaling == TP_ROPE_NONE && r->factor != 1.0) return set_error(TP_ERR_ARG, "rope.factor belongs to a scaling");
+    if (!(r->attention_factor >= 0.0) || r->attention_factor > 1e6)
+        return set_error(TP_ERR_ARG, "rope.attention_factor must be 0 (the default) or positive, up to 1e6");
+    if (r->scaling == TP_ROPE_PARTS) {
+        if (!(r->original > 0.0) || !std::isfinite(r->original)) return set_error(TP_ERR_ARG, "rope.original must be positive and finite");
+        if (!(r->slow >= 0.0) || !(r->fast > r->slow) || !std::isfinite(r->fast))
+            return set_error(TP_ERR_ARG, "rope.fast must be finite and above rope.slow >= 0");
+    }
+    return TP_OK;
+}
+
+void rope_turns(const tp_rope_desc &r, Turns *t) {
+    const double two_pi = 6.283185307179586476925;
+    double base = r.base;
+    if (r.scaling == TP_ROPE_NTK && r.dim > 2) base *= std::pow(r.factor, static_cast<double>(r.dim) / (r.dim - 2));
+    for (int i = 0; i < r.dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / r.dim);
+        if (r.scaling == TP_ROPE_LINEAR) f /= r.factor;
+        if (r.scaling == TP_ROPE_PARTS) {
+            double keep = (r.original * f / two_pi - r.slow) / (r.fast - r.slow);
+            keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+            f = f * keep + f / r.factor * (1.0 - keep);
+        }
+        t->per_position[i] = static_cast<uint64_t>(f / two_pi * 0x1p64);
+    }
+    for (int i = r.dim / 2; i < kMaxPairs; ++i) t->per_position[i] = 0;
+    double a = r.attention_factor;
+    if (a == 0.0) a = r.scaling == TP_ROPE_PARTS ? 0.1 * std::log(r.factor) + 1.0 : 1.0;
+    t->a = static_cast<float>(a);
+}
+
+// Fills in what follows from the sizes and launches.  `T` shards, `in_place`:
+// only what is rotated is touched.
+static tp_status launch_qkv(QkvPlan &p, int T, int elem, int mode, const char *name, cudaStream_t st) {
+    // 16 bytes a chunk; with pairs (i, i + half) both chunks have to begin on one, else 4 elements
+    // a chunk, or one where the half is odd or twice an odd number
+    int ve = 16 / elem;
+    if (!p.interleaved)
+        while (ve > 1 && p.half % ve) ve = ve > 4 ? 4 : 1;
+    if (p.interleaved && p.half == 0) p.interleaved = 0;
+    const int chunks = p.D / ve, partners = p.interleaved ? 0 : p.half / ve;
+    p.pair_items = partners;
+    const int rotated = p.interleaved ? ((2 * p.half + ve - 1) / ve + 1) / 2 : partners;
+    const int items = p.in_place ? rotated : partners + (chunks - 2 * partners + 1) / 2;
+    const int group = p.per + (p.in_place ? 1 : 2);
+    const int slots = p.grouped ? p.hk * group : p.hq + p.hk * (p.in_place ? 1 : 2);
+    if (items == 0) return TP_OK;  // nothing turns, in place
+    // several tokens a block where there are enough blocks all the same
+    p.tokens = 1;
+    while (p.tokens < kMaxTokens && p.at.n / (2 * p.tokens) >= 8 * num_sms()) p.tokens *= 2;
+    p.block_items = p.tokens * T * slots * items;
+    p.by_items = Divisor(items);
+    p.by_slots = Divisor(slots);
+    p.by_shards = Divisor(T);
+    p.by_group = Divisor(group);
+    const int blocks = (p.at.n + p.tokens - 1) / p.tokens;
+    // few tokens: a token's items over several blocks
+    int across = 1;
+    while (blocks * across < 2 * num_sms() && across * 2 * kThreads < p.block_items) across *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, across);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_on() ? 1 : 0;
+    void (*k)(QkvPlan) = nullptr;
+    using B = __nv_bfloat16;
+    if (elem == 4)
+        k = mode == ROTATE ? (ve == 4 ? qkv_kernel<float, 4, ROTATE> : qkv_kernel<float, 1, ROTATE>)
+                           : (ve == 4 ? qkv_kernel<float, 4, APPEND> : qkv_kernel<float, 1, APPEND>);
+    else if (mode == ROTATE)
+        k = ve == 8 ? qkv_kernel<B, 8, ROTATE> : ve == 4 ? qkv_kernel<B, 4, ROTATE> : qkv_kernel<B, 1, ROTATE>;
+    else if (mode == APPEND)
+        k = ve == 8 ? qkv_kernel<B, 8, APPEND> : ve == 4 ? qkv_kernel<B, 4, APPEND> : qkv_kernel<B, 1, APPEND>;
+    else
+        k = ve == 8 ? qkv_kernel<B, 8, APPEND8> : ve == 4 ? qkv_kernel<B, 4, APPEND8> : qkv_kernel<B, 1, APPEND8>;
+    launch_begin(name, st);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k, p);
+    launch_end(name, st);
+    return cuda_check(e, name);
+}
+
+}  // namespace attn
+}  // namespace tpmlp
+
+using namespace tpmlp;
+using attn::kMaxRows;
+
+struct tp_rotary {
+    tp_rotary_desc d;
+    int M;
+    attn::Turns turns;
+};
+
+struct tp_paged {
+    tp_paged_desc d;
+    int word;        // of g_tp_index
+    unsigned owner;  // what is written there
+    float scale;
+    attn::Turns turns;
+};
+
+static tp_status at_pointer(const void *p, const char *name, int i, int n, unsigned align) {
+    char at[16] = "";
+    if (n > 1) snprintf(at, sizeof(at), "[%d]", i);
+    if (!p) return set_error(TP_ERR_ARG, "%s%s is NULL", name, at);
+    if (reinterpret_cast<uintptr_t>(p) & (align - 1))
+        return set_error(TP_ERR_ARG, "%s%s is not %u-byte aligned", name, at, align);
+    return TP_OK;
+}
+
+// copies an array of n pointers into a plan after checking them
+template <typename P>
+static tp_status at_array(P *const *in, int n, const char *name, P **out) {
+    if (!in) return set_error(TP_ERR_ARG, "%s: pointer array is NULL", name);
+    for (int i = 0; i < n; ++i) {
+        TRY(at_pointer(in[i], name, i, n, 16));
+        out[i] = in[i];
+    }
+    return TP_OK;
+}
+
+static tp_status at_heads(int T, int heads, int kv_heads, int head_dim, int grouped) {
+    if (grouped != 0 && grouped != 1) return set_error(TP_ERR_ARG, "grouped must be 0 or 1");
+    if (T < 1 || T > TP_MAX_SHARDS) return set_error(TP_ERR_SHAPE, "T=%d outside 1..%d", T, TP_MAX_SHARDS);
+    if (kv_heads < 1 || kv_heads % T) return set_error(TP_ERR_SHAPE, "kv_heads=%d must be a positive multiple of T=%d", kv_heads, T);
+    if (heads < 1 || heads > 4096 || heads % kv_heads)
+        return set_error(TP_ERR_SHAPE, "heads=%d must be a multiple of kv_heads=%d, up to 4096", heads, kv_heads);
+    if (head_dim < 8 || head_dim % 8) return set_error(TP_ERR_SHAPE, "head_dim=%d must be a positive multiple of 8", head_dim);
+    if (head_dim > attn::kMaxHeadDim)
+        return set_error(TP_ERR_UNSUPPORTED, "head_dim=%d above the kernels' %d", head_dim, attn::kMaxHeadDim);
+    return TP_OK;
+}
+
+static tp_status rotate(tp_rotary *h, const void *const *in, const char *in_name, const int32_t *positions,
+                        void *const *out, const char *out_name, bool back, void *stream) {
+    if (!h) return set_error(TP_ERR_ARG, "handle is NULL");
+    const tp_rotary_desc &d = h->d;
+    if (h->M == 0) return TP_OK;
+    attn::QkvPlan p = {};
+    TRY(at_array(in, d.T, in_name, p.x));
+    TRY(at_array(out, d.T, out_name, p.y));
+    int same = 0;
+    for (int i = 0; i < d.T; ++i) same += p.x[i] == p.y[i];
+    if (same != 0 && same != d.T)
+        return set_error(TP_ERR_ARG, "%s and %s: either every shard in place or none", in_name, out_name);
+    if (positions) TRY(at_pointer(positions, "positions", 0, 1, 4));
+    p.at.positions = positions;
+    p.at.n = h->M;
+    p.batch = attn::Divisor(d.B);
+    p.hq = d.heads / d.T;
+    p.hk = d.kv_heads / d.T;
+    p.per = d.heads / d.kv_heads;
+    p.grouped = d.grouped;
+    p.columns = p.hq + 2 * p.hk;
+    p.D = d.head_dim;
+    p.half = d.rope.dim / 2;
+    p.interleaved = d.rope.pairs == TP_ROPE_INTERLEAVED;
+    p.in_place = same != 0;
+    p.sign = back ? -1.0f : 1.0f;
+    p.turns = h->turns;
+    return attn::launch_qkv(p, d.T, d.dtype == TP_DT_F32 ? 4 : 2, attn::ROTATE, back ? "rotary_bwd" : "rotary_fwd",
+                            static_cast<cudaStream_t>(stream));
+}
+
+static tp_status at_rows(const tp_paged_desc &d, const int32_t *positions, const int32_t *sequences, int n,
+                         const int32_t *table, int table_rows, int table_cols, const float *k_amax, const float *v_amax,
+                         attn::Pages &at) {
+    if (n > kMaxRows) return set_error(TP_ERR_SHAPE, "n=%d above %d rows", n, kMaxRows);
+    if (table_rows < 1 || table_rows > kMaxRows || table_cols < 1 || table_cols > kMaxRows)
+        return set_error(TP_ERR_SHAPE, "table of %d x %d outside 1..%d", table_rows, table_cols, kMaxRows);
+    TRY(at_pointer(positions, "positions", 0, 1, 4));
+    if (sequences)
+        TRY(at_pointer(sequences, "sequences", 0, 1, 4));
+    else if (n > table_rows)
+        return set_error(TP_ERR_SHAPE, "n=%d rows without sequences, but a table of %d", n, table_rows);
+    TRY(at_pointer(table, "table", 0, 1, 4));
+    if (d.dtype == TP_DT_FP8) {
+        TRY(at_pointer(k_amax, "k_amax", 0, 1, 4));
+        TRY(at_pointer(v_amax, "v_amax", 0, 1, 4));
+    }
+    at.positions = positions;
+    at.sequences = sequences;
+    at.table = table;
+    at.n = n;
+    at.table_rows = table_rows;
+    at.table_cols = table_cols;
+    at.pages = d.pages;
+    at.page_size = d.page_size;
+    at.page = attn::Divisor(d.page_size);
+    return TP_OK;
+}
+
+// Index words: a kernel that meets an index out of range writes its handle's
+// number, which no other handle of the process has, so that what a handle
+// before left in the word says nothing.
+constexpr int kIndexWords = 1024;
+__device__ unsigned g_tp_index[kIndexWords];
+static std::mutex g_index_mu;
+static bool g_index_used[kIndexWords];
+static unsigned g_index_owners = 0;
+
+static tp_status index_word(int word, unsigned **at) {
+    static unsigned *base[64] = {};
+    int dev = 0;
+    TRY(cuda_check(cudaGetDevice(&dev), "cudaGetDevice"));
+    if (dev < 0 || dev >= 64) return set_error(TP_ERR_UNSUPPORTED, "device ordinal %d above 63", dev);
+    std::lock_guard<std::mutex> lock(g_index_mu);
+    if (!base[dev]) {
+        void *p = nullptr;
+        TRY(cuda_check(cudaGetSymbolAddress(&p, g_tp_index), "cudaGetSymbolAddress(index)"));
+        base[dev] = static_cast<unsigned *>(p);
+    }
+    *at = base[dev] + word;
+    return TP_OK;
+}
+
+extern "C" {
+
+tp_status tp_rotary_create(const tp_rotary_desc *desc, tp_rotary **out) {
+    if (!out) return set_error(TP_ERR_ARG, "out is NULL");
+    *out = nullptr;
+    if (!desc) return set_error(TP_ERR_ARG, "descriptor is NULL");
+    if (desc->dtype != TP_DT_F32 && desc->dtype != TP_DT_BF16)
+        return set_error(TP_ERR_ARG, "bad dtype %d (the rotation takes TP_DT_F32 and TP_DT_BF16)", desc->dtype);
+    TRY(at_heads(desc->T, desc->heads, desc->kv_heads, desc->head_dim, desc->grouped));
+    TRY(attn::rope_validate(&desc->rope, desc->head_dim));
+    if (desc->S < 0 || desc->B < 0) return set_error(TP_ERR_SHAPE, "negative S or B");
+    const long long M = static_cast<long long>(desc->S) * desc->B;
+    if (M > (1ll << 24)) return set_error(TP_ERR_SHAPE, "M = S*B = %lld exceeds 2^24 tokens", M);
+    tp_rotary *h = new (std::nothrow) tp_rotary;
+    if (!h) return set_error(TP_ERR_ARG, "out of host memory");
+    h->d = *desc;
+    h->M = static_cast<int>(M);
+    attn::rope_turns(desc->rope, &h->turns);
+    *out = h;
+    return TP_OK;
+}
+
+void tp_rotary_destroy(tp_rotary *h) { delete h; }
+
+tp_status tp_rotary_fwd(tp_rotary *h, const void *const *X, const int32_t *positions, void *const *Y, void *stream) {
+    return rotate(h, X, "X", positions, Y, "Y", false, stream);
+}
+
+tp_status tp_rotary_bwd(tp_rotary *h, const void *const *dY, const int32_t *positions, void *const *dX, void *stream) {
+    return rotate(h, dY, "dY", positions, dX, "dX", true, stream);
+}
+
+tp_status tp_paged_create(const tp_paged_desc *desc, tp_paged **out) {
+    if (!out) return set_error(TP_ERR_ARG, "out is NULL");
+    *out = nullptr;
+    if (!desc) return set_error(TP_ERR_ARG, "descriptor is NULL");
+    if (desc->dtype != TP_DT_F32 && desc->dtype != TP_DT_BF16 && desc->dtype != TP_DT_FP8)
+        return set_error(TP_ERR_ARG, "bad dtype %d", desc->dtype);
+    TRY(at_heads(desc->T, desc->heads, desc->kv_heads, desc->head_dim, desc->grouped));
+    if (desc->dtype == TP_DT_FP8 && desc->head_dim % 16)
+        return set_error(TP_ERR_SHAPE, "head_dim=%d must be a multiple of 16 with TP_DT_FP8", desc->head_dim);
+    TRY(attn::rope_validate(&desc->rope, desc->head_dim));
+    if (desc->page_size < 16 || desc->page_size % 16 || desc->page_size > kMaxRows)
+        return set_error(TP_ERR_SHAPE, "page_size=%d must be a multiple of 16 in 16..%d", desc->page_size, kMaxRows);
+    if (desc->pages < 1) return set_error(TP_ERR_SHAPE, "pages=%d must be positive", desc->pages);
+    if (desc->window < 0) return set_error(TP_ERR_ARG, "window=%d is negative", desc->window);
+    if (!std::isfinite(desc->scale)) return set_error(TP_ERR_ARG, "scale must be finite");
+    tp_paged *h = new (std::nothrow) tp_paged;
+    if (!h) return set_error(TP_ERR_ARG, "out of host memory");
+    h->d = *desc;
+    h->scale = desc->scale != 0.0f ? desc->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(desc->head_dim)));
+    attn::rope_turns(desc->rope, &h->turns);
+    {
+        std::lock_guard<std::mutex> lock(g_index_mu);
+        h->word = 0;
+        while (h->word < kIndexWords && g_index_used[h->word]) ++h->word;
+        if (h->word < kIndexWords) {
+            g_index_used[h->word] = true;
+            if (++g_index_owners == 0) ++g_index_owners;
+            h->owner = g_index_owners;
+        }
+    }
+    if (h->word == kIndexWords) {
+        delete h;
+        return set_error(TP_ERR_UNSUPPORTED, "more than %d live handles (each owns an index word)", kIndexWords);
+    }
+    *out = h;
+    return TP_OK;
+}
+
+void tp_paged_destroy(tp_paged *h) {
+    if (!h) return;
+    {
+        std::lock_guard<std::mutex> lock(g_index_mu);
+        g_index_used[h->word] = false;
+    }
+    delete h;
+}
+
+size_t tp_paged_workspace_bytes(const tp_paged *h) { return h ? attn::decode_workspace_bytes(h->d) : 0; }
+
+tp_status tp_paged_sync_status(tp_paged *h, void *stream) {
+    if (!h) return set_error(TP_ERR_ARG, "handle is NULL");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    unsigned *at = nullptr, v = 0;
+    TRY(index_word(h->word, &at));
+    TRY(cuda_check(cudaStreamSynchronize(st), "cudaStreamSynchronize"));
+    TRY(cuda_check(cudaMemcpy(&v, at, sizeof(v), cudaMemcpyDeviceToHost), "cudaMemcpy(index)"));
+    if (v != h->owner) return TP_OK;
+    v = 0;
+    TRY(cuda_check(cudaMemcpy(at, &v, sizeof(v), cudaMemcpyHostToDevice), "cudaMemcpy(index)"));
+    return set_error(TP_ERR_INDEX, "a page, sequence or position was out of range");
+}
+
+tp_status tp_paged_append(tp_paged *h, const void *const *X, const int32_t *positions, const int32_t *sequences, int n,
+                          const int32_t *table, int table_rows, int table_cols, const float *k_amax,
+                          const float *v_amax, void *const *Q, void *const *K, void *const *V, void *stream) {
+    if (!h) return set_error(TP_ERR_ARG, "handle is NULL");
+    const tp_paged_desc &d = h->d;
+    if (n < 0) return set_error(TP_ERR_SHAPE, "n=%d is negative", n);
+    if (n == 0) return TP_OK;
+    attn::QkvPlan p = {};
+    TRY(at_rows(d, positions, sequences, n, table, table_rows, table_cols, k_amax, v_amax, p.at));
+    TRY(at_array(X, d.T, "X", p.x));
+    TRY(at_array(Q, d.T, "Q", p.y));
+    TRY(at_array(K, d.T, "K", p.k));
+    TRY(at_array(V, d.T, "V", p.v));
+    TRY(index_word(h->word, &p.at.index_word));
+    p.at.owner = h->owner;
+    p.k_amax = k_amax;
+    p.v_amax = v_amax;
+    p.hq = d.heads / d.T;
+    p.hk = d.kv_heads / d.T;
+    p.per = d.heads / d.kv_heads;
+    p.grouped = d.grouped;
+    p.columns = p.hq + 2 * p.hk;
+    p.D = d.head_dim;
+    p.half = d.rope.dim / 2;
+    p.interleaved = d.rope.pairs == TP_ROPE_INTERLEAVED;
+    p.sign = 1.0f;
+    p.turns = h->turns;
+    return attn::launch_qkv(p, d.T, d.dtype == TP_DT_F32 ? 4 : 2, d.dtype == TP_DT_FP8 ? attn::APPEND8 : attn::APPEND,
+                            "paged_append", static_cast<cudaStream_t>(stream));
+}
+
+tp_status tp_paged_decode(tp_paged *h, const void *const *Q, const int32_t *positions, const int32_t *sequences, int n,
+                          const int32_t *table, int table_rows, int table_cols, const float *k_amax,
+                          const float *v_amax, const void *const *K, const void *const *V, void *const *O,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+    if (!h) return set_error(TP_ERR_ARG, "handle is NULL");
+    const tp_paged_desc &d = h->d;
+    if (n < 0) return set_error(TP_ERR_SHAPE, "n=%d is negative", n);
+    if (n == 0) return TP_OK;
+    attn::DecodePlan p = {};
+    TRY(at_rows(d, positions, sequences, n, table, table_rows, table_cols, k_amax, v_amax, p.at));
+    TRY(at_array(Q, d.T, "Q", p.q));
+    TRY(at_array(K, d.T, "K", p.k));
+    TRY(at_array(V, d.T, "V", p.v));
+    TRY(at_array(O, d.T, "O", p.o));
+    const size_t need = tp_paged_workspace_bytes(h);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return set_error(TP_ERR_ARG, "workspace is NULL or not 256-byte aligned");
+    if (workspace_bytes < need)
+        return set_error(TP_ERR_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    TRY(index_word(h->word, &p.at.index_word));
+    p.at.owner = h->owner;
+    p.k_amax = k_amax;
+    p.v_amax = v_amax;
+    p.hq = d.heads / d.T;
+    p.hk = d.kv_heads / d.T;
+    p.per = d.heads / d.kv_heads;
+    p.D = d.head_dim;
+    p.window = d.window;
+    p.scale_log2 = static_cast<float>(static_cast<double>(h->scale) * 1.4426950408889634);
+    p.row_heads = d.kv_heads;  // times the groups
+    return attn::launch_decode(p, d.dtype, workspace, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
