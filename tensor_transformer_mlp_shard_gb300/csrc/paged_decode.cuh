@@ -40,12 +40,6 @@ constexpr int kMostBlocks = 1024;       // of a launch, and so of the workspace
 
 enum CacheKind : int { CACHE_BF16 = 0, CACHE_FP8 = 1, CACHE_F32 = 2 };
 
-// 16 positions of a row for one warp
-struct Step {
-    long long off;  // elements from the cache's start to its first position
-    int lo, hi;     // the positions [lo, hi) of the 16 that the row sees
-};
-
 // A segment of a row: what the warps need to walk it.
 struct Segment {
     const int32_t *pages;       // the row's table
@@ -53,37 +47,47 @@ struct Segment {
     int first, last;            // positions that the row sees
 };
 
-__device__ __forceinline__ Step step_at(const DecodePlan &p, const Segment &s, int unit, int warp) {
-    Step r;
+// A step: the 16 positions of a unit that are the warp's.  They lie in one page;
+// `block` is their place in the cache in blocks of 16 rows of head_dim, kNone
+// where the row sees none of them or the page is out of range.
+constexpr uint32_t kNone = 0xffffffffu;
+struct Step {
+    uint32_t block;
+    int lo, hi;  // the positions [lo, hi) of the 16 that the row sees
+};
+
+__device__ __forceinline__ uint32_t block_at(const DecodePlan &p, const Segment &s, int unit, int warp) {
     const int base = unit * kUnit + warp * 16;
-    r.lo = max(s.first - base, 0);
-    r.hi = min(s.last + 1 - base, 16);
-    r.off = 0;
-    if (r.hi <= r.lo) {
-        r.lo = r.hi = 0;
-        return r;
-    }
+    if (unit >= s.t1 || base > s.last || base + 15 < s.first) return kNone;
     uint32_t in_page;
     const int page = s.pages[p.at.page.divmod(base, in_page)];
     if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.at.pages)) {
         bad_index(p.at);
-        r.lo = r.hi = 0;
-        return r;
+        return kNone;
     }
-    r.off = ((static_cast<long long>(page) * p.hk + s.head) * p.at.page_size + in_page) * p.D;
-    return r;
+    return (static_cast<uint32_t>(page) * p.hk + s.head) * (p.at.page_size / 16) + in_page / 16;
+}
+
+__device__ __forceinline__ Step step_at(const Segment &s, int unit, int warp, uint32_t block) {
+    const int base = unit * kUnit + warp * 16;
+    return {block, max(s.first - base, 0), min(s.last + 1 - base, 16)};
 }
 
 // keys and values pass through once: they need no place in L1
-__device__ __forceinline__ uint4 stream16(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
+__device__ __forceinline__ void stream(uint32_t (&w)[4], const void *p) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
 }
-__device__ __forceinline__ uint2 stream8(const void *p) {
-    uint2 v;
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
+__device__ __forceinline__ void stream(uint32_t (&w)[2], const void *p) {
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+}
+// where `in`; else the registers keep what they hold
+__device__ __forceinline__ void stream_if(uint32_t (&w)[4], const void *p, bool in) {
+    asm volatile("{\n .reg .pred q;\n setp.ne.s32 q, %5, 0;\n @q ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+                 : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]) : "l"(p), "r"(static_cast<int>(in)));
+}
+__device__ __forceinline__ void stream_if(uint32_t (&w)[2], const void *p, bool in) {
+    asm volatile("{\n .reg .pred q;\n setp.ne.s32 q, %3, 0;\n @q ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n}"
+                 : "+r"(w[0]), "+r"(w[1]) : "l"(p), "r"(static_cast<int>(in)));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -103,19 +107,19 @@ template <int KIND>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     if constexpr (KIND == CACHE_BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// two E4M3 codes (the low and high byte) as two fp16 numbers, exactly
-__device__ __forceinline__ uint32_t half2_of_codes(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// four E4M3 codes as two pairs of fp16 numbers, exactly (NaN stays NaN)
+__device__ __forceinline__ void halves_of_codes(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(lo), "=r"(hi) : "r"(codes));
 }
 
 // ---------------------------------------------------------------------------
@@ -215,51 +219,61 @@ struct TensorCore {
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) acc[b][i][n][r] = 0.0f;
+        zero(kr);
+        zero(vr);
     }
 
+    // The step's keys, or values, to registers.  Elements behind the head's width
+    // are zero from the beginning and stay so.  Rows that are not seen are
+    // not read: a key's score is masked, and a value is zero, for whatever
+    // the registers held times a weight of zero need not be.
     __device__ __forceinline__ void load_k(const DecodePlan &p, const void *base, const Step &s) {
-        const Cache *k = static_cast<const Cache *>(base) + s.off;
+        const Cache *k = static_cast<const Cache *>(base) + static_cast<uint64_t>(s.block) * (16 * p.D) + (g * p.D + KE * t);
+        const bool whole = s.lo == 0 && s.hi == 16;
+        if (whole && p.D == DP) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = g + 8 * r;
-            const bool in = row >= s.lo && row < s.hi;
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                const int e = 4 * KE * c + KE * t;
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (in && e < p.D) w = stream16(k + row * p.D + e);
-                kr[r][c][0] = w.x;
-                kr[r][c][1] = w.y;
-                kr[r][c][2] = w.z;
-                kr[r][c][3] = w.w;
+                for (int c = 0; c < KC; ++c) stream(kr[r][c], k + 8 * r * DP + 4 * KE * c);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = g + 8 * r;
+#pragma unroll
+                for (int c = 0; c < KC; ++c)
+                    stream_if(kr[r][c], k + 8 * r * p.D + 4 * KE * c, row >= s.lo && row < s.hi && 4 * KE * c + KE * t < p.D);
             }
         }
     }
 
     __device__ __forceinline__ void load_v(const DecodePlan &p, const void *base, const Step &s) {
-        const Cache *v = static_cast<const Cache *>(base) + s.off;
+        const Cache *v = static_cast<const Cache *>(base) + static_cast<uint64_t>(s.block) * (16 * p.D) + (2 * t * p.D + VD * g);
+        const bool whole = s.lo == 0 && s.hi == 16;
+        if (whole && p.D == DP) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 2 * t + (r & 1) + 8 * (r >> 1);
-            const bool in = row >= s.lo && row < s.hi;
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int b = 0; b < VB; ++b) {
-                const int e = 8 * VD * b + VD * g;
-                if constexpr (VW == 4) {
-                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                    if (in && e < p.D) w = stream16(v + row * p.D + e);
-                    vr[r][b][0] = w.x;
-                    vr[r][b][1] = w.y;
-                    vr[r][b][2] = w.z;
-                    vr[r][b][3] = w.w;
-                } else {
-                    uint2 w = make_uint2(0u, 0u);
-                    if (in && e < p.D) w = stream8(v + row * p.D + e);
-                    vr[r][b][0] = w.x;
-                    vr[r][b][1] = w.y;
-                }
+                for (int b = 0; b < VB; ++b) stream(vr[r][b], v + ((r & 1) + 8 * (r >> 1)) * DP + 8 * VD * b);
+        } else {
+            if (!whole) zero(vr);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 2 * t + (r & 1) + 8 * (r >> 1);
+#pragma unroll
+                for (int b = 0; b < VB; ++b)
+                    stream_if(vr[r][b], v + ((r & 1) + 8 * (r >> 1)) * p.D + 8 * VD * b,
+                              row >= s.lo && row < s.hi && 8 * VD * b + VD * g < p.D);
             }
         }
+    }
+    template <int A, int B, int C>
+    __device__ __forceinline__ static void zero(uint32_t (&x)[A][B][C]) {
+#pragma unroll
+        for (int a = 0; a < A; ++a)
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+#pragma unroll
+                for (int c = 0; c < C; ++c) x[a][b][c] = 0u;
     }
 
     float s[NT][4];
@@ -279,9 +293,9 @@ struct TensorCore {
                 if constexpr (k8) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const uint32_t x0 = kr[0][c][2 * w + u], x1 = kr[1][c][2 * w + u];
-                        const uint32_t a0 = half2_of_codes(x0 & 0xffffu), a2 = half2_of_codes(x0 >> 16);
-                        const uint32_t a1 = half2_of_codes(x1 & 0xffffu), a3 = half2_of_codes(x1 >> 16);
+                        uint32_t a0, a1, a2, a3;
+                        halves_of_codes(kr[0][c][2 * w + u], a0, a2);
+                        halves_of_codes(kr[1][c][2 * w + u], a1, a3);
                         const int k = 4 * c + 2 * w + u;
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma16816<KIND>(c2[n][u], a0, a1, a2, a3, q[n][k][0], q[n][k][1]);
@@ -294,12 +308,19 @@ struct TensorCore {
                 }
             }
         }
-        const bool in0 = g >= st.lo && g < st.hi, in1 = g + 8 >= st.lo && g + 8 < st.hi;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                s[n][r] = (r < 2 ? in0 : in1) ? (c2[n][0][r] + c2[n][1][r]) * sc[n][r & 1] : -INFINITY;
+            for (int r = 0; r < 4; ++r) s[n][r] = (c2[n][0][r] + c2[n][1][r]) * sc[n][r & 1];
+        if (st.lo > 0 || st.hi < 16) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = r < 2 ? g : g + 8;
+                    if (row < st.lo || row >= st.hi) s[n][r] = -INFINITY;
+                }
+        }
     }
 
     uint32_t ph[NT][2], pl[NT][2];  // weights as the sum of two 16-bit numbers
@@ -379,10 +400,8 @@ struct TensorCore {
                     if constexpr (k8) {
                         const uint32_t x = __byte_perm(vr[0][b][w], vr[1][b][w], u ? 0x7362 : 0x5140);
                         const uint32_t y = __byte_perm(vr[2][b][w], vr[3][b][w], u ? 0x7362 : 0x5140);
-                        a0 = half2_of_codes(x & 0xffffu);
-                        a1 = half2_of_codes(x >> 16);
-                        a2 = half2_of_codes(y & 0xffffu);
-                        a3 = half2_of_codes(y >> 16);
+                        halves_of_codes(x, a0, a1);
+                        halves_of_codes(y, a2, a3);
                     } else {
                         a0 = __byte_perm(vr[0][b][w], vr[1][b][w], 0x5410);
                         a1 = __byte_perm(vr[0][b][w], vr[1][b][w], 0x7632);
@@ -400,17 +419,15 @@ struct TensorCore {
         }
     }
 
-    // the whole step: next is loaded as registers become free
+    // the whole step; the next one's loads start as registers become free
     __device__ __forceinline__ void step(const DecodePlan &p, const void *k, const void *v, const Step &now, const Step &next) {
-        scores(now);
-        load_k(p, k, next);
-        softmax();
-        values();
-        load_v(p, v, next);
-    }
-    __device__ __forceinline__ void first(const DecodePlan &p, const void *k, const void *v, const Step &now) {
-        load_k(p, k, now);
-        load_v(p, v, now);
+        if (now.block != kNone) scores(now);
+        if (next.block != kNone) load_k(p, k, next);
+        if (now.block != kNone) {
+            softmax();
+            values();
+        }
+        if (next.block != kNone) load_v(p, v, next);
     }
 
     // the warp's state to shared memory: out [kHeads][DP], top and sum [kHeads]
@@ -449,7 +466,7 @@ struct FloatCore {
     using Act = float;
     static constexpr int kHeads = NH;
     static constexpr int kTileElems = DP;
-    static constexpr int kBlocksPerSm = NH * DP >= 1024 ? 2 : NH * DP >= 512 ? 3 : 4;
+    static constexpr int kBlocksPerSm = NH * DP >= 1024 ? 2 : NH * DP > 64 ? 3 : 4;
     static constexpr int J = DP / 32;        // 16-byte loads of a lane's row
     static constexpr int I = 8 / J;          // positions of a lane at a time
     static constexpr int kSub = 16 / (4 * I);
@@ -457,7 +474,7 @@ struct FloatCore {
     const float *q;   // [NH][DP]
     float m[NH], l[NH];
     float acc[NH][J][4];
-    float4 kr[I][J], vr[I][J];
+    uint32_t kr[I][J][4], vr[I][J][4];
     int tg, sub;
 
     __device__ __forceinline__ void begin(const DecodePlan &p, const Act *qrow, int, int nq, float *smem_q) {
@@ -480,95 +497,111 @@ struct FloatCore {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[h][j][r] = 0.0f;
         }
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) kr[i][j][r] = vr[i][j][r] = 0u;
     }
 
-    __device__ __forceinline__ void load(const DecodePlan &p, float4 (&to)[I][J], const void *base, const Step &s, int part) {
-        const float *x = static_cast<const float *>(base) + s.off;
+    // the lane's positions of one part of a step; rows that are not seen are zero
+    __device__ __forceinline__ void load(const DecodePlan &p, uint32_t (&to)[I][J][4], const void *base, const Step &s, int part) {
+        const float *x = static_cast<const float *>(base) + static_cast<uint64_t>(s.block) * (16 * p.D) + ((part * 4 * I + tg) * p.D + 4 * sub);
+        const bool whole = s.lo == 0 && s.hi == 16;
+        if (whole && p.D == DP) {
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            const int row = part * 4 * I + 4 * i + tg;
-            const bool in = row >= s.lo && row < s.hi;
+            for (int i = 0; i < I; ++i)
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int e = 32 * j + 4 * sub;
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (in && e < p.D) w = stream16(x + row * p.D + e);
-                to[i][j] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+                for (int j = 0; j < J; ++j) stream(to[i][j], x + 4 * i * DP + 32 * j);
+        } else {
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                const int row = part * 4 * I + 4 * i + tg;
+                const bool in = row >= s.lo && row < s.hi;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    if (!whole) to[i][j][0] = to[i][j][1] = to[i][j][2] = to[i][j][3] = 0u;
+                    stream_if(to[i][j], x + 4 * i * p.D + 32 * j, in && 32 * j + 4 * sub < p.D);
+                }
             }
         }
+    }
+    __device__ __forceinline__ static float f(uint32_t x) { return __uint_as_float(x); }
+
+    __device__ __forceinline__ void part_of(const DecodePlan &p, const void *k, const void *v, const Step &now, int part,
+                                            const Step &then, int then_part) {
+        float s[I][NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+#pragma unroll
+            for (int i = 0; i < I; ++i) s[i][h] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float4 x = *reinterpret_cast<const float4 *>(q + h * DP + 32 * j + 4 * sub);
+#pragma unroll
+                for (int i = 0; i < I; ++i)
+                    s[i][h] = fmaf(x.x, f(kr[i][j][0]), fmaf(x.y, f(kr[i][j][1]), fmaf(x.z, f(kr[i][j][2]), fmaf(x.w, f(kr[i][j][3]), s[i][h]))));
+            }
+        }
+        if (then.block != kNone) load(p, kr, k, then, then_part);
+        bool rise = false;
+        float top[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            top[h] = m[h];
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                float x = s[i][h];
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                const int row = part * 4 * I + 4 * i + tg;
+                s[i][h] = row >= now.lo && row < now.hi ? x : -INFINITY;
+                top[h] = fmaxf(top[h], s[i][h]);
+            }
+            rise |= top[h] > m[h];
+        }
+        if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                const float by = top[h] == -INFINITY ? 1.0f : exp2_fast(m[h] - top[h]);
+                m[h] = top[h];
+                l[h] *= by;
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[h][j][r] *= by;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            const float top_of = m[h] == -INFINITY ? 0.0f : m[h];
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                const float w = exp2_fast(s[i][h] - top_of);
+                l[h] += w;
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[h][j][r] = fmaf(w, f(vr[i][j][r]), acc[h][j][r]);
+            }
+        }
+        if (then.block != kNone) load(p, vr, v, then, then_part);
     }
 
     __device__ __forceinline__ void step(const DecodePlan &p, const void *k, const void *v, const Step &now, const Step &next) {
-#pragma unroll
-        for (int part = 0; part < kSub; ++part) {
-            const Step &then = part + 1 < kSub ? now : next;
-            const int then_part = part + 1 < kSub ? part + 1 : 0;
-            float s[I][NH];
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-#pragma unroll
-                for (int i = 0; i < I; ++i) s[i][h] = 0.0f;
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const float4 x = *reinterpret_cast<const float4 *>(q + h * DP + 32 * j + 4 * sub);
-#pragma unroll
-                    for (int i = 0; i < I; ++i)
-                        s[i][h] = fmaf(x.x, kr[i][j].x, fmaf(x.y, kr[i][j].y, fmaf(x.z, kr[i][j].z, fmaf(x.w, kr[i][j].w, s[i][h]))));
-                }
+        if (now.block != kNone) {
+#pragma unroll 1
+            for (int part = 0; part < kSub; ++part) {
+                const bool end = part + 1 == kSub;
+                const Step then = {end ? next.block : now.block, end ? next.lo : now.lo, end ? next.hi : now.hi};
+                part_of(p, k, v, now, part, then, end ? 0 : part + 1);
             }
-            load(p, kr, k, then, then_part);
-            float w[I][NH];
-            bool rise = false;
-            float top[NH];
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                top[h] = m[h];
-#pragma unroll
-                for (int i = 0; i < I; ++i) {
-                    float x = s[i][h];
-                    x += __shfl_xor_sync(0xffffffffu, x, 1);
-                    x += __shfl_xor_sync(0xffffffffu, x, 2);
-                    x += __shfl_xor_sync(0xffffffffu, x, 4);
-                    const int row = part * 4 * I + 4 * i + tg;
-                    s[i][h] = row >= now.lo && row < now.hi ? x : -INFINITY;
-                    top[h] = fmaxf(top[h], s[i][h]);
-                }
-                rise |= top[h] > m[h];
-            }
-            if (__any_sync(0xffffffffu, rise)) {
-#pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    const float f = top[h] == -INFINITY ? 1.0f : exp2_fast(m[h] - top[h]);
-                    m[h] = top[h];
-                    l[h] *= f;
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[h][j][r] *= f;
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                const float top_of = m[h] == -INFINITY ? 0.0f : m[h];
-#pragma unroll
-                for (int i = 0; i < I; ++i) {
-                    w[i][h] = exp2_fast(s[i][h] - top_of);
-                    l[h] += w[i][h];
-#pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        acc[h][j][0] = fmaf(w[i][h], vr[i][j].x, acc[h][j][0]);
-                        acc[h][j][1] = fmaf(w[i][h], vr[i][j].y, acc[h][j][1]);
-                        acc[h][j][2] = fmaf(w[i][h], vr[i][j].z, acc[h][j][2]);
-                        acc[h][j][3] = fmaf(w[i][h], vr[i][j].w, acc[h][j][3]);
-                    }
-                }
-            }
-            load(p, vr, v, then, then_part);
+        } else if (next.block != kNone) {
+            load(p, kr, k, next, 0);
+            load(p, vr, v, next, 0);
         }
-    }
-    __device__ __forceinline__ void first(const DecodePlan &p, const void *k, const void *v, const Step &now) {
-        load(p, kr, k, now, 0);
-        load(p, vr, v, now, 0);
     }
 
     __device__ __forceinline__ void finish(const DecodePlan &p, float *out, float *top, float *sum) {
@@ -735,18 +768,23 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
         const long long q_at = (static_cast<long long>(r) * p.hq + at.query) * p.D;
         const void *k = p.k[at.shard], *v = p.v[at.shard];
 
-        Step now = step_at(p, s, s.t0, warp);
+        // lane i looks up the i-th of the next 32 steps
+        uint32_t blocks_now = block_at(p, s, s.t0 + lane, warp);
         core.begin(p, static_cast<const Act *>(p.q[at.shard]) + q_at, at.shard * p.hk + at.kv, nq, q_smem);
-        core.first(p, k, v, now);
-        Step next = {0, 0, 0};
-        if (s.t0 + 1 < s.t1) next = step_at(p, s, s.t0 + 1, warp);
-        for (int unit = s.t0; unit < s.t1; ++unit) {
-            Step after = {0, 0, 0};
-            if (unit + 2 < s.t1) after = step_at(p, s, unit + 2, warp);
-            if (now.hi) core.step(p, k, v, now, next);
-            else core.first(p, k, v, next);
-            now = next;
-            next = after;
+        Step now = {kNone, 0, 0};
+        Step next = step_at(s, s.t0, warp, __shfl_sync(0xffffffffu, blocks_now, 0));
+        core.step(p, k, v, now, next);
+        for (int from = s.t0; from < s.t1; from += 32) {
+            const uint32_t blocks_next = block_at(p, s, from + 32 + lane, warp);
+            const int n = min(32, s.t1 - from);
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                now = next;
+                const uint32_t then = i == 31 ? __shfl_sync(0xffffffffu, blocks_next, 0) : __shfl_sync(0xffffffffu, blocks_now, i + 1);
+                next = step_at(s, from + i + 1, warp, then);
+                core.step(p, k, v, now, next);
+            }
+            blocks_now = blocks_next;
         }
         __syncthreads();  // the segment before has been read from shared memory
         core.finish(p, out + warp * NH * DP, top + warp * NH, sum + warp * NH);
