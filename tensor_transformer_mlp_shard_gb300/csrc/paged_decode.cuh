@@ -1,24 +1,25 @@
 // Decode attention over a paged cache: o = sum_j w_j v_j, w = softmax(scale q.k_j).
 //
 // Bound by HBM: each key and value is read once, for all queries of its head.
-// The positions of all rows and key heads are one list of units (64 positions),
-// in order of row, head, position; every block takes an equal stretch of it
+// The positions of all rows and key heads are one list of units (64 positions;
+// fp32: 32), in order of row, head, position; every block takes an equal stretch of it
 // (as many blocks as are resident), so that uneven lengths load the SMs
 // evenly and one long row is split over all of them.  Within a stretch, the
 // units of one (row, head) are a segment; a segment that ends in another block
 // leaves its running maximum, sum and unnormalised output in the workspace, at
 // most two a block, and a second kernel joins them, in the blocks' order.
 //
-// Four warps share a unit, 16 positions each, and keep softmax states of their
-// own until the segment ends: no barrier in the loop.  Keys and values go from
-// memory into registers, already in the layout of the matrix instructions: the
-// contraction over the head's elements may take them in any order, so a
-// lane loads 16 contiguous bytes and its elements stand for whichever the
+// Four warps share a unit, 16 (fp32: 8) positions each, and keep softmax states
+// of their own until the segment ends: no barrier in the loop.  Each warp has a
+// ring of stages in shared memory that it fills by asynchronous 16-byte copies,
+// several steps ahead; what bounds the kernel is how many bytes are on their
+// way.  From there its lanes read fragments of the matrix instructions as they
+// lie: the contraction over the head's elements may take them in any order, so a
+// lane reads 16 contiguous bytes and its elements stand for whichever the
 // instruction calls k; the same holds for the rows of V^T, which only name
 // output elements.  Positions are the 16 rows of K and of P^T, the queries of a
 // head its 8 columns, so that one query wastes tensor work (which is cheap
-// here) and no bytes.  While a step's scores and products are computed, the
-// next step's keys are on their way, and then its values.
+// here) and no bytes.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -35,7 +36,6 @@ namespace attn {
 
 constexpr int kWarps = 4;
 constexpr int kBlock = 32 * kWarps;
-constexpr int kUnit = 16 * kWarps;      // positions
 constexpr int kMostBlocks = 1024;       // of a launch, and so of the workspace
 
 enum CacheKind : int { CACHE_BF16 = 0, CACHE_FP8 = 1, CACHE_F32 = 2 };
@@ -47,47 +47,85 @@ struct Segment {
     int first, last;            // positions that the row sees
 };
 
-// A step: the 16 positions of a unit that are the warp's.  They lie in one page;
-// `block` is their place in the cache in blocks of 16 rows of head_dim, kNone
+// A step: the R positions of a unit that are the warp's.  They lie in one page;
+// `block` is their place in the cache in blocks of R rows of head_dim, kNone
 // where the row sees none of them or the page is out of range.
 constexpr uint32_t kNone = 0xffffffffu;
-struct Step {
-    uint32_t block;
-    int lo, hi;  // the positions [lo, hi) of the 16 that the row sees
-};
-
+template <int R>
 __device__ __forceinline__ uint32_t block_at(const DecodePlan &p, const Segment &s, int unit, int warp) {
-    const int base = unit * kUnit + warp * 16;
-    if (unit >= s.t1 || base > s.last || base + 15 < s.first) return kNone;
+    const int base = unit * (R * kWarps) + warp * R;
+    if (unit >= s.t1 || base > s.last || base + R - 1 < s.first) return kNone;
     uint32_t in_page;
     const int page = s.pages[p.at.page.divmod(base, in_page)];
     if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.at.pages)) {
         bad_index(p.at);
         return kNone;
     }
-    return (static_cast<uint32_t>(page) * p.hk + s.head) * (p.at.page_size / 16) + in_page / 16;
+    return (static_cast<uint32_t>(page) * p.hk + s.head) * (p.at.page_size / R) + in_page / R;
 }
 
-__device__ __forceinline__ Step step_at(const Segment &s, int unit, int warp, uint32_t block) {
-    const int base = unit * kUnit + warp * 16;
-    return {block, max(s.first - base, 0), min(s.last + 1 - base, 16)};
+// the positions [lo, hi) of a step that the row sees
+struct Seen {
+    int lo, hi;
+};
+template <int R>
+__device__ __forceinline__ Seen seen_at(const Segment &s, int unit, int warp) {
+    const int base = unit * (R * kWarps) + warp * R;
+    return {max(s.first - base, 0), min(s.last + 1 - base, R)};
 }
 
-// keys and values pass through once: they need no place in L1
-__device__ __forceinline__ void stream(uint32_t (&w)[4], const void *p) {
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+// `bytes` of 16 bytes, 0 or 16, the rest zero
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void stream(uint32_t (&w)[2], const void *p) {
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// where `in`; else the registers keep what they hold
-__device__ __forceinline__ void stream_if(uint32_t (&w)[4], const void *p, bool in) {
-    asm volatile("{\n .reg .pred q;\n setp.ne.s32 q, %5, 0;\n @q ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
-                 : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]) : "l"(p), "r"(static_cast<int>(in)));
+
+// R rows of ROW bytes (the padded width) in a stage, the eight 16-byte pieces of
+// a 128-byte line exchanged so that the fragments' reads meet no bank twice:
+// keys are read four pieces of 8 rows at a time, values one or two pieces of
+// every other row.
+template <int ROW>
+__device__ __forceinline__ int swizzle_k(int row) {
+    return ROW % 128 ? 0 : (row & 1) << 6;
 }
-__device__ __forceinline__ void stream_if(uint32_t (&w)[2], const void *p, bool in) {
-    asm volatile("{\n .reg .pred q;\n setp.ne.s32 q, %3, 0;\n @q ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n}"
-                 : "+r"(w[0]), "+r"(w[1]) : "l"(p), "r"(static_cast<int>(in)));
+__device__ __forceinline__ int swizzle_v(int row) { return ((row >> 1) & 3) << 5; }
+
+// A step's keys and values on their way to a stage: eight lanes (four, for rows of
+// 64 bytes) copy a line of a row.  What lies behind the head's width, and rows
+// that are not seen, become zero.
+template <class Core, bool WHOLE>
+__device__ __forceinline__ void fetch_rows(int row_bytes, const char *k, const char *v, const Seen &s, uint32_t to) {
+    constexpr int R = Core::kRows, ROW = Core::kRowBytes, kLine = ROW < 128 ? ROW : 128, kLanes = kLine / 16, kStep = 32 / kLanes;
+    const int lane = threadIdx.x & 31, row0 = lane / kLanes, at = 16 * (lane % kLanes);
+    const int off = row0 * row_bytes + at;
+    const uint32_t lane_to = to + row0 * ROW + at;
+#pragma unroll
+    for (int i = 0; i < R / kStep; ++i) {
+        const int row = i * kStep + row0;
+        const bool in = WHOLE || (row >= s.lo && row < s.hi);
+#pragma unroll
+        for (int j = 0; j < ROW / kLine; ++j) {
+            const int bytes = in && j * kLine + at < row_bytes ? 16 : 0;
+            const uint32_t d = lane_to + i * kStep * ROW + j * kLine;
+            const int from = off + i * kStep * row_bytes + j * kLine;
+            copy16(d ^ Core::swizzle_keys(row), k + from, bytes);
+            copy16((d + R * ROW) ^ Core::swizzle_values(row), v + from, bytes);
+        }
+    }
+}
+template <class Core>
+__device__ __forceinline__ void fetch(const DecodePlan &p, const void *k, const void *v, const Seen &s, uint32_t block, uint32_t to) {
+    const int row_bytes = p.D * static_cast<int>(sizeof(typename Core::Cache));
+    const uint64_t at = static_cast<uint64_t>(block) * (Core::kRows * row_bytes);
+    const char *kp = static_cast<const char *>(k) + at, *vp = static_cast<const char *>(v) + at;
+    if (s.lo == 0 && s.hi == Core::kRows)
+        fetch_rows<Core, true>(row_bytes, kp, vp, s, to);
+    else
+        fetch_rows<Core, false>(row_bytes, kp, vp, s, to);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -135,7 +173,12 @@ struct TensorCore {
     using Act = __nv_bfloat16;
     static constexpr int kHeads = 8 * NT;
     static constexpr int kTileElems = DP;
-    static constexpr int kBlocksPerSm = DP == 256 ? 2 : DP == 128 ? (NT == 2 ? 2 : k8 ? 4 : 3) : NT == 2 ? 4 : 5;
+    static constexpr int kRows = 16, kRowBytes = DP * static_cast<int>(sizeof(Cache));
+    // about 192 KB of stages an SM
+    static constexpr int kStages = kRowBytes == 64 ? 6 : kRowBytes == 128 ? 4 : 3;
+    static constexpr int kBlocksPerSm = kRowBytes == 64 ? 4 : kRowBytes == 128 ? 3 : kRowBytes == 256 ? 2 : 1;
+    __device__ __forceinline__ static int swizzle_keys(int row) { return swizzle_k<kRowBytes>(row); }
+    __device__ __forceinline__ static int swizzle_values(int row) { return swizzle_v(row); }
     static constexpr int KC = k8 ? DP / 64 : DP / 32;       // 16-byte loads of a lane's key row
     static constexpr int KE = k8 ? 16 : 8;                  // elements of one
     static constexpr int VD = k8 && DP % 128 == 0 ? 16 : 8; // elements of a lane's value load
@@ -146,8 +189,6 @@ struct TensorCore {
     float sc[NT][2];     // score to log2 units, of the lane's queries
     float m[NT][2], l[NT][2];
     float acc[VB][VD / 2][NT][4];
-    uint32_t kr[2][KC][4];
-    uint32_t vr[4][VB][VW];
     int g, t;
 
     // the group's nq queries, from the row of its first
@@ -219,66 +260,11 @@ struct TensorCore {
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) acc[b][i][n][r] = 0.0f;
-        zero(kr);
-        zero(vr);
-    }
-
-    // The step's keys, or values, to registers.  Elements behind the head's width
-    // are zero from the beginning and stay so.  Rows that are not seen are
-    // not read: a key's score is masked, and a value is zero, for whatever
-    // the registers held times a weight of zero need not be.
-    __device__ __forceinline__ void load_k(const DecodePlan &p, const void *base, const Step &s) {
-        const Cache *k = static_cast<const Cache *>(base) + static_cast<uint64_t>(s.block) * (16 * p.D) + (g * p.D + KE * t);
-        const bool whole = s.lo == 0 && s.hi == 16;
-        if (whole && p.D == DP) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int c = 0; c < KC; ++c) stream(kr[r][c], k + 8 * r * DP + 4 * KE * c);
-        } else {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = g + 8 * r;
-#pragma unroll
-                for (int c = 0; c < KC; ++c)
-                    stream_if(kr[r][c], k + 8 * r * p.D + 4 * KE * c, row >= s.lo && row < s.hi && 4 * KE * c + KE * t < p.D);
-            }
-        }
-    }
-
-    __device__ __forceinline__ void load_v(const DecodePlan &p, const void *base, const Step &s) {
-        const Cache *v = static_cast<const Cache *>(base) + static_cast<uint64_t>(s.block) * (16 * p.D) + (2 * t * p.D + VD * g);
-        const bool whole = s.lo == 0 && s.hi == 16;
-        if (whole && p.D == DP) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int b = 0; b < VB; ++b) stream(vr[r][b], v + ((r & 1) + 8 * (r >> 1)) * DP + 8 * VD * b);
-        } else {
-            if (!whole) zero(vr);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 2 * t + (r & 1) + 8 * (r >> 1);
-#pragma unroll
-                for (int b = 0; b < VB; ++b)
-                    stream_if(vr[r][b], v + ((r & 1) + 8 * (r >> 1)) * p.D + 8 * VD * b,
-                              row >= s.lo && row < s.hi && 8 * VD * b + VD * g < p.D);
-            }
-        }
-    }
-    template <int A, int B, int C>
-    __device__ __forceinline__ static void zero(uint32_t (&x)[A][B][C]) {
-#pragma unroll
-        for (int a = 0; a < A; ++a)
-#pragma unroll
-            for (int b = 0; b < B; ++b)
-#pragma unroll
-                for (int c = 0; c < C; ++c) x[a][b][c] = 0u;
     }
 
     float s[NT][4];
 
-    __device__ __forceinline__ void scores(const Step &st) {
+    __device__ __forceinline__ void scores(const char *k, const Seen &st) {
         float c2[NT][2][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -288,14 +274,24 @@ struct TensorCore {
                 for (int r = 0; r < 4; ++r) c2[n][x][r] = 0.0f;
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
+            uint32_t kr[2][4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(
+                    k + (((g + 8 * r) * kRowBytes + 64 * c + 16 * t) ^ swizzle_k<kRowBytes>(g)));
+                kr[r][0] = x.x;
+                kr[r][1] = x.y;
+                kr[r][2] = x.z;
+                kr[r][3] = x.w;
+            }
 #pragma unroll
             for (int w = 0; w < 2; ++w) {  // word pairs of the load
                 if constexpr (k8) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         uint32_t a0, a1, a2, a3;
-                        halves_of_codes(kr[0][c][2 * w + u], a0, a2);
-                        halves_of_codes(kr[1][c][2 * w + u], a1, a3);
+                        halves_of_codes(kr[0][2 * w + u], a0, a2);
+                        halves_of_codes(kr[1][2 * w + u], a1, a3);
                         const int k = 4 * c + 2 * w + u;
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma16816<KIND>(c2[n][u], a0, a1, a2, a3, q[n][k][0], q[n][k][1]);
@@ -303,7 +299,7 @@ struct TensorCore {
                 } else {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        mma16816<KIND>(c2[n][w], kr[0][c][2 * w], kr[1][c][2 * w], kr[0][c][2 * w + 1], kr[1][c][2 * w + 1],
+                        mma16816<KIND>(c2[n][w], kr[0][2 * w], kr[1][2 * w], kr[0][2 * w + 1], kr[1][2 * w + 1],
                                        q[n][2 * c + w][0], q[n][2 * c + w][1]);
                 }
             }
@@ -388,9 +384,26 @@ struct TensorCore {
         }
     }
 
-    __device__ __forceinline__ void values() {
+    __device__ __forceinline__ void values(const char *v) {
 #pragma unroll
         for (int b = 0; b < VB; ++b) {
+            uint32_t vr[4][VW];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 2 * t + (r & 1) + 8 * (r >> 1);  // swizzled as row 2t is
+                const char *at = v + ((row * kRowBytes + 32 * VW * b + 4 * VW * g) ^ (t << 5));
+                if constexpr (VW == 4) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(at);
+                    vr[r][0] = x.x;
+                    vr[r][1] = x.y;
+                    vr[r][2] = x.z;
+                    vr[r][3] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(at);
+                    vr[r][0] = x.x;
+                    vr[r][1] = x.y;
+                }
+            }
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
                 // the same element of two neighbouring positions to one register
@@ -398,15 +411,15 @@ struct TensorCore {
                 for (int u = 0; u < (k8 ? 2 : 1); ++u) {
                     uint32_t a0, a1, a2, a3;
                     if constexpr (k8) {
-                        const uint32_t x = __byte_perm(vr[0][b][w], vr[1][b][w], u ? 0x7362 : 0x5140);
-                        const uint32_t y = __byte_perm(vr[2][b][w], vr[3][b][w], u ? 0x7362 : 0x5140);
+                        const uint32_t x = __byte_perm(vr[0][w], vr[1][w], u ? 0x7362 : 0x5140);
+                        const uint32_t y = __byte_perm(vr[2][w], vr[3][w], u ? 0x7362 : 0x5140);
                         halves_of_codes(x, a0, a1);
                         halves_of_codes(y, a2, a3);
                     } else {
-                        a0 = __byte_perm(vr[0][b][w], vr[1][b][w], 0x5410);
-                        a1 = __byte_perm(vr[0][b][w], vr[1][b][w], 0x7632);
-                        a2 = __byte_perm(vr[2][b][w], vr[3][b][w], 0x5410);
-                        a3 = __byte_perm(vr[2][b][w], vr[3][b][w], 0x7632);
+                        a0 = __byte_perm(vr[0][w], vr[1][w], 0x5410);
+                        a1 = __byte_perm(vr[0][w], vr[1][w], 0x7632);
+                        a2 = __byte_perm(vr[2][w], vr[3][w], 0x5410);
+                        a3 = __byte_perm(vr[2][w], vr[3][w], 0x7632);
                     }
                     const int i = k8 ? 2 * w + u : w;
 #pragma unroll
@@ -419,15 +432,11 @@ struct TensorCore {
         }
     }
 
-    // the whole step; the next one's loads start as registers become free
-    __device__ __forceinline__ void step(const DecodePlan &p, const void *k, const void *v, const Step &now, const Step &next) {
-        if (now.block != kNone) scores(now);
-        if (next.block != kNone) load_k(p, k, next);
-        if (now.block != kNone) {
-            softmax();
-            values();
-        }
-        if (next.block != kNone) load_v(p, v, next);
+    // one step, its stage in shared memory
+    __device__ __forceinline__ void step(const DecodePlan &, const char *stage, const Seen &seen) {
+        scores(stage, seen);
+        softmax();
+        values(stage + kRows * kRowBytes);
     }
 
     // the warp's state to shared memory: out [kHeads][DP], top and sum [kHeads]
@@ -466,15 +475,17 @@ struct FloatCore {
     using Act = float;
     static constexpr int kHeads = NH;
     static constexpr int kTileElems = DP;
-    static constexpr int kBlocksPerSm = NH * DP >= 1024 ? 2 : NH * DP > 64 ? 3 : 4;
-    static constexpr int J = DP / 32;        // 16-byte loads of a lane's row
-    static constexpr int I = 8 / J;          // positions of a lane at a time
-    static constexpr int kSub = 16 / (4 * I);
+    static constexpr int kRows = DP <= 64 ? 16 : 8, kRowBytes = DP * 4;
+    static constexpr int kStages = DP == 96 || DP == 192 ? 4 : 3;
+    static constexpr int kBlocksPerSm = DP <= 128 ? 2 : 1;
+    static constexpr int J = DP / 32;        // 16-byte pieces of a row that a lane has
+    static constexpr int I = kRows / 4;      // positions of a lane
+    __device__ __forceinline__ static int swizzle_keys(int) { return 0; }
+    __device__ __forceinline__ static int swizzle_values(int) { return 0; }
 
     const float *q;   // [NH][DP]
     float m[NH], l[NH];
     float acc[NH][J][4];
-    uint32_t kr[I][J][4], vr[I][J][4];
     int tg, sub;
 
     __device__ __forceinline__ void begin(const DecodePlan &p, const Act *qrow, int, int nq, float *smem_q) {
@@ -497,54 +508,28 @@ struct FloatCore {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[h][j][r] = 0.0f;
         }
-#pragma unroll
-        for (int i = 0; i < I; ++i)
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) kr[i][j][r] = vr[i][j][r] = 0u;
     }
 
-    // the lane's positions of one part of a step; rows that are not seen are zero
-    __device__ __forceinline__ void load(const DecodePlan &p, uint32_t (&to)[I][J][4], const void *base, const Step &s, int part) {
-        const float *x = static_cast<const float *>(base) + static_cast<uint64_t>(s.block) * (16 * p.D) + ((part * 4 * I + tg) * p.D + 4 * sub);
-        const bool whole = s.lo == 0 && s.hi == 16;
-        if (whole && p.D == DP) {
-#pragma unroll
-            for (int i = 0; i < I; ++i)
-#pragma unroll
-                for (int j = 0; j < J; ++j) stream(to[i][j], x + 4 * i * DP + 32 * j);
-        } else {
-#pragma unroll
-            for (int i = 0; i < I; ++i) {
-                const int row = part * 4 * I + 4 * i + tg;
-                const bool in = row >= s.lo && row < s.hi;
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    if (!whole) to[i][j][0] = to[i][j][1] = to[i][j][2] = to[i][j][3] = 0u;
-                    stream_if(to[i][j], x + 4 * i * p.D + 32 * j, in && 32 * j + 4 * sub < p.D);
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ static float f(uint32_t x) { return __uint_as_float(x); }
-
-    __device__ __forceinline__ void part_of(const DecodePlan &p, const void *k, const void *v, const Step &now, int part,
-                                            const Step &then, int then_part) {
+    __device__ __forceinline__ void step(const DecodePlan &, const char *stage, const Seen &seen) {
+        const float *k = reinterpret_cast<const float *>(stage) + tg * DP + 4 * sub, *v = k + kRows * DP;
         float s[I][NH];
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
+        for (int h = 0; h < NH; ++h)
 #pragma unroll
             for (int i = 0; i < I; ++i) s[i][h] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const float4 x = *reinterpret_cast<const float4 *>(q + h * DP + 32 * j + 4 * sub);
+        for (int j = 0; j < J; ++j) {
+            float4 x[I];
+#pragma unroll
+            for (int i = 0; i < I; ++i) x[i] = *reinterpret_cast<const float4 *>(k + 4 * i * DP + 32 * j);
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                const float4 y = *reinterpret_cast<const float4 *>(q + h * DP + 32 * j + 4 * sub);
 #pragma unroll
                 for (int i = 0; i < I; ++i)
-                    s[i][h] = fmaf(x.x, f(kr[i][j][0]), fmaf(x.y, f(kr[i][j][1]), fmaf(x.z, f(kr[i][j][2]), fmaf(x.w, f(kr[i][j][3]), s[i][h]))));
+                    s[i][h] = fmaf(y.x, x[i].x, fmaf(y.y, x[i].y, fmaf(y.z, x[i].z, fmaf(y.w, x[i].w, s[i][h]))));
             }
         }
-        if (then.block != kNone) load(p, kr, k, then, then_part);
         bool rise = false;
         float top[NH];
 #pragma unroll
@@ -556,8 +541,8 @@ struct FloatCore {
                 x += __shfl_xor_sync(0xffffffffu, x, 1);
                 x += __shfl_xor_sync(0xffffffffu, x, 2);
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
-                const int row = part * 4 * I + 4 * i + tg;
-                s[i][h] = row >= now.lo && row < now.hi ? x : -INFINITY;
+                const int row = 4 * i + tg;
+                s[i][h] = row >= seen.lo && row < seen.hi ? x : -INFINITY;
                 top[h] = fmaxf(top[h], s[i][h]);
             }
             rise |= top[h] > m[h];
@@ -579,29 +564,23 @@ struct FloatCore {
             const float top_of = m[h] == -INFINITY ? 0.0f : m[h];
 #pragma unroll
             for (int i = 0; i < I; ++i) {
-                const float w = exp2_fast(s[i][h] - top_of);
-                l[h] += w;
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[h][j][r] = fmaf(w, f(vr[i][j][r]), acc[h][j][r]);
+                s[i][h] = exp2_fast(s[i][h] - top_of);
+                l[h] += s[i][h];
             }
         }
-        if (then.block != kNone) load(p, vr, v, then, then_part);
-    }
-
-    __device__ __forceinline__ void step(const DecodePlan &p, const void *k, const void *v, const Step &now, const Step &next) {
-        if (now.block != kNone) {
-#pragma unroll 1
-            for (int part = 0; part < kSub; ++part) {
-                const bool end = part + 1 == kSub;
-                const Step then = {end ? next.block : now.block, end ? next.lo : now.lo, end ? next.hi : now.hi};
-                part_of(p, k, v, now, part, then, end ? 0 : part + 1);
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float4 x = *reinterpret_cast<const float4 *>(v + 4 * i * DP + 32 * j);
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    acc[h][j][0] = fmaf(s[i][h], x.x, acc[h][j][0]);
+                    acc[h][j][1] = fmaf(s[i][h], x.y, acc[h][j][1]);
+                    acc[h][j][2] = fmaf(s[i][h], x.z, acc[h][j][2]);
+                    acc[h][j][3] = fmaf(s[i][h], x.w, acc[h][j][3]);
+                }
             }
-        } else if (next.block != kNone) {
-            load(p, kr, k, next, 0);
-            load(p, vr, v, next, 0);
-        }
     }
 
     __device__ __forceinline__ void finish(const DecodePlan &p, float *out, float *top, float *sum) {
@@ -641,7 +620,9 @@ struct FloatCore {
 struct Row {
     int first, last, t0, units;
 };
+template <int R>
 __device__ __forceinline__ Row row_at(const DecodePlan &p, int r, bool *bad) {
+    constexpr int kUnit = R * kWarps;
     Row x;
     const int pos = p.at.positions[r];
     const int seq = p.at.sequences ? p.at.sequences[r] : r;
@@ -693,12 +674,12 @@ inline __host__ __device__ int part_floats(int nh, int D) { return (nh * (D + 2)
 template <class Core>
 __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(const __grid_constant__ DecodePlan p) {
     using Act = typename Core::Act;
-    constexpr int DP = Core::kTileElems, NH = Core::kHeads;
-    extern __shared__ __align__(16) float smem[];
-    float *out = smem;                       // [kWarps][NH][DP]
-    float *top = out + kWarps * NH * DP;     // [kWarps][NH]
-    float *sum = top + kWarps * NH;          // [kWarps][NH]
-    float *q_smem = sum + kWarps * NH;       // fp32: [NH][DP]
+    constexpr int DP = Core::kTileElems, NH = Core::kHeads, R = Core::kRows, S = Core::kStages;
+    constexpr int kStage = 2 * R * Core::kRowBytes, kRing = S * kStage;
+    static_assert(NH * DP * 4 <= kRing, "a warp's output takes the place of its ring");
+    extern __shared__ __align__(128) char ring[];  // [kWarps][S] stages; at a segment's end [kWarps] outputs [NH][DP]
+    __shared__ float top[kWarps * NH], sum[kWarps * NH];
+    __shared__ __align__(16) float q_smem[sizeof(Act) == 4 ? NH * DP : 4];
     __shared__ long long scan[kWarps], start_unit;
     __shared__ int start_row;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -710,7 +691,7 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
     long long mine = 0;
     for (int r = r0; r < r1; ++r) {
         bool bad;
-        mine += row_at(p, r, &bad).units;
+        mine += row_at<R>(p, r, &bad).units;
         if (bad && blockIdx.x == 0) bad_index(p.at);
     }
     mine *= p.row_heads;
@@ -739,7 +720,7 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
         long long u = before;
         int r = r0;
         for (;; ++r) {
-            const long long n = static_cast<long long>(row_at(p, r, nullptr).units) * p.row_heads;
+            const long long n = static_cast<long long>(row_at<R>(p, r, nullptr).units) * p.row_heads;
             if (u0 < u + n) break;
             u += n;
         }
@@ -751,7 +732,7 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
     Core core;
     int r = start_row;
     long long row_begin = start_unit;  // unit of the row's first head
-    Row row = row_at(p, r, nullptr);
+    Row row = row_at<R>(p, r, nullptr);
     int rh = static_cast<int>((u0 - row_begin) / row.units);
     bool listed = false;
     for (long long u = u0; u < u1;) {
@@ -769,25 +750,38 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
         const void *k = p.k[at.shard], *v = p.v[at.shard];
 
         // lane i looks up the i-th of the next 32 steps
-        uint32_t blocks_now = block_at(p, s, s.t0 + lane, warp);
+        uint32_t blocks_now = block_at<R>(p, s, s.t0 + lane, warp);
         core.begin(p, static_cast<const Act *>(p.q[at.shard]) + q_at, at.shard * p.hk + at.kv, nq, q_smem);
-        Step now = {kNone, 0, 0};
-        Step next = step_at(s, s.t0, warp, __shfl_sync(0xffffffffu, blocks_now, 0));
-        core.step(p, k, v, now, next);
+        __syncthreads();  // the segment before has been read from shared memory
+        char *mine_at = ring + warp * kRing;
+        const uint32_t mine_to = static_cast<uint32_t>(__cvta_generic_to_shared(mine_at));
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) {
+            const uint32_t block = __shfl_sync(0xffffffffu, blocks_now, i);
+            if (block != kNone) fetch<Core>(p, k, v, seen_at<R>(s, s.t0 + i, warp), block, mine_to + i * kStage);
+            copies_end();
+        }
+        int stage = 0, ahead = S - 1;
         for (int from = s.t0; from < s.t1; from += 32) {
-            const uint32_t blocks_next = block_at(p, s, from + 32 + lane, warp);
+            const uint32_t blocks_next = block_at<R>(p, s, from + 32 + lane, warp);
             const int n = min(32, s.t1 - from);
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
-                now = next;
-                const uint32_t then = i == 31 ? __shfl_sync(0xffffffffu, blocks_next, 0) : __shfl_sync(0xffffffffu, blocks_now, i + 1);
-                next = step_at(s, from + i + 1, warp, then);
-                core.step(p, k, v, now, next);
+                copies_wait<S - 2>();
+                __syncwarp();  // every lane's copies of this step are there, and the step before has been read
+                const uint32_t then = __shfl_sync(0xffffffffu, i + S - 1 < 32 ? blocks_now : blocks_next, (i + S - 1) & 31);
+                if (then != kNone) fetch<Core>(p, k, v, seen_at<R>(s, from + i + S - 1, warp), then, mine_to + ahead * kStage);
+                copies_end();
+                if (__shfl_sync(0xffffffffu, blocks_now, i) != kNone)
+                    core.step(p, mine_at + stage * kStage, seen_at<R>(s, from + i, warp));
+                stage = stage + 1 == S ? 0 : stage + 1;
+                ahead = ahead + 1 == S ? 0 : ahead + 1;
             }
             blocks_now = blocks_next;
         }
-        __syncthreads();  // the segment before has been read from shared memory
-        core.finish(p, out + warp * NH * DP, top + warp * NH, sum + warp * NH);
+        copies_wait<0>();
+        __syncwarp();
+        core.finish(p, reinterpret_cast<float *>(mine_at), top + warp * NH, sum + warp * NH);
         __syncthreads();
 
         const bool whole = u == seg_begin && seg_end <= u1;
@@ -805,7 +799,7 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
             for (int w = 0; w < kWarps; ++w) {
                 const float x = top[w * NH + h], by = x == -INFINITY ? 0.0f : exp2_fast(x - most);
                 all = fmaf(sum[w * NH + h], by, all);
-                const float4 *o = reinterpret_cast<const float4 *>(out + (w * NH + h) * DP + e);
+                const float4 *o = reinterpret_cast<const float4 *>(ring + w * kRing) + (h * DP + e) / 4;
                 const float4 a = o[0], b = o[1];
                 f[0] = fmaf(a.x, by, f[0]); f[1] = fmaf(a.y, by, f[1]); f[2] = fmaf(a.z, by, f[2]); f[3] = fmaf(a.w, by, f[3]);
                 f[4] = fmaf(b.x, by, f[4]); f[5] = fmaf(b.y, by, f[5]); f[6] = fmaf(b.z, by, f[6]); f[7] = fmaf(b.w, by, f[7]);
@@ -837,7 +831,7 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
             rh = 0;
             ++r;
             row_begin = seg_end;
-            row = row_at(p, r, nullptr);
+            row = row_at<R>(p, r, nullptr);
         }
     }
     if (!p.by_segment && !listed && threadIdx.x == 0) p.joins[c] = make_int4(0, 0, 0, 0);
@@ -925,8 +919,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) join_kernel(const __gri
 // is room for in the workspace).
 template <class Core>
 tp_status launch_core(DecodePlan &p, int *grid, cudaStream_t st) {
-    constexpr int kSmem = sizeof(float) * (kWarps * Core::kHeads * (Core::kTileElems + 2) +
-                                           (sizeof(typename Core::Act) == 4 ? Core::kHeads * Core::kTileElems : 0));
+    constexpr int kSmem = kWarps * Core::kStages * 2 * Core::kRows * Core::kRowBytes;
     static int per_sm[64] = {};  // by device
     static std::mutex mu;
     int dev = 0, resident;

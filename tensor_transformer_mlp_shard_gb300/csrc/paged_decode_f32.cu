@@ -12,7 +12,11 @@ static tp_status launch_width(DecodePlan &p, int *grid, cudaStream_t st) {
 }
 
 tp_status launch_decode_f32(DecodePlan &p, int *grid, cudaStream_t st) {
-    return p.D <= 64 ? launch_width<64>(p, grid, st) : p.D <= 128 ? launch_width<128>(p, grid, st) : launch_width<256>(p, grid, st);
+    return p.D <= 64    ? launch_width<64>(p, grid, st)
+           : p.D <= 96  ? launch_width<96>(p, grid, st)
+           : p.D <= 128 ? launch_width<128>(p, grid, st)
+           : p.D <= 192 ? launch_width<192>(p, grid, st)
+                        : launch_width<256>(p, grid, st);
 }
 
 }  // namespace attn

@@ -532,8 +532,8 @@ tp_status tp_paged_create(const tp_paged_desc *desc, tp_paged **out) {
     if (desc->page_size < 16 || desc->page_size % 16 || desc->page_size > kMaxRows)
         return set_error(TP_ERR_SHAPE, "page_size=%d must be a multiple of 16 in 16..%d", desc->page_size, kMaxRows);
     if (desc->pages < 1) return set_error(TP_ERR_SHAPE, "pages=%d must be positive", desc->pages);
-    if (static_cast<long long>(desc->pages) * (desc->kv_heads / desc->T) * (desc->page_size / 16) >= 0xffffffffll)
-        return set_error(TP_ERR_SHAPE, "pages=%d of %d positions and %d key heads: 2^36 rows of a cache or more", desc->pages,
+    if (static_cast<long long>(desc->pages) * (desc->kv_heads / desc->T) * (desc->page_size / 8) >= 0xffffffffll)
+        return set_error(TP_ERR_SHAPE, "pages=%d of %d positions and %d key heads: 2^35 rows of a cache or more", desc->pages,
                          desc->page_size, desc->kv_heads / desc->T);
     if (desc->window < 0) return set_error(TP_ERR_ARG, "window=%d is negative", desc->window);
     if (!std::isfinite(desc->scale)) return set_error(TP_ERR_ARG, "scale must be finite");
