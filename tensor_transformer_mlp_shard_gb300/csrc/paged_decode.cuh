@@ -26,6 +26,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <mutex>
 #include <type_traits>
 
@@ -37,6 +38,7 @@ namespace attn {
 constexpr int kWarps = 4;
 constexpr int kBlock = 32 * kWarps;
 constexpr int kMostBlocks = 1024;       // of a launch, and so of the workspace
+constexpr int kSegmentCost = 2;         // units that a segment costs besides its own
 
 enum CacheKind : int { CACHE_BF16 = 0, CACHE_FP8 = 1, CACHE_F32 = 2 };
 
@@ -680,18 +682,18 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
     extern __shared__ __align__(128) char ring[];  // [kWarps][S] stages; at a segment's end [kWarps] outputs [NH][DP]
     __shared__ float top[kWarps * NH], sum[kWarps * NH];
     __shared__ __align__(16) float q_smem[sizeof(Act) == 4 ? NH * DP : 4];
-    __shared__ long long scan[kWarps], start_unit;
+    __shared__ long long scan[kWarps], start_cost;
     __shared__ int start_row;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     wait_for_stream();
     let_next_start();
 
-    // units of all rows, and the row that this block's stretch starts in
+    // cost of all rows, and the row that this block's stretch starts in
     const int each = (p.at.n + kBlock - 1) / kBlock, r0 = min(threadIdx.x * each, p.at.n), r1 = min(r0 + each, p.at.n);
     long long mine = 0;
     for (int r = r0; r < r1; ++r) {
         bool bad;
-        mine += row_at<R>(p, r, &bad).units;
+        mine += row_at<R>(p, r, &bad).units + kSegmentCost;
         if (bad && blockIdx.x == 0) bad_index(p.at);
     }
     mine *= p.row_heads;
@@ -709,43 +711,47 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
         total += scan[w];
     }
     before -= mine;
-    const long long blocks = total < gridDim.x ? total : gridDim.x;
+    const long long blocks = min(total, static_cast<long long>(gridDim.x));
     const int c = blockIdx.x;
     if (c >= blocks) {
         if (!p.by_segment && threadIdx.x == 0) p.joins[c] = make_int4(0, 0, 0, 0);
         return;
     }
-    const long long u0 = total * c / blocks, u1 = total * (c + 1) / blocks;
-    if (u0 >= before && u0 < before + mine) {
-        long long u = before;
+    const long long from_cost = total * c / blocks, to_cost = total * (c + 1) / blocks;
+    if (from_cost >= before && from_cost < before + mine) {
+        long long x = before;
         int r = r0;
         for (;; ++r) {
-            const long long n = static_cast<long long>(row_at<R>(p, r, nullptr).units) * p.row_heads;
-            if (u0 < u + n) break;
-            u += n;
+            const long long n = static_cast<long long>(row_at<R>(p, r, nullptr).units + kSegmentCost) * p.row_heads;
+            if (from_cost < x + n) break;
+            x += n;
         }
         start_row = r;
-        start_unit = u;
+        start_cost = x;
     }
     __syncthreads();
 
     Core core;
     int r = start_row;
-    long long row_begin = start_unit;  // unit of the row's first head
     Row row = row_at<R>(p, r, nullptr);
-    int rh = static_cast<int>((u0 - row_begin) / row.units);
+    int rh = static_cast<int>((from_cost - start_cost) / (row.units + kSegmentCost));
+    long long at_cost = start_cost + static_cast<long long>(rh) * (row.units + kSegmentCost);  // where the segment's cost begins
     bool listed = false;
-    for (long long u = u0; u < u1;) {
-        const long long seg_begin = row_begin + static_cast<long long>(rh) * row.units, seg_end = seg_begin + row.units;
+    for (; at_cost < to_cost;) {
+        // a segment's cost before its first unit belongs to whoever has that unit
+        const long long first_unit = at_cost + kSegmentCost;
+        const int u0 = static_cast<int>(max(from_cost - first_unit, 0ll));
+        const int u1 = static_cast<int>(min(to_cost - first_unit, static_cast<long long>(row.units)));
+        if (u1 <= u0) break;
         const HeadAt at = head_at(p, rh);
         const int nq = queries_of(p, rh);
         Segment s;
         s.head = at.kv;
         s.first = row.first;
         s.last = row.last;
-        s.t0 = row.t0 + static_cast<int>(u - seg_begin);
-        s.t1 = row.t0 + static_cast<int>((seg_end < u1 ? seg_end : u1) - seg_begin);
-        s.pages = p.at.table + static_cast<long long>(p.at.sequences && row.last >= 0 ? p.at.sequences[r] : row.last >= 0 ? r : 0) * p.at.table_cols;
+        s.t0 = row.t0 + u0;
+        s.t1 = row.t0 + u1;
+        s.pages = p.at.table + static_cast<long long>(row.last < 0 ? 0 : p.at.sequences ? p.at.sequences[r] : r) * p.at.table_cols;
         const long long q_at = (static_cast<long long>(r) * p.hq + at.query) * p.D;
         const void *k = p.k[at.shard], *v = p.v[at.shard];
 
@@ -784,9 +790,9 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
         core.finish(p, reinterpret_cast<float *>(mine_at), top + warp * NH, sum + warp * NH);
         __syncthreads();
 
-        const bool whole = u == seg_begin && seg_end <= u1;
+        const bool whole = u0 == 0 && u1 == row.units;
         // slot 0: began in an earlier block; 1: ends in a later one
-        float *part = p.partial + (static_cast<long long>(c) * 2 + (u == seg_begin ? 1 : 0)) * part_floats(p.nh, p.D);
+        float *part = p.partial + (static_cast<long long>(c) * 2 + (u0 == 0 ? 1 : 0)) * part_floats(p.nh, p.D);
         const float vscale = p.v_amax ? 1.0f / cache_scale(p.v_amax, at.shard * p.hk + at.kv) : 1.0f;
         const int chunks = p.D / 8;
         for (int i = threadIdx.x; i < nq * chunks; i += kBlock) {
@@ -817,20 +823,19 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
                 }
             }
         }
-        if (u == seg_begin && threadIdx.x == 0) {
+        if (u0 == 0 && threadIdx.x == 0) {
             // the block that holds the segment's last unit
-            const int last = static_cast<int>((seg_end * blocks + total - 1) / total) - 1;
+            const int last = static_cast<int>(((first_unit + row.units) * blocks + total - 1) / total) - 1;
             if (p.by_segment)
                 p.joins[r * p.row_heads + rh] = make_int4(r, rh, c, last);
             else if (!whole)
                 p.joins[c] = make_int4(r, rh, c, last);
         }
-        listed |= u == seg_begin && !whole;
-        u = seg_end < u1 ? seg_end : u1;
-        if (u == seg_end && ++rh == p.row_heads && u < u1) {
+        listed |= u0 == 0 && !whole;
+        at_cost = first_unit + row.units;
+        if (++rh == p.row_heads && at_cost < to_cost) {
             rh = 0;
             ++r;
-            row_begin = seg_end;
             row = row_at<R>(p, r, nullptr);
         }
     }
