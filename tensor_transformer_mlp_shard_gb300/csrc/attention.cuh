@@ -93,6 +93,7 @@ struct DecodePlan {
     const float *k_amax, *v_amax;
     float *partial;        // [blocks][2][nh * (D + 2)]
     int4 *joins;           // [blocks]
+    int resident;          // blocks that run at once
     int by_segment;        // joins are listed by (row, head) rather than by block
 };
 size_t decode_workspace_bytes(const tp_paged_desc &d);

@@ -37,8 +37,14 @@ namespace attn {
 
 constexpr int kWarps = 4;
 constexpr int kBlock = 32 * kWarps;
-constexpr int kMostBlocks = 1024;       // of a launch, and so of the workspace
-constexpr int kSegmentCost = 2;         // units that a segment costs besides its own
+constexpr int kMostResident = 768;      // blocks that run at once
+constexpr int kMostBlocks = 2 * kMostResident;  // of a launch, and so of the workspace
+// A segment costs its block this many positions besides its own (its pages,
+// queries and first keys have to arrive, its parts to be added): without it the
+// blocks that have short rows end last (fp32 window case 37 us, with it 27).
+constexpr int kSegmentPositions = 128;
+// With so many units a resident block, one unit in kTailShare goes to half as many blocks more.
+constexpr int kSpread = 32, kTailShare = 8;
 
 enum CacheKind : int { CACHE_BF16 = 0, CACHE_FP8 = 1, CACHE_F32 = 2 };
 
@@ -321,7 +327,11 @@ struct TensorCore {
         }
     }
 
-    uint32_t ph[NT][2], pl[NT][2];  // weights as the sum of two 16-bit numbers
+    // The weights as the sum of two 16-bit numbers (2^-17 of a weight for bf16,
+    // 2^-22 for fp16): one bf16 would be off by as much as the output's own
+    // rounding.  The second product is free for bf16 caches, bound by memory, and
+    // costs 2% with codes (8-bit batch 132 us with one fp16, 135 us with two).
+    uint32_t ph[NT][2], pl[NT][2];
 
     __device__ __forceinline__ void softmax() {
         float top[NT][2];
@@ -357,7 +367,7 @@ struct TensorCore {
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float w[4], rest[4];
+            float w[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const float top_of = m[n][r & 1] == -INFINITY ? 0.0f : m[n][r & 1];
@@ -367,21 +377,16 @@ struct TensorCore {
             l[n][1] += w[1] + w[3];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                uint32_t hi;
                 if constexpr (k8) {
                     const __half2 x = __floats2half2_rn(w[2 * r], w[2 * r + 1]);
-                    hi = *reinterpret_cast<const uint32_t *>(&x);
-                    rest[2 * r] = w[2 * r] - __low2float(x);
-                    rest[2 * r + 1] = w[2 * r + 1] - __high2float(x);
-                    const __half2 y = __floats2half2_rn(rest[2 * r], rest[2 * r + 1]);
+                    const __half2 y = __floats2half2_rn(w[2 * r] - __low2float(x), w[2 * r + 1] - __high2float(x));
+                    ph[n][r] = transpose8(*reinterpret_cast<const uint32_t *>(&x));
                     pl[n][r] = transpose8(*reinterpret_cast<const uint32_t *>(&y));
                 } else {
-                    hi = pack_bf16x2(w[2 * r], w[2 * r + 1]);
-                    rest[2 * r] = w[2 * r] - bf16_lo(hi);
-                    rest[2 * r + 1] = w[2 * r + 1] - bf16_hi(hi);
-                    pl[n][r] = transpose8(pack_bf16x2(rest[2 * r], rest[2 * r + 1]));
+                    const uint32_t hi = pack_bf16x2(w[2 * r], w[2 * r + 1]);
+                    ph[n][r] = transpose8(hi);
+                    pl[n][r] = transpose8(pack_bf16x2(w[2 * r] - bf16_lo(hi), w[2 * r + 1] - bf16_hi(hi)));
                 }
-                ph[n][r] = transpose8(hi);
             }
         }
     }
@@ -673,11 +678,45 @@ __device__ __forceinline__ int queries_of(const DecodePlan &p, int rh) {
 // A group's outputs [nh][D], maxima [nh] and sums [nh], in whole 16 bytes.
 inline __host__ __device__ int part_floats(int nh, int D) { return (nh * (D + 2) + 3) & ~3; }
 
+// Registers a thread so that an SM holds so many blocks and has 8192 left: a block
+// of the kernel before (the join of the call before, say) that is still there
+// must not keep one of these out until another ends (8-bit batch: 137 us with
+// one block late, 125 without).
+constexpr int registers_of(int blocks) {
+    return (65536 - 8192) / (blocks * kBlock) / 8 * 8 < 255 ? (65536 - 8192) / (blocks * kBlock) / 8 * 8 : 255;
+}
+
+// The blocks' shares of the cost.  SMs differ by up to a tenth in what memory
+// gives them, so with enough to do, an eighth of the cost goes to blocks beyond
+// the resident ones, which take it up as those end (batch 167 -> 164 us, long 300
+// -> 295 us; equal shares for four times the resident blocks: 174 and 302 us).
+struct Shares {
+    long long total, main;  // main: of the resident blocks
+    int resident, rest;
+    __device__ __forceinline__ Shares(long long cost, int resident_blocks, int all) : total(cost) {
+        resident = static_cast<int>(min(cost, static_cast<long long>(resident_blocks)));
+        const bool spread = cost >= static_cast<long long>(resident_blocks) * kSpread;
+        rest = spread ? all - resident_blocks : 0;
+        main = spread ? cost - cost / kTailShare : cost;
+    }
+    __device__ __forceinline__ int blocks() const { return resident + rest; }
+    // where block c's share begins
+    __device__ __forceinline__ long long begin(int c) const {
+        return c <= resident ? main * c / resident : main + (total - main) * (c - resident) / rest;
+    }
+    // the block whose share holds x
+    __device__ __forceinline__ int owner(long long x) const {
+        return static_cast<int>(x < main ? ((x + 1) * resident + main - 1) / main - 1
+                                         : resident + ((x + 1 - main) * rest + (total - main) - 1) / (total - main) - 1);
+    }
+};
+
 template <class Core>
-__global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(const __grid_constant__ DecodePlan p) {
+__global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(const __grid_constant__ DecodePlan p) {
     using Act = typename Core::Act;
     constexpr int DP = Core::kTileElems, NH = Core::kHeads, R = Core::kRows, S = Core::kStages;
     constexpr int kStage = 2 * R * Core::kRowBytes, kRing = S * kStage;
+    constexpr int kSegmentCost = kSegmentPositions / (R * kWarps);
     static_assert(NH * DP * 4 <= kRing, "a warp's output takes the place of its ring");
     extern __shared__ __align__(128) char ring[];  // [kWarps][S] stages; at a segment's end [kWarps] outputs [NH][DP]
     __shared__ float top[kWarps * NH], sum[kWarps * NH];
@@ -711,13 +750,13 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
         total += scan[w];
     }
     before -= mine;
-    const long long blocks = min(total, static_cast<long long>(gridDim.x));
+    const Shares shares(total, p.resident, gridDim.x);
     const int c = blockIdx.x;
-    if (c >= blocks) {
+    if (c >= shares.blocks()) {
         if (!p.by_segment && threadIdx.x == 0) p.joins[c] = make_int4(0, 0, 0, 0);
         return;
     }
-    const long long from_cost = total * c / blocks, to_cost = total * (c + 1) / blocks;
+    const long long from_cost = shares.begin(c), to_cost = shares.begin(c + 1);
     if (from_cost >= before && from_cost < before + mine) {
         long long x = before;
         int r = r0;
@@ -825,7 +864,7 @@ __global__ void __launch_bounds__(kBlock, Core::kBlocksPerSm) decode_kernel(cons
         }
         if (u0 == 0 && threadIdx.x == 0) {
             // the block that holds the segment's last unit
-            const int last = static_cast<int>(((first_unit + row.units) * blocks + total - 1) / total) - 1;
+            const int last = shares.owner(first_unit + row.units - 1);
             if (p.by_segment)
                 p.joins[r * p.row_heads + rh] = make_int4(r, rh, c, last);
             else if (!whole)
@@ -850,7 +889,6 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) join_kernel(const __gri
     __shared__ float tops[W], sums[W];
     __shared__ __align__(16) float4 outs[W == 1 ? 1 : W][64];
     wait_for_stream();
-    let_next_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.y * kQueries + (W == 1 ? warp : 0);
     const int4 j = p.joins[blockIdx.x];
@@ -865,19 +903,35 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) join_kernel(const __gri
     const int e0 = 4 * lane, e1 = 128 + 4 * lane;
     float most = -INFINITY, all = 0.0f;
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
-    for (int i = W == 1 ? 0 : warp; i < n; i += W) most = fmaxf(most, part(i)[p.nh * p.D + h]);
-#pragma unroll 4
-    for (int i = W == 1 ? 0 : warp; i < n; i += W) {
-        const float *x = part(i);
-        const float top = x[p.nh * p.D + h], by = top == -INFINITY ? 0.0f : exp2_fast(top - most);
-        all = fmaf(x[p.nh * (p.D + 1) + h], by, all);
-        if (e0 < p.D) {
-            const float4 v = *reinterpret_cast<const float4 *>(x + h * p.D + e0);
-            a.x = fmaf(v.x, by, a.x); a.y = fmaf(v.y, by, a.y); a.z = fmaf(v.z, by, a.z); a.w = fmaf(v.w, by, a.w);
+    for (int i0 = W == 1 ? 0 : warp; i0 < n; i0 += 4 * W) {
+        // four parts at once, so that one wait serves them all
+        float top[4], sum[4];
+        float4 va[4], vb[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            top[u] = -INFINITY;
+            sum[u] = 0.0f;
+            va[u] = vb[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i0 + u * W < n) {
+                const float *x = part(i0 + u * W);
+                top[u] = x[p.nh * p.D + h];
+                sum[u] = x[p.nh * (p.D + 1) + h];
+                if (e0 < p.D) va[u] = *reinterpret_cast<const float4 *>(x + h * p.D + e0);
+                if (e1 < p.D) vb[u] = *reinterpret_cast<const float4 *>(x + h * p.D + e1);
+            }
         }
-        if (e1 < p.D) {
-            const float4 v = *reinterpret_cast<const float4 *>(x + h * p.D + e1);
-            b.x = fmaf(v.x, by, b.x); b.y = fmaf(v.y, by, b.y); b.z = fmaf(v.z, by, b.z); b.w = fmaf(v.w, by, b.w);
+        const float now = fmaxf(most, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+        const float old = most == -INFINITY ? 0.0f : exp2_fast(most - now);
+        most = now;
+        all *= old;
+        a.x *= old; a.y *= old; a.z *= old; a.w *= old;
+        b.x *= old; b.y *= old; b.z *= old; b.w *= old;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float by = top[u] == -INFINITY ? 0.0f : exp2_fast(top[u] - now);
+            all = fmaf(sum[u], by, all);
+            a.x = fmaf(va[u].x, by, a.x); a.y = fmaf(va[u].y, by, a.y); a.z = fmaf(va[u].z, by, a.z); a.w = fmaf(va[u].w, by, a.w);
+            b.x = fmaf(vb[u].x, by, b.x); b.y = fmaf(vb[u].y, by, b.y); b.z = fmaf(vb[u].z, by, b.z); b.w = fmaf(vb[u].w, by, b.w);
         }
     }
     if constexpr (W > 1) {
@@ -942,7 +996,8 @@ tp_status launch_core(DecodePlan &p, int *grid, cudaStream_t st) {
         }
         resident = per_sm[dev] * num_sms();
     }
-    *grid = resident < kMostBlocks ? resident : kMostBlocks;
+    p.resident = resident < kMostResident ? resident : kMostResident;
+    *grid = p.resident + p.resident / 2;
     const long long segments = static_cast<long long>(p.at.n) * p.row_heads;
     p.by_segment = segments <= *grid;
     cudaLaunchConfig_t cfg = {};

@@ -151,7 +151,6 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
     __shared__ long long slot_of[kMaxTokens];  // APPEND: the slot's row of the cache, of key head 0
     __shared__ int active[kMaxTokens];
     wait_for_stream();
-    let_next_start();
     const int token0 = blockIdx.x * p.tokens;
     const int step = kThreads * gridDim.y;
     int i = blockIdx.y * kThreads + threadIdx.x;
@@ -255,6 +254,9 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
         if (i >= p.block_items) break;
         load(i);
     }
+    // not earlier: blocks of this kernel between those of the next one leave an SM's
+    // registers in pieces, and the next kernel's last block without a place
+    let_next_start();
 }
 
 // ---------------------------------------------------------------------------
