@@ -920,13 +920,19 @@ class Rope:
                         0.0 if self.attention_factor is None else float(self.attention_factor))
 
 
+# a C array of an address and those `step`, 2 `step`, ... bytes on (a third of the time of packing a range)
+_pack_parts = [eval("lambda a, s: pack(%s)" % ", ".join("a + %d * s" % i for i in range(k)), {"pack": _pack[k]})
+               for k in range(MAX_SHARDS + 1)]
+
+
 def _shards(name, ts, count, n, dtype, dev):
     """The addresses of `count` shards of n elements, a list of tensors or one
     tensor whose equal parts they are, as a C array; all on device `dev`."""
-    if type(ts) is torch.Tensor and ts.dtype is dtype and ts.numel() == count * n and ts.get_device() == dev \
-            and ts.is_contiguous():
-        at, step = ts.data_ptr(), n * dtype.itemsize
-        return _pack[count](*range(at, at + count * step, step)) if n else _pack[count](*[at] * count)
+    try:
+        if ts.dtype is dtype and ts.get_device() == dev and ts.is_contiguous() and ts.numel() == count * n:
+            return _pack1(ts.data_ptr()) if count == 1 else _pack_parts[count](ts.data_ptr(), n * dtype.itemsize)
+    except AttributeError:
+        pass
     if isinstance(ts, torch.Tensor):
         ts, count, n = [ts], 1, count * n
     out = _pointers(name, ts, count, n, dtype)
@@ -938,10 +944,21 @@ def _shards(name, ts, count, n, dtype, dev):
 
 def _vector(name, t, n, dtype, dev):
     """Address of a contiguous tensor of n elements on device `dev`."""
-    at = _pointer(name, t, n, dtype)
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
-    return at
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() == n:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _pointer(name, t, n, dtype)
+    raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+
+
+def _stream_on(dev, stream):
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+
+
+# (torch.cuda.current_device without its check for a lazy start: a CUDA tensor is at hand)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 class TPRotary:
@@ -971,11 +988,11 @@ class TPRotary:
             self._h = None
 
     def _run(self, call, x, x_name, y, y_name, positions, stream):
-        dev = torch.cuda.current_device() if self.M else 0
+        dev = _device() if self.M else 0
         px = _shards(x_name, x, self.T, self._n, self._act, dev)
         py = px if y is None else _shards(y_name, y, self.T, self._n, self._act, dev)
         at = None if positions is None else _vector("positions", positions, self.M, torch.int32, dev)
-        status = call(self._h, px, at, py, _stream(stream))
+        status = call(self._h, px, at, py, _stream_on(dev, stream))
         if status:
             _check(status)
 
@@ -1041,11 +1058,10 @@ class TPPagedAttention:
         return int(lib().tp_paged_sync_status(self._h, _stream(stream)))
 
     def _rows(self, positions, sequences, table, k_amax, v_amax, dev):
-        if not isinstance(positions, torch.Tensor) or positions.dim() != 1:
-            raise ValueError("positions: must be a CUDA tensor [n]")
-        if not isinstance(table, torch.Tensor) or table.dim() != 2:
-            raise ValueError("table: must be a CUDA tensor [sequences, columns]")
-        n, (rows, cols) = positions.shape[0], table.shape
+        try:
+            (n,), (rows, cols) = positions.shape, table.shape
+        except (AttributeError, ValueError):
+            raise ValueError("positions: must be a CUDA tensor [n], table: one [sequences, columns]") from None
         at = (_vector("positions", positions, n, torch.int32, dev),
               None if sequences is None else _vector("sequences", sequences, n, torch.int32, dev), n,
               _vector("table", table, rows * cols, torch.int32, dev), rows, cols)
@@ -1058,13 +1074,13 @@ class TPPagedAttention:
         """New tokens X [n, (heads + 2 kv_heads) / T * head_dim] a shard: turned
         queries to Q [n, heads / T * head_dim], turned keys and values to the
         slots of their positions.  No two rows name the same slot."""
-        dev, T, act = torch.cuda.current_device(), self.T, self._act
+        dev, T, act = _device(), self.T, self._act
         rows = self._rows(positions, sequences, table, k_amax, v_amax, dev)
         n = rows[2]
         status = self._append(self._h, _shards("X", X, T, n * self._x_n, act, dev), *rows,
                               _shards("Q", Q, T, n * self._q_n, act, dev),
                               _shards("K", K, T, self._cache_n, self.cache_dtype, dev),
-                              _shards("V", V, T, self._cache_n, self.cache_dtype, dev), _stream(stream))
+                              _shards("V", V, T, self._cache_n, self.cache_dtype, dev), _stream_on(dev, stream))
         if status:
             _check(status)
 
@@ -1073,14 +1089,14 @@ class TPPagedAttention:
         row's queries over positions max(0, p - window + 1)..p of its sequence;
         zero for padding.  workspace: see alloc_workspace, one for each of the
         calls that may overlap."""
-        dev, T, act = torch.cuda.current_device(), self.T, self._act
+        dev, T, act = _device(), self.T, self._act
         rows = self._rows(positions, sequences, table, k_amax, v_amax, dev)
         n = rows[2]
         ws, nws = _workspace(workspace)
         status = self._decode(self._h, _shards("Q", Q, T, n * self._q_n, act, dev), *rows,
                               _shards("K", K, T, self._cache_n, self.cache_dtype, dev),
                               _shards("V", V, T, self._cache_n, self.cache_dtype, dev),
-                              _shards("O", O, T, n * self._q_n, act, dev), ws, nws, _stream(stream))
+                              _shards("O", O, T, n * self._q_n, act, dev), ws, nws, _stream_on(dev, stream))
         if status:
             _check(status)
 
