@@ -8,7 +8,11 @@
 // all heads share, are computed once, by one thread a pair, while the first
 // loads are on their way, and kept in shared memory; a table in memory would
 // cost as many bytes as a head.  An item is two chunks of a head: with pairs
-// (i, i + dim/2) a chunk and its partner, else neighbours.
+// (i, i + dim/2) a chunk and its partner, else neighbours.  A thread has one
+// item of every token, so that where it lies is worked out once for all of the
+// block's tokens, and copies it to a ring of its own in shared memory, three
+// tokens ahead: the bytes on their way do not cost registers, and no thread
+// waits for another.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -31,7 +35,11 @@ namespace tpmlp {
 namespace attn {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;  // tokens of a block
+constexpr int kMaxTokens = 8;   // tokens of a block
+constexpr int kFlight = 3;     // of them that a thread copies ahead
+
+// the most that a block asks for: 8 tokens of 128 pairs, the ring of 256 threads
+static_assert(sizeof(float) * 2 * kMaxTokens * kMaxPairs + kFlight * 2 * 16 * kThreads < 48 * 1024 - 512, "a kernel's shared memory unasked");
 
 enum Mode : int { ROTATE = 0, APPEND = 1, APPEND8 = 2 };
 
@@ -45,10 +53,13 @@ struct QkvPlan {
     int hq, hk, per, grouped, columns;        // columns: heads of a row, hq + 2 hk
     int D, half, interleaved;                 // half: pairs of a head
     int pair_items;                           // items of a head whose chunks are partners
+    int rest_items;                           // the others
     int in_place;
-    int tokens;                               // of a block
-    int block_items;                          // tokens * T * slots * items
+    int side, passes;                         // tokens of a block: `side` at a time, `passes` times
+    int rounds;                               // of `threads` items of side tokens
+    int round_items;                          // side * T * slots * items
     Divisor by_items, by_slots, by_shards, by_group;
+    int turn_pitch;                           // of the cosines of a token in shared memory
     float sign;                               // -1: the transposed rotation
     Turns turns;
 };
@@ -62,20 +73,21 @@ struct Chunk {  // VE elements as they are stored
     Word w;
     __device__ __forceinline__ void load(const E *p) { w = *reinterpret_cast<const Word *>(p); }
     __device__ __forceinline__ void store(E *p) const { *reinterpret_cast<Word *>(p) = w; }
-    __device__ __forceinline__ void unpack(float *f) const {
+    __device__ __forceinline__ void unpack(float (&f)[VE]) const {
         const E *e = reinterpret_cast<const E *>(&w);
 #pragma unroll
         for (int i = 0; i < VE; ++i) f[i] = static_cast<float>(e[i]);
     }
-    __device__ __forceinline__ void pack(const float *f) {
+    __device__ __forceinline__ void pack(const float (&f)[VE]) {
         E *e = reinterpret_cast<E *>(&w);
 #pragma unroll
         for (int i = 0; i < VE; ++i) e[i] = static_cast<E>(f[i]);
     }
 };
 
+// fp32 to codes in one rounding
 template <int VE>
-__device__ __forceinline__ void store_codes(uint8_t *p, const float *f, float scale) {
+__device__ __forceinline__ void store_codes(uint8_t *p, const float (&f)[VE], float scale) {
     uint8_t c[VE];
 #pragma unroll
     for (int i = 0; i < VE; ++i) c[i] = __nv_cvt_float_to_fp8(f[i] * scale, __NV_SATFINITE, __NV_E4M3);
@@ -91,14 +103,14 @@ enum Kind : int { QUERY = 0, KEY = 1, VALUE = 2 };
 
 // Where a thread's item is.
 struct Item {
-    int token;        // of the block; -1: none
+    int token;        // of the side's; -1: none
     int shard, kind, head, column, a, b;  // a, b: the chunks' first elements (b = -1: none)
 };
 
 template <int VE>
 __device__ __forceinline__ Item item_at(const QkvPlan &p, int i) {
     Item it;
-    if (i >= p.block_items) {
+    if (i >= p.round_items) {
         it.token = -1;
         return it;
     }
@@ -123,136 +135,197 @@ __device__ __forceinline__ Item item_at(const QkvPlan &p, int i) {
         it.a = n * VE;
         it.b = it.a + p.half;
     } else {
-        it.a = 2 * (p.pair_items * VE + (n - p.pair_items) * VE);
-        it.b = it.a + VE < (p.in_place ? 2 * p.half : p.D) ? it.a + VE : -1;
+        // two halves of what is left, so that neighbouring threads read neighbouring chunks
+        it.a = (p.pair_items + n) * VE;
+        it.b = it.a + p.rest_items * VE;
+        if (it.b >= (p.in_place ? 2 * p.half : p.D)) it.b = -1;
     }
     return it;
 }
 
+// N cosines or sines from shared memory (N = 4: 16-byte aligned, 2: 8-byte)
+template <int N>
+__device__ __forceinline__ void read_turns(float *to, const float *from) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(from + i);
+            to[i] = v.x; to[i + 1] = v.y; to[i + 2] = v.z; to[i + 3] = v.w;
+        }
+    } else if constexpr (N == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(from);
+        to[0] = v.x; to[1] = v.y;
+    } else {
+        to[0] = from[0];
+    }
+}
+
 // the pairs (first + 2i, first + 2i + 1) of a chunk, those that turn
 template <int VE>
-__device__ __forceinline__ void turn_neighbours(float *f, int first, int half, const float *cs, const float *sn) {
+__device__ __forceinline__ void turn_neighbours(float (&f)[VE], int first, int half, const float *cs, const float *sn) {
+    if (first / 2 >= half) return;
+    float c[VE / 2], s[VE / 2];
+    read_turns<VE / 2>(c, cs + first / 2);
+    read_turns<VE / 2>(s, sn + first / 2);
 #pragma unroll
-    for (int e = 0; e + 1 < VE; e += 2) {
-        const int i = (first + e) / 2;
-        if (i < half) {
-            const float c = cs[i], s = sn[i], x = f[e], y = f[e + 1];
-            f[e] = x * c - y * s;
-            f[e + 1] = y * c + x * s;
+    for (int e = 0; e < VE; e += 2)
+        if ((first + e) / 2 < half) {
+            const float x = f[e], y = f[e + 1];
+            f[e] = x * c[e / 2] - y * s[e / 2];
+            f[e + 1] = y * c[e / 2] + x * s[e / 2];
         }
-    }
 }
 
 template <typename E, int VE, int MODE>
 __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ QkvPlan p) {
-    constexpr int U = 2;  // items of a thread in flight
-    // cosines and sines by token
-    __shared__ __align__(16) float cs[kMaxTokens][kMaxPairs], sn[kMaxTokens][kMaxPairs];
+    constexpr int kBytes = Chunk<E, VE>::kBytes;
+    constexpr bool kRing = kBytes == 16;  // narrower chunks are loaded when they are needed
+    // [tokens][pairs] cosines, as many sines, then [kFlight][2][threads] chunks
+    extern __shared__ __align__(16) char smem[];
     __shared__ long long slot_of[kMaxTokens];  // APPEND: the slot's row of the cache, of key head 0
     __shared__ int active[kMaxTokens];
-    wait_for_stream();
-    const int token0 = blockIdx.x * p.tokens;
-    const int step = kThreads * gridDim.y;
-    int i = blockIdx.y * kThreads + threadIdx.x;
-    Item it[U];
-    Chunk<E, VE> a[U], b[U];
+    const int tokens = p.side * p.passes, token0 = blockIdx.x * tokens, pitch = p.turn_pitch;
+    float *cs = reinterpret_cast<float *>(smem), *sn = cs + tokens * pitch;
+    uint4 *ring = reinterpret_cast<uint4 *>(sn + tokens * pitch) + threadIdx.x;
+    const uint32_t ring_to = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     const long long width = static_cast<long long>(p.columns) * p.D;
-    auto load = [&](int from) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            it[u] = item_at<VE>(p, from + u * step);
-            if (it[u].token < 0 || token0 + it[u].token >= p.at.n) {
-                it[u].token = -1;
-                continue;
-            }
-            const E *x = static_cast<const E *>(p.x[it[u].shard]) + (token0 + it[u].token) * width + it[u].column * p.D;
-            a[u].load(x + it[u].a);
-            if (it[u].b >= 0) b[u].load(x + it[u].b);
-        }
-    };
-    load(i);
-    const int pairs = p.half > 0 ? p.half : 1;
-    for (int k = threadIdx.x; k < p.tokens * pairs; k += kThreads) {
-        const int t = k / pairs, pair = k - t * pairs, m = token0 + t;
-        if (m >= p.at.n) break;
-        const int pos = MODE == ROTATE && !p.at.positions ? static_cast<int>(p.batch.div(m)) : p.at.positions[m];
-        if (pair == 0) {
-            int ok = pos >= 0;
-            if (MODE != ROTATE && ok) {
-                const int seq = p.at.sequences ? p.at.sequences[m] : m;
-                uint32_t off;
-                const int col = p.at.page.divmod(pos, off);
-                ok = static_cast<unsigned>(seq) < static_cast<unsigned>(p.at.table_rows) && col < p.at.table_cols;
-                const int page = ok ? p.at.table[static_cast<long long>(seq) * p.at.table_cols + col] : -1;
-                ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.at.pages);
-                if (!ok && blockIdx.y == 0) bad_index(p.at);
-                // the heads of a page lie page_size rows apart
-                slot_of[t] = static_cast<long long>(page) * p.hk * p.at.page_size + off;
-            }
-            active[t] = ok;
-        }
-        const float2 r = turn(p.turns, pair, pos);
-        cs[t][pair] = r.x;
-        sn[t][pair] = r.y * p.sign;
-    }
-    __syncthreads();
-    while (true) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (it[u].token < 0) continue;
-            const int t = it[u].token;
-            if (!active[t] && (MODE != ROTATE || p.in_place)) continue;  // padding stays as it was
-            const bool two = it[u].b >= 0;
-            float fa[VE], fb[VE];
-            a[u].unpack(fa);
-            if (two) b[u].unpack(fb);
-            if (it[u].kind != VALUE && active[t]) {
-                if (p.interleaved) {
-                    turn_neighbours<VE>(fa, it[u].a, p.half, cs[t], sn[t]);
-                    a[u].pack(fa);
-                    if (two) {
-                        turn_neighbours<VE>(fb, it[u].b, p.half, cs[t], sn[t]);
-                        b[u].pack(fb);
-                    }
-                } else if (it[u].a < p.half) {
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        const float c = cs[t][it[u].a + e], s = sn[t][it[u].a + e], x = fa[e], y = fb[e];
-                        fa[e] = x * c - y * s;
-                        fb[e] = y * c + x * s;
-                    }
-                    a[u].pack(fa);
-                    b[u].pack(fb);
-                }
-            }
-            const long long m = token0 + t;
+    bool turned = false;
+    wait_for_stream();
+    for (int round = blockIdx.y; round < p.rounds; round += gridDim.y) {
+        const Item it = item_at<VE>(p, round * blockDim.x + threadIdx.x);
+        const bool two = it.b >= 0;
+        const E *x = nullptr;
+        E *y = nullptr;  // ROTATE, queries
+        void *cache = nullptr;
+        long long y_step = 0;
+        float scale = 1.0f;
+        int count = 0;   // of the thread's tokens
+        if (it.token >= 0) {
+            const int m = token0 + it.token;
+            count = m < p.at.n ? min(p.passes, (p.at.n - m + p.side - 1) / p.side) : 0;
+            x = static_cast<const E *>(p.x[it.shard]) + it.column * p.D + m * width;
             if (MODE == ROTATE) {
-                E *y = static_cast<E *>(p.y[it[u].shard]) + m * width + it[u].column * p.D;
-                a[u].store(y + it[u].a);
-                if (two) b[u].store(y + it[u].b);
-            } else if (it[u].kind == QUERY) {
-                E *y = static_cast<E *>(p.y[it[u].shard]) + (m * p.hq + it[u].head) * p.D;
-                a[u].store(y + it[u].a);
-                if (two) b[u].store(y + it[u].b);
+                y = static_cast<E *>(p.y[it.shard]) + it.column * p.D;
+                y_step = width;
+            } else if (it.kind == QUERY) {
+                y = static_cast<E *>(p.y[it.shard]) + it.head * p.D;
+                y_step = static_cast<long long>(p.hq) * p.D;
             } else {
-                void *to = it[u].kind == KEY ? p.k[it[u].shard] : p.v[it[u].shard];
-                const long long row = (slot_of[t] + static_cast<long long>(it[u].head) * p.at.page_size) * p.D;
-                if (MODE == APPEND) {
-                    E *y = static_cast<E *>(to) + row;
-                    a[u].store(y + it[u].a);
-                    if (two) b[u].store(y + it[u].b);
+                cache = it.kind == KEY ? p.k[it.shard] : p.v[it.shard];
+                if (MODE == APPEND8) scale = cache_scale(it.kind == KEY ? p.k_amax : p.v_amax, it.shard * p.hk + it.head);
+            }
+            if (y) y += m * y_step;
+            y_step *= p.side;
+        }
+        const long long x_step = width * p.side;
+        // the thread's chunks of its pass-th token to slot `to` of its ring
+        auto copy = [&](int pass, int to) {
+            if (pass < count) {
+                const E *from = x + pass * x_step;
+                const uint32_t at = ring_to + to * (2 * 16) * blockDim.x;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from + it.a) : "memory");
+                if (two)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + 16 * blockDim.x), "l"(from + it.b) : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        if constexpr (kRing) {
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) copy(i, i);
+        }
+        if (!turned) {
+            const int pairs = p.half > 0 ? p.half : 1;
+            for (int k = threadIdx.x; k < tokens * pairs; k += blockDim.x) {
+                const int t = k / pairs, pair = k - t * pairs, m = token0 + t;
+                if (m >= p.at.n) break;
+                const int pos = MODE == ROTATE && !p.at.positions ? static_cast<int>(p.batch.div(m)) : p.at.positions[m];
+                if (pair == 0) {
+                    int ok = pos >= 0;
+                    if (MODE != ROTATE && ok) {
+                        const int seq = p.at.sequences ? p.at.sequences[m] : m;
+                        uint32_t off;
+                        const int col = p.at.page.divmod(pos, off);
+                        ok = static_cast<unsigned>(seq) < static_cast<unsigned>(p.at.table_rows) && col < p.at.table_cols;
+                        const int page = ok ? p.at.table[static_cast<long long>(seq) * p.at.table_cols + col] : -1;
+                        ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.at.pages);
+                        if (!ok && blockIdx.y == 0) bad_index(p.at);
+                        // the heads of a page lie page_size rows apart
+                        slot_of[t] = static_cast<long long>(page) * p.hk * p.at.page_size + off;
+                    }
+                    active[t] = ok;
+                }
+                const float2 r = turn(p.turns, pair, pos);
+                cs[t * pitch + pair] = r.x;
+                sn[t * pitch + pair] = r.y * p.sign;
+            }
+            turned = true;
+            __syncthreads();
+        }
+        int slot = 0;
+        for (int pass = 0; pass < count; ++pass) {
+            Chunk<E, VE> a, b;
+            if constexpr (kRing) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kFlight - 1) : "memory");
+                const uint4 *r = ring + slot * 2 * blockDim.x;
+                a.w = r[0];
+                if (two) b.w = r[blockDim.x];
+            } else {
+                const E *from = x + pass * x_step;
+                a.load(from + it.a);
+                if (two) b.load(from + it.b);
+            }
+            const int t = pass * p.side + it.token;
+            const bool on = active[t];
+            if (on || (MODE == ROTATE && !p.in_place)) {  // otherwise padding stays as it was
+                float fa[VE], fb[VE];
+                a.unpack(fa);
+                if (two) b.unpack(fb);
+                if (it.kind != VALUE && on) {
+                    const float *c_of = cs + t * pitch, *s_of = sn + t * pitch;
+                    if (p.interleaved) {
+                        if constexpr (VE > 1) {
+                            turn_neighbours<VE>(fa, it.a, p.half, c_of, s_of);
+                            a.pack(fa);
+                            if (two) {
+                                turn_neighbours<VE>(fb, it.b, p.half, c_of, s_of);
+                                b.pack(fb);
+                            }
+                        }
+                    } else if (it.a < p.half) {
+                        float c[VE], s[VE];
+                        read_turns<VE>(c, c_of + it.a);
+                        read_turns<VE>(s, s_of + it.a);
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) {
+                            const float f = fa[e], g = fb[e];
+                            fa[e] = f * c[e] - g * s[e];
+                            fb[e] = g * c[e] + f * s[e];
+                        }
+                        a.pack(fa);
+                        b.pack(fb);
+                    }
+                }
+                if (MODE == ROTATE || it.kind == QUERY) {
+                    E *to = y + pass * y_step;
+                    a.store(to + it.a);
+                    if (two) b.store(to + it.b);
                 } else {
-                    // fp32 goes to the code in one rounding
-                    const float scale = cache_scale(it[u].kind == KEY ? p.k_amax : p.v_amax, it[u].shard * p.hk + it[u].head);
-                    uint8_t *y = static_cast<uint8_t *>(to) + row;
-                    store_codes<VE>(y + it[u].a, fa, scale);
-                    if (two) store_codes<VE>(y + it[u].b, fb, scale);
+                    const long long row = (slot_of[t] + static_cast<long long>(it.head) * p.at.page_size) * p.D;
+                    if (MODE == APPEND) {
+                        E *to = static_cast<E *>(cache) + row;
+                        a.store(to + it.a);
+                        if (two) b.store(to + it.b);
+                    } else {
+                        uint8_t *to = static_cast<uint8_t *>(cache) + row;
+                        store_codes<VE>(to + it.a, fa, scale);
+                        if (two) store_codes<VE>(to + it.b, fb, scale);
+                    }
                 }
             }
+            if constexpr (kRing) copy(pass + kFlight, slot);
+            slot = slot + 1 == kFlight ? 0 : slot + 1;
         }
-        i += U * step;
-        if (i >= p.block_items) break;
-        load(i);
+        if constexpr (kRing) asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     // not earlier: blocks of this kernel between those of the next one leave an SM's
     // registers in pieces, and the next kernel's last block without a place
@@ -313,41 +386,52 @@ static tp_status launch_qkv(QkvPlan &p, int T, int elem, int mode, const char *n
     p.pair_items = partners;
     const int rotated = p.interleaved ? ((2 * p.half + ve - 1) / ve + 1) / 2 : partners;
     const int items = p.in_place ? rotated : partners + (chunks - 2 * partners + 1) / 2;
+    p.rest_items = items - partners;
     const int group = p.per + (p.in_place ? 1 : 2);
     const int slots = p.grouped ? p.hk * group : p.hq + p.hk * (p.in_place ? 1 : 2);
     if (items == 0) return TP_OK;  // nothing turns, in place
-    // several tokens a block where there are enough blocks all the same
-    p.tokens = 1;
-    while (p.tokens < kMaxTokens && p.at.n / (2 * p.tokens) >= 8 * num_sms()) p.tokens *= 2;
-    p.block_items = p.tokens * T * slots * items;
+    const int per_token = T * slots * items;
+    // narrow tensors: several tokens side by side
+    p.side = 1;
+    while (p.side < 4 && 2 * p.side * per_token <= kThreads) p.side *= 2;
+    p.round_items = p.side * per_token;
+    // rounds of equally many threads
+    p.rounds = (p.round_items + kThreads - 1) / kThreads;
+    const int threads = ((p.round_items + p.rounds - 1) / p.rounds + 31) / 32 * 32;
     p.by_items = Divisor(items);
     p.by_slots = Divisor(slots);
     p.by_shards = Divisor(T);
     p.by_group = Divisor(group);
-    const int blocks = (p.at.n + p.tokens - 1) / p.tokens;
-    // few tokens: a token's items over several blocks
-    int across = 1;
-    while (blocks * across < 2 * num_sms() && across * 2 * kThreads < p.block_items) across *= 2;
+    void (*k)(QkvPlan) = nullptr;
+    using B = __nv_bfloat16;
+    if (elem == 4)
+        k = mode == ROTATE ? (ve == 4 ? qkv_kernel<float, 4, ROTATE> : qkv_kernel<float, 1, ROTATE>)
+                           : (ve == 4 ? qkv_kernel<float, 4, APPEND> : qkv_kernel<float, 1, APPEND>);
+    else
+        k = mode == ROTATE   ? (ve == 8 ? qkv_kernel<B, 8, ROTATE> : ve == 4 ? qkv_kernel<B, 4, ROTATE> : qkv_kernel<B, 1, ROTATE>)
+            : mode == APPEND ? (ve == 8 ? qkv_kernel<B, 8, APPEND> : ve == 4 ? qkv_kernel<B, 4, APPEND> : qkv_kernel<B, 1, APPEND>)
+                             : (ve == 8 ? qkv_kernel<B, 8, APPEND8> : ve == 4 ? qkv_kernel<B, 4, APPEND8> : qkv_kernel<B, 1, APPEND8>);
+    // Tokens after one another, where there are enough blocks all the same: 4, and 8
+    // with the lookups in the table before them (32768 tokens backward 118 us with 4,
+    // 121 with 8; 8092 into the cache 38 us with 8, 40 with 4).
+    const int most = mode == ROTATE ? 4 : 8;
+    p.passes = 1;
+    while (2 * p.passes * p.side <= most && p.at.n / (2 * p.passes * p.side) >= 4 * num_sms()) p.passes *= 2;
+    p.turn_pitch = p.half > 0 ? (p.half + 7) / 8 * 8 : 8;
+    const int ring = ve * elem == 16 ? kFlight * 2 * 16 * threads : 0, turns = sizeof(float) * 2 * p.side * p.turn_pitch;
+    const int blocks = (p.at.n + p.side * p.passes - 1) / (p.side * p.passes);
+    // few tokens: the rounds on blocks of their own
+    const int across = blocks < 2 * num_sms() ? p.rounds : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks, across);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = ring + p.passes * turns;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_on() ? 1 : 0;
-    void (*k)(QkvPlan) = nullptr;
-    using B = __nv_bfloat16;
-    if (elem == 4)
-        k = mode == ROTATE ? (ve == 4 ? qkv_kernel<float, 4, ROTATE> : qkv_kernel<float, 1, ROTATE>)
-                           : (ve == 4 ? qkv_kernel<float, 4, APPEND> : qkv_kernel<float, 1, APPEND>);
-    else if (mode == ROTATE)
-        k = ve == 8 ? qkv_kernel<B, 8, ROTATE> : ve == 4 ? qkv_kernel<B, 4, ROTATE> : qkv_kernel<B, 1, ROTATE>;
-    else if (mode == APPEND)
-        k = ve == 8 ? qkv_kernel<B, 8, APPEND> : ve == 4 ? qkv_kernel<B, 4, APPEND> : qkv_kernel<B, 1, APPEND>;
-    else
-        k = ve == 8 ? qkv_kernel<B, 8, APPEND8> : ve == 4 ? qkv_kernel<B, 4, APPEND8> : qkv_kernel<B, 1, APPEND8>;
     launch_begin(name, st);
     cudaError_t e = cudaLaunchKernelEx(&cfg, k, p);
     launch_end(name, st);
