@@ -43,6 +43,12 @@ constexpr int kMostBlocks = 2 * kMostResident;  // of a launch, and so of the wo
 // queries and first keys have to arrive, its parts to be added): without it the
 // blocks that have short rows end last (fp32 window case 37 us, with it 27).
 constexpr int kSegmentPositions = 128;
+// A row up to this long is read by one warp where there are more segments than
+// blocks.
+#ifndef KSHORT
+#define KSHORT 128
+#endif
+constexpr int kShortPositions = KSHORT;
 // With so many units a resident block, one unit in kTailShare goes to half as many blocks more.
 constexpr int kSpread = 32, kTailShare = 8;
 
@@ -51,18 +57,19 @@ enum CacheKind : int { CACHE_BF16 = 0, CACHE_FP8 = 1, CACHE_F32 = 2 };
 // A segment of a row: what the warps need to walk it.
 struct Segment {
     const int32_t *pages;       // the row's table
-    int head, t0, t1;           // key head of the shard; units [t0, t1)
+    int head, t0, t1;           // key head of the shard; steps [t0, t1)
     int first, last;            // positions that the row sees
 };
 
-// A step: the R positions of a unit that are the warp's.  They lie in one page;
+// A step: R positions, the step-th R of the sequence.  They lie in one page;
 // `block` is their place in the cache in blocks of R rows of head_dim, kNone
 // where the row sees none of them or the page is out of range.
 constexpr uint32_t kNone = 0xffffffffu;
 template <int R>
-__device__ __forceinline__ uint32_t block_at(const DecodePlan &p, const Segment &s, int unit, int warp) {
-    const int base = unit * (R * kWarps) + warp * R;
-    if (unit >= s.t1 || base > s.last || base + R - 1 < s.first) return kNone;
+__device__ __forceinline__ uint32_t block_at(const DecodePlan &p, const Segment &s, int step) {
+    if (step >= s.t1) return kNone;
+    const int base = step * R;
+    if (base > s.last || base + R - 1 < s.first) return kNone;
     uint32_t in_page;
     const int page = s.pages[p.at.page.divmod(base, in_page)];
     if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.at.pages)) {
@@ -77,8 +84,8 @@ struct Seen {
     int lo, hi;
 };
 template <int R>
-__device__ __forceinline__ Seen seen_at(const Segment &s, int unit, int warp) {
-    const int base = unit * (R * kWarps) + warp * R;
+__device__ __forceinline__ Seen seen_at(const Segment &s, int step) {
+    const int base = step * R;
     return {max(s.first - base, 0), min(s.last + 1 - base, R)};
 }
 
@@ -475,7 +482,8 @@ struct TensorCore {
 // fp32 products
 // ---------------------------------------------------------------------------
 // Eight lanes share a position, DP / 8 elements each; the four groups of lanes
-// keep softmax states of their own.  Queries lie in shared memory, scaled.
+// keep softmax states of their own.  Queries lie in shared memory, scaled, a copy
+// for each warp.
 template <int DP, int NH>
 struct FloatCore {
     using Cache = float;
@@ -495,17 +503,17 @@ struct FloatCore {
     float acc[NH][J][4];
     int tg, sub;
 
-    __device__ __forceinline__ void begin(const DecodePlan &p, const Act *qrow, int, int nq, float *smem_q) {
+    __device__ __forceinline__ void begin(const DecodePlan &p, const Act *qrow, int, int nq, float *warp_q) {
         const int lane = threadIdx.x & 31;
         tg = lane >> 3;
         sub = lane & 7;
-        q = smem_q;
-        __syncthreads();  // nobody reads the segment before's queries any more
-        for (int i = threadIdx.x; i < NH * DP; i += kBlock) {
+        q = warp_q;
+        __syncwarp();  // no lane reads the segment before's queries any more
+        for (int i = lane; i < NH * DP; i += 32) {
             const int h = i / DP, e = i - h * DP;
-            smem_q[i] = h < nq && e < p.D ? qrow[static_cast<long long>(h) * p.D + e] * p.scale_log2 : 0.0f;
+            warp_q[i] = h < nq && e < p.D ? qrow[static_cast<long long>(h) * p.D + e] * p.scale_log2 : 0.0f;
         }
-        __syncthreads();
+        __syncwarp();
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
             m[h] = -INFINITY;
@@ -711,16 +719,59 @@ struct Shares {
     }
 };
 
+// One warp's steps of a segment: every `by`-th from its `first` one, through its
+// ring of stages.
+template <class Core>
+__device__ __forceinline__ void walk(Core &core, const DecodePlan &p, const Segment &s, const void *k, const void *v, int first, int by,
+                                     char *ring) {
+    constexpr int R = Core::kRows, S = Core::kStages, kStage = 2 * R * Core::kRowBytes;
+    const int lane = threadIdx.x & 31, t0 = s.t0 + first;
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    // lane i looks up the i-th of the next 32 steps
+    uint32_t blocks_now = block_at<R>(p, s, t0 + by * lane);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        const uint32_t block = __shfl_sync(0xffffffffu, blocks_now, i);
+        if (block != kNone) fetch<Core>(p, k, v, seen_at<R>(s, t0 + by * i), block, to + i * kStage);
+        copies_end();
+    }
+    int stage = 0, ahead = S - 1;
+    for (int from = t0; from < s.t1; from += 32 * by) {
+        uint32_t blocks_next = kNone;
+        if (from + 32 * by < s.t1) blocks_next = block_at<R>(p, s, from + by * (32 + lane));
+        const int n = min(32, (s.t1 - from + by - 1) / by);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            copies_wait<S - 2>();
+            __syncwarp();  // every lane's copies of this step are there, and the step before has been read
+            const uint32_t then = __shfl_sync(0xffffffffu, i + S - 1 < 32 ? blocks_now : blocks_next, (i + S - 1) & 31);
+            if (then != kNone) fetch<Core>(p, k, v, seen_at<R>(s, from + by * (i + S - 1)), then, to + ahead * kStage);
+            copies_end();
+            if (__shfl_sync(0xffffffffu, blocks_now, i) != kNone)
+                core.step(p, ring + stage * kStage, seen_at<R>(s, from + by * i));
+            stage = stage + 1 == S ? 0 : stage + 1;
+            ahead = ahead + 1 == S ? 0 : ahead + 1;
+        }
+        blocks_now = blocks_next;
+    }
+    copies_wait<0>();
+    __syncwarp();
+}
+
 template <class Core>
 __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(const __grid_constant__ DecodePlan p) {
     using Act = typename Core::Act;
     constexpr int DP = Core::kTileElems, NH = Core::kHeads, R = Core::kRows, S = Core::kStages;
     constexpr int kStage = 2 * R * Core::kRowBytes, kRing = S * kStage;
-    constexpr int kSegmentCost = kSegmentPositions / (R * kWarps);
+    constexpr int kSegmentCost = kSegmentPositions / (R * kWarps), kShort = kShortPositions / (R * kWarps);
+    // with more segments than blocks, a short one is a single warp's
+    const bool alone = !p.by_segment;
+    auto is_short = [&](int units) { return alone && units <= kShort; };
+    auto cost_of = [&](int units) { return is_short(units) ? 1 + units / 2 : units + kSegmentCost; };
     static_assert(NH * DP * 4 <= kRing, "a warp's output takes the place of its ring");
     extern __shared__ __align__(128) char ring[];  // [kWarps][S] stages; at a segment's end [kWarps] outputs [NH][DP]
     __shared__ float top[kWarps * NH], sum[kWarps * NH];
-    __shared__ __align__(16) float q_smem[sizeof(Act) == 4 ? NH * DP : 4];
+    __shared__ __align__(16) float q_smem[sizeof(Act) == 4 ? kWarps * NH * DP : 4];
     __shared__ long long scan[kWarps], start_cost;
     __shared__ int start_row;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -732,7 +783,7 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
     long long mine = 0;
     for (int r = r0; r < r1; ++r) {
         bool bad;
-        mine += row_at<R>(p, r, &bad).units + kSegmentCost;
+        mine += cost_of(row_at<R>(p, r, &bad).units);
         if (bad && blockIdx.x == 0) bad_index(p.at);
     }
     mine *= p.row_heads;
@@ -761,7 +812,7 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
         long long x = before;
         int r = r0;
         for (;; ++r) {
-            const long long n = static_cast<long long>(row_at<R>(p, r, nullptr).units + kSegmentCost) * p.row_heads;
+            const long long n = static_cast<long long>(cost_of(row_at<R>(p, r, nullptr).units)) * p.row_heads;
             if (from_cost < x + n) break;
             x += n;
         }
@@ -771,98 +822,82 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
     __syncthreads();
 
     Core core;
+    char *mine_at = ring + warp * kRing;
+    float *mine_q = sizeof(Act) == 4 ? q_smem + warp * NH * DP : nullptr;
     int r = start_row;
     Row row = row_at<R>(p, r, nullptr);
-    int rh = static_cast<int>((from_cost - start_cost) / (row.units + kSegmentCost));
-    long long at_cost = start_cost + static_cast<long long>(rh) * (row.units + kSegmentCost);  // where the segment's cost begins
+    int rh = static_cast<int>((from_cost - start_cost) / cost_of(row.units));
+    long long at_cost = start_cost + static_cast<long long>(rh) * cost_of(row.units);  // where the segment's cost begins
     bool listed = false;
+    bool unread = false;
+    int turn = 0;  // whose the next short segment is
     for (; at_cost < to_cost;) {
-        // a segment's cost before its first unit belongs to whoever has that unit
-        const long long first_unit = at_cost + kSegmentCost;
-        const int u0 = static_cast<int>(max(from_cost - first_unit, 0ll));
-        const int u1 = static_cast<int>(min(to_cost - first_unit, static_cast<long long>(row.units)));
+        const bool brief = is_short(row.units);
+        // a segment's cost before its first unit belongs to whoever has that unit; a short segment, to
+        // whoever has its beginning
+        const long long first_unit = at_cost + (brief ? 0 : kSegmentCost), end_cost = at_cost + cost_of(row.units);
+        const int u0 = brief ? 0 : static_cast<int>(max(from_cost - first_unit, 0ll));
+        const int u1 = brief ? row.units : static_cast<int>(min(to_cost - first_unit, static_cast<long long>(row.units)));
         if (u1 <= u0) break;
+        const bool mine_too = !brief || (at_cost >= from_cost && (turn++ & (kWarps - 1)) == warp);
         const HeadAt at = head_at(p, rh);
         const int nq = queries_of(p, rh);
         Segment s;
         s.head = at.kv;
         s.first = row.first;
         s.last = row.last;
-        s.t0 = row.t0 + u0;
-        s.t1 = row.t0 + u1;
+        s.t0 = (row.t0 + u0) * kWarps;
+        s.t1 = (row.t0 + u1) * kWarps;
         s.pages = p.at.table + static_cast<long long>(row.last < 0 ? 0 : p.at.sequences ? p.at.sequences[r] : r) * p.at.table_cols;
         const long long q_at = (static_cast<long long>(r) * p.hq + at.query) * p.D;
         const void *k = p.k[at.shard], *v = p.v[at.shard];
+        const float vscale = p.v_amax ? 1.0f / cache_scale(p.v_amax, at.shard * p.hk + at.kv) : 1.0f;
+        const int chunks = p.D / 8;
 
-        // lane i looks up the i-th of the next 32 steps
-        uint32_t blocks_now = block_at<R>(p, s, s.t0 + lane, warp);
-        core.begin(p, static_cast<const Act *>(p.q[at.shard]) + q_at, at.shard * p.hk + at.kv, nq, q_smem);
-        __syncthreads();  // the segment before has been read from shared memory
-        char *mine_at = ring + warp * kRing;
-        const uint32_t mine_to = static_cast<uint32_t>(__cvta_generic_to_shared(mine_at));
-#pragma unroll
-        for (int i = 0; i < S - 1; ++i) {
-            const uint32_t block = __shfl_sync(0xffffffffu, blocks_now, i);
-            if (block != kNone) fetch<Core>(p, k, v, seen_at<R>(s, s.t0 + i, warp), block, mine_to + i * kStage);
-            copies_end();
+        // the warps' outputs of a segment before have been read
+        if (!brief || unread) __syncthreads();
+        unread = !brief;
+        if (mine_too) {
+            core.begin(p, static_cast<const Act *>(p.q[at.shard]) + q_at, at.shard * p.hk + at.kv, nq, mine_q);
+            walk<Core>(core, p, s, k, v, brief ? 0 : warp, brief ? 1 : kWarps, mine_at);
+            core.finish(p, reinterpret_cast<float *>(mine_at), top + warp * NH, sum + warp * NH);
+            __syncwarp();
         }
-        int stage = 0, ahead = S - 1;
-        for (int from = s.t0; from < s.t1; from += 32) {
-            const uint32_t blocks_next = block_at<R>(p, s, from + 32 + lane, warp);
-            const int n = min(32, s.t1 - from);
-#pragma unroll 1
-            for (int i = 0; i < n; ++i) {
-                copies_wait<S - 2>();
-                __syncwarp();  // every lane's copies of this step are there, and the step before has been read
-                const uint32_t then = __shfl_sync(0xffffffffu, i + S - 1 < 32 ? blocks_now : blocks_next, (i + S - 1) & 31);
-                if (then != kNone) fetch<Core>(p, k, v, seen_at<R>(s, from + i + S - 1, warp), then, mine_to + ahead * kStage);
-                copies_end();
-                if (__shfl_sync(0xffffffffu, blocks_now, i) != kNone)
-                    core.step(p, mine_at + stage * kStage, seen_at<R>(s, from + i, warp));
-                stage = stage + 1 == S ? 0 : stage + 1;
-                ahead = ahead + 1 == S ? 0 : ahead + 1;
-            }
-            blocks_now = blocks_next;
-        }
-        copies_wait<0>();
-        __syncwarp();
-        core.finish(p, reinterpret_cast<float *>(mine_at), top + warp * NH, sum + warp * NH);
-        __syncthreads();
+        if (!brief) __syncthreads();
 
         const bool whole = u0 == 0 && u1 == row.units;
         // slot 0: began in an earlier block; 1: ends in a later one
         float *part = p.partial + (static_cast<long long>(c) * 2 + (u0 == 0 ? 1 : 0)) * part_floats(p.nh, p.D);
-        const float vscale = p.v_amax ? 1.0f / cache_scale(p.v_amax, at.shard * p.hk + at.kv) : 1.0f;
-        const int chunks = p.D / 8;
-        for (int i = threadIdx.x; i < nq * chunks; i += kBlock) {
-            const int h = i / chunks, e = (i - h * chunks) * 8;
-            float most = -INFINITY;
+        const int w0 = brief ? warp : 0, w1 = brief ? warp + 1 : kWarps;  // whose states make the segment's
+        if (mine_too) {
+            for (int i = brief ? lane : threadIdx.x; i < nq * chunks; i += brief ? 32 : kBlock) {
+                const int h = i / chunks, e = (i - h * chunks) * 8;
+                float most = -INFINITY, all = 0.0f, f[8] = {};
+                for (int w = w0; w < w1; ++w) most = fmaxf(most, top[w * NH + h]);
+                for (int w = w0; w < w1; ++w) {
+                    const float x = top[w * NH + h], by = x == -INFINITY ? 0.0f : exp2_fast(x - most);
+                    all = fmaf(sum[w * NH + h], by, all);
+                    const float4 *o = reinterpret_cast<const float4 *>(ring + w * kRing) + (h * DP + e) / 4;
+                    const float4 a = o[0], b = o[1];
+                    f[0] = fmaf(a.x, by, f[0]); f[1] = fmaf(a.y, by, f[1]); f[2] = fmaf(a.z, by, f[2]); f[3] = fmaf(a.w, by, f[3]);
+                    f[4] = fmaf(b.x, by, f[4]); f[5] = fmaf(b.y, by, f[5]); f[6] = fmaf(b.z, by, f[6]); f[7] = fmaf(b.w, by, f[7]);
+                }
+                if (whole) {
+                    const float by = all == 0.0f ? 0.0f : vscale / all;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) most = fmaxf(most, top[w * NH + h]);
-            float all = 0.0f, f[8] = {};
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float x = top[w * NH + h], by = x == -INFINITY ? 0.0f : exp2_fast(x - most);
-                all = fmaf(sum[w * NH + h], by, all);
-                const float4 *o = reinterpret_cast<const float4 *>(ring + w * kRing) + (h * DP + e) / 4;
-                const float4 a = o[0], b = o[1];
-                f[0] = fmaf(a.x, by, f[0]); f[1] = fmaf(a.y, by, f[1]); f[2] = fmaf(a.z, by, f[2]); f[3] = fmaf(a.w, by, f[3]);
-                f[4] = fmaf(b.x, by, f[4]); f[5] = fmaf(b.y, by, f[5]); f[6] = fmaf(b.z, by, f[6]); f[7] = fmaf(b.w, by, f[7]);
-            }
-            if (whole) {
-                const float by = all == 0.0f ? 0.0f : vscale / all;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = all == 0.0f ? 0.0f : f[j] * by;
-                store8(static_cast<Act *>(p.o[at.shard]) + q_at + static_cast<long long>(h) * p.D + e, f);
-            } else {
-                store8(part + h * p.D + e, f);
-                if (e == 0) {
-                    part[p.nh * p.D + h] = most;
-                    part[p.nh * (p.D + 1) + h] = all;
+                    for (int j = 0; j < 8; ++j) f[j] = all == 0.0f ? 0.0f : f[j] * by;
+                    store8(static_cast<Act *>(p.o[at.shard]) + q_at + static_cast<long long>(h) * p.D + e, f);
+                } else {
+                    store8(part + h * p.D + e, f);
+                    if (e == 0) {
+                        part[p.nh * p.D + h] = most;
+                        part[p.nh * (p.D + 1) + h] = all;
+                    }
                 }
             }
+            __syncwarp();
         }
-        if (u0 == 0 && threadIdx.x == 0) {
+        if (u0 == 0 && !brief && threadIdx.x == 0) {
             // the block that holds the segment's last unit
             const int last = shares.owner(first_unit + row.units - 1);
             if (p.by_segment)
@@ -871,7 +906,7 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
                 p.joins[c] = make_int4(r, rh, c, last);
         }
         listed |= u0 == 0 && !whole;
-        at_cost = first_unit + row.units;
+        at_cost = end_cost;
         if (++rh == p.row_heads && at_cost < to_cost) {
             rh = 0;
             ++r;

@@ -17,6 +17,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <mutex>
@@ -88,18 +89,28 @@ struct Chunk {  // VE elements as they are stored
 // fp32 to codes in one rounding
 template <int VE>
 __device__ __forceinline__ void store_codes(uint8_t *p, const float (&f)[VE], float scale) {
-    uint8_t c[VE];
+    alignas(8) uint8_t c[VE];
 #pragma unroll
     for (int i = 0; i < VE; ++i) c[i] = __nv_cvt_float_to_fp8(f[i] * scale, __NV_SATFINITE, __NV_E4M3);
     if constexpr (VE == 8)
         *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(c);
     else if constexpr (VE == 4)
         *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(c);
+    else if constexpr (VE == 2)
+        *reinterpret_cast<uint16_t *>(p) = *reinterpret_cast<const uint16_t *>(c);
     else
         *p = c[0];
 }
 
 enum Kind : int { QUERY = 0, KEY = 1, VALUE = 2 };
+
+template <int BYTES>
+__device__ __forceinline__ void copy_chunk(uint32_t to, const void *from) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
+}
 
 // Where a thread's item is.
 struct Item {
@@ -179,14 +190,15 @@ __device__ __forceinline__ void turn_neighbours(float (&f)[VE], int first, int h
 template <typename E, int VE, int MODE>
 __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ QkvPlan p) {
     constexpr int kBytes = Chunk<E, VE>::kBytes;
-    constexpr bool kRing = kBytes == 16;  // narrower chunks are loaded when they are needed
+    constexpr bool kRing = kBytes >= 4;  // what asynchronous copies take
     // [tokens][pairs] cosines, as many sines, then [kFlight][2][threads] chunks
     extern __shared__ __align__(16) char smem[];
     __shared__ long long slot_of[kMaxTokens];  // APPEND: the slot's row of the cache, of key head 0
     __shared__ int active[kMaxTokens];
     const int tokens = p.side * p.passes, token0 = blockIdx.x * tokens, pitch = p.turn_pitch;
     float *cs = reinterpret_cast<float *>(smem), *sn = cs + tokens * pitch;
-    uint4 *ring = reinterpret_cast<uint4 *>(sn + tokens * pitch) + threadIdx.x;
+    using Word = typename Chunk<E, VE>::Word;
+    Word *ring = reinterpret_cast<Word *>(sn + tokens * pitch) + threadIdx.x;
     const uint32_t ring_to = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     const long long width = static_cast<long long>(p.columns) * p.D;
     bool turned = false;
@@ -222,10 +234,9 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
         auto copy = [&](int pass, int to) {
             if (pass < count) {
                 const E *from = x + pass * x_step;
-                const uint32_t at = ring_to + to * (2 * 16) * blockDim.x;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from + it.a) : "memory");
-                if (two)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + 16 * blockDim.x), "l"(from + it.b) : "memory");
+                const uint32_t at = ring_to + to * (2 * kBytes) * blockDim.x;
+                copy_chunk<kBytes>(at, from + it.a);
+                if (two) copy_chunk<kBytes>(at + kBytes * blockDim.x, from + it.b);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -262,17 +273,25 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
             __syncthreads();
         }
         int slot = 0;
+        Chunk<E, VE> next_a, next_b;
+        auto load_next = [&](int pass) {
+            if (pass >= count) return;
+            const E *from = x + pass * x_step;
+            next_a.load(from + it.a);
+            if (two) next_b.load(from + it.b);
+        };
+        if constexpr (!kRing) load_next(0);
         for (int pass = 0; pass < count; ++pass) {
             Chunk<E, VE> a, b;
             if constexpr (kRing) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kFlight - 1) : "memory");
-                const uint4 *r = ring + slot * 2 * blockDim.x;
+                const Word *r = ring + slot * 2 * blockDim.x;
                 a.w = r[0];
                 if (two) b.w = r[blockDim.x];
             } else {
-                const E *from = x + pass * x_step;
-                a.load(from + it.a);
-                if (two) b.load(from + it.b);
+                a = next_a;
+                b = next_b;
+                load_next(pass + 1);
             }
             const int t = pass * p.side + it.token;
             const bool on = active[t];
@@ -283,7 +302,7 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
                 if (it.kind != VALUE && on) {
                     const float *c_of = cs + t * pitch, *s_of = sn + t * pitch;
                     if (p.interleaved) {
-                        if constexpr (VE > 1) {
+                        if constexpr (VE >= 4) {  // whole 16 bytes
                             turn_neighbours<VE>(fa, it.a, p.half, c_of, s_of);
                             a.pack(fa);
                             if (two) {
@@ -373,14 +392,21 @@ void rope_turns(const tp_rope_desc &r, Turns *t) {
     t->a = static_cast<float>(a);
 }
 
+template <typename E, int MODE>
+static auto kernel_of(int ve) -> void (*)(QkvPlan) {
+    if constexpr (sizeof(E) == 2)
+        if (ve == 8) return qkv_kernel<E, 8, MODE>;
+    return ve == 4 ? qkv_kernel<E, 4, MODE> : ve == 2 ? qkv_kernel<E, 2, MODE> : qkv_kernel<E, 1, MODE>;
+}
+
 // Fills in what follows from the sizes and launches.  `T` shards, `in_place`:
 // only what is rotated is touched.
 static tp_status launch_qkv(QkvPlan &p, int T, int elem, int mode, const char *name, cudaStream_t st) {
-    // 16 bytes a chunk; with pairs (i, i + half) both chunks have to begin on one, else 4 elements
-    // a chunk, or one where the half is odd or twice an odd number
+    // 16 bytes a chunk; with pairs (i, i + half) both chunks have to begin on one: half
+    // as many elements until the half holds a whole number of them
     int ve = 16 / elem;
     if (!p.interleaved)
-        while (ve > 1 && p.half % ve) ve = ve > 4 ? 4 : 1;
+        while (ve > 1 && p.half % ve) ve /= 2;
     if (p.interleaved && p.half == 0) p.interleaved = 0;
     const int chunks = p.D / ve, partners = p.interleaved ? 0 : p.half / ve;
     p.pair_items = partners;
@@ -403,14 +429,12 @@ static tp_status launch_qkv(QkvPlan &p, int T, int elem, int mode, const char *n
     p.by_shards = Divisor(T);
     p.by_group = Divisor(group);
     void (*k)(QkvPlan) = nullptr;
-    using B = __nv_bfloat16;
     if (elem == 4)
-        k = mode == ROTATE ? (ve == 4 ? qkv_kernel<float, 4, ROTATE> : qkv_kernel<float, 1, ROTATE>)
-                           : (ve == 4 ? qkv_kernel<float, 4, APPEND> : qkv_kernel<float, 1, APPEND>);
+        k = mode == ROTATE ? kernel_of<float, ROTATE>(ve) : kernel_of<float, APPEND>(ve);
     else
-        k = mode == ROTATE   ? (ve == 8 ? qkv_kernel<B, 8, ROTATE> : ve == 4 ? qkv_kernel<B, 4, ROTATE> : qkv_kernel<B, 1, ROTATE>)
-            : mode == APPEND ? (ve == 8 ? qkv_kernel<B, 8, APPEND> : ve == 4 ? qkv_kernel<B, 4, APPEND> : qkv_kernel<B, 1, APPEND>)
-                             : (ve == 8 ? qkv_kernel<B, 8, APPEND8> : ve == 4 ? qkv_kernel<B, 4, APPEND8> : qkv_kernel<B, 1, APPEND8>);
+        k = mode == ROTATE   ? kernel_of<__nv_bfloat16, ROTATE>(ve)
+            : mode == APPEND ? kernel_of<__nv_bfloat16, APPEND>(ve)
+                             : kernel_of<__nv_bfloat16, APPEND8>(ve);
     // Tokens after one another, where there are enough blocks all the same: 4, and 8
     // with the lookups in the table before them (32768 tokens backward 118 us with 4,
     // 121 with 8; 8092 into the cache 38 us with 8, 40 with 4).
@@ -418,10 +442,10 @@ static tp_status launch_qkv(QkvPlan &p, int T, int elem, int mode, const char *n
     p.passes = 1;
     while (2 * p.passes * p.side <= most && p.at.n / (2 * p.passes * p.side) >= 4 * num_sms()) p.passes *= 2;
     p.turn_pitch = p.half > 0 ? (p.half + 7) / 8 * 8 : 8;
-    const int ring = ve * elem == 16 ? kFlight * 2 * 16 * threads : 0, turns = sizeof(float) * 2 * p.side * p.turn_pitch;
+    const int ring = ve * elem >= 4 ? kFlight * 2 * ve * elem * threads : 0, turns = sizeof(float) * 2 * p.side * p.turn_pitch;
     const int blocks = (p.at.n + p.side * p.passes - 1) / (p.side * p.passes);
     // few tokens: the rounds on blocks of their own
-    const int across = blocks < 2 * num_sms() ? p.rounds : 1;
+    const int across = std::min(p.rounds, std::max(1, 8 * num_sms() / blocks));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks, across);
     cfg.blockDim = dim3(threads);

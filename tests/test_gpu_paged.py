@@ -338,3 +338,17 @@ def test_far_offsets(tp):
     assert bool(V[pages - 1, :, 0].any()) and not bool(V[:pages - 1].any()) and not bool(K[:pages - 1].any())
     v = x[0, 8 * D:].double()
     assert ((o[0].double() - v).abs() <= v.abs() * (2.0 ** -4 + 2.0 ** -7) + 2.0 ** -10 * 8 / 448).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("shape", [(4, 4, 64, 2), (8, 8, 128, 1), (12, 2, 80, 1), (2, 1, 256, 1)])
+def test_decode_short_and_long_rows(tp, dtype, shape):
+    """More (row, head) pairs than blocks, short rows between long and empty ones."""
+    heads, kv, D, T = shape
+    rng = np.random.default_rng(D)
+    lengths = [int(x) for x in rng.integers(0, 140, size=1200 // kv)]
+    for i in (0, 3, 4, 50, 51, 52, 149):
+        lengths[i] = 700 + 130 * i
+    lengths[5:9] = [128, 129, 127, 1]
+    decode_case(tp, rng, lengths, heads, kv, D, 32, T, dtype)
+    decode_case(tp, rng, lengths, heads, kv, D, 16, T, dtype, window=40)
