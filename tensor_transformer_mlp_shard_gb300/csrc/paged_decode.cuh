@@ -109,12 +109,12 @@ __device__ __forceinline__ int swizzle_k(int row) {
 }
 __device__ __forceinline__ int swizzle_v(int row) { return ((row >> 1) & 3) << 5; }
 
-// A step's keys and values on their way to a stage: eight lanes (four, for rows of
-// 64 bytes) copy a line of a row.  What lies behind the head's width, and rows
+// A step's keys and values on their way to a stage: eight lanes copy a line of a row
+// (four, half a line, where rows are not whole lines).  What lies behind the head's width, and rows
 // that are not seen, become zero.
 template <class Core, bool WHOLE>
 __device__ __forceinline__ void fetch_rows(int row_bytes, const char *k, const char *v, const Seen &s, uint32_t to) {
-    constexpr int R = Core::kRows, ROW = Core::kRowBytes, kLine = ROW < 128 ? ROW : 128, kLanes = kLine / 16, kStep = 32 / kLanes;
+    constexpr int R = Core::kRows, ROW = Core::kRowBytes, kLine = ROW % 128 ? 64 : 128, kLanes = kLine / 16, kStep = 32 / kLanes;
     const int lane = threadIdx.x & 31, row0 = lane / kLanes, at = 16 * (lane % kLanes);
     const int off = row0 * row_bytes + at;
     const uint32_t lane_to = to + row0 * ROW + at;
@@ -189,9 +189,10 @@ struct TensorCore {
     static constexpr int kHeads = 8 * NT;
     static constexpr int kTileElems = DP;
     static constexpr int kRows = 16, kRowBytes = DP * static_cast<int>(sizeof(Cache));
-    // about 192 KB of stages an SM
-    static constexpr int kStages = kRowBytes == 64 ? 6 : kRowBytes == 128 ? 4 : 3;
-    static constexpr int kBlocksPerSm = kRowBytes == 64 ? 4 : kRowBytes == 128 ? 3 : kRowBytes == 256 ? 2 : 1;
+    // about 192 KB of stages an SM; 16 queries over codes take more registers, so fewer blocks
+    static constexpr bool kFewer = k8 && NT == 2;
+    static constexpr int kStages = kRowBytes == 64 ? (kFewer ? 8 : 6) : kRowBytes == 128 ? (kFewer ? 6 : 4) : kRowBytes % 256 ? 4 : 3;
+    static constexpr int kBlocksPerSm = (kRowBytes == 64 ? 4 : kRowBytes == 128 ? 3 : kRowBytes <= 256 ? 2 : 1) - kFewer;
     __device__ __forceinline__ static int swizzle_keys(int row) { return swizzle_k<kRowBytes>(row); }
     __device__ __forceinline__ static int swizzle_values(int row) { return swizzle_v(row); }
     static constexpr int KC = k8 ? DP / 64 : DP / 32;       // 16-byte loads of a lane's key row
@@ -206,17 +207,15 @@ struct TensorCore {
     float acc[VB][VD / 2][NT][4];
     int g, t;
 
-    // the group's nq queries, from the row of its first
-    __device__ __forceinline__ void begin(const DecodePlan &p, const Act *qrow, int kv_head, int nq, float *) {
+    // the group's nq queries, from the row of its first, on their way
+    __device__ __forceinline__ void fetch_queries(const DecodePlan &p, const Act *qrow, int nq, uint32_t) {
         const int lane = threadIdx.x & 31;
         g = lane >> 2;
         t = lane & 3;
-        float kscale = 1.0f;
-        if (k8) kscale = 1.0f / cache_scale(p.k_amax, kv_head);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int h = 8 * n + g;
-            const Act *src = qrow + static_cast<long long>(h) * p.D;
+            const Act *src = qrow + h * p.D;
 #pragma unroll
             for (int c = 0; c < DP / 32; ++c) {
                 // bf16: lane's 8 elements 32c + 8t; codes: its 16 elements 64(c/2) + 16t, 8 at a time
@@ -228,6 +227,15 @@ struct TensorCore {
                 q[n][2 * c + 1][0] = w.z;
                 q[n][2 * c + 1][1] = w.w;
             }
+        }
+    }
+
+    // the queries are there: nothing seen yet
+    __device__ __forceinline__ void begin(const DecodePlan &p, int kv_head, const float *) {
+        float kscale = 1.0f;
+        if (k8) kscale = 1.0f / cache_scale(p.k_amax, kv_head);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
             float unit = p.scale_log2;
             if constexpr (k8) {
                 // fp16 holds a bf16 number's bits but not its range: the query times a power of two
@@ -482,8 +490,8 @@ struct TensorCore {
 // fp32 products
 // ---------------------------------------------------------------------------
 // Eight lanes share a position, DP / 8 elements each; the four groups of lanes
-// keep softmax states of their own.  Queries lie in shared memory, scaled, a copy
-// for each warp.
+// keep softmax states of their own.  Queries lie in shared memory, a copy for each
+// warp.
 template <int DP, int NH>
 struct FloatCore {
     using Cache = float;
@@ -503,17 +511,21 @@ struct FloatCore {
     float acc[NH][J][4];
     int tg, sub;
 
-    __device__ __forceinline__ void begin(const DecodePlan &p, const Act *qrow, int, int nq, float *warp_q) {
+    // the group's nq queries to the warp's place in shared memory, on their way
+    __device__ __forceinline__ void fetch_queries(const DecodePlan &p, const Act *qrow, int nq, uint32_t to) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = lane; i < NH * DP / 4; i += 32) {
+            const int h = i / (DP / 4), e = 4 * (i % (DP / 4));
+            copy16(to + 16 * i, qrow + (h < nq && e < p.D ? h * p.D + e : 0), h < nq && e < p.D ? 16 : 0);
+        }
+    }
+
+    __device__ __forceinline__ void begin(const DecodePlan &, int, const float *warp_q) {
         const int lane = threadIdx.x & 31;
         tg = lane >> 3;
         sub = lane & 7;
         q = warp_q;
-        __syncwarp();  // no lane reads the segment before's queries any more
-        for (int i = lane; i < NH * DP; i += 32) {
-            const int h = i / DP, e = i - h * DP;
-            warp_q[i] = h < nq && e < p.D ? qrow[static_cast<long long>(h) * p.D + e] * p.scale_log2 : 0.0f;
-        }
-        __syncwarp();
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
             m[h] = -INFINITY;
@@ -525,7 +537,7 @@ struct FloatCore {
         }
     }
 
-    __device__ __forceinline__ void step(const DecodePlan &, const char *stage, const Seen &seen) {
+    __device__ __forceinline__ void step(const DecodePlan &p, const char *stage, const Seen &seen) {
         const float *k = reinterpret_cast<const float *>(stage) + tg * DP + 4 * sub, *v = k + kRows * DP;
         float s[I][NH];
 #pragma unroll
@@ -557,7 +569,7 @@ struct FloatCore {
                 x += __shfl_xor_sync(0xffffffffu, x, 2);
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
                 const int row = 4 * i + tg;
-                s[i][h] = row >= seen.lo && row < seen.hi ? x : -INFINITY;
+                s[i][h] = row >= seen.lo && row < seen.hi ? x * p.scale_log2 : -INFINITY;
                 top[h] = fmaxf(top[h], s[i][h]);
             }
             rise |= top[h] > m[h];
@@ -719,57 +731,79 @@ struct Shares {
     }
 };
 
-// One warp's steps of a segment: every `by`-th from its `first` one, through its
-// ring of stages.
+// A segment's part that a block, or one warp of it, takes.
+struct Work {
+    Segment s;
+    int r, rh, u0, u1, units;  // row, head of the row; units [u0, u1) of `units`
+    bool brief;                // one warp's
+    bool valid;
+};
+
+// One warp's steps of a segment are every `by`-th from its first one.  They pass
+// through its ring of S stages, of which the last kOut also take its output
+// at the end; the first kEarly stages of the next segment are under way by then.
 template <class Core>
-__device__ __forceinline__ void walk(Core &core, const DecodePlan &p, const Segment &s, const void *k, const void *v, int first, int by,
-                                     char *ring) {
-    constexpr int R = Core::kRows, S = Core::kStages, kStage = 2 * R * Core::kRowBytes;
-    const int lane = threadIdx.x & 31, t0 = s.t0 + first;
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-    // lane i looks up the i-th of the next 32 steps
-    uint32_t blocks_now = block_at<R>(p, s, t0 + by * lane);
+struct Ring {
+    static constexpr int R = Core::kRows, S = Core::kStages, kStage = 2 * R * Core::kRowBytes, kBytes = S * kStage;
+    static constexpr int kOut = (Core::kHeads * Core::kTileElems * 4 + kStage - 1) / kStage;
+    static constexpr int kEarly = S - kOut < S - 1 ? S - kOut : S - 1;
+    static_assert(kEarly >= 1, "a stage for the next segment beside the output");
+
+    // lane i's look-up of the i-th of 32 steps
+    __device__ __forceinline__ static uint32_t look_up(const DecodePlan &p, const Segment &s, int first, int by) {
+        return block_at<R>(p, s, first + by * (threadIdx.x & 31));
+    }
+    template <int FROM, int TO>
+    __device__ __forceinline__ static void begin(const DecodePlan &p, const Segment &s, const void *k, const void *v, int first, int by,
+                                                 uint32_t blocks, uint32_t to) {
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-        const uint32_t block = __shfl_sync(0xffffffffu, blocks_now, i);
-        if (block != kNone) fetch<Core>(p, k, v, seen_at<R>(s, t0 + by * i), block, to + i * kStage);
-        copies_end();
-    }
-    int stage = 0, ahead = S - 1;
-    for (int from = t0; from < s.t1; from += 32 * by) {
-        uint32_t blocks_next = kNone;
-        if (from + 32 * by < s.t1) blocks_next = block_at<R>(p, s, from + by * (32 + lane));
-        const int n = min(32, (s.t1 - from + by - 1) / by);
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            copies_wait<S - 2>();
-            __syncwarp();  // every lane's copies of this step are there, and the step before has been read
-            const uint32_t then = __shfl_sync(0xffffffffu, i + S - 1 < 32 ? blocks_now : blocks_next, (i + S - 1) & 31);
-            if (then != kNone) fetch<Core>(p, k, v, seen_at<R>(s, from + by * (i + S - 1)), then, to + ahead * kStage);
+        for (int i = FROM; i < TO; ++i) {
+            const uint32_t block = __shfl_sync(0xffffffffu, blocks, i);
+            if (block != kNone) fetch<Core>(p, k, v, seen_at<R>(s, first + by * i), block, to + i * kStage);
             copies_end();
-            if (__shfl_sync(0xffffffffu, blocks_now, i) != kNone)
-                core.step(p, ring + stage * kStage, seen_at<R>(s, from + by * i));
-            stage = stage + 1 == S ? 0 : stage + 1;
-            ahead = ahead + 1 == S ? 0 : ahead + 1;
         }
-        blocks_now = blocks_next;
     }
-    copies_wait<0>();
-    __syncwarp();
-}
+    // begin<0, kEarly> has been called
+    __device__ __forceinline__ static void walk(Core &core, const DecodePlan &p, const Segment &s, const void *k, const void *v, int first,
+                                                int by, uint32_t blocks_now, char *ring) {
+        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+        begin<kEarly, S - 1>(p, s, k, v, first, by, blocks_now, to);
+        int stage = 0, ahead = S - 1;
+        for (int from = first; from < s.t1; from += 32 * by) {
+            uint32_t blocks_next = kNone;
+            if (from + 32 * by < s.t1) blocks_next = look_up(p, s, from + 32 * by, by);
+            const int n = min(32, (s.t1 - from + by - 1) / by);
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                copies_wait<S - 2>();
+                __syncwarp();  // every lane's copies of this step are there, and the step before has been read
+                const uint32_t then = __shfl_sync(0xffffffffu, i + S - 1 < 32 ? blocks_now : blocks_next, (i + S - 1) & 31);
+                if (then != kNone) fetch<Core>(p, k, v, seen_at<R>(s, from + by * (i + S - 1)), then, to + ahead * kStage);
+                copies_end();
+                if (__shfl_sync(0xffffffffu, blocks_now, i) != kNone)
+                    core.step(p, ring + stage * kStage, seen_at<R>(s, from + by * i));
+                stage = stage + 1 == S ? 0 : stage + 1;
+                ahead = ahead + 1 == S ? 0 : ahead + 1;
+            }
+            blocks_now = blocks_next;
+        }
+        copies_wait<0>();
+        __syncwarp();
+    }
+};
 
 template <class Core>
 __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(const __grid_constant__ DecodePlan p) {
     using Act = typename Core::Act;
-    constexpr int DP = Core::kTileElems, NH = Core::kHeads, R = Core::kRows, S = Core::kStages;
-    constexpr int kStage = 2 * R * Core::kRowBytes, kRing = S * kStage;
+    constexpr int DP = Core::kTileElems, NH = Core::kHeads, R = Core::kRows;
+    using Stages = Ring<Core>;
+    constexpr int kRing = Stages::kBytes, kOutAt = (Core::kStages - Stages::kOut) * Stages::kStage;
     constexpr int kSegmentCost = kSegmentPositions / (R * kWarps), kShort = kShortPositions / (R * kWarps);
     // with more segments than blocks, a short one is a single warp's
     const bool alone = !p.by_segment;
     auto is_short = [&](int units) { return alone && units <= kShort; };
     auto cost_of = [&](int units) { return is_short(units) ? 1 + units / 2 : units + kSegmentCost; };
-    static_assert(NH * DP * 4 <= kRing, "a warp's output takes the place of its ring");
-    extern __shared__ __align__(128) char ring[];  // [kWarps][S] stages; at a segment's end [kWarps] outputs [NH][DP]
+    extern __shared__ __align__(128) char ring[];  // [kWarps][stages]
     __shared__ float top[kWarps * NH], sum[kWarps * NH];
     __shared__ __align__(16) float q_smem[sizeof(Act) == 4 ? kWarps * NH * DP : 4];
     __shared__ long long scan[kWarps], start_cost;
@@ -821,97 +855,134 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
     }
     __syncthreads();
 
-    Core core;
-    char *mine_at = ring + warp * kRing;
-    float *mine_q = sizeof(Act) == 4 ? q_smem + warp * NH * DP : nullptr;
-    int r = start_row;
-    Row row = row_at<R>(p, r, nullptr);
+    // the parts of the block's share that this warp has, one after another
+    int r = start_row, turn = 0;
+    Row row = row_at<R>(p, r, nullptr), after = row_at<R>(p, min(r + 1, p.at.n - 1), nullptr);
     int rh = static_cast<int>((from_cost - start_cost) / cost_of(row.units));
     long long at_cost = start_cost + static_cast<long long>(rh) * cost_of(row.units);  // where the segment's cost begins
-    bool listed = false;
-    bool unread = false;
-    int turn = 0;  // whose the next short segment is
-    for (; at_cost < to_cost;) {
-        const bool brief = is_short(row.units);
-        // a segment's cost before its first unit belongs to whoever has that unit; a short segment, to
-        // whoever has its beginning
-        const long long first_unit = at_cost + (brief ? 0 : kSegmentCost), end_cost = at_cost + cost_of(row.units);
-        const int u0 = brief ? 0 : static_cast<int>(max(from_cost - first_unit, 0ll));
-        const int u1 = brief ? row.units : static_cast<int>(min(to_cost - first_unit, static_cast<long long>(row.units)));
-        if (u1 <= u0) break;
-        const bool mine_too = !brief || (at_cost >= from_cost && (turn++ & (kWarps - 1)) == warp);
-        const HeadAt at = head_at(p, rh);
-        const int nq = queries_of(p, rh);
-        Segment s;
-        s.head = at.kv;
-        s.first = row.first;
-        s.last = row.last;
-        s.t0 = (row.t0 + u0) * kWarps;
-        s.t1 = (row.t0 + u1) * kWarps;
-        s.pages = p.at.table + static_cast<long long>(row.last < 0 ? 0 : p.at.sequences ? p.at.sequences[r] : r) * p.at.table_cols;
-        const long long q_at = (static_cast<long long>(r) * p.hq + at.query) * p.D;
-        const void *k = p.k[at.shard], *v = p.v[at.shard];
-        const float vscale = p.v_amax ? 1.0f / cache_scale(p.v_amax, at.shard * p.hk + at.kv) : 1.0f;
-        const int chunks = p.D / 8;
-
-        // the warps' outputs of a segment before have been read
-        if (!brief || unread) __syncthreads();
-        unread = !brief;
-        if (mine_too) {
-            core.begin(p, static_cast<const Act *>(p.q[at.shard]) + q_at, at.shard * p.hk + at.kv, nq, mine_q);
-            walk<Core>(core, p, s, k, v, brief ? 0 : warp, brief ? 1 : kWarps, mine_at);
-            core.finish(p, reinterpret_cast<float *>(mine_at), top + warp * NH, sum + warp * NH);
-            __syncwarp();
+    auto take = [&]() {
+        Work w;
+        w.valid = false;
+        while (at_cost < to_cost) {
+            w.brief = is_short(row.units);
+            // a segment's cost before its first unit belongs to whoever has that unit; a short segment, to
+            // whoever has its beginning
+            const long long first_unit = at_cost + (w.brief ? 0 : kSegmentCost);
+            w.units = row.units;
+            w.u0 = w.brief ? 0 : static_cast<int>(max(from_cost - first_unit, 0ll));
+            w.u1 = w.brief ? row.units : static_cast<int>(min(to_cost - first_unit, static_cast<long long>(row.units)));
+            w.valid = w.brief ? at_cost >= from_cost && (turn++ & (kWarps - 1)) == warp : w.u1 > w.u0;
+            w.r = r;
+            w.rh = rh;
+            w.s.t0 = (row.t0 + w.u0) * kWarps;
+            w.s.t1 = (row.t0 + w.u1) * kWarps;
+            w.s.first = row.first;
+            w.s.last = row.last;
+            at_cost += cost_of(row.units);
+            if (++rh == p.row_heads && at_cost < to_cost) {
+                rh = 0;
+                ++r;
+                row = after;
+                after = row_at<R>(p, min(r + 1, p.at.n - 1), nullptr);
+            }
+            if (w.valid) break;
         }
-        if (!brief) __syncthreads();
+        return w;
+    };
+    // what follows from a part's row and head
+    auto place = [&](Work &w, HeadAt &at) {
+        at = head_at(p, w.rh);
+        w.s.head = at.kv;
+        w.s.pages = p.at.table + static_cast<long long>(w.s.last < 0 ? 0 : p.at.sequences ? p.at.sequences[w.r] : w.r) * p.at.table_cols;
+    };
+    auto first_of = [&](const Work &w) { return w.s.t0 + (w.brief ? 0 : warp); };
+    auto by_of = [&](const Work &w) { return w.brief ? 1 : kWarps; };
+    char *mine_at = ring + warp * kRing;
+    const uint32_t mine_to = static_cast<uint32_t>(__cvta_generic_to_shared(mine_at));
+    float *mine_q = sizeof(Act) == 4 ? q_smem + warp * NH * DP : nullptr;
+    const uint32_t mine_q_to = sizeof(Act) == 4 ? static_cast<uint32_t>(__cvta_generic_to_shared(mine_q)) : 0u;
+    const int chunks = p.D / 8;
 
-        const bool whole = u0 == 0 && u1 == row.units;
+    Core core;
+    auto start = [&](const Work &w, const HeadAt &at, uint32_t blocks) {
+        core.fetch_queries(p, static_cast<const Act *>(p.q[at.shard]) + (static_cast<long long>(w.r) * p.hq + at.query) * p.D,
+                           queries_of(p, w.rh), mine_q_to);
+        Stages::template begin<0, Stages::kEarly>(p, w.s, p.k[at.shard], p.v[at.shard], first_of(w), by_of(w), blocks, mine_to);
+    };
+    bool listed = false;
+    Work w = take();
+    HeadAt at = {};
+    uint32_t blocks = kNone;
+    if (w.valid) {
+        place(w, at);
+        blocks = Stages::look_up(p, w.s, first_of(w), by_of(w));
+        start(w, at, blocks);
+    }
+    while (w.valid) {
+        core.begin(p, at.shard * p.hk + at.kv, mine_q);
+        // the next part's pages are looked up meanwhile
+        Work x = take();
+        HeadAt x_at = {};
+        uint32_t x_blocks = kNone;
+        if (x.valid) {
+            place(x, x_at);
+            x_blocks = Stages::look_up(p, x.s, first_of(x), by_of(x));
+        }
+        Stages::walk(core, p, w.s, p.k[at.shard], p.v[at.shard], first_of(w), by_of(w), blocks, mine_at);
+        // its first keys and values are on their way while this one's are added up
+        if (x.valid) start(x, x_at, x_blocks);
+        core.finish(p, reinterpret_cast<float *>(mine_at + kOutAt), top + warp * NH, sum + warp * NH);
+        if (w.brief)
+            __syncwarp();
+        else
+            __syncthreads();
+
+        const int nq = queries_of(p, w.rh);
+        const long long q_at = (static_cast<long long>(w.r) * p.hq + at.query) * p.D;
+        const float vscale = p.v_amax ? 1.0f / cache_scale(p.v_amax, at.shard * p.hk + at.kv) : 1.0f;
+        const bool whole = w.u0 == 0 && w.u1 == w.units;
         // slot 0: began in an earlier block; 1: ends in a later one
-        float *part = p.partial + (static_cast<long long>(c) * 2 + (u0 == 0 ? 1 : 0)) * part_floats(p.nh, p.D);
-        const int w0 = brief ? warp : 0, w1 = brief ? warp + 1 : kWarps;  // whose states make the segment's
-        if (mine_too) {
-            for (int i = brief ? lane : threadIdx.x; i < nq * chunks; i += brief ? 32 : kBlock) {
-                const int h = i / chunks, e = (i - h * chunks) * 8;
-                float most = -INFINITY, all = 0.0f, f[8] = {};
-                for (int w = w0; w < w1; ++w) most = fmaxf(most, top[w * NH + h]);
-                for (int w = w0; w < w1; ++w) {
-                    const float x = top[w * NH + h], by = x == -INFINITY ? 0.0f : exp2_fast(x - most);
-                    all = fmaf(sum[w * NH + h], by, all);
-                    const float4 *o = reinterpret_cast<const float4 *>(ring + w * kRing) + (h * DP + e) / 4;
-                    const float4 a = o[0], b = o[1];
-                    f[0] = fmaf(a.x, by, f[0]); f[1] = fmaf(a.y, by, f[1]); f[2] = fmaf(a.z, by, f[2]); f[3] = fmaf(a.w, by, f[3]);
-                    f[4] = fmaf(b.x, by, f[4]); f[5] = fmaf(b.y, by, f[5]); f[6] = fmaf(b.z, by, f[6]); f[7] = fmaf(b.w, by, f[7]);
-                }
-                if (whole) {
-                    const float by = all == 0.0f ? 0.0f : vscale / all;
+        float *part = p.partial + (static_cast<long long>(c) * 2 + (w.u0 == 0 ? 1 : 0)) * part_floats(p.nh, p.D);
+        const int w0 = w.brief ? warp : 0, w1 = w.brief ? warp + 1 : kWarps;  // whose states make the segment's
+        for (int i = w.brief ? lane : threadIdx.x; i < nq * chunks; i += w.brief ? 32 : kBlock) {
+            const int h = i / chunks, e = (i - h * chunks) * 8;
+            float most = -INFINITY, all = 0.0f, f[8] = {};
+            for (int j = w0; j < w1; ++j) most = fmaxf(most, top[j * NH + h]);
+            for (int j = w0; j < w1; ++j) {
+                const float t = top[j * NH + h], by = t == -INFINITY ? 0.0f : exp2_fast(t - most);
+                all = fmaf(sum[j * NH + h], by, all);
+                const float4 *o = reinterpret_cast<const float4 *>(ring + j * kRing + kOutAt) + (h * DP + e) / 4;
+                const float4 a = o[0], b = o[1];
+                f[0] = fmaf(a.x, by, f[0]); f[1] = fmaf(a.y, by, f[1]); f[2] = fmaf(a.z, by, f[2]); f[3] = fmaf(a.w, by, f[3]);
+                f[4] = fmaf(b.x, by, f[4]); f[5] = fmaf(b.y, by, f[5]); f[6] = fmaf(b.z, by, f[6]); f[7] = fmaf(b.w, by, f[7]);
+            }
+            if (whole) {
+                const float by = all == 0.0f ? 0.0f : vscale / all;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = all == 0.0f ? 0.0f : f[j] * by;
-                    store8(static_cast<Act *>(p.o[at.shard]) + q_at + static_cast<long long>(h) * p.D + e, f);
-                } else {
-                    store8(part + h * p.D + e, f);
-                    if (e == 0) {
-                        part[p.nh * p.D + h] = most;
-                        part[p.nh * (p.D + 1) + h] = all;
-                    }
+                for (int j = 0; j < 8; ++j) f[j] = all == 0.0f ? 0.0f : f[j] * by;
+                store8(static_cast<Act *>(p.o[at.shard]) + q_at + static_cast<long long>(h) * p.D + e, f);
+            } else {
+                store8(part + h * p.D + e, f);
+                if (e == 0) {
+                    part[p.nh * p.D + h] = most;
+                    part[p.nh * (p.D + 1) + h] = all;
                 }
             }
+        }
+        if (w.u0 == 0 && !w.brief && threadIdx.x == 0 && (p.by_segment || !whole)) {
+            // up to the block that holds the segment's last unit: u1 lies where the share ends, unless that is c
+            const int last = whole ? c : shares.owner(to_cost + (w.units - w.u1) - 1);
+            p.joins[p.by_segment ? w.r * p.row_heads + w.rh : c] = make_int4(w.r, w.rh, c, last);
+            listed = !whole;
+        }
+        // the outputs have been read: the next steps may take their stages
+        if (w.brief)
             __syncwarp();
-        }
-        if (u0 == 0 && !brief && threadIdx.x == 0) {
-            // the block that holds the segment's last unit
-            const int last = shares.owner(first_unit + row.units - 1);
-            if (p.by_segment)
-                p.joins[r * p.row_heads + rh] = make_int4(r, rh, c, last);
-            else if (!whole)
-                p.joins[c] = make_int4(r, rh, c, last);
-        }
-        listed |= u0 == 0 && !whole;
-        at_cost = end_cost;
-        if (++rh == p.row_heads && at_cost < to_cost) {
-            rh = 0;
-            ++r;
-            row = row_at<R>(p, r, nullptr);
-        }
+        else
+            __syncthreads();
+        w = x;
+        at = x_at;
+        blocks = x_blocks;
     }
     if (!p.by_segment && !listed && threadIdx.x == 0) p.joins[c] = make_int4(0, 0, 0, 0);
 }
