@@ -25,7 +25,7 @@ size_t decode_workspace_bytes(const tp_paged_desc &d) {
 }
 
 template <typename Act>
-static tp_status launch_join(const DecodePlan &p, int grid, cudaStream_t st) {
+static tp_status launch_join(DecodePlan &p, int grid, cudaStream_t st) {
     const long long segments = static_cast<long long>(p.at.n) * p.row_heads;
     const int entries = p.by_segment ? static_cast<int>(segments) : grid;
     // parts of a segment: with more than 8, 16 warps take them
@@ -33,6 +33,8 @@ static tp_status launch_join(const DecodePlan &p, int grid, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(entries, many ? p.nh : (p.nh + 3) / 4);
     cfg.blockDim = dim3(many ? 512 : 128);
+    // a few blocks leave room for the next kernel's beside them
+    p.join_early = static_cast<int>(cfg.gridDim.x * cfg.gridDim.y) <= num_sms();
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -42,13 +42,10 @@ constexpr int kMostBlocks = 2 * kMostResident;  // of a launch, and so of the wo
 // A segment costs its block this many positions besides its own (its pages,
 // queries and first keys have to arrive, its parts to be added): without it the
 // blocks that have short rows end last (fp32 window case 37 us, with it 27).
-constexpr int kSegmentPositions = 128;
+constexpr int kSegmentPositions = 192;
 // A row up to this long is read by one warp where there are more segments than
 // blocks.
-#ifndef KSHORT
-#define KSHORT 128
-#endif
-constexpr int kShortPositions = KSHORT;
+constexpr int kShortPositions = 128;
 // With so many units a resident block, one unit in kTailShare goes to half as many blocks more.
 constexpr int kSpread = 32, kTailShare = 8;
 
@@ -190,7 +187,7 @@ struct TensorCore {
     static constexpr int kTileElems = DP;
     static constexpr int kRows = 16, kRowBytes = DP * static_cast<int>(sizeof(Cache));
     // about 192 KB of stages an SM; 16 queries over codes take more registers, so fewer blocks
-    static constexpr bool kFewer = k8 && NT == 2;
+        static constexpr bool kFewer = k8 && NT == 2;
     static constexpr int kStages = kRowBytes == 64 ? (kFewer ? 8 : 6) : kRowBytes == 128 ? (kFewer ? 6 : 4) : kRowBytes % 256 ? 4 : 3;
     static constexpr int kBlocksPerSm = (kRowBytes == 64 ? 4 : kRowBytes == 128 ? 3 : kRowBytes <= 256 ? 2 : 1) - kFewer;
     __device__ __forceinline__ static int swizzle_keys(int row) { return swizzle_k<kRowBytes>(row); }
@@ -756,7 +753,7 @@ struct Ring {
     template <int FROM, int TO>
     __device__ __forceinline__ static void begin(const DecodePlan &p, const Segment &s, const void *k, const void *v, int first, int by,
                                                  uint32_t blocks, uint32_t to) {
-#pragma unroll
+#pragma unroll 1
         for (int i = FROM; i < TO; ++i) {
             const uint32_t block = __shfl_sync(0xffffffffu, blocks, i);
             if (block != kNone) fetch<Core>(p, k, v, seen_at<R>(s, first + by * i), block, to + i * kStage);
@@ -802,7 +799,7 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
     // with more segments than blocks, a short one is a single warp's
     const bool alone = !p.by_segment;
     auto is_short = [&](int units) { return alone && units <= kShort; };
-    auto cost_of = [&](int units) { return is_short(units) ? 1 + units / 2 : units + kSegmentCost; };
+    auto cost_of = [&](int units) { return is_short(units) ? units + 1 : units + kSegmentCost; };
     extern __shared__ __align__(128) char ring[];  // [kWarps][stages]
     __shared__ float top[kWarps * NH], sum[kWarps * NH];
     __shared__ __align__(16) float q_smem[sizeof(Act) == 4 ? kWarps * NH * DP : 4];
@@ -995,6 +992,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) join_kernel(const __gri
     __shared__ float tops[W], sums[W];
     __shared__ __align__(16) float4 outs[W == 1 ? 1 : W][64];
     wait_for_stream();
+    if (p.join_early) let_next_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.y * kQueries + (W == 1 ? warp : 0);
     const int4 j = p.joins[blockIdx.x];
