@@ -46,7 +46,9 @@
  *     and returns early.  Every MLP and sub-block handle owns a status word
  *     of its own, which tp_mlp_sync_status() / tp_layer_sync_status() report
  *     (and clear); the calls without a handle (single layers, FP8 quantiser)
- *     share one word, which tp_sync_status() reports (and clears).
+ *     share one word, which tp_sync_status() reports (and clears).  Page tables
+ *     are read on the device: a kernel that meets an index out of range leaves
+ *     that row or page out, and tp_paged_sync_status() reports TP_ERR_INDEX.
  *     tp_last_error() gives a message for the last failing call of the
  *     calling thread.
  */
@@ -720,8 +722,11 @@ TP_API tp_status tp_paged_append(tp_paged *h, const void *const *X, const int32_
  * only scores of -infinity.  A row whose sequence or position is out of range
  * (as above) gives zero, a page out of range is left out of the sum; both set
  * the handle's index word.
+ * A value that is not finite leaves its element of the rows that see it not
+ * finite (infinite, or NaN), a score of NaN or +infinity the whole row NaN.
  * Scores, softmax and sums are fp32; bf16 and FP8 weights enter the products as
- * the sum of two 16-bit numbers.  The long axis is split over blocks, whose
+ * the sum of two 16-bit numbers, and fp32 numbers, with more than four queries to
+ * a key head, as two tf32 (2^-21 of a product).  The long axis is split over blocks, whose
  * results are joined in a fixed order: outputs are deterministic.
  * workspace: >= tp_paged_workspace_bytes, 256-byte aligned; contents on entry
  * are ignored. */
@@ -824,8 +829,8 @@ TP_API tp_status tp_set_band_rows(int rows);
  * SMs the previous kernel in the stream has left, set up their barriers and
  * tensor memory there, and wait in griddepcontrol.wait until that kernel
  * has completed and its writes are visible before they read an operand or
- * write an output, so stream order and results are unchanged.  The block norm
- * and AdamW kernels are launched the same way.  on = 0 launches all of them in
+ * write an output, so stream order and results are unchanged.  The block norm,
+ * AdamW, rotary and paged-attention kernels are launched the same way.  on = 0 launches all of them in
  * plain stream order.  TP_ERR_ARG unless on is 0 or 1. */
 TP_API tp_status tp_set_launch_overlap(int on);
 

@@ -9,7 +9,7 @@ namespace attn {
 // up to 8 or 16 to the columns of the matrix instructions (16 only up to 128
 // elements a head, where their outputs fit a lane's registers), up to 4 in fp32.
 static void cut_queries(int dtype, int D, int per, int *groups, int *nh) {
-    const int most = dtype == TP_DT_F32 ? 4 : D <= 128 ? 16 : 8;
+    const int most = D <= 128 ? 16 : 8;
     *groups = (per + most - 1) / most;
     *nh = (per + *groups - 1) / *groups;
 }

@@ -49,6 +49,11 @@ constexpr int kShortPositions = 128;
 // With so many units a resident block, one unit in kTailShare goes to half as many blocks more.
 constexpr int kSpread = 32, kTailShare = 8;
 
+// Queries of an fp32 key head that plain fp32 products take; more go to Tf32Core,
+// whose splits cost the same for up to 8 (4 queries of 256 elements: 59 us, by
+// tf32 71; 16 of 128: 140 us in four passes, by tf32 78).
+constexpr int kFloatQueries = 4;
+
 enum CacheKind : int { CACHE_BF16 = 0, CACHE_FP8 = 1, CACHE_F32 = 2 };
 
 // A segment of a row: what the warps need to walk it.
@@ -637,6 +642,214 @@ struct FloatCore {
 };
 
 // ---------------------------------------------------------------------------
+// fp32 products by tf32: more than four queries of an fp32 cache
+// ---------------------------------------------------------------------------
+// A number is split into the tf32 it is cut to and the rest, whose own tf32 part is
+// taken: x = hi + lo to 2^-21, and x y = hi hi + hi lo + lo hi to 3 2^-22, in fp32
+// sums.  Fragments as in TensorCore, with 4-byte elements: a lane's 16 bytes of a
+// key are two contractions of 8, and the rows of V^T the elements 2i and 2i + 1 of
+// its four.  Sums of hi hi are kept apart in the scores: where they are not
+// finite, the rest (inf - inf) says nothing.  Queries lie in shared memory.
+__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+
+template <int DP, int NT>
+struct Tf32Core {
+    using Cache = float;
+    using Act = float;
+    static constexpr int kHeads = 8 * NT;
+    static constexpr int kTileElems = DP;
+    static constexpr int kRows = DP <= 128 ? 16 : 8, kRowBytes = DP * 4, H = kRows / 8;
+    static constexpr int kStages = DP == 128 || DP == 256 ? 3 : DP == 64 ? 3 : 4;
+    static constexpr int kBlocksPerSm = DP == 64 ? 2 : 1;
+    // keys are read four pieces of 8 rows at a time, values two of four rows
+    __device__ __forceinline__ static int swizzle_keys(int row) { return (row & 1) << 6; }
+    __device__ __forceinline__ static int swizzle_values(int row) { return (row & 3) << 5; }
+
+    const char *q;  // [kHeads][DP], its 16-byte pieces exchanged as a key's
+    float m[NT][2], l[NT][2];
+    float acc[DP / 32][2][NT][4];
+    int g, t;
+
+    __device__ __forceinline__ void fetch_queries(const DecodePlan &p, const Act *qrow, int nq, uint32_t to) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll 4
+        for (int i = lane; i < kHeads * DP / 4; i += 32) {
+            const int h = i / (DP / 4), e = 4 * (i % (DP / 4));
+            const bool in = h < nq && e < p.D;
+            copy16(to + ((16 * i) ^ swizzle_keys(h)), qrow + (in ? h * p.D + e : 0), in ? 16 : 0);
+        }
+    }
+
+    __device__ __forceinline__ void begin(const DecodePlan &, int, const float *warp_q) {
+        const int lane = threadIdx.x & 31;
+        g = lane >> 2;
+        t = lane & 3;
+        q = reinterpret_cast<const char *>(warp_q);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                m[n][r] = -INFINITY;
+                l[n][r] = 0.0f;
+            }
+#pragma unroll
+        for (int b = 0; b < DP / 32; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[b][i][n][r] = 0.0f;
+    }
+
+    __device__ __forceinline__ void step(const DecodePlan &p, const char *stage, const Seen &seen) {
+        float big[NT][4] = {}, rest[NT][4] = {};
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) {
+            uint32_t hi[2][4] = {}, lo[2][4] = {};  // of the two contractions: rows g and g + 8, elements 2u and 2u + 1
+#pragma unroll
+            for (int r = 0; r < H; ++r) {
+                const float4 x = *reinterpret_cast<const float4 *>(stage + (((g + 8 * r) * kRowBytes + 64 * c + 16 * t) ^ swizzle_keys(g)));
+                split_tf32(x.x, hi[0][r], lo[0][r]);
+                split_tf32(x.y, hi[0][r + 2], lo[0][r + 2]);
+                split_tf32(x.z, hi[1][r], lo[1][r]);
+                split_tf32(x.w, hi[1][r + 2], lo[1][r + 2]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float4 y = *reinterpret_cast<const float4 *>(q + (((8 * n + g) * kRowBytes + 64 * c + 16 * t) ^ swizzle_keys(g)));
+                uint32_t qh[4], ql[4];
+                split_tf32(y.x, qh[0], ql[0]);
+                split_tf32(y.y, qh[1], ql[1]);
+                split_tf32(y.z, qh[2], ql[2]);
+                split_tf32(y.w, qh[3], ql[3]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    mma1688(big[n], hi[u], qh[2 * u], qh[2 * u + 1]);
+                    mma1688(rest[n], hi[u], ql[2 * u], ql[2 * u + 1]);
+                    mma1688(rest[n], lo[u], qh[2 * u], qh[2 * u + 1]);
+                }
+            }
+        }
+        float s[NT][2 * H];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2 * H; ++r) {
+                const int row = r < 2 ? g : g + 8;
+                const float x = fabsf(big[n][r]) <= 3.4e38f ? big[n][r] + rest[n][r] : big[n][r];
+                s[n][r] = row >= seen.lo && row < seen.hi ? x * p.scale_log2 : -INFINITY;
+            }
+
+        float top[NT][2];
+        bool rise = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float x = H == 2 ? fmaxf(s[n][r], s[n][r + 2 * (H - 1)]) : s[n][r];
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                top[n][r] = x;
+                rise |= x > m[n][r];
+            }
+        if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float now = fmaxf(m[n][r], top[n][r]);
+                    const float f = now == -INFINITY ? 1.0f : exp2_fast(m[n][r] - now);
+                    m[n][r] = now;
+                    l[n][r] *= f;
+#pragma unroll
+                    for (int b = 0; b < DP / 32; ++b)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            acc[b][i][n][r] *= f;
+                            acc[b][i][n][r + 2] *= f;
+                        }
+                }
+        }
+        // P^T as the second operand: positions t and t + 4 (of each 8) of query g, from the lanes that have them
+        uint32_t ph[NT][H][2], pl[NT][H][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int r = 0; r < 2 * H; ++r) {
+                const float top_of = m[n][r & 1] == -INFINITY ? 0.0f : m[n][r & 1];
+                s[n][r] = exp2_fast(s[n][r] - top_of);
+                l[n][r & 1] += s[n][r];
+            }
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int from = 4 * (t + 4 * j) + g / 2;
+                    const float even = __shfl_sync(0xffffffffu, s[n][2 * h], from), odd = __shfl_sync(0xffffffffu, s[n][2 * h + 1], from);
+                    split_tf32(g & 1 ? odd : even, ph[n][h][j], pl[n][h][j]);
+                }
+        }
+        const char *v = stage + kRows * kRowBytes;
+#pragma unroll
+        for (int b = 0; b < DP / 32; ++b)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                // positions t and t + 4 of the 8, the lane's four elements
+                const float4 x = *reinterpret_cast<const float4 *>(v + (((t + 8 * h) * kRowBytes + 128 * b + 16 * g) ^ (t << 5)));
+                const float4 y = *reinterpret_cast<const float4 *>(v + (((t + 4 + 8 * h) * kRowBytes + 128 * b + 16 * g) ^ (t << 5)));
+                uint32_t hi[2][4], lo[2][4];
+                split_tf32(x.x, hi[0][0], lo[0][0]);
+                split_tf32(x.y, hi[0][1], lo[0][1]);
+                split_tf32(x.z, hi[1][0], lo[1][0]);
+                split_tf32(x.w, hi[1][1], lo[1][1]);
+                split_tf32(y.x, hi[0][2], lo[0][2]);
+                split_tf32(y.y, hi[0][3], lo[0][3]);
+                split_tf32(y.z, hi[1][2], lo[1][2]);
+                split_tf32(y.w, hi[1][3], lo[1][3]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma1688(acc[b][i][n], hi[i], ph[n][h][0], ph[n][h][1]);
+                        mma1688(acc[b][i][n], hi[i], pl[n][h][0], pl[n][h][1]);
+                        mma1688(acc[b][i][n], lo[i], ph[n][h][0], ph[n][h][1]);
+                    }
+            }
+    }
+
+    __device__ __forceinline__ void finish(const DecodePlan &, float *out, float *top, float *sum) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float x = l[n][r];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                const int h = 8 * n + 2 * t + r;
+                if (g == 0) {
+                    top[h] = m[n][r];
+                    sum[h] = x;
+                }
+#pragma unroll
+                for (int b = 0; b < DP / 32; ++b)
+                    *reinterpret_cast<float4 *>(out + h * DP + 32 * b + 4 * g) =
+                        make_float4(acc[b][0][n][r], acc[b][0][n][r + 2], acc[b][1][n][r], acc[b][1][n][r + 2]);
+            }
+    }
+};
+
+// ---------------------------------------------------------------------------
 // the blocks' stretches
 // ---------------------------------------------------------------------------
 // Where a row's positions lie, and how many units a key head of it has (at
@@ -844,7 +1057,7 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
         int r = r0;
         for (;; ++r) {
             const long long n = static_cast<long long>(cost_of(row_at<R>(p, r, nullptr).units)) * p.row_heads;
-            if (from_cost < x + n) break;
+            if (from_cost < x + n || r + 1 == r1) break;
             x += n;
         }
         start_row = r;
@@ -855,7 +1068,7 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
     // the parts of the block's share that this warp has, one after another
     int r = start_row, turn = 0;
     Row row = row_at<R>(p, r, nullptr), after = row_at<R>(p, min(r + 1, p.at.n - 1), nullptr);
-    int rh = static_cast<int>((from_cost - start_cost) / cost_of(row.units));
+    int rh = min(static_cast<int>((from_cost - start_cost) / cost_of(row.units)), p.row_heads - 1);
     long long at_cost = start_cost + static_cast<long long>(rh) * cost_of(row.units);  // where the segment's cost begins
     auto take = [&]() {
         Work w;
@@ -876,9 +1089,9 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
             w.s.first = row.first;
             w.s.last = row.last;
             at_cost += cost_of(row.units);
-            if (++rh == p.row_heads && at_cost < to_cost) {
+            if (++rh == p.row_heads) {
+                if (++r == p.at.n) at_cost = to_cost;
                 rh = 0;
-                ++r;
                 row = after;
                 after = row_at<R>(p, min(r + 1, p.at.n - 1), nullptr);
             }

@@ -6,9 +6,12 @@ namespace attn {
 
 template <int DP>
 static tp_status launch_width(DecodePlan &p, int *grid, cudaStream_t st) {
+    if constexpr (DP <= 128)
+        if (p.nh > 8) return launch_core<Tf32Core<DP, 2>>(p, grid, st);
     return p.nh == 1   ? launch_core<FloatCore<DP, 1>>(p, grid, st)
            : p.nh == 2 ? launch_core<FloatCore<DP, 2>>(p, grid, st)
-                       : launch_core<FloatCore<DP, 4>>(p, grid, st);
+           : p.nh <= kFloatQueries ? launch_core<FloatCore<DP, 4>>(p, grid, st)
+                       : launch_core<Tf32Core<DP, 1>>(p, grid, st);
 }
 
 tp_status launch_decode_f32(DecodePlan &p, int *grid, cudaStream_t st) {

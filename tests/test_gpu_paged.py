@@ -352,3 +352,72 @@ def test_decode_short_and_long_rows(tp, dtype, shape):
     lengths[5:9] = [128, 129, 127, 1]
     decode_case(tp, rng, lengths, heads, kv, D, 32, T, dtype)
     decode_case(tp, rng, lengths, heads, kv, D, 16, T, dtype, window=40)
+
+
+@pytest.mark.parametrize("heads", [2, 16])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_infinite_values(tp, dtype, heads):
+    """An infinite value leaves its element not finite, of the queries of its head alone, and nothing else; one or
+    eight queries a key head."""
+    rng = np.random.default_rng(13)
+    table, pages = table_for(rng, [50, 50], 16)
+    h = tp.TPPagedAttention(heads, 2, 64, 16, pages, dtype=dtype)
+    K, V = (torch.randn(h.cache_shape, device="cuda").to(TORCH[dtype]) for _ in range(2))
+    q = torch.randn(2, heads * 64, device="cuda").to(TORCH[dtype])
+    V[int(table[1, 1]), 1, 4, 9] = float("-inf")
+    K[int(table[0, 2]), 0, 3] = float("-inf")     # mixed signs of q: inf - inf
+    o = torch.empty_like(q)
+    h.decode(q, cuda_i32([49, 49]), cuda_i32(table), K, V, o, tp.alloc_workspace(h.workspace_bytes()))
+    o = o.view(2, heads, 64).float().cpu()
+    per = heads // 2
+    assert torch.isnan(o[0, :per]).all() and torch.isfinite(o[0, per:]).all()
+    assert not torch.isfinite(o[1, per:, 9]).any()   # infinite, or NaN: a weight's second part may be zero
+    o[1, per:, 9] = 0
+    assert torch.isfinite(o[1]).all()
+
+
+FIRST_CALL = """
+import torch, sys
+sys.path.insert(0, {root!r})
+import tensor_transformer_mlp_shard_gb300 as tp
+dt = {dtype!r}
+h = tp.TPPagedAttention(8, 2, 64, 16, 12, dtype=dt)
+r = tp.TPRotary(3, 1, 8, 2, 64, dtype="f32" if dt == "f32" else "bf16")
+act = torch.float32 if dt == "f32" else torch.bfloat16
+x = torch.randn(3, 12 * 64, device="cuda").to(act)
+K, V = (torch.zeros(h.cache_shape, dtype=h.cache_dtype, device="cuda") for _ in range(2))
+q, o = (torch.zeros(3, 8 * 64, dtype=act, device="cuda") for _ in range(2))
+at = torch.tensor([0, 40, -1], dtype=torch.int32, device="cuda")
+table = torch.arange(9, dtype=torch.int32, device="cuda").view(3, 3)
+ws = tp.alloc_workspace(h.workspace_bytes())
+a = dict(k_amax=torch.ones(2, device="cuda"), v_amax=torch.ones(2, device="cuda")) if dt == "fp8" else dict()
+def step(out):
+    h.append(x, at, table, K, V, q, **a)
+    h.decode(q, at, table, K, V, out, ws, **a)
+    r.fwd(x)
+    r.bwd(x)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):          # the process's first calls of these kernels
+    step(o)
+x0 = x.clone()
+g.replay()
+torch.cuda.synchronize()
+x.copy_(x0)
+want = torch.empty_like(o)
+step(want)
+torch.cuda.synchronize()
+assert torch.equal(o, want) and bool(o[1].any()) and not bool(o[2].any()) and h.sync_status() == 0
+print("same")
+"""
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+def test_first_call_may_be_captured(dtype):
+    """No call before the capture: what a kernel needs to be set up is not a stream's work."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(root=root, dtype=dtype)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
