@@ -58,25 +58,58 @@ __device__ __forceinline__ void bad_index(const Pages &p) { *reinterpret_cast<vo
 // product in 32 bits (or 64, far out) loses.
 struct Turns {
     uint64_t per_position[kMaxPairs];
-    float a;  // attention factor
+    float a, a_rest;  // attention factor, and what its rounding lost
 };
 
 tp_status rope_validate(const tp_rope_desc *r, int head_dim);
 void rope_turns(const tp_rope_desc &r, Turns *t);
 
-// a cos and a sin of pair i at position p: the angle to 2^-33 of a turn, taken
-// to the nearest quarter turn in integers so that the rest, at most an eighth,
-// is fp32 to 2^-25 of itself
-__device__ __forceinline__ float2 turn(const Turns &t, int i, int p) {
-    const uint64_t phase = t.per_position[i] * static_cast<uint32_t>(p);
+// a cos and a sin at position p of a pair's turn, rounded as if they had been exact (but
+// for one in 500): keys in 8 bits should lie on the same side of a code's edge
+// as the definition's.  The angle to 2^-33 of a turn is taken to the nearest
+// quarter in integers; the rest x, an eighth of a turn at most, and the first
+// two terms of either series are pairs of fp32 numbers (Dekker's products and
+// Knuth's sums), the later terms, Taylor's up to x^13, single ones.  About 60
+// operations a pair and token, against some 1500 of its heads.
+__device__ __forceinline__ float2 turn(const Turns &t, uint64_t per_position, int p) {
+    const uint64_t phase = per_position * static_cast<uint32_t>(p);
     const uint32_t hi = static_cast<uint32_t>((phase + 0x80000000ull) >> 32);
     const uint32_t quarter = (hi + 0x20000000u) >> 30;
     const int rest = static_cast<int>(hi - (quarter << 30));
-    float s, c;
-    sincospif(static_cast<float>(rest) * 0x1p-31f, &s, &c);
-    const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
+    const float rough = static_cast<float>(rest);
+    const float r = rough * 0x1p-31f, r_rest = static_cast<float>(rest - static_cast<int>(rough)) * 0x1p-31f;  // half turns
+    constexpr float kPi = 0x1.921fb6p+1f, kPiRest = -0x1.777a5cp-24f;                // pi
+    constexpr float kSixth = 0x1.555556p-3f, kSixthRest = -0x1.555556p-28f;          // 1 / 3!
+    constexpr float k24th = 0x1.555556p-5f, k24thRest = -0x1.555556p-30f;            // 1 / 4!
+    const float x = __fmul_rn(r, kPi), x_rest = fmaf(r, kPi, -x) + fmaf(r, kPiRest, r_rest * kPi);
+    const float z = __fmul_rn(x, x), z_rest = fmaf(x + x, x_rest, fmaf(x, x, -z));
+    // sin x = x - x^3 / 6 + x^5 p(z)
+    float q = 1.0f / 6227020800.0f;
+    q = fmaf(q, z, -1.0f / 39916800.0f);
+    q = fmaf(q, z, 1.0f / 362880.0f);
+    q = fmaf(q, z, -1.0f / 5040.0f);
+    q = fmaf(q, z, 1.0f / 120.0f);
+    const float u = __fmul_rn(z, x), u_rest = fmaf(z, x_rest, fmaf(z_rest, x, fmaf(z, x, -u)));
+    const float v = __fmul_rn(u, kSixth), v_rest = fmaf(u, kSixthRest, fmaf(u_rest, kSixth, fmaf(u, kSixth, -v)));
+    const float s0 = __fsub_rn(x, v), sb = __fsub_rn(s0, x);
+    const float s1 = __fsub_rn(x, __fsub_rn(s0, sb)) - __fadd_rn(v, sb) + (fmaf(__fmul_rn(z, u), q, x_rest) - v_rest);
+    // cos x = 1 - z / 2 + z^2 / 24 + z^3 p(z)
+    q = 1.0f / 479001600.0f;
+    q = fmaf(q, z, -1.0f / 3628800.0f);
+    q = fmaf(q, z, 1.0f / 40320.0f);
+    q = fmaf(q, z, -1.0f / 720.0f);
+    const float w = __fmul_rn(z, z), w_rest = fmaf(z + z, z_rest, fmaf(z, z, -w));
+    const float y = __fmul_rn(w, k24th), y_rest = fmaf(w, k24thRest, fmaf(w_rest, k24th, fmaf(w, k24th, -y)));
+    const float h = __fmul_rn(0.5f, z), c = __fsub_rn(1.0f, h), c_rest = __fsub_rn(__fsub_rn(1.0f, c), h);
+    const float c0 = __fadd_rn(c, y), cb = __fsub_rn(c0, c);
+    const float c1 = __fsub_rn(c, __fsub_rn(c0, cb)) + __fsub_rn(y, cb) + (fmaf(__fmul_rn(w, z), q, y_rest) + fmaf(-0.5f, z_rest, c_rest));
+    // times a, in one rounding each
+    const float sa = __fmul_rn(s0, t.a), ca = __fmul_rn(c0, t.a);
+    const float sn = sa + fmaf(s1, t.a, fmaf(s0, t.a_rest, fmaf(s0, t.a, -sa)));
+    const float cs = ca + fmaf(c1, t.a, fmaf(c0, t.a_rest, fmaf(c0, t.a, -ca)));
+    const float cosine = quarter & 1 ? sn : cs, sine = quarter & 1 ? cs : sn;
     // quarter 0: (c, s)  1: (-s, c)  2: (-c, -s)  3: (s, -c)
-    return make_float2((quarter == 1 || quarter == 2 ? -x : x) * t.a, (quarter & 2 ? -y : y) * t.a);
+    return make_float2(quarter == 1 || quarter == 2 ? -cosine : cosine, quarter & 2 ? -sine : sine);
 }
 
 // Decode attention (paged_decode.cu).

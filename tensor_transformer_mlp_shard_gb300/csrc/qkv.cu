@@ -171,6 +171,12 @@ __device__ __forceinline__ void read_turns(float *to, const float *from) {
     }
 }
 
+// products and sums rounded one by one, as the definition in fp32 has them
+__device__ __forceinline__ void turn_pair(float x, float y, float c, float s, float &to_x, float &to_y) {
+    to_x = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+    to_y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+}
+
 // the pairs (first + 2i, first + 2i + 1) of a chunk, those that turn
 template <int VE>
 __device__ __forceinline__ void turn_neighbours(float (&f)[VE], int first, int half, const float *cs, const float *sn) {
@@ -182,8 +188,7 @@ __device__ __forceinline__ void turn_neighbours(float (&f)[VE], int first, int h
     for (int e = 0; e < VE; e += 2)
         if ((first + e) / 2 < half) {
             const float x = f[e], y = f[e + 1];
-            f[e] = x * c[e / 2] - y * s[e / 2];
-            f[e + 1] = y * c[e / 2] + x * s[e / 2];
+            turn_pair(x, y, c[e / 2], s[e / 2], f[e], f[e + 1]);
         }
 }
 
@@ -245,29 +250,36 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
             for (int i = 0; i < kFlight; ++i) copy(i, i);
         }
         if (!turned) {
-            const int pairs = p.half > 0 ? p.half : 1;
-            for (int k = threadIdx.x; k < tokens * pairs; k += blockDim.x) {
-                const int t = k / pairs, pair = k - t * pairs, m = token0 + t;
-                if (m >= p.at.n) break;
-                const int pos = MODE == ROTATE && !p.at.positions ? static_cast<int>(p.batch.div(m)) : p.at.positions[m];
-                if (pair == 0) {
-                    int ok = pos >= 0;
-                    if (MODE != ROTATE && ok) {
-                        const int seq = p.at.sequences ? p.at.sequences[m] : m;
-                        uint32_t off;
-                        const int col = p.at.page.divmod(pos, off);
-                        ok = static_cast<unsigned>(seq) < static_cast<unsigned>(p.at.table_rows) && col < p.at.table_cols;
-                        const int page = ok ? p.at.table[static_cast<long long>(seq) * p.at.table_cols + col] : -1;
-                        ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.at.pages);
-                        if (!ok && blockIdx.y == 0) bad_index(p.at);
-                        // the heads of a page lie page_size rows apart
-                        slot_of[t] = static_cast<long long>(page) * p.hk * p.at.page_size + off;
-                    }
-                    active[t] = ok;
+            auto position = [&](int m) {
+                return MODE == ROTATE && !p.at.positions ? static_cast<int>(p.batch.div(m)) : p.at.positions[m];
+            };
+            if (threadIdx.x < tokens && token0 + static_cast<int>(threadIdx.x) < p.at.n) {
+                const int m = token0 + threadIdx.x, pos = position(m);
+                int ok = pos >= 0;
+                if (MODE != ROTATE && ok) {
+                    const int seq = p.at.sequences ? p.at.sequences[m] : m;
+                    uint32_t off;
+                    const int col = p.at.page.divmod(pos, off);
+                    ok = static_cast<unsigned>(seq) < static_cast<unsigned>(p.at.table_rows) && col < p.at.table_cols;
+                    const int page = ok ? p.at.table[static_cast<long long>(seq) * p.at.table_cols + col] : -1;
+                    ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.at.pages);
+                    if (!ok && blockIdx.y == 0) bad_index(p.at);
+                    // the heads of a page lie page_size rows apart
+                    slot_of[threadIdx.x] = static_cast<long long>(page) * p.hk * p.at.page_size + off;
                 }
-                const float2 r = turn(p.turns, pair, pos);
-                cs[t * pitch + pair] = r.x;
-                sn[t * pitch + pair] = r.y * p.sign;
+                active[threadIdx.x] = ok;
+            }
+            // a thread keeps to one pair, whose turn a position is read once: the lanes' different ones come
+            // one after another
+            const int groups = max(1, static_cast<int>(blockDim.x) / max(1, p.half));
+            for (int k = threadIdx.x; k < groups * p.half; k += blockDim.x) {
+                const int pair = k % p.half;
+                const uint64_t per_position = p.turns.per_position[pair];
+                for (int t = k / p.half; t < tokens && token0 + t < p.at.n; t += groups) {
+                    const float2 r = turn(p.turns, per_position, position(token0 + t));
+                    cs[t * pitch + pair] = r.x;
+                    sn[t * pitch + pair] = r.y * p.sign;
+                }
             }
             turned = true;
             __syncthreads();
@@ -317,8 +329,7 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
 #pragma unroll
                         for (int e = 0; e < VE; ++e) {
                             const float f = fa[e], g = fb[e];
-                            fa[e] = f * c[e] - g * s[e];
-                            fb[e] = g * c[e] + f * s[e];
+                            turn_pair(f, g, c[e], s[e], fa[e], fb[e]);
                         }
                         a.pack(fa);
                         b.pack(fb);
@@ -390,6 +401,7 @@ void rope_turns(const tp_rope_desc &r, Turns *t) {
     double a = r.attention_factor;
     if (a == 0.0) a = r.scaling == TP_ROPE_PARTS ? 0.1 * std::log(r.factor) + 1.0 : 1.0;
     t->a = static_cast<float>(a);
+    t->a_rest = static_cast<float>(a - t->a);
 }
 
 template <typename E, int MODE>
