@@ -894,6 +894,7 @@ class TPAdamW:
 # ---------------------------------------------------------------------------
 # attention around the projections
 # ---------------------------------------------------------------------------
+_i32, _f32 = torch.int32, torch.float32  # (an attribute of torch takes as long to find as one of a tensor)
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 
 
@@ -991,7 +992,7 @@ class TPRotary:
         dev = _device() if self.M else 0
         px = _shards(x_name, x, self.T, self._n, self._act, dev)
         py = px if y is None else _shards(y_name, y, self.T, self._n, self._act, dev)
-        at = None if positions is None else _vector("positions", positions, self.M, torch.int32, dev)
+        at = None if positions is None else _vector("positions", positions, self.M, _i32, dev)
         status = call(self._h, px, at, py, _stream_on(dev, stream))
         if status:
             _check(status)
@@ -1062,13 +1063,13 @@ class TPPagedAttention:
             (n,), (rows, cols) = positions.shape, table.shape
         except (AttributeError, ValueError):
             raise ValueError("positions: must be a CUDA tensor [n], table: one [sequences, columns]") from None
-        at = (_vector("positions", positions, n, torch.int32, dev),
-              None if sequences is None else _vector("sequences", sequences, n, torch.int32, dev), n,
-              _vector("table", table, rows * cols, torch.int32, dev), rows, cols)
+        at = (_vector("positions", positions, n, _i32, dev),
+              None if sequences is None else _vector("sequences", sequences, n, _i32, dev), n,
+              _vector("table", table, rows * cols, _i32, dev), rows, cols)
         if self.dtype != "fp8":
             return at + (None, None)
-        return at + (_vector("k_amax", k_amax, self.kv_heads, torch.float32, dev),
-                     _vector("v_amax", v_amax, self.kv_heads, torch.float32, dev))
+        return at + (_vector("k_amax", k_amax, self.kv_heads, _f32, dev),
+                     _vector("v_amax", v_amax, self.kv_heads, _f32, dev))
 
     def append(self, X, positions, table, K, V, Q, sequences=None, k_amax=None, v_amax=None, stream=None):
         """New tokens X [n, (heads + 2 kv_heads) / T * head_dim] a shard: turned

@@ -495,12 +495,11 @@ struct tp_paged {
 };
 
 static tp_status at_pointer(const void *p, const char *name, int i, int n, unsigned align) {
+    if (p && !(reinterpret_cast<uintptr_t>(p) & (align - 1))) return TP_OK;
     char at[16] = "";
     if (n > 1) snprintf(at, sizeof(at), "[%d]", i);
     if (!p) return set_error(TP_ERR_ARG, "%s%s is NULL", name, at);
-    if (reinterpret_cast<uintptr_t>(p) & (align - 1))
-        return set_error(TP_ERR_ARG, "%s%s is not %u-byte aligned", name, at, align);
-    return TP_OK;
+    return set_error(TP_ERR_ARG, "%s%s is not %u-byte aligned", name, at, align);
 }
 
 // copies an array of n pointers into a plan after checking them
