@@ -88,7 +88,7 @@ struct Seen {
 template <int R>
 __device__ __forceinline__ Seen seen_at(const Segment &s, int step) {
     const int base = step * R;
-    return {max(s.first - base, 0), min(s.last + 1 - base, R)};
+    return {max(s.first - base, 0), min(s.last - base, R - 1) + 1};
 }
 
 // `bytes` of 16 bytes, 0 or 16, the rest zero

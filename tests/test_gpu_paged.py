@@ -421,3 +421,70 @@ def test_first_call_may_be_captured(dtype):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(root=root, dtype=dtype)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+def test_the_last_positions(tp, dtype):
+    """Positions up to the largest int32, through a window, in a table whose other pages are gone."""
+    page_size, window, kv, D = 4096, 70, 2, 32
+    cols = 2 ** 31 // page_size
+    h = tp.TPPagedAttention(6, kv, D, page_size, 3, dtype=dtype, window=window, rope=tp.Rope(dim=0))
+    table = torch.full((2, cols), -1, dtype=torch.int32, device="cuda")
+    table[0, cols - 1], table[1, cols - 2], table[1, cols - 1] = 2, 0, 1
+    at = [2 ** 31 - 1, (cols - 1) * page_size + 20]      # the second sees the end of a page and the beginning of the next
+    rng = np.random.default_rng(14)
+    n = window + 1
+    amax = dict(k_amax=torch.full((kv,), 5.0, device="cuda"), v_amax=torch.full((kv,), 5.0, device="cuda")) if dtype == "fp8" else {}
+    K, V = (torch.full(h.cache_shape, 0x7F if dtype == "fp8" else float("nan"), dtype=h.cache_dtype, device="cuda") for _ in range(2))
+    q = torch.empty(n, 6 * D, dtype=TORCH[dtype], device="cuda")
+    keys, values_ = [], []
+    for s, p in enumerate(at):
+        x, xf = values(rng, (n, (6 + 2 * kv) * D), dtype)
+        positions = [p - window + 1 + i for i in range(window)] + [-1]
+        h.append(x, cuda_i32(positions), table, K, V, q, sequences=cuda_i32([s] * n), **amax)
+        keys.append(xf[:window, 6 * D:(6 + kv) * D].reshape(window, kv, D))
+        values_.append(xf[:window, (6 + kv) * D:].reshape(window, kv, D))
+    q, qf = values(rng, (2, 6 * D), dtype)
+    o = torch.empty_like(q)
+    h.decode(q, cuda_i32(at), table, K, V, o, tp.alloc_workspace(h.workspace_bytes()), **amax)
+    assert h.sync_status() == 0
+    for s in range(2):
+        Kf, Vf = (x[s].transpose(1, 0, 2)[None] for x in (keys, values_))
+        pad = np.zeros((1, kv, 80, D))
+        pad_v = pad.copy()
+        pad[:, :, :window], pad_v[:, :, :window] = Kf, Vf
+        want = ref.decode(qf[s:s + 1].reshape(1, 6, D), [window - 1], [0], np.zeros((1, 1), int), pad, pad_v, D ** -0.5)
+        bound = decode_bound(*want, D, dtype)
+        if dtype == "fp8":   # the cache's own rounding, 2^-4 of keys and values: a score by 2^-4 spread
+            bound = bound + want[1] * (2 * 2.0 ** -4 * want[2][..., None] + 2.0 ** -4)
+        check(o[s:s + 1], want[0], bound, f"row {s}")
+
+
+def test_no_rows(tp):
+    h, q, at, table, K, V, ws = plain(tp)
+    h.decode(q[:0], at[:0], table, K, V, q[:0], ws)
+    h.append(torch.empty(0, 12 * 64, device="cuda", dtype=torch.bfloat16), at[:0], table, K, V, q[:0])
+    assert h.sync_status() == 0
+
+
+def test_more_queries_than_a_group(tp):
+    for dtype in ("bf16", "f32", "fp8"):
+        decode_case(tp, np.random.default_rng(15), [90, 3], 130, 1, 64, 16, 1, dtype)
+
+
+def test_binding_refuses_on_the_gpu(tp):
+    h, q, at, table, K, V, ws = plain(tp)
+    o = torch.empty_like(q)
+    for bad in (dict(Q=q.float()), dict(Q=q[:, ::2]), dict(Q=q.cpu()), dict(K=K[:-1]), dict(K=K.transpose(0, 1)), dict(positions=at.long()),
+                dict(positions=at[:, None]), dict(table=table.t()), dict(table=table.float()), dict(O=o[:-1]), dict(workspace=ws.cpu())):
+        kw = {**dict(Q=q, positions=at, table=table, K=K, V=V, O=o, workspace=ws), **bad}
+        with pytest.raises(ValueError):
+            h.decode(**kw)
+    with pytest.raises(tp.TpError):
+        h.decode(q, at, table, K, V, o, None)
+    with pytest.raises(tp.TpError):
+        h.decode(q, at, table, K, V, o, ws[:-256])
+    with pytest.raises(tp.TpError):
+        h.decode(q, at, table[:2].contiguous(), K, V, o, ws)    # more rows than sequences
+    with pytest.raises(ValueError):
+        tp.TPPagedAttention(8, 2, 64, 16, 8, dtype="fp8").decode(q, at, table, K[:8], V[:8], o, ws)
