@@ -58,7 +58,7 @@ tp_status launch_decode(DecodePlan &p, int dtype, void *workspace, cudaStream_t 
     tp_status s = dtype == TP_DT_F32   ? launch_decode_f32(p, &grid, st)
                   : dtype == TP_DT_FP8 ? launch_decode_fp8(p, &grid, st)
                                        : launch_decode_bf16(p, &grid, st);
-    if (s != TP_OK) return s;
+    if (s != TP_OK || grid == 0) return s;
     return dtype == TP_DT_F32 ? launch_join<float>(p, grid, st) : launch_join<__nv_bfloat16>(p, grid, st);
 }
 

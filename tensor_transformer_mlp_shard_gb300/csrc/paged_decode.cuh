@@ -46,6 +46,9 @@ constexpr int kSegmentPositions = 192;
 // A row up to this long is read by one warp where there are more segments than
 // blocks.
 constexpr int kShortPositions = 128;
+// Rows that see up to kClusterPositions, their segments no more than clusters of
+// kCluster blocks fit three quarters of the resident blocks: a cluster each.
+constexpr int kCluster = 8, kClusterPositions = 4096;
 // With so many units a resident block, one unit in kTailShare goes to half as many blocks more.
 constexpr int kSpread = 32, kTailShare = 8;
 
@@ -908,6 +911,26 @@ __device__ __forceinline__ int queries_of(const DecodePlan &p, int rh) {
 // A group's outputs [nh][D], maxima [nh] and sums [nh], in whole 16 bytes.
 inline __host__ __device__ int part_floats(int nh, int D) { return (nh * (D + 2) + 3) & ~3; }
 
+// Elements e.. of query h from the states of warps w0..w1 (their outputs `pitch`
+// bytes apart): eight of the sum, its maximum, the sum of weights.
+template <int NH, int DP>
+__device__ __forceinline__ void add_warps(const char *outs, int pitch, const float *top, const float *sum, int h, int e, int w0, int w1,
+                                          float (&f)[8], float &most, float &all) {
+    most = -INFINITY;
+    all = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+    for (int j = w0; j < w1; ++j) most = fmaxf(most, top[j * NH + h]);
+    for (int j = w0; j < w1; ++j) {
+        const float t = top[j * NH + h], by = t == -INFINITY ? 0.0f : exp2_fast(t - most);
+        all = fmaf(sum[j * NH + h], by, all);
+        const float4 *o = reinterpret_cast<const float4 *>(outs + j * pitch) + (h * DP + e) / 4;
+        const float4 a = o[0], b = o[1];
+        f[0] = fmaf(a.x, by, f[0]); f[1] = fmaf(a.y, by, f[1]); f[2] = fmaf(a.z, by, f[2]); f[3] = fmaf(a.w, by, f[3]);
+        f[4] = fmaf(b.x, by, f[4]); f[5] = fmaf(b.y, by, f[5]); f[6] = fmaf(b.z, by, f[6]); f[7] = fmaf(b.w, by, f[7]);
+    }
+}
+
 // Registers a thread so that an SM holds so many blocks and has 8192 left: a block
 // of the kernel before (the join of the call before, say) that is still there
 // must not keep one of these out until another ends (8-bit batch: 137 us with
@@ -1156,16 +1179,8 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
         const int w0 = w.brief ? warp : 0, w1 = w.brief ? warp + 1 : kWarps;  // whose states make the segment's
         for (int i = w.brief ? lane : threadIdx.x; i < nq * chunks; i += w.brief ? 32 : kBlock) {
             const int h = i / chunks, e = (i - h * chunks) * 8;
-            float most = -INFINITY, all = 0.0f, f[8] = {};
-            for (int j = w0; j < w1; ++j) most = fmaxf(most, top[j * NH + h]);
-            for (int j = w0; j < w1; ++j) {
-                const float t = top[j * NH + h], by = t == -INFINITY ? 0.0f : exp2_fast(t - most);
-                all = fmaf(sum[j * NH + h], by, all);
-                const float4 *o = reinterpret_cast<const float4 *>(ring + j * kRing + kOutAt) + (h * DP + e) / 4;
-                const float4 a = o[0], b = o[1];
-                f[0] = fmaf(a.x, by, f[0]); f[1] = fmaf(a.y, by, f[1]); f[2] = fmaf(a.z, by, f[2]); f[3] = fmaf(a.w, by, f[3]);
-                f[4] = fmaf(b.x, by, f[4]); f[5] = fmaf(b.y, by, f[5]); f[6] = fmaf(b.z, by, f[6]); f[7] = fmaf(b.w, by, f[7]);
-            }
+            float most, all, f[8];
+            add_warps<NH, DP>(ring + kOutAt, kRing, top, sum, h, e, w0, w1, f, most, all);
             if (whole) {
                 const float by = all == 0.0f ? 0.0f : vscale / all;
 #pragma unroll
@@ -1195,6 +1210,121 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
         blocks = x_blocks;
     }
     if (!p.by_segment && !listed && threadIdx.x == 0) p.joins[c] = make_int4(0, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------
+// few and short segments: a cluster for each
+// ---------------------------------------------------------------------------
+// The blocks of a cluster take equal parts of one segment and add them up through
+// each other's shared memory: no second launch, no look at the other rows.  One
+// sequence of 2000 positions, 8 key heads: KSC us a call, 11.1 by the list and its join.
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// the address of a block's own shared memory in block `rank` of its cluster
+__device__ __forceinline__ uint32_t in_block(uint32_t at, uint32_t rank) {
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(rank));
+    return to;
+}
+__device__ __forceinline__ float cluster_read(uint32_t at) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 cluster_read4(uint32_t at) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at) : "memory");
+    return x;
+}
+
+template <class Core>
+__global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) cluster_kernel(const __grid_constant__ DecodePlan p) {
+    using Act = typename Core::Act;
+    using Stages = Ring<Core>;
+    constexpr int DP = Core::kTileElems, NH = Core::kHeads, R = Core::kRows;
+    constexpr int kRing = Stages::kBytes, kOutAt = (Core::kStages - Stages::kOut) * Stages::kStage;
+    static_assert(NH * DP * 4 <= kOutAt, "the block's sum lies before its first warp's output");
+    extern __shared__ __align__(128) char ring[];  // [kWarps][stages]; then the block's output [NH][DP]
+    __shared__ float top[kWarps * NH], sum[kWarps * NH], tops[NH], sums[NH];
+    __shared__ __align__(16) float q_smem[sizeof(Act) == 4 ? kWarps * NH * DP : 4];
+    const int warp = threadIdx.x >> 5, rank = static_cast<int>(cluster_rank());
+    const int segment = blockIdx.x / kCluster, r = segment / p.row_heads, rh = segment - r * p.row_heads;
+    wait_for_stream();
+    let_next_start();
+    bool bad;
+    const Row row = row_at<R>(p, r, &bad);
+    if (bad && rank == 0 && threadIdx.x == 0) bad_index(p.at);
+    const HeadAt at = head_at(p, rh);
+    const int nq = queries_of(p, rh), chunks = p.D / 8;
+    Segment s;
+    s.head = at.kv;
+    s.t0 = (row.t0 + row.units * rank / kCluster) * kWarps;
+    s.t1 = (row.t0 + row.units * (rank + 1) / kCluster) * kWarps;
+    s.first = row.first;
+    s.last = row.last;
+    s.pages = p.at.table + static_cast<long long>(row.last < 0 ? 0 : p.at.sequences ? p.at.sequences[r] : r) * p.at.table_cols;
+    const long long q_at = (static_cast<long long>(r) * p.hq + at.query) * p.D;
+    char *mine_at = ring + warp * kRing;
+    const uint32_t mine_to = static_cast<uint32_t>(__cvta_generic_to_shared(mine_at));
+    float *mine_q = sizeof(Act) == 4 ? q_smem + warp * NH * DP : nullptr;
+
+    Core core;
+    const uint32_t blocks = Stages::look_up(p, s, s.t0 + warp, kWarps);
+    core.fetch_queries(p, static_cast<const Act *>(p.q[at.shard]) + q_at, nq,
+                       sizeof(Act) == 4 ? static_cast<uint32_t>(__cvta_generic_to_shared(mine_q)) : 0u);
+    Stages::template begin<0, Stages::kEarly>(p, s, p.k[at.shard], p.v[at.shard], s.t0 + warp, kWarps, blocks, mine_to);
+    core.begin(p, at.shard * p.hk + at.kv, mine_q);
+    Stages::walk(core, p, s, p.k[at.shard], p.v[at.shard], s.t0 + warp, kWarps, blocks, mine_at);
+    core.finish(p, reinterpret_cast<float *>(mine_at + kOutAt), top + warp * NH, sum + warp * NH);
+    __syncthreads();
+    // the block's sum, to where its first warp's stages were
+    for (int i = threadIdx.x; i < nq * chunks; i += kBlock) {
+        const int h = i / chunks, e = (i - h * chunks) * 8;
+        float most, all, f[8];
+        add_warps<NH, DP>(ring + kOutAt, kRing, top, sum, h, e, 0, kWarps, f, most, all);
+        store8(reinterpret_cast<float *>(ring) + h * DP + e, f);
+        if (e == 0) {
+            tops[h] = most;
+            sums[h] = all;
+        }
+    }
+    cluster_meet();
+    const float vscale = p.v_amax ? 1.0f / cache_scale(p.v_amax, at.shard * p.hk + at.kv) : 1.0f;
+    const uint32_t out_to = static_cast<uint32_t>(__cvta_generic_to_shared(ring)), tops_to = static_cast<uint32_t>(__cvta_generic_to_shared(tops)),
+                   sums_to = static_cast<uint32_t>(__cvta_generic_to_shared(sums));
+    // four elements a thread, the blocks' in turn
+    for (int i = rank * kBlock + threadIdx.x; i < nq * chunks * 2; i += kCluster * kBlock) {
+        const int h = i / (2 * chunks), e = (i - h * 2 * chunks) * 4;
+        float most = -INFINITY, all = 0.0f, t[kCluster], l[kCluster];
+        float4 x[kCluster], f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int c = 0; c < kCluster; ++c) {
+            t[c] = cluster_read(in_block(tops_to + 4 * h, c));
+            l[c] = cluster_read(in_block(sums_to + 4 * h, c));
+            x[c] = cluster_read4(in_block(out_to + 4 * (h * DP + e), c));
+            most = fmaxf(most, t[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < kCluster; ++c) {
+            const float by = t[c] == -INFINITY ? 0.0f : exp2_fast(t[c] - most);
+            all = fmaf(l[c], by, all);
+            f.x = fmaf(x[c].x, by, f.x); f.y = fmaf(x[c].y, by, f.y); f.z = fmaf(x[c].z, by, f.z); f.w = fmaf(x[c].w, by, f.w);
+        }
+        const float by = all == 0.0f ? 0.0f : vscale / all;
+        const float4 o = all == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(f.x * by, f.y * by, f.z * by, f.w * by);
+        Act *to = static_cast<Act *>(p.o[at.shard]) + q_at + static_cast<long long>(h) * p.D + e;
+        if constexpr (sizeof(Act) == 2)
+            *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        else
+            *reinterpret_cast<float4 *>(to) = o;
+    }
+    cluster_meet();  // no block leaves while another reads its memory
 }
 
 // Joins the parts of the segments that several blocks read: W warps a query,
@@ -1291,44 +1421,58 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) join_kernel(const __gri
     }
 }
 
-// Launches the kernel of a core: as many blocks as are resident (or as there
-// is room for in the workspace).
+// Launches the kernels of a core: as many blocks as are resident (or as there is
+// room for in the workspace), or the clusters; *grid is 0 where nothing is to join.
 template <class Core>
 tp_status launch_core(DecodePlan &p, int *grid, cudaStream_t st) {
-    constexpr int kSmem = kWarps * Core::kStages * 2 * Core::kRows * Core::kRowBytes;
+    constexpr int kSmem = kWarps * Ring<Core>::kBytes;
     static int per_sm[64] = {};  // by device
     static std::mutex mu;
-    int dev = 0, resident;
+    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_check(e, "cudaGetDevice");
     if (dev < 0 || dev >= 64) return set_error(TP_ERR_UNSUPPORTED, "device ordinal %d above 63", dev);
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!per_sm[dev]) {
+            int n = 0;
             e = cudaFuncSetAttribute(decode_kernel<Core>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-            if (e == cudaSuccess)
-                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm[dev], decode_kernel<Core>, kBlock, kSmem);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(cluster_kernel<Core>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<Core>, kBlock, kSmem);
             if (e != cudaSuccess) return cuda_check(e, "paged_decode");
-            if (per_sm[dev] < 1) return set_error(TP_ERR_CUDA, "paged_decode: no block fits an SM");
+            if (n < 1) return set_error(TP_ERR_CUDA, "paged_decode: no block fits an SM");
+            per_sm[dev] = n;
         }
-        resident = per_sm[dev] * num_sms();
+        p.resident = std::min(per_sm[dev] * num_sms(), kMostResident);
     }
-    p.resident = resident < kMostResident ? resident : kMostResident;
-    *grid = p.resident + p.resident / 2;
     const long long segments = static_cast<long long>(p.at.n) * p.row_heads;
-    p.by_segment = segments <= *grid;
+    long long seen = static_cast<long long>(p.at.table_cols) * p.at.page_size;
+    if (p.window > 0) seen = std::min(seen, static_cast<long long>(p.window));
+    const bool clusters = seen <= kClusterPositions && segments * kCluster * 4 <= p.resident * 3;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(*grid);
     cfg.blockDim = dim3(kBlock);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
-    cfg.numAttrs = pdl_on() ? 1 : 0;
+    if (pdl_on()) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (clusters) {
+        *grid = 0;
+        cfg.gridDim = dim3(static_cast<unsigned>(segments) * kCluster);
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = kCluster;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    } else {
+        *grid = p.resident + p.resident / 2;
+        cfg.gridDim = dim3(*grid);
+        p.by_segment = segments <= *grid;
+    }
     launch_begin("paged_decode", st);
-    e = cudaLaunchKernelEx(&cfg, decode_kernel<Core>, p);
+    e = clusters ? cudaLaunchKernelEx(&cfg, cluster_kernel<Core>, p) : cudaLaunchKernelEx(&cfg, decode_kernel<Core>, p);
     launch_end("paged_decode", st);
     return cuda_check(e, "paged_decode");
 }

@@ -109,9 +109,13 @@ class Cache:
 
 
 def decode_case(tp, rng, lengths, heads, kv, D, page_size, T=1, dtype="bf16", window=0, sequences=None, positions=None,
-                scale=None, q_std=1.0):
+                scale=None, q_std=1.0, capacity=0):
     """Runs decode on a seeded case and checks every shard; returns what it made."""
     table, pages = table_for(rng, lengths, page_size)
+    if capacity > table.shape[1] * page_size:   # a table with room to grow
+        wide = np.full((len(lengths), -(-capacity // page_size)), -1, dtype=np.int32)
+        wide[:, :table.shape[1]] = table
+        table = wide
     amax = None
     if dtype == "fp8":
         amax = [torch.from_numpy((3.0 + rng.random(kv)).astype(np.float32)) for _ in range(2)]

@@ -488,3 +488,15 @@ def test_binding_refuses_on_the_gpu(tp):
         h.decode(q, at, table[:2].contiguous(), K, V, o, ws)    # more rows than sequences
     with pytest.raises(ValueError):
         tp.TPPagedAttention(8, 2, 64, 16, 8, dtype="fp8").decode(q, at, table, K[:8], V[:8], o, ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 256])
+@pytest.mark.parametrize("per", [1, 3, 6, 13])
+def test_decode_few_rows(tp, dtype, D, per):
+    """Few short rows, which clusters of blocks take, and the same where the table could hold long ones, which are
+    dealt out by the list."""
+    for lengths in ([2000], [1, 0, 700, 65, 511]):
+        for capacity in (0, 20000):
+            decode_case(tp, np.random.default_rng(D + per), lengths, 2 * per, 2, D, 16, 1, dtype, capacity=capacity)
+    decode_case(tp, np.random.default_rng(D + per), [5000, 333], 2 * per, 2, D, 32, 2, dtype, window=600)
