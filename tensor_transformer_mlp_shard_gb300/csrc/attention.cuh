@@ -127,6 +127,7 @@ struct DecodePlan {
     float *partial;        // [blocks][2][nh * (D + 2)]
     int4 *joins;           // [blocks]
     int resident;          // blocks that run at once
+    int cluster;           // blocks of a segment, where each has some (0: dealt out)
     int join_early;        // the kernel after the join may start beside it
     int by_segment;        // joins are listed by (row, head) rather than by block
 };

@@ -46,9 +46,14 @@ constexpr int kSegmentPositions = 192;
 // A row up to this long is read by one warp where there are more segments than
 // blocks.
 constexpr int kShortPositions = 128;
-// Rows that see up to kClusterPositions, their segments no more than clusters of
-// kCluster blocks fit three quarters of the resident blocks: a cluster each.
-constexpr int kCluster = 8, kClusterPositions = 4096;
+// Rows that may see no more than kBlockPositions a block of a cluster of up to
+// kCluster, and whose clusters fit three quarters of the resident blocks, have a
+// cluster each.  So have rows of up to kBlockPositions, a block each, however
+// many they are, but not where all are short: blocks come and go more slowly
+// than a resident block's warps take such rows (1624 segments of up to 305
+// positions, 8-bit: 30 us, 34 by the list; 2110 of up to 51, bf16: 29 us, 15 by
+// the list).
+constexpr int kCluster = 8, kBlockPositions = 512;
 // With so many units a resident block, one unit in kTailShare goes to half as many blocks more.
 constexpr int kSpread = 32, kTailShare = 8;
 
@@ -1217,7 +1222,8 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
 // ---------------------------------------------------------------------------
 // The blocks of a cluster take equal parts of one segment and add them up through
 // each other's shared memory: no second launch, no look at the other rows.  One
-// sequence of 2000 positions, 8 key heads: KSC us a call, 11.1 by the list and its join.
+// sequence of 2000 positions, 8 key heads: 8.2 us a call, 11.1 by the list and its
+// join (5.9 and 8.4 us in a captured graph).
 __device__ __forceinline__ void cluster_meet() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -1254,7 +1260,7 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) cluster_kernel(con
     __shared__ float top[kWarps * NH], sum[kWarps * NH], tops[NH], sums[NH];
     __shared__ __align__(16) float q_smem[sizeof(Act) == 4 ? kWarps * NH * DP : 4];
     const int warp = threadIdx.x >> 5, rank = static_cast<int>(cluster_rank());
-    const int segment = blockIdx.x / kCluster, r = segment / p.row_heads, rh = segment - r * p.row_heads;
+    const int size = p.cluster, segment = blockIdx.x / size, r = segment / p.row_heads, rh = segment - r * p.row_heads;
     wait_for_stream();
     let_next_start();
     bool bad;
@@ -1264,8 +1270,8 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) cluster_kernel(con
     const int nq = queries_of(p, rh), chunks = p.D / 8;
     Segment s;
     s.head = at.kv;
-    s.t0 = (row.t0 + row.units * rank / kCluster) * kWarps;
-    s.t1 = (row.t0 + row.units * (rank + 1) / kCluster) * kWarps;
+    s.t0 = (row.t0 + row.units * rank / size) * kWarps;
+    s.t1 = (row.t0 + row.units * (rank + 1) / size) * kWarps;
     s.first = row.first;
     s.last = row.last;
     s.pages = p.at.table + static_cast<long long>(row.last < 0 ? 0 : p.at.sequences ? p.at.sequences[r] : r) * p.at.table_cols;
@@ -1299,15 +1305,20 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) cluster_kernel(con
     const uint32_t out_to = static_cast<uint32_t>(__cvta_generic_to_shared(ring)), tops_to = static_cast<uint32_t>(__cvta_generic_to_shared(tops)),
                    sums_to = static_cast<uint32_t>(__cvta_generic_to_shared(sums));
     // four elements a thread, the blocks' in turn
-    for (int i = rank * kBlock + threadIdx.x; i < nq * chunks * 2; i += kCluster * kBlock) {
+    for (int i = rank * kBlock + threadIdx.x; i < nq * chunks * 2; i += size * kBlock) {
         const int h = i / (2 * chunks), e = (i - h * 2 * chunks) * 4;
         float most = -INFINITY, all = 0.0f, t[kCluster], l[kCluster];
         float4 x[kCluster], f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int c = 0; c < kCluster; ++c) {
-            t[c] = cluster_read(in_block(tops_to + 4 * h, c));
-            l[c] = cluster_read(in_block(sums_to + 4 * h, c));
-            x[c] = cluster_read4(in_block(out_to + 4 * (h * DP + e), c));
+            t[c] = -INFINITY;
+            l[c] = 0.0f;
+            x[c] = f;
+            if (c < size) {
+                t[c] = cluster_read(in_block(tops_to + 4 * h, c));
+                l[c] = cluster_read(in_block(sums_to + 4 * h, c));
+                x[c] = cluster_read4(in_block(out_to + 4 * (h * DP + e), c));
+            }
             most = fmaxf(most, t[c]);
         }
 #pragma unroll
@@ -1448,7 +1459,10 @@ tp_status launch_core(DecodePlan &p, int *grid, cudaStream_t st) {
     const long long segments = static_cast<long long>(p.at.n) * p.row_heads;
     long long seen = static_cast<long long>(p.at.table_cols) * p.at.page_size;
     if (p.window > 0) seen = std::min(seen, static_cast<long long>(p.window));
-    const bool clusters = seen <= kClusterPositions && segments * kCluster * 4 <= p.resident * 3;
+    p.cluster = seen > kShortPositions && seen <= kBlockPositions && segments < (1ll << 30) ? 1 : 0;
+    for (int size = 1; size <= kCluster; size *= 2)
+        if (segments * size * 4 <= p.resident * 3 && seen <= size * kBlockPositions && (size == 1 || seen > (size - 1) * Core::kRows * kWarps))
+            p.cluster = size;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kBlock);
     cfg.dynamicSmemBytes = kSmem;
@@ -1459,11 +1473,11 @@ tp_status launch_core(DecodePlan &p, int *grid, cudaStream_t st) {
         attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     }
-    if (clusters) {
+    if (p.cluster) {
         *grid = 0;
-        cfg.gridDim = dim3(static_cast<unsigned>(segments) * kCluster);
+        cfg.gridDim = dim3(static_cast<unsigned>(segments) * p.cluster);
         attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attr[cfg.numAttrs].val.clusterDim.x = kCluster;
+        attr[cfg.numAttrs].val.clusterDim.x = p.cluster;
         attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
         ++cfg.numAttrs;
     } else {
@@ -1472,7 +1486,7 @@ tp_status launch_core(DecodePlan &p, int *grid, cudaStream_t st) {
         p.by_segment = segments <= *grid;
     }
     launch_begin("paged_decode", st);
-    e = clusters ? cudaLaunchKernelEx(&cfg, cluster_kernel<Core>, p) : cudaLaunchKernelEx(&cfg, decode_kernel<Core>, p);
+    e = p.cluster ? cudaLaunchKernelEx(&cfg, cluster_kernel<Core>, p) : cudaLaunchKernelEx(&cfg, decode_kernel<Core>, p);
     launch_end("paged_decode", st);
     return cuda_check(e, "paged_decode");
 }

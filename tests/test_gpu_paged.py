@@ -500,3 +500,13 @@ def test_decode_few_rows(tp, dtype, D, per):
         for capacity in (0, 20000):
             decode_case(tp, np.random.default_rng(D + per), lengths, 2 * per, 2, D, 16, 1, dtype, capacity=capacity)
     decode_case(tp, np.random.default_rng(D + per), [5000, 333], 2 * per, 2, D, 32, 2, dtype, window=600)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("rows,length", [(1, 100), (2, 200), (3, 1000), (5, 450), (40, 480), (150, 500), (150, 120)])
+def test_decode_clusters_of_all_sizes(tp, dtype, rows, length):
+    """From eight blocks a segment to one, and more of them than are resident."""
+    rng = np.random.default_rng(rows)
+    lengths = [length] + [int(x) for x in rng.integers(0, length + 1, size=rows - 1)]
+    for D in (64, 128) if rows < 100 else (128,):
+        decode_case(tp, rng, lengths, 8, 4, D, 16, 2, dtype)
