@@ -938,8 +938,8 @@ __device__ __forceinline__ void add_warps(const char *outs, int pitch, const flo
 
 // Registers a thread so that an SM holds so many blocks and has 8192 left: a block
 // of the kernel before (the join of the call before, say) that is still there
-// must not keep one of these out until another ends (8-bit batch: 137 us with
-// one block late, 125 without).
+// must not keep one of these out until another ends (8-bit batch: 166 to
+// 173 us with one block late, 135 without).
 constexpr int registers_of(int blocks) {
     return (65536 - 8192) / (blocks * kBlock) / 8 * 8 < 255 ? (65536 - 8192) / (blocks * kBlock) / 8 * 8 : 255;
 }
@@ -1491,7 +1491,7 @@ tp_status launch_core(DecodePlan &p, int *grid, cudaStream_t st) {
     return cuda_check(e, "paged_decode");
 }
 
-// by the padded width (64, 128, 256) and the queries of a group
+// by the padded width (64, 128, 192, 256; fp32 also 96) and the queries of a group
 tp_status launch_decode_bf16(DecodePlan &p, int *grid, cudaStream_t st);
 tp_status launch_decode_fp8(DecodePlan &p, int *grid, cudaStream_t st);
 tp_status launch_decode_f32(DecodePlan &p, int *grid, cudaStream_t st);

@@ -8,11 +8,12 @@
 // all heads share, are computed once, by one thread a pair, while the first
 // loads are on their way, and kept in shared memory; a table in memory would
 // cost as many bytes as a head.  An item is two chunks of a head: with pairs
-// (i, i + dim/2) a chunk and its partner, else neighbours.  A thread has one
-// item of every token, so that where it lies is worked out once for all of the
-// block's tokens, and copies it to a ring of its own in shared memory, three
-// tokens ahead: the bytes on their way do not cost registers, and no thread
-// waits for another.
+// (i, i + dim/2) a chunk and its partner, else one from either half of what is
+// left.  A thread has one item of every token, so that where it lies is worked
+// out once for all of the block's tokens, and copies it to a ring of its own in
+// shared memory, three tokens ahead: the bytes on their way do not cost
+// registers, and no thread waits for another (but where an odd half puts the
+// partners across the chunks of other threads).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -39,8 +40,8 @@ constexpr int kThreads = 256;
 constexpr int kMaxTokens = 8;   // tokens of a block
 constexpr int kFlight = 3;     // of them that a thread copies ahead
 
-// the most that a block asks for: 8 tokens of 128 pairs, the ring of 256 threads
-static_assert(sizeof(float) * 2 * kMaxTokens * kMaxPairs + kFlight * 2 * 16 * kThreads < 48 * 1024 - 512, "a kernel's shared memory unasked");
+// the most that a block asks for: 8 tokens of 128 pairs, twice, the ring of 256 threads
+static_assert(sizeof(float) * 4 * kMaxTokens * kMaxPairs + kFlight * 2 * 16 * kThreads < 48 * 1024 - 512, "a kernel's shared memory unasked");
 
 enum Mode : int { ROTATE = 0, APPEND = 1, APPEND8 = 2 };
 
@@ -57,7 +58,7 @@ struct QkvPlan {
     int rest_items;                           // the others
     int in_place;
     int side, passes;                         // tokens of a block: `side` at a time, `passes` times
-    int rounds;                               // of `threads` items of side tokens
+    int rounds, round_threads;                // of so many items of side tokens
     int round_items;                          // side * T * slots * items
     Divisor by_items, by_slots, by_shards, by_group;
     int turn_pitch;                           // of the cosines of a token in shared memory
@@ -68,11 +69,8 @@ struct QkvPlan {
 template <typename E, int VE>
 struct Chunk {  // VE elements as they are stored
     static constexpr int kBytes = VE * sizeof(E);
-    using Word = typename std::conditional<kBytes == 16, uint4,
-                 typename std::conditional<kBytes == 8, uint2,
-                 typename std::conditional<kBytes == 4, uint32_t, uint16_t>::type>::type>::type;
+    using Word = typename std::conditional<kBytes == 16, uint4, typename std::conditional<kBytes == 8, uint2, uint32_t>::type>::type;
     Word w;
-    __device__ __forceinline__ void load(const E *p) { w = *reinterpret_cast<const Word *>(p); }
     __device__ __forceinline__ void store(E *p) const { *reinterpret_cast<Word *>(p) = w; }
     __device__ __forceinline__ void unpack(float (&f)[VE]) const {
         const E *e = reinterpret_cast<const E *>(&w);
@@ -96,10 +94,8 @@ __device__ __forceinline__ void store_codes(uint8_t *p, const float (&f)[VE], fl
         *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(c);
     else if constexpr (VE == 4)
         *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(c);
-    else if constexpr (VE == 2)
-        *reinterpret_cast<uint16_t *>(p) = *reinterpret_cast<const uint16_t *>(c);
     else
-        *p = c[0];
+        *reinterpret_cast<uint16_t *>(p) = *reinterpret_cast<const uint16_t *>(c);
 }
 
 enum Kind : int { QUERY = 0, KEY = 1, VALUE = 2 };
@@ -116,6 +112,7 @@ __device__ __forceinline__ void copy_chunk(uint32_t to, const void *from) {
 struct Item {
     int token;        // of the side's; -1: none
     int shard, kind, head, column, a, b;  // a, b: the chunks' first elements (b = -1: none)
+    int n;            // of the head's items
 };
 
 template <int VE>
@@ -141,7 +138,7 @@ __device__ __forceinline__ Item item_at(const QkvPlan &p, int i) {
         it.kind = s < p.hq ? QUERY : s < p.hq + p.hk ? KEY : VALUE;
         it.head = it.kind == QUERY ? s : it.kind == KEY ? s - p.hq : s - p.hq - p.hk;
     }
-    const int n = item;
+    const int n = it.n = item;
     if (n < p.pair_items) {
         it.a = n * VE;
         it.b = it.a + p.half;
@@ -154,20 +151,18 @@ __device__ __forceinline__ Item item_at(const QkvPlan &p, int i) {
     return it;
 }
 
-// N cosines or sines from shared memory (N = 4: 16-byte aligned, 2: 8-byte)
+// N cosines or sines from shared memory
 template <int N>
 __device__ __forceinline__ void read_turns(float *to, const float *from) {
-    if constexpr (N % 4 == 0) {
+    if constexpr (N == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(from);
+        to[0] = v.x; to[1] = v.y;
+    } else {
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
             const float4 v = *reinterpret_cast<const float4 *>(from + i);
             to[i] = v.x; to[i + 1] = v.y; to[i + 2] = v.z; to[i + 3] = v.w;
         }
-    } else if constexpr (N == 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(from);
-        to[0] = v.x; to[1] = v.y;
-    } else {
-        to[0] = from[0];
     }
 }
 
@@ -192,24 +187,87 @@ __device__ __forceinline__ void turn_neighbours(float (&f)[VE], int first, int h
         }
 }
 
-template <typename E, int VE, int MODE>
+// The 16 bytes of a head from element j0 on, wherever they begin, from the chunks
+// of its items: `head` is the first item's place among a stage's chunks, of which
+// the second halves lie `half_at` further.  What lies outside the chunks that
+// turn is any of them.
+template <typename E, int VE>
+__device__ __forceinline__ void window(uint32_t (&to)[4], int j0, const QkvPlan &p, const uint4 *head, int half_at) {
+    const int last = (2 * p.half - 1) / VE, c = j0 >= 0 ? j0 / VE : -1, by = j0 & (VE - 1);
+    auto chunk = [&](int i) {
+        i = min(max(i, 0), last);
+        return i < p.rest_items ? head[i] : head[half_at + i - p.rest_items];
+    };
+    const uint4 x = chunk(c), y = chunk(c + 1);
+    uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    constexpr int kWord = 4 / sizeof(E);  // elements of a word
+    static_assert(VE == 4 * kWord, "chunks of 16 bytes");
+    if (by & (2 * kWord)) {
+#pragma unroll
+        for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+    }
+    if (by & kWord) {
+#pragma unroll
+        for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+    }
+    if constexpr (kWord == 2) {
+        if (by & 1) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) to[k] = w[k];
+}
+
+// The elements of a chunk that turn, with partners from other chunks; cs and sn are
+// by element, the sines with their signs.
+template <typename E, int VE>
+__device__ __forceinline__ void turn_apart(Chunk<E, VE> &chunk, float (&f)[VE], int first, const QkvPlan &p, const uint4 *head, int half_at,
+                                           const float *cs, const float *sn) {
+    if (first >= 2 * p.half) return;
+    alignas(16) uint32_t partner[4];
+    window<E, VE>(partner, first < p.half ? first + p.half : first - p.half, p, head, half_at);
+    const E *x = reinterpret_cast<const E *>(partner);
+    float g[VE], c[VE], s[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) g[e] = static_cast<float>(x[e]);
+    if (first < p.half && first + VE > p.half) {  // both halves' elements: the later ones' partners are elsewhere
+        window<E, VE>(partner, first - p.half, p, head, half_at);
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+            if (first + e >= p.half) g[e] = static_cast<float>(x[e]);
+    }
+    read_turns<VE>(c, cs + first);
+    read_turns<VE>(s, sn + first);
+    E *own = reinterpret_cast<E *>(&chunk.w);
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+        if (first + e < 2 * p.half) {
+            f[e] = __fadd_rn(__fmul_rn(f[e], c[e]), __fmul_rn(g[e], s[e]));
+            own[e] = static_cast<E>(f[e]);
+        }
+}
+
+// APART: pairs (i, i + half) of an odd half, whose partners lie across the chunks:
+// the block meets once a token, when all of its chunks are there.
+template <typename E, int VE, int MODE, bool APART>
 __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ QkvPlan p) {
     constexpr int kBytes = Chunk<E, VE>::kBytes;
-    constexpr bool kRing = kBytes >= 4;  // what asynchronous copies take
-    // [tokens][pairs] cosines, as many sines, then [kFlight][2][threads] chunks
+    using Word = typename Chunk<E, VE>::Word;
+    // [tokens][pairs] cosines (APART: [elements]), as many sines, then [kFlight][2][threads] chunks
     extern __shared__ __align__(16) char smem[];
     __shared__ long long slot_of[kMaxTokens];  // APPEND: the slot's row of the cache, of key head 0
     __shared__ int active[kMaxTokens];
     const int tokens = p.side * p.passes, token0 = blockIdx.x * tokens, pitch = p.turn_pitch;
     float *cs = reinterpret_cast<float *>(smem), *sn = cs + tokens * pitch;
-    using Word = typename Chunk<E, VE>::Word;
     Word *ring = reinterpret_cast<Word *>(sn + tokens * pitch) + threadIdx.x;
     const uint32_t ring_to = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     const long long width = static_cast<long long>(p.columns) * p.D;
     bool turned = false;
     wait_for_stream();
     for (int round = blockIdx.y; round < p.rounds; round += gridDim.y) {
-        const Item it = item_at<VE>(p, round * blockDim.x + threadIdx.x);
+        const Item it = item_at<VE>(p, static_cast<int>(threadIdx.x) < p.round_threads ? round * p.round_threads + static_cast<int>(threadIdx.x) : p.round_items);
         const bool two = it.b >= 0;
         const E *x = nullptr;
         E *y = nullptr;  // ROTATE, queries
@@ -245,10 +303,8 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        if constexpr (kRing) {
 #pragma unroll
-            for (int i = 0; i < kFlight; ++i) copy(i, i);
-        }
+        for (int i = 0; i < (APART ? kFlight - 1 : kFlight); ++i) copy(i, i);
         if (!turned) {
             auto position = [&](int m) {
                 return MODE == ROTATE && !p.at.positions ? static_cast<int>(p.batch.div(m)) : p.at.positions[m];
@@ -277,43 +333,45 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
                 const uint64_t per_position = p.turns.per_position[pair];
                 for (int t = k / p.half; t < tokens && token0 + t < p.at.n; t += groups) {
                     const float2 r = turn(p.turns, per_position, position(token0 + t));
+                    const float s = r.y * p.sign;
                     cs[t * pitch + pair] = r.x;
-                    sn[t * pitch + pair] = r.y * p.sign;
+                    sn[t * pitch + pair] = APART ? -s : s;
+                    if (APART) {
+                        cs[t * pitch + p.half + pair] = r.x;
+                        sn[t * pitch + p.half + pair] = s;
+                    }
                 }
             }
             turned = true;
             __syncthreads();
         }
         int slot = 0;
-        Chunk<E, VE> next_a, next_b;
-        auto load_next = [&](int pass) {
-            if (pass >= count) return;
-            const E *from = x + pass * x_step;
-            next_a.load(from + it.a);
-            if (two) next_b.load(from + it.b);
-        };
-        if constexpr (!kRing) load_next(0);
-        for (int pass = 0; pass < count; ++pass) {
-            Chunk<E, VE> a, b;
-            if constexpr (kRing) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(kFlight - 1) : "memory");
-                const Word *r = ring + slot * 2 * blockDim.x;
-                a.w = r[0];
-                if (two) b.w = r[blockDim.x];
+        for (int pass = 0; pass < (APART ? p.passes : count); ++pass) {
+            if constexpr (APART) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kFlight - 2) : "memory");
+                __syncthreads();  // and the token before has been read
+                copy(pass + kFlight - 1, slot == 0 ? kFlight - 1 : slot - 1);
             } else {
-                a = next_a;
-                b = next_b;
-                load_next(pass + 1);
+                asm volatile("cp.async.wait_group %0;" ::"n"(kFlight - 1) : "memory");
             }
+            const bool here = !APART || pass < count;
+            const Word *stage = ring + slot * 2 * blockDim.x;
+            Chunk<E, VE> a, b;
+            a.w = stage[0];
+            if (two) b.w = stage[blockDim.x];
             const int t = pass * p.side + it.token;
-            const bool on = active[t];
-            if (on || (MODE == ROTATE && !p.in_place)) {  // otherwise padding stays as it was
+            const bool on = here && active[t];
+            if (on || (MODE == ROTATE && !p.in_place && here)) {  // otherwise padding stays as it was
                 float fa[VE], fb[VE];
                 a.unpack(fa);
                 if (two) b.unpack(fb);
                 if (it.kind != VALUE && on) {
                     const float *c_of = cs + t * pitch, *s_of = sn + t * pitch;
-                    if (p.interleaved) {
+                    if constexpr (APART) {
+                        const uint4 *head = stage - it.n;
+                        turn_apart<E, VE>(a, fa, it.a, p, head, blockDim.x, c_of, s_of);
+                        if (two) turn_apart<E, VE>(b, fb, it.b, p, head, blockDim.x, c_of, s_of);
+                    } else if (p.interleaved) {
                         if constexpr (VE >= 4) {  // whole 16 bytes
                             turn_neighbours<VE>(fa, it.a, p.half, c_of, s_of);
                             a.pack(fa);
@@ -345,17 +403,18 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(const __grid_constant__ Q
                         E *to = static_cast<E *>(cache) + row;
                         a.store(to + it.a);
                         if (two) b.store(to + it.b);
-                    } else {
+                    } else if constexpr (MODE == APPEND8) {
                         uint8_t *to = static_cast<uint8_t *>(cache) + row;
                         store_codes<VE>(to + it.a, fa, scale);
                         if (two) store_codes<VE>(to + it.b, fb, scale);
                     }
                 }
             }
-            if constexpr (kRing) copy(pass + kFlight, slot);
+            if constexpr (!APART) copy(pass + kFlight, slot);
             slot = slot + 1 == kFlight ? 0 : slot + 1;
         }
-        if constexpr (kRing) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if constexpr (APART) __syncthreads();  // the next round's copies take the stages
     }
     // not earlier: blocks of this kernel between those of the next one leave an SM's
     // registers in pieces, and the next kernel's last block without a place
@@ -405,24 +464,30 @@ void rope_turns(const tp_rope_desc &r, Turns *t) {
 }
 
 template <typename E, int MODE>
-static auto kernel_of(int ve) -> void (*)(QkvPlan) {
-    if constexpr (sizeof(E) == 2)
-        if (ve == 8) return qkv_kernel<E, 8, MODE>;
-    return ve == 4 ? qkv_kernel<E, 4, MODE> : ve == 2 ? qkv_kernel<E, 2, MODE> : qkv_kernel<E, 1, MODE>;
+static auto kernel_of(int ve, bool apart) -> void (*)(QkvPlan) {
+    constexpr int kMost = 16 / sizeof(E);
+    if (apart) return qkv_kernel<E, kMost, MODE, true>;
+    if constexpr (kMost == 8)
+        if (ve == 8) return qkv_kernel<E, 8, MODE, false>;
+    return ve == 4 ? qkv_kernel<E, 4, MODE, false> : qkv_kernel<E, 2, MODE, false>;
 }
 
 // Fills in what follows from the sizes and launches.  `T` shards, `in_place`:
 // only what is rotated is touched.
 static tp_status launch_qkv(QkvPlan &p, int T, int elem, int mode, const char *name, cudaStream_t st) {
     // 16 bytes a chunk; with pairs (i, i + half) both chunks have to begin on one: half
-    // as many elements until the half holds a whole number of them
+    // as many elements until the half holds a whole number of them, of an even half.
+    // An odd one would leave single elements, and goes by whole chunks with the
+    // partners across them (APART: bf16, 5160 tokens of 112 heads, 57 pairs 113 us,
+    // by elements 205; a half of 28 131 us by chunks of 4, 149 across).
+    const bool apart = !p.interleaved && p.half % 2;
     int ve = 16 / elem;
-    if (!p.interleaved)
-        while (ve > 1 && p.half % ve) ve /= 2;
+    if (!p.interleaved && !apart)
+        while (p.half % ve) ve /= 2;
     if (p.interleaved && p.half == 0) p.interleaved = 0;
-    const int chunks = p.D / ve, partners = p.interleaved ? 0 : p.half / ve;
+    const int chunks = p.D / ve, partners = p.interleaved || apart ? 0 : p.half / ve;
     p.pair_items = partners;
-    const int rotated = p.interleaved ? ((2 * p.half + ve - 1) / ve + 1) / 2 : partners;
+    const int rotated = p.interleaved || apart ? ((2 * p.half + ve - 1) / ve + 1) / 2 : partners;
     const int items = p.in_place ? rotated : partners + (chunks - 2 * partners + 1) / 2;
     p.rest_items = items - partners;
     const int group = p.per + (p.in_place ? 1 : 2);
@@ -433,28 +498,31 @@ static tp_status launch_qkv(QkvPlan &p, int T, int elem, int mode, const char *n
     p.side = 1;
     while (p.side < 4 && 2 * p.side * per_token <= kThreads) p.side *= 2;
     p.round_items = p.side * per_token;
-    // rounds of equally many threads
-    p.rounds = (p.round_items + kThreads - 1) / kThreads;
-    const int threads = ((p.round_items + p.rounds - 1) / p.rounds + 31) / 32 * 32;
+    // rounds of equally many items: of whole warps, or of whole heads where the items
+    // of a head need each other's chunks
+    const int unit = apart ? items : 32, most_items = kThreads / unit * unit;
+    p.rounds = (p.round_items + most_items - 1) / most_items;
+    p.round_threads = ((p.round_items + p.rounds - 1) / p.rounds + unit - 1) / unit * unit;
+    const int threads = (p.round_threads + 31) / 32 * 32;
     p.by_items = Divisor(items);
     p.by_slots = Divisor(slots);
     p.by_shards = Divisor(T);
     p.by_group = Divisor(group);
     void (*k)(QkvPlan) = nullptr;
     if (elem == 4)
-        k = mode == ROTATE ? kernel_of<float, ROTATE>(ve) : kernel_of<float, APPEND>(ve);
+        k = mode == ROTATE ? kernel_of<float, ROTATE>(ve, apart) : kernel_of<float, APPEND>(ve, apart);
     else
-        k = mode == ROTATE   ? kernel_of<__nv_bfloat16, ROTATE>(ve)
-            : mode == APPEND ? kernel_of<__nv_bfloat16, APPEND>(ve)
-                             : kernel_of<__nv_bfloat16, APPEND8>(ve);
+        k = mode == ROTATE   ? kernel_of<__nv_bfloat16, ROTATE>(ve, apart)
+            : mode == APPEND ? kernel_of<__nv_bfloat16, APPEND>(ve, apart)
+                             : kernel_of<__nv_bfloat16, APPEND8>(ve, apart);
     // Tokens after one another, where there are enough blocks all the same: 4, and 8
     // with the lookups in the table before them (32768 tokens backward 118 us with 4,
     // 121 with 8; 8092 into the cache 38 us with 8, 40 with 4).
     const int most = mode == ROTATE ? 4 : 8;
     p.passes = 1;
     while (2 * p.passes * p.side <= most && p.at.n / (2 * p.passes * p.side) >= 4 * num_sms()) p.passes *= 2;
-    p.turn_pitch = p.half > 0 ? (p.half + 7) / 8 * 8 : 8;
-    const int ring = ve * elem >= 4 ? kFlight * 2 * ve * elem * threads : 0, turns = sizeof(float) * 2 * p.side * p.turn_pitch;
+    p.turn_pitch = p.half > 0 ? ((apart ? 2 * p.half : p.half) + 7) / 8 * 8 : 8;
+    const int ring = kFlight * 2 * ve * elem * threads, turns = sizeof(float) * 2 * p.side * p.turn_pitch;
     const int blocks = (p.at.n + p.side * p.passes - 1) / (p.side * p.passes);
     // few tokens: the rounds on blocks of their own
     const int across = std::min(p.rounds, std::max(1, 8 * num_sms() / blocks));

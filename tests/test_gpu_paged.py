@@ -510,3 +510,12 @@ def test_decode_clusters_of_all_sizes(tp, dtype, rows, length):
     lengths = [length] + [int(x) for x in rng.integers(0, length + 1, size=rows - 1)]
     for D in (64, 128) if rows < 100 else (128,):
         decode_case(tp, rng, lengths, 8, 4, D, 16, 2, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("D,dim", [(208, 138), (128, 98), (32, 6)])
+def test_append_halves_of_any_width(tp, dtype, D, dim):
+    rng = np.random.default_rng(dim)
+    positions, sequences, table, pages = ragged(rng, [40, 3, 700], [0, 50, 9], 32)
+    append_case(tp, positions, sequences, table, pages, 32, 32, 8, D, 2, dtype, dim=dim)
+    append_case(tp, np.where(np.arange(len(positions)) % 7 == 0, -1, positions), sequences, table, pages, 32, 32, 8, D, 4, dtype, True, dim=dim)

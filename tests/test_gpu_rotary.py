@@ -171,3 +171,11 @@ def test_stream_and_graph(tp):
 def test_no_tokens(tp):
     h = tp.TPRotary(0, 4, 8, 4, 64)
     h.fwd(torch.empty(0, 16 * 64, device="cuda", dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,dim", [(200, 138), (128, 98), (256, 250), (72, 70), (40, 6)])
+def test_halves_of_any_width(tp, dtype, D, dim):
+    """Halves that are not whole chunks, heads over several rounds of a block's threads, several tokens a block."""
+    for S, grouped, place, T in ((3, False, True, 2), (700, True, False, 1), (1301, False, True, 4)):
+        run(tp, S, 1, 48 if S == 3 else 12, 16 if S == 3 else 4, D, T, dtype, grouped, place=place, back=grouped, dim=dim)
