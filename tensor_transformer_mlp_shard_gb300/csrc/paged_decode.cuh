@@ -48,11 +48,14 @@ constexpr int kSegmentPositions = 192;
 constexpr int kShortPositions = 128;
 // Rows that may see no more than kBlockPositions a block of a cluster of up to
 // kCluster, and whose clusters fit three quarters of the resident blocks, have a
-// cluster each.  So have rows of up to kBlockPositions, a block each, however
-// many they are, but not where all are short: blocks come and go more slowly
-// than a resident block's warps take such rows (1624 segments of up to 305
-// positions, 8-bit: 30 us, 34 by the list; 2110 of up to 51, bf16: 29 us, 15 by
-// the list).
+// cluster each.  So have rows of more than kShortPositions and up to
+// kBlockPositions, a block each, where that makes no more than twice the resident
+// blocks: a table's columns say little about the rows, and blocks come and go more
+// slowly than a resident block's warps take short ones (bf16, 304 segments of 144
+// elements, twice the resident: of up to 500 positions 18.5 us, 21.4 by the list,
+// of up to 30 both 9; 2432 segments: 114 and 105 us, 64 and 28).  Four times, where
+// a window is the bound, which most rows will fill (8-bit, 1072 segments of 235,
+// 2.4 times the resident: 25 us, 30 by the list).
 constexpr int kCluster = 8, kBlockPositions = 512;
 // With so many units a resident block, one unit in kTailShare goes to half as many blocks more.
 constexpr int kSpread = 32, kTailShare = 8;
@@ -200,7 +203,7 @@ struct TensorCore {
     static constexpr int kTileElems = DP;
     static constexpr int kRows = 16, kRowBytes = DP * static_cast<int>(sizeof(Cache));
     // about 192 KB of stages an SM; 16 queries over codes take more registers, so fewer blocks
-        static constexpr bool kFewer = k8 && NT == 2;
+    static constexpr bool kFewer = k8 && NT == 2;
     static constexpr int kStages = kRowBytes == 64 ? (kFewer ? 8 : 6) : kRowBytes == 128 ? (kFewer ? 6 : 4) : kRowBytes % 256 ? 4 : 3;
     static constexpr int kBlocksPerSm = (kRowBytes == 64 ? 4 : kRowBytes == 128 ? 3 : kRowBytes <= 256 ? 2 : 1) - kFewer;
     __device__ __forceinline__ static int swizzle_keys(int row) { return swizzle_k<kRowBytes>(row); }
@@ -1458,8 +1461,9 @@ tp_status launch_core(DecodePlan &p, int *grid, cudaStream_t st) {
     }
     const long long segments = static_cast<long long>(p.at.n) * p.row_heads;
     long long seen = static_cast<long long>(p.at.table_cols) * p.at.page_size;
-    if (p.window > 0) seen = std::min(seen, static_cast<long long>(p.window));
-    p.cluster = seen > kShortPositions && seen <= kBlockPositions && segments < (1ll << 30) ? 1 : 0;
+    const bool windowed = p.window > 0 && p.window < seen;
+    if (windowed) seen = p.window;
+    p.cluster = seen > kShortPositions && seen <= kBlockPositions && segments <= (windowed ? 4 : 2) * p.resident ? 1 : 0;
     for (int size = 1; size <= kCluster; size *= 2)
         if (segments * size * 4 <= p.resident * 3 && seen <= size * kBlockPositions && (size == 1 || seen > (size - 1) * Core::kRows * kWarps))
             p.cluster = size;

@@ -519,3 +519,12 @@ def test_append_halves_of_any_width(tp, dtype, D, dim):
     positions, sequences, table, pages = ragged(rng, [40, 3, 700], [0, 50, 9], 32)
     append_case(tp, positions, sequences, table, pages, 32, 32, 8, D, 2, dtype, dim=dim)
     append_case(tp, np.where(np.arange(len(positions)) % 7 == 0, -1, positions), sequences, table, pages, 32, 32, 8, D, 4, dtype, True, dim=dim)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("D,per", [(144, 9), (192, 16), (208, 12), (256, 16), (256, 17)])
+def test_decode_wide_heads_and_groups(tp, dtype, D, per):
+    """Long rows among short ones by the list, few rows by clusters, rows that a window bounds."""
+    decode_case(tp, np.random.default_rng(D + per), [2100, 0, 1, 900, 17, 33] + [60] * 30, 4 * per, 4, D, 32, 2, dtype)
+    decode_case(tp, np.random.default_rng(D - per), [1300, 129], 2 * per, 2, D, 16, 1, dtype)
+    decode_case(tp, np.random.default_rng(per), [700, 3, 500, 200] * 20, 2 * per, 2, D, 64, 2, dtype, window=140)
