@@ -51,9 +51,9 @@ constexpr int kShortPositions = 128;
 // cluster each.  So have rows of more than kShortPositions and up to
 // kBlockPositions, a block each, where that makes no more than twice the resident
 // blocks: a table's columns say little about the rows, and blocks come and go more
-// slowly than a resident block's warps take short ones (bf16, 304 segments of 144
-// elements, twice the resident: of up to 500 positions 18.5 us, 21.4 by the list,
-// of up to 30 both 9; 2432 segments: 114 and 105 us, 64 and 28).  Four times, where
+// slowly than a resident block's warps take short ones (8-bit, 608 segments of 256
+// elements, twice the resident: of up to 500 positions 28 us, 34 by the list, of up
+// to 30 13 and 11; 2432 segments: 84 and 84 us, 49 and 19).  Four times, where
 // a window is the bound, which most rows will fill (8-bit, 1072 segments of 235,
 // 2.4 times the resident: 25 us, 30 by the list).
 constexpr int kCluster = 8, kBlockPositions = 512;
@@ -202,10 +202,12 @@ struct TensorCore {
     static constexpr int kHeads = 8 * NT;
     static constexpr int kTileElems = DP;
     static constexpr int kRows = 16, kRowBytes = DP * static_cast<int>(sizeof(Cache));
-    // about 192 KB of stages an SM; 16 queries over codes take more registers, so fewer blocks
+    // about 192 KB of stages an SM; 16 queries over codes take more registers, so fewer blocks.
+    // Rows of 384 bytes: two blocks of two stages rather than one of four, whose warps were too
+    // few (152 rows of up to 1000 positions, 8 key heads of 144 elements: 71 us, 88 with one)
     static constexpr bool kFewer = k8 && NT == 2;
-    static constexpr int kStages = kRowBytes == 64 ? (kFewer ? 8 : 6) : kRowBytes == 128 ? (kFewer ? 6 : 4) : kRowBytes % 256 ? 4 : 3;
-    static constexpr int kBlocksPerSm = (kRowBytes == 64 ? 4 : kRowBytes == 128 ? 3 : kRowBytes <= 256 ? 2 : 1) - kFewer;
+    static constexpr int kStages = kRowBytes == 64 ? (kFewer ? 8 : 6) : kRowBytes == 128 ? (kFewer ? 6 : 4) : kRowBytes == 384 ? 2 : kRowBytes % 256 ? 4 : 3;
+    static constexpr int kBlocksPerSm = (kRowBytes == 384 ? 2 : kRowBytes == 64 ? 4 : kRowBytes == 128 ? 3 : kRowBytes <= 256 ? 2 : 1) - kFewer;
     __device__ __forceinline__ static int swizzle_keys(int row) { return swizzle_k<kRowBytes>(row); }
     __device__ __forceinline__ static int swizzle_values(int row) { return swizzle_v(row); }
     static constexpr int KC = k8 ? DP / 64 : DP / 32;       // 16-byte loads of a lane's key row
@@ -512,8 +514,9 @@ struct FloatCore {
     static constexpr int kHeads = NH;
     static constexpr int kTileElems = DP;
     static constexpr int kRows = DP <= 64 ? 16 : 8, kRowBytes = DP * 4;
-    static constexpr int kStages = DP == 96 || DP == 192 ? 4 : 3;
-    static constexpr int kBlocksPerSm = DP <= 128 ? 2 : 1;
+    // 192 elements: as for bf16 (24 heads over 8, 76 rows of up to 500: 53 us, 63 by one block)
+    static constexpr int kStages = DP == 96 ? 4 : DP == 192 ? 2 : 3;
+    static constexpr int kBlocksPerSm = DP <= 192 ? 2 : 1;
     static constexpr int J = DP / 32;        // 16-byte pieces of a row that a lane has
     static constexpr int I = kRows / 4;      // positions of a lane
     __device__ __forceinline__ static int swizzle_keys(int) { return 0; }
@@ -677,9 +680,11 @@ struct Tf32Core {
     using Act = float;
     static constexpr int kHeads = 8 * NT;
     static constexpr int kTileElems = DP;
-    static constexpr int kRows = DP <= 128 ? 16 : 8, kRowBytes = DP * 4, H = kRows / 8;
-    static constexpr int kStages = DP == 128 || DP == 256 ? 3 : DP == 64 ? 3 : 4;
-    static constexpr int kBlocksPerSm = DP == 64 ? 2 : 1;
+    // two blocks an SM where their stages and queries fit beside each other (64 heads of 72
+    // elements over 8, 64 rows of up to 4000: 110 us, 150 by one block)
+    static constexpr int kBlocksPerSm = DP == 64 || (DP <= 128 && NT == 1) ? 2 : 1;
+    static constexpr int kRows = DP <= 96 || (DP == 128 && NT == 2) ? 16 : 8, kRowBytes = DP * 4, H = kRows / 8;
+    static constexpr int kStages = DP % 96 ? 3 : 4 / kBlocksPerSm;
     // keys are read four pieces of 8 rows at a time, values two of four rows
     __device__ __forceinline__ static int swizzle_keys(int row) { return (row & 1) << 6; }
     __device__ __forceinline__ static int swizzle_values(int row) { return (row & 3) << 5; }
