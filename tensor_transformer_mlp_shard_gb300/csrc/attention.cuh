@@ -64,20 +64,23 @@ struct Turns {
 tp_status rope_validate(const tp_rope_desc *r, int head_dim);
 void rope_turns(const tp_rope_desc &r, Turns *t);
 
-// a cos and a sin at position p of a pair's turn, rounded as if they had been exact (but
-// for one in 500): keys in 8 bits should lie on the same side of a code's edge
-// as the definition's.  The angle to 2^-33 of a turn is taken to the nearest
-// quarter in integers; the rest x, an eighth of a turn at most, and the first
-// two terms of either series are pairs of fp32 numbers (Dekker's products and
-// Knuth's sums), the later terms, Taylor's up to x^13, single ones.  About 60
-// operations a pair and token, against some 1500 of its heads.
+// a cos and a sin at position p of a pair's turn, rounded as if they had been exact
+// (up to position 32768 but for one in 1000; one in 50 with 32 bits of the angle):
+// keys in 8 bits should lie on the same side of a code's edge as the definition's.
+// The angle is taken to the nearest quarter in integers; the rest x, an eighth of
+// a turn at most, and the first two terms of either series are pairs of fp32
+// numbers (Dekker's products and Knuth's sums), the later terms, Taylor's up to
+// x^13, single ones.  About 60 operations a pair and token, against some 1500 of
+// its heads.
 __device__ __forceinline__ float2 turn(const Turns &t, uint64_t per_position, int p) {
     const uint64_t phase = per_position * static_cast<uint32_t>(p);
     const uint32_t hi = static_cast<uint32_t>((phase + 0x80000000ull) >> 32);
     const uint32_t quarter = (hi + 0x20000000u) >> 30;
     const int rest = static_cast<int>(hi - (quarter << 30));
     const float rough = static_cast<float>(rest);
-    const float r = rough * 0x1p-31f, r_rest = static_cast<float>(rest - static_cast<int>(rough)) * 0x1p-31f;  // half turns
+    // in half turns, with what the 32 bits and the conversion lost
+    const float r = rough * 0x1p-31f;
+    const float r_rest = fmaf(static_cast<float>(static_cast<int>(static_cast<uint32_t>(phase))), 0x1p-63f, static_cast<float>(rest - static_cast<int>(rough)) * 0x1p-31f);
     constexpr float kPi = 0x1.921fb6p+1f, kPiRest = -0x1.777a5cp-24f;                // pi
     constexpr float kSixth = 0x1.555556p-3f, kSixthRest = -0x1.555556p-28f;          // 1 / 3!
     constexpr float k24th = 0x1.555556p-5f, k24thRest = -0x1.555556p-30f;            // 1 / 4!
