@@ -724,10 +724,13 @@ TP_API tp_status tp_paged_append(tp_paged *h, const void *const *X, const int32_
  * the handle's index word.
  * A value that is not finite leaves its element of the rows that see it not
  * finite (infinite, or NaN), a score of NaN or +infinity the whole row NaN.
- * Scores, softmax and sums are fp32; bf16 and FP8 weights enter the products as
- * the sum of two 16-bit numbers, and fp32 numbers, with more than four queries to
- * a key head, as two tf32 (2^-21 of a product).  The long axis is split over blocks, whose
- * results are joined in a fixed order: outputs are deterministic.
+ * Scores, softmax and sums are fp32.  Weights enter the products with bf16 caches
+ * as the sum of two bf16 numbers (to 2^-17 of a weight); with FP8 as that of two
+ * fp16 numbers, to 2^-22 of itself or of the largest weight of the 16 positions that
+ * are read together (far below a row's largest: to 2^-17 down to 2^-70 of it, none
+ * below 2^-88); fp32 numbers, with more than four queries to a key head, as two
+ * tf32 (2^-21 of a product).  The long axis is split over blocks, whose results are
+ * joined in a fixed order: outputs are deterministic.
  * workspace: >= tp_paged_workspace_bytes, 256-byte aligned; contents on entry
  * are ignored. */
 TP_API tp_status tp_paged_decode(tp_paged *h, const void *const *Q, const int32_t *positions,

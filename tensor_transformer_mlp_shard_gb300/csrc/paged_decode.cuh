@@ -357,15 +357,33 @@ struct TensorCore {
         }
     }
 
-    // The weights as the sum of two 16-bit numbers (2^-17 of a weight for bf16,
-    // 2^-22 for fp16): one bf16 would be off by as much as the output's own
-    // rounding.  The second product is free for bf16 caches, bound by memory, and
-    // costs 2% with codes (8-bit batch 132 us with one fp16, 135 us with two).
+    // The weights as the sum of two 16-bit numbers: one bf16 would be off by as much
+    // as the output's own rounding.  The second product is free for bf16 caches,
+    // bound by memory, and costs 2% with codes (8-bit batch 132 us with one fp16, 135
+    // us with two).  Two bf16 hold a weight to 2^-17 of itself.  Two fp16 hold it to
+    // 2^-22, but not finer than 2^-25, where their steps end; and small weights may
+    // be all that an output is made of, where the value at the dominant position is
+    // zero.  So with codes the weights are 2^kUp at the reference m, and m follows the
+    // steps' largest down as well as up: a step whose largest weight is below
+    // 2^(kUp - kDrop) has m lowered to it, and its weights are held to 2^-22 of that one.
+    // Softmaxes without a dominant position hardly get there (scores of standard
+    // deviation 3.6: one step of 16 in 2000), and pay for the look (8-bit batch 141 us,
+    // 139 without; each row with such a position 143 us).
+    static constexpr float kUp = k8 ? 15.0f : 0.0f, kDrop = 18.0f;
+    // The sum of weights stays below 2^kMostSum when the reference falls, and so the
+    // outputs finite: weights below 2^-70 of the largest are held to fewer digits, below
+    // 2^-88 to none.
+    static constexpr int kMostSum = 64;
+    // In a step that moves the reference down, or up by kRise, positions that are alone at
+    // the top (none from kSmall to kLarge) go first, and those below kSmall in another pass.
+    static constexpr float kRise = 14.0f, kSmall = 0x1p-8f, kLarge = 0x1p6f;
+    static constexpr int kPasses = 6;  // at most: the last takes all that is left
     uint32_t ph[NT][2], pl[NT][2];
 
-    __device__ __forceinline__ void softmax() {
+    // scores to weights; codes: whether the reference has far to go, up (it has been) or down
+    __device__ __forceinline__ bool softmax() {
         float top[NT][2];
-        bool rise = false;
+        bool move = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -375,9 +393,24 @@ struct TensorCore {
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                 top[n][r] = x;
-                rise |= x > m[n][r];
+                if constexpr (k8)
+                    move |= !(fabsf(x - m[n][r] - (kUp - 0.5f * kDrop)) <= 0.5f * kDrop);  // 2^-3 to 2^15
+                else
+                    move |= x > m[n][r];
             }
-        if (__any_sync(0xffffffffu, rise)) {
+        bool far = false;
+        if (__any_sync(0xffffffffu, move)) {
+            if constexpr (k8) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        // rounded up, so that no weight is above 2^kUp
+                        top[n][r] = __fadd_ru(top[n][r], -kUp);
+                        far |= top[n][r] > m[n][r] + kRise || top[n][r] < m[n][r] - kDrop;
+                    }
+                far = __any_sync(0xffffffffu, far);
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -386,39 +419,100 @@ struct TensorCore {
                     const float f = now == -INFINITY ? 1.0f : exp2_fast(m[n][r] - now);
                     m[n][r] = now;
                     l[n][r] *= f;
-#pragma unroll
-                    for (int b = 0; b < VB; ++b)
-#pragma unroll
-                        for (int i = 0; i < VD / 2; ++i) {
-                            acc[b][i][n][r] *= f;
-                            acc[b][i][n][r + 2] *= f;
-                        }
+                    scale_outputs(n, r, f);
                 }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float w[4];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const float top_of = m[n][r & 1] == -INFINITY ? 0.0f : m[n][r & 1];
-                w[r] = exp2_fast(s[n][r] - top_of);
+                s[n][r] = exp2_fast(s[n][r] - top_of);
             }
-            l[n][0] += w[0] + w[2];
-            l[n][1] += w[1] + w[3];
+        return far;
+    }
+
+    __device__ __forceinline__ void scale_outputs(int n, int r, float f) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                if constexpr (k8) {
-                    const __half2 x = __floats2half2_rn(w[2 * r], w[2 * r + 1]);
-                    const __half2 y = __floats2half2_rn(w[2 * r] - __low2float(x), w[2 * r + 1] - __high2float(x));
-                    ph[n][r] = transpose8(*reinterpret_cast<const uint32_t *>(&x));
-                    pl[n][r] = transpose8(*reinterpret_cast<const uint32_t *>(&y));
-                } else {
-                    const uint32_t hi = pack_bf16x2(w[2 * r], w[2 * r + 1]);
-                    ph[n][r] = transpose8(hi);
-                    pl[n][r] = transpose8(pack_bf16x2(w[2 * r] - bf16_lo(hi), w[2 * r + 1] - bf16_hi(hi)));
-                }
+        for (int b = 0; b < VB; ++b)
+#pragma unroll
+            for (int i = 0; i < VD / 2; ++i) {
+                acc[b][i][n][r] *= f;
+                acc[b][i][n][r + 2] *= f;
+            }
+    }
+
+    // four weights of the lane into the sums and, as pairs of 16-bit numbers, transposed
+    __device__ __forceinline__ void take(int n, const float (&w)[4]) {
+        l[n][0] += w[0] + w[2];
+        l[n][1] += w[1] + w[3];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            if constexpr (k8) {
+                const __half2 x = __floats2half2_rn(w[2 * r], w[2 * r + 1]);
+                const __half2 y = __floats2half2_rn(w[2 * r] - __low2float(x), w[2 * r + 1] - __high2float(x));
+                ph[n][r] = transpose8(*reinterpret_cast<const uint32_t *>(&x));
+                pl[n][r] = transpose8(*reinterpret_cast<const uint32_t *>(&y));
+            } else {
+                const uint32_t hi = pack_bf16x2(w[2 * r], w[2 * r + 1]);
+                ph[n][r] = transpose8(hi);
+                pl[n][r] = transpose8(pack_bf16x2(w[2 * r] - bf16_lo(hi), w[2 * r + 1] - bf16_hi(hi)));
             }
         }
+    }
+
+    // Lowers the reference to the weights that are left where they are small, and takes
+    // them, or the uppermost where these are alone.  Returns whether any are left: a
+    // query's largest never is.  No lane goes a way of its own.
+    __device__ __forceinline__ bool take_lowered(int pass) {
+        bool left = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float w[4], x[2];
+            int exponent[2];
+            bool small = false;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                x[c] = fmaxf(s[n][c], s[n][c + 2]);
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) x[c] = fmaxf(x[c], __shfl_xor_sync(0xffffffffu, x[c], o));
+                exponent[c] = x[c] > 0.0f ? static_cast<int>(__float_as_uint(x[c]) >> 23) - 127 : 0;
+                small |= exponent[c] < static_cast<int>(kUp - kDrop);
+            }
+            if (__any_sync(0xffffffffu, small)) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float all = l[n][c];
+#pragma unroll
+                    for (int o = 4; o < 32; o *= 2) all += __shfl_xor_sync(0xffffffffu, all, o);
+                    const int sum = static_cast<int>(__float_as_uint(all) >> 23) - 126;  // all < 2^sum; NaN: above kMostSum
+                    const int by = exponent[c] < static_cast<int>(kUp - kDrop) ? max(min(14 - exponent[c], kMostSum - sum), 0) : 0;
+                    const float now = __fadd_ru(m[n][c], -static_cast<float>(by));
+                    const float f = by > 0 ? exp2_fast(m[n][c] - now) : 1.0f;
+                    m[n][c] = now;
+                    l[n][c] *= f;
+                    scale_outputs(n, c, f);
+                    s[n][c] *= f;
+                    s[n][c + 2] *= f;
+                    x[c] *= f;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const bool among = (s[n][c] >= kSmall && s[n][c] < kLarge) || (s[n][c + 2] >= kSmall && s[n][c + 2] < kLarge);
+                const uint32_t lanes = __ballot_sync(0xffffffffu, among) & (0x11111111u << t);
+                const bool alone = x[c] >= kLarge && lanes == 0u && pass < kPasses - 1;
+#pragma unroll
+                for (int r = c; r < 4; r += 2) {
+                    const bool later = alone && s[n][r] < kSmall;  // NaN is taken
+                    w[r] = later ? 0.0f : s[n][r];
+                    s[n][r] = later ? s[n][r] : 0.0f;
+                    left |= s[n][r] > 0.0f;
+                }
+            }
+            take(n, w);
+        }
+        return __any_sync(0xffffffffu, left);
     }
 
     __device__ __forceinline__ void values(const char *v) {
@@ -472,8 +566,21 @@ struct TensorCore {
     // one step, its stage in shared memory
     __device__ __forceinline__ void step(const DecodePlan &, const char *stage, const Seen &seen) {
         scores(stage, seen);
-        softmax();
-        values(stage + kRows * kRowBytes);
+        const bool far = softmax();
+        const char *v = stage + kRows * kRowBytes;
+        if (k8 && far) {
+            bool left;
+            int pass = 0;
+            do {
+                left = take_lowered(pass++);
+                __syncwarp();
+                values(v);
+            } while (left);
+        } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) take(n, s[n]);
+            values(v);
+        }
     }
 
     // the warp's state to shared memory: out [kHeads][DP], top and sum [kHeads]
