@@ -769,8 +769,9 @@ struct FloatCore {
 // taken: x = hi + lo to 2^-21, and x y = hi hi + hi lo + lo hi to 3 2^-22, in fp32
 // sums.  Fragments as in TensorCore, with 4-byte elements: a lane's 16 bytes of a
 // key are two contractions of 8, and the rows of V^T the elements 2i and 2i + 1 of
-// its four.  Sums of hi hi are kept apart in the scores: where they are not
-// finite, the rest (inf - inf) says nothing.  Queries lie in shared memory.
+// its four.  Queries lie in shared memory.  Sums of hi hi are kept apart in the scores.
+// A step with a score that is not finite has its scores by plain products: the rest of
+// an infinity is NaN, and NaN may be cut to an infinity.
 __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -833,6 +834,24 @@ struct Tf32Core {
                     for (int r = 0; r < 4; ++r) acc[b][i][n][r] = 0.0f;
     }
 
+    // The lane's scores by fp32 products, where tf32 left one that is not finite.
+    __device__ __forceinline__ void plain_scores(const char *stage, float (&s)[NT][2 * H]) const {
+#pragma unroll 1
+        for (int i = 0; i < NT * 2 * H; ++i) {
+            const int n = i / (2 * H), r = i - n * 2 * H, row = r < 2 ? g : g + 8, query = 8 * n + 2 * t + (r & 1);
+            float x = 0.0f;
+#pragma unroll 1
+            for (int e = 0; e < 4 * DP; e += 16) {
+                const float4 k = *reinterpret_cast<const float4 *>(stage + ((row * kRowBytes + e) ^ swizzle_keys(row)));
+                const float4 y = *reinterpret_cast<const float4 *>(q + ((query * kRowBytes + e) ^ swizzle_keys(query)));
+                x = fmaf(y.x, k.x, fmaf(y.y, k.y, fmaf(y.z, k.z, fmaf(y.w, k.w, x))));
+            }
+#pragma unroll
+            for (int j = 0; j < NT * 2 * H; ++j)
+                if (j == i) s[j / (2 * H)][j % (2 * H)] = x;
+        }
+    }
+
     __device__ __forceinline__ void step(const DecodePlan &p, const char *stage, const Seen &seen) {
         float big[NT][4] = {}, rest[NT][4] = {};
 #pragma unroll
@@ -863,13 +882,21 @@ struct Tf32Core {
             }
         }
         float s[NT][2 * H];
+        bool odd = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2 * H; ++r) {
+                s[n][r] = big[n][r] + rest[n][r];
+                odd |= !(fabsf(s[n][r]) <= 3.4e38f);
+            }
+        if (__any_sync(0xffffffffu, odd)) plain_scores(stage, s);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int r = 0; r < 2 * H; ++r) {
                 const int row = r < 2 ? g : g + 8;
-                const float x = fabsf(big[n][r]) <= 3.4e38f ? big[n][r] + rest[n][r] : big[n][r];
-                s[n][r] = row >= seen.lo && row < seen.hi ? x * p.scale_log2 : -INFINITY;
+                s[n][r] = row >= seen.lo && row < seen.hi ? s[n][r] * p.scale_log2 : -INFINITY;
             }
 
         float top[NT][2];

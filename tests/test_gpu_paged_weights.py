@@ -150,3 +150,35 @@ def test_every_weight(tp, dtype, per, scores):
         vals.append(v)
     for capacity in (0, 40000):
         run(tp, rng, [n] * n, [k] * n, vals, per, dtype, D, spread_keys=[0 * k] * n, capacity=capacity)
+
+
+@pytest.mark.parametrize("per", [1, 4, 5, 12])
+@pytest.mark.parametrize("capacity", [1, 200])
+def test_fp32_numbers_at_the_ends_of_their_range(tp, per, capacity):
+    """NaN with its mark in the last place, and the largest numbers, in keys, queries and values."""
+    D, top = 64, float(np.finfo(np.float32).max)
+    h = tp.TPPagedAttention(per, 1, D, 16, 6, dtype="f32", scale=1.0, rope=tp.Rope(dim=0))
+    K, V = np.zeros((6, 1, 16, D), dtype=np.float32), np.ones((6, 1, 16, D), dtype=np.float32)
+    q = np.zeros((6, per, D), dtype=np.float32)
+    q[0, :, 7] = -1.0                                    # NaN times a negative number
+    K[0, 0, 3, 7] = np.array(0x7f800001, dtype=np.uint32).view(np.float32)
+    K[1, 0, 3, 9], q[1, :, 9] = top, 2.0 ** -125         # scores of 8 and 0
+    K[2, 0, 3, 9], q[2, :, 9] = 2.0 ** -125, -top        # of -8 and 0
+    K[3, 0, 3, 9], q[3, :, 9] = -top, 1.0                # one weighs nothing
+    K[4, 0, 3, 9], q[4, :, 9] = float("-inf"), 1.0
+    V[5, 0, 3] = top                                     # a quarter of the largest number
+    V[:5, 0, 3] = 3.0
+    V[5, 0, :3] = 0.0
+    table = np.full((6, capacity), -1, dtype=np.int32)
+    table[:, 0] = np.arange(6)
+    o = torch.empty(6, per * D, device="cuda")
+    h.decode(torch.from_numpy(q).view(6, -1).cuda(), cuda_i32([3] * 6), cuda_i32(table), torch.from_numpy(K).cuda(),
+             torch.from_numpy(V).cuda(), o, tp.alloc_workspace(h.workspace_bytes()))
+    o = o.double().cpu().numpy()
+    assert np.isnan(o[0]).all()
+    for row, score in ((1, 8.0), (2, -8.0)):
+        w = 1.0 / (1.0 + 3.0 * np.exp(-score))
+        # scores of 8 to 2^-19 of themselves, products and sums to 2^-19
+        assert np.abs(o[row] / (1.0 + 2.0 * w) - 1.0).max() <= 8 * 2.0 ** -19 + 2.0 ** -19
+    assert (o[3] == 1.0).all() and (o[4] == 1.0).all()
+    assert np.abs(o[5] / (top / 4) - 1.0).max() <= 2.0 ** -19
