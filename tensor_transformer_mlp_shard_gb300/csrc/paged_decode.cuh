@@ -765,20 +765,31 @@ struct FloatCore {
 // ---------------------------------------------------------------------------
 // fp32 products by tf32: more than four queries of an fp32 cache
 // ---------------------------------------------------------------------------
-// A number is split into the tf32 it is cut to and the rest, whose own tf32 part is
-// taken: x = hi + lo to 2^-21, and x y = hi hi + hi lo + lo hi to 3 2^-22, in fp32
-// sums.  Fragments as in TensorCore, with 4-byte elements: a lane's 16 bytes of a
-// key are two contractions of 8, and the rows of V^T the elements 2i and 2i + 1 of
-// its four.  Queries lie in shared memory.  Sums of hi hi are kept apart in the scores.
-// A step with a score that is not finite has its scores by plain products: the rest of
-// an infinity is NaN, and NaN may be cut to an infinity.
+// Keys, queries and weights are split into the nearest tf32 and the rest, at most
+// 2^-11 of them and of either sign, whose own tf32 part is taken (to 2^-23 of the
+// number); values into the tf32 they are cut to and the rest, at most 2^-10 (to 2^-21),
+// so that the largest ones stay finite.  x y = hi hi + hi lo + lo hi misses lo lo
+// and what the rests miss, in fp32 sums: 2^-21 of a key's product, 2^-19.8 of a value's.
+// (With all cut lo lo would have the product's sign and reach 2^-20 in the scores; with
+// a look for the largest numbers at every one 40 heads of 256 over 8, 16 rows of up to
+// 4000, take 192 us, now 146.)  Fragments as in TensorCore, with 4-byte elements: a
+// lane's 16 bytes of a key are two contractions of 8, and the rows of V^T the
+// elements 2i and 2i + 1 of its four.  Queries lie in shared memory.  Sums of hi hi are
+// kept apart in the scores.  A step with a score that is not finite has its scores
+// by plain products: the rest of an infinity is NaN, NaN may be cut to an infinity, and
+// the largest numbers rounded to one.
 __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+__device__ __forceinline__ void split_cut(float x, uint32_t &hi, uint32_t &lo) {
     hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+// NaN comes out in lo at least, a number of 2^128 - 2^116 or more as an infinity and its opposite
+__device__ __forceinline__ void split_nearest(float x, uint32_t &hi, uint32_t &lo) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
     lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
@@ -860,19 +871,19 @@ struct Tf32Core {
 #pragma unroll
             for (int r = 0; r < H; ++r) {
                 const float4 x = *reinterpret_cast<const float4 *>(stage + (((g + 8 * r) * kRowBytes + 64 * c + 16 * t) ^ swizzle_keys(g)));
-                split_tf32(x.x, hi[0][r], lo[0][r]);
-                split_tf32(x.y, hi[0][r + 2], lo[0][r + 2]);
-                split_tf32(x.z, hi[1][r], lo[1][r]);
-                split_tf32(x.w, hi[1][r + 2], lo[1][r + 2]);
+                split_nearest(x.x, hi[0][r], lo[0][r]);
+                split_nearest(x.y, hi[0][r + 2], lo[0][r + 2]);
+                split_nearest(x.z, hi[1][r], lo[1][r]);
+                split_nearest(x.w, hi[1][r + 2], lo[1][r + 2]);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float4 y = *reinterpret_cast<const float4 *>(q + (((8 * n + g) * kRowBytes + 64 * c + 16 * t) ^ swizzle_keys(g)));
                 uint32_t qh[4], ql[4];
-                split_tf32(y.x, qh[0], ql[0]);
-                split_tf32(y.y, qh[1], ql[1]);
-                split_tf32(y.z, qh[2], ql[2]);
-                split_tf32(y.w, qh[3], ql[3]);
+                split_nearest(y.x, qh[0], ql[0]);
+                split_nearest(y.y, qh[1], ql[1]);
+                split_nearest(y.z, qh[2], ql[2]);
+                split_nearest(y.w, qh[3], ql[3]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     mma1688(big[n], hi[u], qh[2 * u], qh[2 * u + 1]);
@@ -946,7 +957,7 @@ struct Tf32Core {
                 for (int j = 0; j < 2; ++j) {
                     const int from = 4 * (t + 4 * j) + g / 2;
                     const float even = __shfl_sync(0xffffffffu, s[n][2 * h], from), odd = __shfl_sync(0xffffffffu, s[n][2 * h + 1], from);
-                    split_tf32(g & 1 ? odd : even, ph[n][h][j], pl[n][h][j]);
+                    split_nearest(g & 1 ? odd : even, ph[n][h][j], pl[n][h][j]);
                 }
         }
         const char *v = stage + kRows * kRowBytes;
@@ -958,14 +969,14 @@ struct Tf32Core {
                 const float4 x = *reinterpret_cast<const float4 *>(v + (((t + 8 * h) * kRowBytes + 128 * b + 16 * g) ^ (t << 5)));
                 const float4 y = *reinterpret_cast<const float4 *>(v + (((t + 4 + 8 * h) * kRowBytes + 128 * b + 16 * g) ^ (t << 5)));
                 uint32_t hi[2][4], lo[2][4];
-                split_tf32(x.x, hi[0][0], lo[0][0]);
-                split_tf32(x.y, hi[0][1], lo[0][1]);
-                split_tf32(x.z, hi[1][0], lo[1][0]);
-                split_tf32(x.w, hi[1][1], lo[1][1]);
-                split_tf32(y.x, hi[0][2], lo[0][2]);
-                split_tf32(y.y, hi[0][3], lo[0][3]);
-                split_tf32(y.z, hi[1][2], lo[1][2]);
-                split_tf32(y.w, hi[1][3], lo[1][3]);
+                split_cut(x.x, hi[0][0], lo[0][0]);
+                split_cut(x.y, hi[0][1], lo[0][1]);
+                split_cut(x.z, hi[1][0], lo[1][0]);
+                split_cut(x.w, hi[1][1], lo[1][1]);
+                split_cut(y.x, hi[0][2], lo[0][2]);
+                split_cut(y.y, hi[0][3], lo[0][3]);
+                split_cut(y.z, hi[1][2], lo[1][2]);
+                split_cut(y.w, hi[1][3], lo[1][3]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll

@@ -152,6 +152,33 @@ def test_every_weight(tp, dtype, per, scores):
         run(tp, rng, [n] * n, [k] * n, vals, per, dtype, D, spread_keys=[0 * k] * n, capacity=capacity)
 
 
+@pytest.mark.parametrize("per", [1, 5, 8, 12])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_fp32_products_to_their_last_digits(tp, per, D):
+    """Scores of one product each, their mantissas just below a step of eleven bits: two positions a row, the
+    first's weight is the output.  It is off by 2^-21 of the scores (64) for the products and, for both scores'
+    sums and roundings to log2 units (92), four of 2^-24, times at most 1/4; its own products and sums add 2^-20."""
+    rng = np.random.default_rng(per)
+    rows = 64
+    h = tp.TPPagedAttention(per, 1, D, 16, rows, dtype="f32", scale=64.0, rope=tp.Rope(dim=0))
+    below = 2.0 ** -10 - rng.integers(1, 8, rows) * 2.0 ** -23
+    x = np.float32(1 + rng.integers(0, 4, rows) * 2.0 ** -10 + below)
+    q = np.zeros((rows, per, D), dtype=np.float32)
+    q[..., 0] = x[:, None]
+    K = np.zeros((rows, 1, 16, D), dtype=np.float32)
+    V = K.copy()
+    K[:, 0, 0, 0] = x
+    K[:, 0, 1, 0] = np.float32(np.round(x.astype(np.float64) * 2 ** 10) / 2 ** 10 - rng.integers(0, 3, rows) * 2.0 ** -8)
+    V[:, 0, 0] = 1.0
+    o = torch.empty(rows, per * D, device="cuda")
+    h.decode(torch.from_numpy(q).view(rows, -1).cuda(), cuda_i32([1] * rows), cuda_i32(np.arange(rows)[:, None]),
+             torch.from_numpy(K).cuda(), torch.from_numpy(V).cuda(), o, tp.alloc_workspace(h.workspace_bytes()))
+    score = 64.0 * x.astype(np.float64)[:, None] * K[:, 0, :2, 0].astype(np.float64)
+    want = 1.0 / (1.0 + np.exp(score[:, 1] - score[:, 0]))
+    off = np.abs(o.double().cpu().numpy() - want[:, None])
+    assert off.max() <= 0.25 * (64 * 2.0 ** -21 + 4 * 92 * 2.0 ** -24 * np.log(2)) + 2.0 ** -20
+
+
 @pytest.mark.parametrize("per", [1, 4, 5, 12])
 @pytest.mark.parametrize("capacity", [1, 200])
 def test_fp32_numbers_at_the_ends_of_their_range(tp, per, capacity):
