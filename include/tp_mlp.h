@@ -730,8 +730,7 @@ TP_API tp_status tp_paged_append(tp_paged *h, const void *const *X, const int32_
  * are read together (far below a row's largest: to 2^-17 down to 2^-70 of it, none
  * below 2^-88); fp32 numbers, with more than four queries to a key head, as two
  * tf32 (to 2^-21 of a key's product, 2^-19.8 of a value's).  The long axis is split
- * over blocks, whose results are
- * joined in a fixed order: outputs are deterministic.
+ * over blocks, whose results are joined in a fixed order: outputs are deterministic.
  * workspace: >= tp_paged_workspace_bytes, 256-byte aligned; contents on entry
  * are ignored. */
 TP_API tp_status tp_paged_decode(tp_paged *h, const void *const *Q, const int32_t *positions,

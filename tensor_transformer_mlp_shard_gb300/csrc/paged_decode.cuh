@@ -398,18 +398,21 @@ struct TensorCore {
                 else
                     move |= x > m[n][r];
             }
-        bool far = false;
+        bool far = false, up = false;
         if (__any_sync(0xffffffffu, move)) {
             if constexpr (k8) {
+                bool rise = false, fall = false;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         // rounded up, so that no weight is above 2^kUp
                         top[n][r] = __fadd_ru(top[n][r], -kUp);
-                        far |= top[n][r] > m[n][r] + kRise || top[n][r] < m[n][r] - kDrop;
+                        rise |= top[n][r] > m[n][r] + kRise;
+                        fall |= top[n][r] < m[n][r] - kDrop;
                     }
-                far = __any_sync(0xffffffffu, far);
+                up = __any_sync(0xffffffffu, rise);
+                far = __any_sync(0xffffffffu, fall);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -429,6 +432,14 @@ struct TensorCore {
                 const float top_of = m[n][r & 1] == -INFINITY ? 0.0f : m[n][r & 1];
                 s[n][r] = exp2_fast(s[n][r] - top_of);
             }
+        if (up && !far) {  // a row's first step, as a rule: nothing to do but beside a dominant position
+            bool small = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) small |= s[n][r] > 0.0f && s[n][r] < kSmall;
+            far = __any_sync(0xffffffffu, small);
+        }
         return far;
     }
 
