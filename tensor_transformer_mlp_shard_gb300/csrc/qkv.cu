@@ -442,21 +442,69 @@ tp_status rope_validate(const tp_rope_desc *r, int head_dim) {
     return TP_OK;
 }
 
+// A number as the sum of two doubles, to about 2^-100: a position multiplies what
+// 53 bits of a frequency lose by up to 2^31.  Sums after Knuth, products after Dekker
+// with the machine's fma; every product goes through fma, so that no compiler
+// takes it into a sum of its own.
+struct Pair {
+    double hi, lo;
+};
+static Pair pair_sum(double a, double b) {
+    const double s = a + b, x = s - a;
+    return {s, (a - (s - x)) + (b - x)};
+}
+static Pair operator*(Pair a, Pair b) {
+    const double p = std::fma(a.hi, b.hi, 0.0), rest = std::fma(a.hi, b.hi, -p);
+    return pair_sum(p, std::fma(a.hi, b.lo, std::fma(a.lo, b.hi, rest)));
+}
+static Pair operator+(Pair a, Pair b) {
+    const Pair s = pair_sum(a.hi, b.hi);
+    return pair_sum(s.hi, s.lo + (a.lo + b.lo));
+}
+static Pair inverse(Pair a) {
+    const double x = 1.0 / a.hi;
+    const Pair off = Pair{1.0, 0.0} + a * Pair{-x, 0.0};  // 1 - a x
+    return pair_sum(x, std::fma(x, off.hi, 0.0));
+}
+static Pair power(Pair a, int n) {
+    Pair y = {1.0, 0.0};
+    for (; n > 0; n >>= 1, a = a * a)
+        if (n & 1) y = y * a;
+    return y;
+}
+// a^(-1/n): a double's root and one step of Newton's method, which squares its error
+static Pair inverse_root(double a, int n) {
+    const Pair x = {std::pow(a, -1.0 / n), 0.0};
+    const Pair off = Pair{1.0, 0.0} + power(x, n) * Pair{-a, 0.0};  // 1 - a x^n
+    return pair_sum(x.hi, std::fma(x.hi, off.hi / n, 0.0));
+}
+
 void rope_turns(const tp_rope_desc &r, Turns *t) {
-    const double two_pi = 6.283185307179586476925;
-    double base = r.base;
-    if (r.scaling == TP_ROPE_NTK && r.dim > 2) base *= std::pow(r.factor, static_cast<double>(r.dim) / (r.dim - 2));
-    for (int i = 0; i < r.dim / 2; ++i) {
-        double f = std::pow(base, -2.0 * i / r.dim);
-        if (r.scaling == TP_ROPE_LINEAR) f /= r.factor;
+    const Pair turn = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / 2 pi
+    const int half = r.dim / 2;
+    const Pair slower = inverse({r.factor, 0.0});
+    // of neighbouring pairs; with NTK base^(-1/half) s^(-1/(half - 1))
+    Pair ratio = {1.0, 0.0};
+    if (half > 0) ratio = inverse_root(r.base, half);
+    if (r.scaling == TP_ROPE_NTK && half > 1) ratio = ratio * inverse_root(r.factor, half - 1);
+    for (int i = 0; i < half; ++i) {
+        Pair f = power(ratio, i);
+        if (r.scaling == TP_ROPE_LINEAR) f = f * slower;
         if (r.scaling == TP_ROPE_PARTS) {
-            double keep = (r.original * f / two_pi - r.slow) / (r.fast - r.slow);
-            keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
-            f = f * keep + f / r.factor * (1.0 - keep);
+            // k f + (1 - k) f / s
+            Pair keep = {(r.original * (f.hi * turn.hi) - r.slow) / (r.fast - r.slow), 0.0};
+            if (keep.hi > -1.0 && keep.hi < 2.0)
+                keep = (f * turn * Pair{r.original, 0.0} + Pair{-r.slow, 0.0}) * inverse(pair_sum(r.fast, -r.slow));
+            if (!(keep.hi > 0.0)) keep = {0.0, 0.0};
+            if (keep.hi >= 1.0) keep = {1.0, 0.0};
+            f = f * (keep + (Pair{1.0, 0.0} + keep * Pair{-1.0, 0.0}) * slower);
         }
-        t->per_position[i] = static_cast<uint64_t>(f / two_pi * 0x1p64);
+        // to the nearest 2^-64 of a turn
+        const Pair turns = f * turn;
+        const double whole = std::floor(turns.hi * 0x1p64);
+        t->per_position[i] = static_cast<uint64_t>(whole) + static_cast<uint64_t>(std::llrint((turns.hi * 0x1p64 - whole) + turns.lo * 0x1p64));
     }
-    for (int i = r.dim / 2; i < kMaxPairs; ++i) t->per_position[i] = 0;
+    for (int i = half; i < kMaxPairs; ++i) t->per_position[i] = 0;
     double a = r.attention_factor;
     if (a == 0.0) a = r.scaling == TP_ROPE_PARTS ? 0.1 * std::log(r.factor) + 1.0 : 1.0;
     t->a = static_cast<float>(a);
