@@ -667,8 +667,8 @@ TP_API tp_status tp_rotary_bwd(tp_rotary *h, const void *const *dY, const int32_
  * each, of the handle's type, or bytes with TP_DT_FP8: E4M3 codes, code =
  * fp8(x * scale) saturating, scale = 448 / amax of the key head (1 when amax is
  * not in [2^-100, 3e38]) from k_amax and v_amax, fp32 [kv_heads] on the device
- * (4-byte aligned; NULL otherwise).  A cache is read with the amax it was
- * written with.
+ * (4-byte aligned; ignored with the other types).  A cache is read with the amax it
+ * was written with.
  * Table: int32 [sequences, table_cols] on the device; position p of sequence s
  * is slot p % page_size of page table[s][p / page_size].  Entries that no
  * position of a call needs are not read as pages (-1, say).

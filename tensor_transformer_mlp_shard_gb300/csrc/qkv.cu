@@ -836,8 +836,8 @@ tp_status tp_paged_append(tp_paged *h, const void *const *X, const int32_t *posi
     TRY(at_array(V, d.T, "V", p.v));
     TRY(index_word(h->word, &p.at.index_word));
     p.at.owner = h->owner;
-    p.k_amax = k_amax;
-    p.v_amax = v_amax;
+    p.k_amax = d.dtype == TP_DT_FP8 ? k_amax : nullptr;
+    p.v_amax = d.dtype == TP_DT_FP8 ? v_amax : nullptr;
     p.hq = d.heads / d.T;
     p.hk = d.kv_heads / d.T;
     p.per = d.heads / d.kv_heads;
@@ -873,8 +873,8 @@ tp_status tp_paged_decode(tp_paged *h, const void *const *Q, const int32_t *posi
         return set_error(TP_ERR_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     TRY(index_word(h->word, &p.at.index_word));
     p.at.owner = h->owner;
-    p.k_amax = k_amax;
-    p.v_amax = v_amax;
+    p.k_amax = d.dtype == TP_DT_FP8 ? k_amax : nullptr;
+    p.v_amax = d.dtype == TP_DT_FP8 ? v_amax : nullptr;
     p.hq = d.heads / d.T;
     p.hk = d.kv_heads / d.T;
     p.per = d.heads / d.kv_heads;
