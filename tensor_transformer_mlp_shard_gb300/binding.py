@@ -912,6 +912,8 @@ class Rope:
                  slow=1.0, attention_factor=None):
         self.dim, self.base, self.interleaved, self.scaling = dim, base, interleaved, scaling
         self.factor, self.original, self.fast, self.slow = factor, original, fast, slow
+        if attention_factor is not None and not attention_factor:
+            raise ValueError("attention_factor: 0 leaves no queries and keys")
         self.attention_factor = attention_factor
 
     def desc(self, head_dim: int) -> RopeDesc:

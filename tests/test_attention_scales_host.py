@@ -1,0 +1,19 @@
+"""Scales and factors that stand for something else, or that fp32 does not hold (no GPU)."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def tp():
+    from tensor_transformer_mlp_shard_gb300 import build
+    build.build()
+    import tensor_transformer_mlp_shard_gb300 as tp
+    return tp
+
+
+@pytest.mark.parametrize("factor", [0, 0.0, -0.0])
+def test_an_attention_factor_of_zero_is_no_default(tp, factor):
+    """In the descriptor 0 stands for the default, which is None here."""
+    with pytest.raises(ValueError, match="attention_factor"):
+        tp.Rope(attention_factor=factor)
+    assert tp.Rope().desc(64).attention_factor == 0.0
+    assert tp.Rope(attention_factor=0.5).desc(64).attention_factor == 0.5
