@@ -17,3 +17,14 @@ def test_an_attention_factor_of_zero_is_no_default(tp, factor):
         tp.Rope(attention_factor=factor)
     assert tp.Rope().desc(64).attention_factor == 0.0
     assert tp.Rope(attention_factor=0.5).desc(64).attention_factor == 0.5
+
+
+PAGED = dict(heads=8, kv_heads=4, head_dim=64, page_size=16, pages=10, T=2)
+
+
+@pytest.mark.parametrize("scale", [1e-46, -1e-50, 5e-324])
+def test_a_scale_below_fp32_is_no_default(tp, scale):
+    """Zero in the descriptor, which stands for 1 / sqrt(head_dim)."""
+    with pytest.raises(ValueError, match="scale"):
+        tp.TPPagedAttention(**PAGED, scale=scale)
+    tp.TPPagedAttention(**PAGED, scale=1e-44)
