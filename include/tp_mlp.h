@@ -682,7 +682,7 @@ typedef struct {
     int page_size;                    /* positions a page: a multiple of 16 */
     int pages;                        /* pages of the cache, >= 1 */
     int window;                       /* positions that a token sees, its own among them; 0: all */
-    float scale;                      /* of the scores, finite; 0: 1 / sqrt(head_dim) */
+    float scale;                      /* of the scores, below 2^128 / log2(e); 0: 1 / sqrt(head_dim) */
     tp_rope_desc rope;                /* dim 0: keys and queries as they are */
 } tp_paged_desc;
 

@@ -773,7 +773,9 @@ tp_status tp_paged_create(const tp_paged_desc *desc, tp_paged **out) {
         return set_error(TP_ERR_SHAPE, "pages=%d of %d positions and %d key heads: 2^35 rows of a cache or more", desc->pages,
                          desc->page_size, desc->kv_heads / desc->T);
     if (desc->window < 0) return set_error(TP_ERR_ARG, "window=%d is negative", desc->window);
-    if (!std::isfinite(desc->scale)) return set_error(TP_ERR_ARG, "scale must be finite");
+    // the scores are taken to base 2
+    if (!std::isfinite(static_cast<float>(static_cast<double>(desc->scale) * 1.4426950408889634)))
+        return set_error(TP_ERR_ARG, "scale must be finite, and below 2^128 / log2(e)");
     tp_paged *h = new (std::nothrow) tp_paged;
     if (!h) return set_error(TP_ERR_ARG, "out of host memory");
     h->d = *desc;

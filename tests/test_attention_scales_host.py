@@ -28,3 +28,12 @@ def test_a_scale_below_fp32_is_no_default(tp, scale):
     with pytest.raises(ValueError, match="scale"):
         tp.TPPagedAttention(**PAGED, scale=scale)
     tp.TPPagedAttention(**PAGED, scale=1e-44)
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3e38, 3.4028e38])
+def test_a_scale_beyond_base_two(tp, scale):
+    """Scores of zero would become infinity times zero."""
+    with pytest.raises(tp.TpError) as e:
+        tp.TPPagedAttention(**PAGED, scale=scale)
+    assert e.value.status == 1
+    tp.TPPagedAttention(**PAGED, scale=2.3e38 if scale > 0 else -2.3e38)
