@@ -1027,7 +1027,7 @@ class TPPagedAttention:
     def __init__(self, heads, kv_heads, head_dim, page_size, pages, T=1, dtype="bf16", grouped=False, rope=None,
                  window=0, scale=None):
         rope = rope or Rope()
-        if scale is not None and not ctypes.c_float(scale).value:
+        if scale is not None and not ctypes.c_float(float(scale)).value:
             raise ValueError("scale: 0 (in fp32) leaves no attention")
         self._d = PagedDesc(int(T), int(heads), int(kv_heads), int(head_dim), DTYPE[dtype], int(bool(grouped)),
                             int(page_size), int(pages), int(window), 0.0 if scale is None else float(scale),

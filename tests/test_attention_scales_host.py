@@ -37,3 +37,9 @@ def test_a_scale_beyond_base_two(tp, scale):
         tp.TPPagedAttention(**PAGED, scale=scale)
     assert e.value.status == 1
     tp.TPPagedAttention(**PAGED, scale=2.3e38 if scale > 0 else -2.3e38)
+
+
+def test_scales_of_any_number_type(tp):
+    import numpy as np
+    for scale in (1, np.float32(0.5), np.float16(0.5), np.int64(2)):
+        tp.TPPagedAttention(**PAGED, scale=scale)
