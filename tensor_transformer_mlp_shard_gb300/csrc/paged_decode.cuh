@@ -1080,6 +1080,9 @@ __device__ __forceinline__ int queries_of(const DecodePlan &p, int rh) {
 // A group's outputs [nh][D], maxima [nh] and sums [nh], in whole 16 bytes.
 inline __host__ __device__ int part_floats(int nh, int D) { return (nh * (D + 2) + 3) & ~3; }
 
+// An output is (sum of values / sum of weights) * value scale, in this order: with
+// codes the weights' sum reaches 2^64 and the scale may be as small as 2^-109.
+
 // Elements e.. of query h from the states of warps w0..w1 (their outputs `pitch`
 // bytes apart): eight of the sum, its maximum, the sum of weights.
 template <int NH, int DP>
@@ -1351,9 +1354,9 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) decode_kernel(cons
             float most, all, f[8];
             add_warps<NH, DP>(ring + kOutAt, kRing, top, sum, h, e, w0, w1, f, most, all);
             if (whole) {
-                const float by = all == 0.0f ? 0.0f : vscale / all;
+                const float by = 1.0f / all;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = all == 0.0f ? 0.0f : f[j] * by;
+                for (int j = 0; j < 8; ++j) f[j] = all == 0.0f ? 0.0f : f[j] * by * vscale;
                 store8(static_cast<Act *>(p.o[at.shard]) + q_at + static_cast<long long>(h) * p.D + e, f);
             } else {
                 store8(part + h * p.D + e, f);
@@ -1491,8 +1494,9 @@ __global__ void __maxnreg__(registers_of(Core::kBlocksPerSm)) cluster_kernel(con
             all = fmaf(l[c], by, all);
             f.x = fmaf(x[c].x, by, f.x); f.y = fmaf(x[c].y, by, f.y); f.z = fmaf(x[c].z, by, f.z); f.w = fmaf(x[c].w, by, f.w);
         }
-        const float by = all == 0.0f ? 0.0f : vscale / all;
-        const float4 o = all == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(f.x * by, f.y * by, f.z * by, f.w * by);
+        const float by = 1.0f / all;
+        const float4 o = all == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                     : make_float4(f.x * by * vscale, f.y * by * vscale, f.z * by * vscale, f.w * by * vscale);
         Act *to = static_cast<Act *>(p.o[at.shard]) + q_at + static_cast<long long>(h) * p.D + e;
         if constexpr (sizeof(Act) == 2)
             *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
@@ -1578,11 +1582,12 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) join_kernel(const __gri
     }
     const HeadAt at = head_at(p, j.y);
     const float vscale = p.v_amax ? 1.0f / cache_scale(p.v_amax, at.shard * p.hk + at.kv) : 1.0f;
-    const float by = all == 0.0f ? 0.0f : vscale / all;
+    const float by = 1.0f / all;
     Act *o = static_cast<Act *>(p.o[at.shard]) + (static_cast<long long>(j.x) * p.hq + at.query + h) * p.D;
     auto put = [&](int e, const float4 &v) {
         if (e >= p.D) return;
-        const float4 r = all == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(v.x * by, v.y * by, v.z * by, v.w * by);
+        const float4 r = all == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                     : make_float4(v.x * by * vscale, v.y * by * vscale, v.z * by * vscale, v.w * by * vscale);
         if constexpr (sizeof(Act) == 2)
             *reinterpret_cast<uint2 *>(o + e) = make_uint2(pack_bf16x2(r.x, r.y), pack_bf16x2(r.z, r.w));
         else

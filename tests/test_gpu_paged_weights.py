@@ -209,3 +209,37 @@ def test_fp32_numbers_at_the_ends_of_their_range(tp, per, capacity):
         assert np.abs(o[row] / (1.0 + 2.0 * w) - 1.0).max() <= 8 * 2.0 ** -19 + 2.0 ** -19
     assert (o[3] == 1.0).all() and (o[4] == 1.0).all()
     assert np.abs(o[5] / (top / 4) - 1.0).max() <= 2.0 ** -19
+
+
+@pytest.mark.parametrize("v_amax", [2.0 ** -99, 2.0 ** -90, 2.9e38])
+@pytest.mark.parametrize("lengths,capacity", [([3000, 60], 0), ([3000, 60], 40000), ([90] * 400, 40000), ([30000], 0)])
+def test_value_scales_at_the_ends_of_their_range(tp, v_amax, lengths, capacity):
+    """Many equal weights, and a dominant position without a value before them, over values as small or large as
+    their calibration may be."""
+    rng = np.random.default_rng(3)
+    D, kv, per, rows = 64, 2, 4, len(lengths)
+    table, pages = table_for(rng, lengths, 16)
+    if capacity > table.shape[1] * 16:
+        table = np.pad(table, ((0, 0), (0, capacity // 16 - table.shape[1])), constant_values=-1)
+    h = tp.TPPagedAttention(per * kv, kv, D, 16, pages, dtype="fp8", scale=1.0, rope=tp.Rope(dim=0))
+    amax = torch.full((kv,), v_amax, device="cuda")
+    codes = torch.from_numpy(rng.integers(0x30, 0x78, (pages, kv, 16, D)).astype(np.uint8))   # 0.5 to 256
+    scale = float(np.float32(448) / np.float32(v_amax))
+    q = torch.zeros(rows, per * kv * D, dtype=torch.bfloat16)
+    q.view(rows, -1, D)[..., 0] = 4.0
+    for gap in (0, 20, 40):
+        K = torch.zeros(pages, kv, 16, D)
+        V = codes.clone()
+        if gap:
+            K[table[:, 0], :, 0, 0] = gap / 4
+            V[table[:, 0], :, 0] = 0
+        K = (K * 16).to(torch.float8_e4m3fn).view(torch.uint8)
+        o = torch.empty(rows, per * kv * D, dtype=torch.bfloat16, device="cuda")
+        at = np.array(lengths) - 1
+        h.decode(q.cuda(), cuda_i32(at), cuda_i32(table), K.cuda(), V.cuda(), o, tp.alloc_workspace(h.workspace_bytes()),
+                 k_amax=torch.full((kv,), AMAX, device="cuda"), v_amax=amax)
+        assert h.sync_status() == 0
+        want, mag, _, seen = ref.decode(q.view(rows, -1, D).double().numpy(), at, np.arange(rows), table, e4m3(K) / 16,
+                                        e4m3(V) / scale, 1.0)
+        # (the outputs at 2^-99 and 40 nats are 2^-148: bf16's own steps end at 2^-133, half of one is 2^-134)
+        check(o, want, bound(want, mag, np.zeros(want.shape[:2]), seen, D, "fp8") + 2.0 ** -134)
