@@ -1,4 +1,5 @@
-"""Calls of the C entry points that the binding does not make."""
+"""Calls that the other tests do not make: arrays that a type has no use for, numbers that are none, launches in plain
+stream order."""
 import numpy as np
 import pytest
 import torch
@@ -34,3 +35,77 @@ def test_calibration_is_of_codes_alone(dtype, lengths):
     assert tp.lib().tp_paged_decode(h._h, one(q2), *rows, one(K2), one(V2), one(o2), ws.data_ptr(), ws.numel(), _stream(None)) == 0
     assert h.sync_status() == 0
     assert same_bits(q, q2) and same_bits(K, K2) and same_bits(V, V2) and same_bits(o, o2)
+
+
+@pytest.mark.parametrize("capacity", [1, 400])   # clusters; single warps of the list, its shares and its join
+@pytest.mark.parametrize("gap", [0, 30])
+def test_codes_that_are_not_numbers(capacity, gap):
+    """NaN codes in keys and values that a row sees, and infinite and NaN queries, beside a dominant position or not."""
+    import tensor_transformer_mlp_shard_gb300 as tp
+    D, per, kv, rows = 64, 4, 2, 120
+    rng = np.random.default_rng(1)
+    lengths = [70] * (rows - 1) + [3000 if capacity > 1 else 70]
+    table, pages = table_for(rng, lengths, 16)
+    if capacity > table.shape[1]:
+        table = np.pad(table, ((0, 0), (0, capacity - table.shape[1])), constant_values=-1)
+    h = tp.TPPagedAttention(per * kv, kv, D, 16, pages, dtype="fp8", scale=1.0)
+    K = (torch.randn(h.cache_shape) * 8).to(torch.float8_e4m3fn)
+    V = (torch.randn(h.cache_shape) * 8).to(torch.float8_e4m3fn)
+    K, V = K.view(torch.uint8), V.view(torch.uint8)
+    K[..., 0] = 0
+    K[table[:, 1], :, 3, 0] = int(torch.tensor(16.0 * gap / 4).to(torch.float8_e4m3fn).view(torch.uint8))
+    q = (torch.randn(rows, per * kv, D) * 0.1).bfloat16()
+    q[..., 0] = 4.0
+    clean = (K.clone(), V.clone(), q.clone())
+    last = lengths[-1] // 16 - 1
+    V[table[1, 2], 0, 5, 7] = 0x7F
+    V[table[rows - 1, last], 1, 5, 9] = 0xFF
+    K[table[2, 0], 1, 15, 3] = 0x7F
+    q[3, 1, 5] = float("nan")
+    q[4, 6, 5] = float("inf")
+    amax = torch.full((kv,), 28.0, device="cuda")
+    out = []
+    for k, v, x in (clean, (K, V, q)):
+        o = torch.full((rows, per * kv * D), 9.0, dtype=torch.bfloat16, device="cuda")
+        h.decode(x.view(rows, -1).cuda(), cuda_i32(np.array(lengths) - 1), cuda_i32(table), k.cuda(), v.cuda(), o,
+                 tp.alloc_workspace(h.workspace_bytes()), k_amax=amax, v_amax=amax)
+        assert h.sync_status() == 0
+        out.append(o.view(rows, per * kv, D).cpu())
+    good, o = out
+    assert torch.isfinite(good).all()
+    bad = torch.zeros(rows, per * kv, D, dtype=torch.bool)
+    bad[1, :per, 7] = bad[rows - 1, per:, 9] = bad[2, per:] = bad[3, 1] = bad[4, 6] = True
+    assert torch.isnan(o[bad]).all()
+    assert same_bits(o[~bad], good[~bad])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+def test_launch_overlap_changes_no_kernel_s_results(dtype):
+    """Rotation, append and decode by clusters, one behind the other, in plain stream order and overlapped."""
+    import tensor_transformer_mlp_shard_gb300 as tp
+    act, n = TORCH[dtype], 300
+    h = tp.TPPagedAttention(8, 2, 64, 16, 19, dtype=dtype)
+    r = tp.TPRotary(n, 1, 8, 2, 64, dtype="f32" if dtype == "f32" else "bf16")
+    x0 = torch.randn(n, 12 * 64, device="cuda").to(act)
+    at, table = cuda_i32(np.arange(n)), cuda_i32(np.arange(19)[None])
+    seq, last = torch.zeros(n, dtype=torch.int32, device="cuda"), cuda_i32([n - 1])
+    amax = dict(k_amax=torch.full((2,), 6.0, device="cuda"), v_amax=torch.full((2,), 6.0, device="cuda")) if dtype == "fp8" else {}
+    ws, got = tp.alloc_workspace(h.workspace_bytes()), []
+    for on in (True, False):
+        tp.set_launch_overlap(on)
+        try:
+            for _ in range(3):
+                x = x0.clone()
+                K, V = (torch.zeros(h.cache_shape, dtype=h.cache_dtype, device="cuda") for _ in range(2))
+                q, o = torch.zeros(n, 8 * 64, dtype=act, device="cuda"), torch.zeros(1, 8 * 64, dtype=act, device="cuda")
+                r.fwd(x)
+                h.append(x, at, table, K, V, q, sequences=seq, **amax)
+                h.decode(q[n - 1:], last, table, K, V, o, ws, **amax)
+                r.bwd(x)
+                got.append((x, K, V, q, o))
+        finally:
+            tp.set_launch_overlap(True)
+    torch.cuda.synchronize()
+    assert h.sync_status() == 0 and bool(got[0][4].any())
+    for other in got[1:]:
+        assert all(same_bits(a, b) for a, b in zip(got[0], other))
