@@ -9,7 +9,8 @@ namespace attn {
 // up to 16 to the columns of the matrix instructions.  Above 128 elements a head
 // codes and fp32 take up to 8: with 16 the outputs leave a lane no registers for
 // the conversions (100 rows of 128 heads x 256 over 8: 8-bit 30 us in two passes,
-// 41 in one; bf16 42 and 41, and with 64 rows of up to 8000 positions 646 and 400).
+// 41 in one; bf16 42 and 41, and with 64 rows of up to 8000 positions 646 and 400,
+// although 16 queries of 256 elements spill some 530 bytes a thread, of 192 some 260).
 static void cut_queries(int dtype, int D, int per, int *groups, int *nh) {
     const int most = dtype == TP_DT_BF16 || D <= 128 ? 16 : 8;
     *groups = (per + most - 1) / most;

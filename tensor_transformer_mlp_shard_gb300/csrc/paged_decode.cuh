@@ -1,16 +1,16 @@
 // Decode attention over a paged cache: o = sum_j w_j v_j, w = softmax(scale q.k_j).
 //
 // Bound by HBM: each key and value is read once, for all queries of its head.
-// The positions of all rows and key heads are one list of units (64 positions;
-// fp32: 32), in order of row, head, position; every block takes an equal stretch of it
-// (as many blocks as are resident), so that uneven lengths load the SMs
+// The positions of all rows and key heads are one list of units (64 positions; of wide
+// fp32 heads 32), in order of row, head, position; every block takes an equal stretch
+// of it (as many blocks as are resident), so that uneven lengths load the SMs
 // evenly and one long row is split over all of them.  Within a stretch, the
 // units of one (row, head) are a segment; a segment that ends in another block
 // leaves its running maximum, sum and unnormalised output in the workspace, at
 // most two a block, and a second kernel joins them, in the blocks' order.
 //
-// Four warps share a unit, 16 (fp32: 8) positions each, and keep softmax states
-// of their own until the segment ends: no barrier in the loop.  Each warp has a
+// Four warps share a unit, 16 or 8 positions (a core's kRows) each, and keep softmax
+// states of their own until the segment ends: no barrier in the loop.  Each warp has a
 // ring of stages in shared memory that it fills by asynchronous 16-byte copies,
 // several steps ahead; what bounds the kernel is how many bytes are on their
 // way.  From there its lanes read fragments of the matrix instructions as they
@@ -156,6 +156,7 @@ __device__ __forceinline__ void fetch(const DecodePlan &p, const void *k, const 
         fetch_rows<Core, false>(row_bytes, kp, vp, s, to);
 }
 
+// 2^x to 2^-22 of itself, zero below 2^-126
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -211,7 +212,6 @@ struct TensorCore {
     __device__ __forceinline__ static int swizzle_keys(int row) { return swizzle_k<kRowBytes>(row); }
     __device__ __forceinline__ static int swizzle_values(int row) { return swizzle_v(row); }
     static constexpr int KC = k8 ? DP / 64 : DP / 32;       // 16-byte loads of a lane's key row
-    static constexpr int KE = k8 ? 16 : 8;                  // elements of one
     static constexpr int VD = k8 && DP % 128 == 0 ? 16 : 8; // elements of a lane's value load
     static constexpr int VB = DP / (8 * VD);
     static constexpr int VW = VD * (k8 ? 1 : 2) / 4;        // 32-bit words of one
