@@ -406,8 +406,9 @@ struct TensorCore {
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        // rounded up, so that no weight is above 2^kUp
-                        top[n][r] = __fadd_ru(top[n][r], -kUp);
+                        // rounded up, so that no weight is above 2^kUp, to a whole number, so that what is
+                        // there is scaled without error however often the reference goes up and down
+                        top[n][r] = ceilf(__fadd_ru(top[n][r], -kUp));
                         rise |= top[n][r] > m[n][r] + kRise;
                         fall |= top[n][r] < m[n][r] - kDrop;
                     }
