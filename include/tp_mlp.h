@@ -728,7 +728,8 @@ TP_API tp_status tp_paged_append(tp_paged *h, const void *const *X, const int32_
  * as the sum of two bf16 numbers (to 2^-17 of a weight); with FP8 as that of two
  * fp16 numbers, to 2^-22 of itself or of the largest weight of the 16 positions that
  * are read together (far below a row's largest: to 2^-17 down to 2^-70 of it, none
- * below 2^-88); fp32 numbers, with more than four queries to a key head, as two
+ * below 2^-88), and the queries as fp16 numbers times a power of two (a head's elements
+ * down to 2^-31 of its largest exactly, none below 2^-39); fp32 numbers, with more than four queries to a key head, as two
  * tf32 (to 2^-21 of a key's product, 2^-19.8 of a value's).  The long axis is split
  * over blocks, whose results are joined in a fixed order: outputs are deterministic.
  * workspace: >= tp_paged_workspace_bytes, 256-byte aligned; contents on entry

@@ -1040,7 +1040,7 @@ __device__ __forceinline__ Row row_at(const DecodePlan &p, int r, bool *bad) {
     const bool ok = pos < 0 || (static_cast<unsigned>(seq) < static_cast<unsigned>(p.at.table_rows) &&
                                 static_cast<int>(p.at.page.div(max(pos, 0))) < p.at.table_cols);
     if (bad) *bad = !ok;
-    x.last = ok ? pos : -1;
+    x.last = ok ? max(pos, -1) : -1;
     x.first = p.window > 0 ? max(0, x.last - p.window + 1) : 0;
     x.t0 = x.first / kUnit;
     x.units = x.last < 0 ? 1 : x.last / kUnit - x.t0 + 1;

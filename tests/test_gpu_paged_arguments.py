@@ -109,3 +109,23 @@ def test_launch_overlap_changes_no_kernel_s_results(dtype):
     assert h.sync_status() == 0 and bool(got[0][4].any())
     for other in got[1:]:
         assert all(same_bits(a, b) for a, b in zip(got[0], other))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("cols", [3, 4000])
+@pytest.mark.parametrize("window", [1, 2, 17, 2 ** 31 - 1])
+def test_padding_at_any_negative_position_with_a_window(dtype, cols, window):
+    """The first position that a row sees, p - window + 1, does not exist for the smallest int32."""
+    import tensor_transformer_mlp_shard_gb300 as tp
+    h = tp.TPPagedAttention(4, 2, 32, 16, 3, dtype=dtype, window=window)
+    act = TORCH[dtype]
+    K, V = (torch.ones(h.cache_shape, device="cuda").to(h.cache_dtype) for _ in range(2))
+    at = cuda_i32([-1, -2 ** 31, 40, -2 ** 31 + 1, -17])
+    table = torch.full((5, cols), -1, dtype=torch.int32, device="cuda")
+    table[2, :3] = cuda_i32([0, 1, 2])
+    q = torch.randn(5, 4 * 32, device="cuda").to(act)
+    o = torch.full_like(q, 5.0)
+    amax = dict(k_amax=torch.ones(2, device="cuda"), v_amax=torch.ones(2, device="cuda")) if dtype == "fp8" else {}
+    h.decode(q, at, table, K, V, o, tp.alloc_workspace(h.workspace_bytes()), **amax)
+    assert h.sync_status() == 0
+    assert not bool(o[[0, 1, 3, 4]].any()) and bool((o[2] != 0).all()) and bool(torch.isfinite(o[2]).all())
