@@ -367,8 +367,8 @@ struct TensorCore {
     // steps' largest down as well as up: a step whose largest weight is below
     // 2^(kUp - kDrop) has m lowered to it, and its weights are held to 2^-22 of that one.
     // Softmaxes without a dominant position hardly get there (scores of standard
-    // deviation 3.6: one step of 16 in 2000), and pay for the look (8-bit batch 141 us,
-    // 139 without; each row with such a position 143 us).
+    // deviation 3.6: one step of 16 in 2000), and pay for the look (8-bit batch 142 us,
+    // 139 without; each row with such a position 144 us).
     static constexpr float kUp = k8 ? 15.0f : 0.0f, kDrop = 18.0f;
     // The sum of weights stays below 2^kMostSum when the reference falls, and so the
     // outputs finite: weights below 2^-70 of the largest are held to fewer digits, below
